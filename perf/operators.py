@@ -116,7 +116,7 @@ def _quantized_rows(rows, cols, seed):
     s = x.abs().amax(-1).div(448.0).clamp_min(TINY)
     q = _pitched(rows, cols)
     q.copy_((x / s.unsqueeze(-1)).view(rows, -1)[:, :cols])
-    return q, s
+    return q, s.t().contiguous().t()
 
 
 def _popularity(e, skew, g):
@@ -139,7 +139,7 @@ def prepare(case, seed):
         wide = _activations(rows, cols + c["pitch"], _dt(c["dtype"]), seed)
         st["x"] = wide[:, :cols]
         st["q"] = _pitched(rows, cols)
-        st["scales"] = torch.empty(rows, _nb(cols), device="cuda")
+        st["scales"] = torch.empty(_nb(cols), rows, device="cuda").t()  # block by block, as the products read them
     elif op == "matmul":
         st["q"], st["scales"] = _quantized_rows(c["m"], c["k"], seed)
         st["w"], st["ws"] = (a[0] for a in _weight(1, c["n"], c["k"], seed, 3))
