@@ -16,17 +16,23 @@ from .build import LIB as LIB_PATH
 __all__ = ["MxError", "lib", "QLinear", "Ffn", "Sub", "Layout", "Options", "LAYOUT_MAGIC", "LAYOUT_VERSION",
            "MX_F32", "MX_BF16", "DeviceLayer", "layer_forward", "layer_forward_ex", "route", "stack_forward",
            "workspace_bytes", "stack_workspace_bytes", "workspace_init", "layer_forward_static", "EXPORTED",
-           "down_sb_bytes", "pack_down_sb"]
+           "down_sb_bytes", "pack_down_sb",
+           "MX_GELU_TANH", "MX_SILU", "Fp8Matrix", "Fp8Rows", "Fp8LayerStruct", "Fp8Weight", "Fp8Layer",
+           "fp8_quantize", "fp8_matmul", "fp8_grouped_matmul", "fp8_moe_forward", "fp8_matmul_workspace_bytes",
+           "fp8_moe_workspace_bytes"]
 
 LAYOUT_MAGIC = 0x4D584D45
 LAYOUT_VERSION = 3
 MX_F32, MX_BF16 = 0, 1
+MX_GELU_TANH, MX_SILU = 0, 1
 
 # Every symbol include/mx_moe.h declares.
 EXPORTED = ("mx_moe_layer_forward", "mx_moe_layer_forward_ex", "mx_moe_workspace_bytes", "mx_moe_workspace_init",
             "mx_moe_route", "mx_moe_stack_forward", "mx_moe_stack_workspace_bytes", "mx_status_string",
             "mx_last_error_string", "mx_version", "mx_moe_profile_enable", "mx_moe_profile_read",
-            "mx_moe_workspace_check", "mx_moe_layer_forward_static", "mx_moe_down_sb_bytes", "mx_moe_pack_down_sb")
+            "mx_moe_workspace_check", "mx_moe_layer_forward_static", "mx_moe_down_sb_bytes", "mx_moe_pack_down_sb",
+            "mx_fp8_quantize", "mx_fp8_matmul", "mx_fp8_grouped_matmul", "mx_fp8_matmul_workspace_bytes",
+            "mx_fp8_moe_forward", "mx_fp8_moe_workspace_bytes")
 
 
 class MxError(RuntimeError):
@@ -62,6 +68,21 @@ class Layout(C.Structure):
 
 class Options(C.Structure):
     _fields_ = [("residual", C.c_void_p), ("pre_rmsnorm", C.c_int32), ("rms_eps", C.c_float)]
+
+
+class Fp8Matrix(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int32), ("cols", C.c_int32),
+                ("count", C.c_int32), ("ld", C.c_int64)]
+
+
+class Fp8Rows(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("scales", C.c_void_p), ("rows", C.c_int32), ("cols", C.c_int32),
+                ("ld", C.c_int64), ("scale_row", C.c_int64), ("scale_block", C.c_int64)]
+
+
+class Fp8LayerStruct(C.Structure):
+    _fields_ = [(name, Fp8Matrix) for name in ("gate", "up", "down", "shared_gate", "shared_up", "shared_down")] + [
+        ("top_k", C.c_int32), ("act_dtype", C.c_int32), ("activation", C.c_int32), ("layer_scalar", C.c_float)]
 
 
 _lock = threading.Lock()
@@ -100,7 +121,17 @@ def lib():
             L.mx_moe_profile_enable.argtypes = [I32]
             L.mx_moe_workspace_check.argtypes = [P, P]
             L.mx_moe_profile_read.argtypes = [C.POINTER(C.c_double), C.POINTER(C.c_int), I32]
-            for name in ("mx_moe_layer_forward", "mx_moe_layer_forward_ex", "mx_moe_layer_forward_static",
+            I64 = C.c_int64
+            L.mx_fp8_quantize.argtypes = [P, I64, I32, I32, C.POINTER(Fp8Rows), P]
+            L.mx_fp8_matmul.argtypes = [C.POINTER(Fp8Rows), C.POINTER(Fp8Matrix), P, I64, I32, P, P, SZ]
+            L.mx_fp8_grouped_matmul.argtypes = [C.POINTER(Fp8Rows), P, C.POINTER(Fp8Matrix), P, I64, I32, P, P, SZ]
+            L.mx_fp8_matmul_workspace_bytes.argtypes = [C.POINTER(Fp8Matrix), I32]
+            L.mx_fp8_matmul_workspace_bytes.restype = SZ
+            L.mx_fp8_moe_forward.argtypes = [P, I32, P, P, C.POINTER(Fp8LayerStruct), P, P, P, P, SZ]
+            L.mx_fp8_moe_workspace_bytes.argtypes = [C.POINTER(Fp8LayerStruct), I32]
+            L.mx_fp8_moe_workspace_bytes.restype = SZ
+            for name in ("mx_fp8_quantize", "mx_fp8_matmul", "mx_fp8_grouped_matmul", "mx_fp8_moe_forward",
+                         "mx_moe_layer_forward", "mx_moe_layer_forward_ex", "mx_moe_layer_forward_static",
                          "mx_moe_workspace_init", "mx_moe_pack_down_sb",
                          "mx_moe_route", "mx_moe_stack_forward", "mx_moe_profile_enable", "mx_moe_profile_read",
                          "mx_moe_workspace_check"):
@@ -321,3 +352,174 @@ def profile_read(reset: bool = True) -> dict:
     n = (C.c_int * 3)()
     _check(lib().mx_moe_profile_read(ms, n, 1 if reset else 0))
     return {name: (ms[i], n[i]) for i, name in enumerate(PROFILE_STAGES)}
+
+
+# ------------------------------------------- FP8 block-scaled operators
+#
+# Tensors carry their own shapes and strides here, so these calls check them: a
+# wrong one raises MxError(-1) like a wrong argument of the library.  Work goes
+# to `stream`, by default the current stream of the tensors' device.
+
+_DTYPES = None  # torch dtype -> mx_dtype, filled on first use
+
+
+def _dtype_code(t, name):
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: MX_F32, torch.bfloat16: MX_BF16}
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise MxError(-1, f"{name} must be float32 or bfloat16, not {t.dtype}")
+    return code
+
+
+def _need(ok, msg):
+    if not ok:
+        raise MxError(-1, msg)
+
+
+def _is(t, dtype):
+    return str(t.dtype) == dtype
+
+
+class _on:
+    """The device of the call's tensors made current, and its stream handle."""
+
+    def __init__(self, device, stream, *others):
+        import torch
+        _need(device.type == "cuda", "tensors must be on a CUDA device")
+        for t in others:
+            _need(t is None or t.device == device, f"all tensors must be on {device}")
+        self.guard = None
+        if torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+        self.stream = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream_handle(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _fp8_matrix(w, scales, name):
+    _need(_is(w, "torch.float8_e4m3fn") and w.dim() in (2, 3), f"{name} must be float8_e4m3fn [count,] rows, cols")
+    rows, cols = w.shape[-2:]
+    count = w.shape[0] if w.dim() == 3 else 1
+    ld = w.stride(-2) if rows > 1 else -(-max(cols, w.stride(-2)) // 16) * 16
+    _need(w.stride(-1) == 1 or cols == 1, f"{name} must have contiguous rows")
+    _need(count == 1 or w.stride(0) == rows * ld, f"{name}: the matrices must follow one another")
+    want = (-(-rows // 128), -(-cols // 128))
+    _need(_is(scales, "torch.float32") and scales.is_contiguous() and tuple(scales.shape[-2:]) == want
+          and scales.numel() == count * want[0] * want[1],
+          f"{name}: scales must be contiguous float32 [{count}, {want[0]}, {want[1]}]")
+    _need(scales.device == w.device, f"{name}: scales must be on {w.device}")
+    return Fp8Matrix(w.data_ptr(), scales.data_ptr(), rows, cols, count, ld)
+
+
+def _fp8_rows(q, scales):
+    _need(q.dim() == 2 and _is(q, "torch.float8_e4m3fn"), "q must be float8_e4m3fn [rows, cols]")
+    rows, cols = q.shape
+    _need(q.stride(1) == 1 or cols == 1, "q must have contiguous rows")
+    _need(scales.dim() == 2 and _is(scales, "torch.float32") and scales.shape[0] == rows
+          and scales.shape[1] == -(-cols // 128), f"scales must be float32 [{rows}, {-(-cols // 128)}]")
+    ld = q.stride(0) if rows > 1 else -(-max(cols, q.stride(0)) // 16) * 16
+    return Fp8Rows(q.data_ptr(), scales.data_ptr(), rows, cols, ld, scales.stride(0), scales.stride(1))
+
+
+class Fp8Weight:
+    """Block-scaled e4m3 matrices on the device: ``w`` float8_e4m3fn [rows, cols] or [count, rows, cols], rows at
+    multiples of 16 bytes; ``scales`` float32 [count,] ceil(rows / 128), ceil(cols / 128).  The tensors are kept and
+    read by every call, not copied."""
+
+    def __init__(self, w, scales):
+        self.w, self.scales = w, scales
+        self.c = _fp8_matrix(w, scales, "w")
+
+
+class Fp8Layer:
+    """One MoE layer with FP8 weights.  ``gate``, ``up`` ([E, I, D]), ``down`` ([E, D, I]) and the three of
+    ``shared`` ([1, S, D], [1, S, D], [1, D, S], or None) are (w, scales) pairs as for Fp8Weight."""
+
+    def __init__(self, gate, up, down, shared=None, top_k=8, act_dtype=MX_BF16, activation=MX_GELU_TANH,
+                 layer_scalar=1.0):
+        self.tensors = [gate, up, down, *(shared or [])]
+        c = Fp8LayerStruct()
+        names = ("gate", "up", "down", "shared_gate", "shared_up", "shared_down")
+        for name, pair in zip(names, self.tensors):
+            setattr(c, name, _fp8_matrix(*pair, name))
+            _need(pair[0].device == gate[0].device, f"{name} must be on {gate[0].device}")
+        c.top_k, c.act_dtype, c.activation, c.layer_scalar = top_k, act_dtype, activation, layer_scalar
+        self.c = c
+        self.device = gate[0].device
+
+
+def fp8_quantize(x, q, scales, pow2=False, stream=None):
+    """Quantise the rows of ``x`` (float32 or bfloat16 [rows, cols]) into ``q`` (float8_e4m3fn) and ``scales``
+    (float32 [rows, ceil(cols / 128)], any strides; ``empty(blocks, rows).t()`` suits the products best)."""
+    _need(x.dim() == 2 and x.shape == q.shape and (x.stride(1) == 1 or x.shape[1] == 1),
+          "x and q must have the same shape, x contiguous rows")
+    r = _fp8_rows(q, scales)
+    if x.shape[0] > 1:
+        r.ld = q.stride(0)
+    with _on(x.device, stream, q, scales) as s:
+        _check(lib().mx_fp8_quantize(x.data_ptr(), max(x.stride(0), x.shape[1]), _dtype_code(x, "x"), int(pow2),
+                                     C.byref(r), s))
+
+
+def fp8_matmul_workspace_bytes(weight: Fp8Weight, rows: int) -> int:
+    return lib().mx_fp8_matmul_workspace_bytes(C.byref(weight.c), rows)
+
+
+def _product(q, scales, offsets, weight, out, ws, stream):
+    r = _fp8_rows(q, scales)
+    _need(out.dim() == 2 and out.shape[0] == r.rows and out.shape[1] == weight.c.rows
+          and (out.stride(1) == 1 or out.shape[1] == 1), f"out must be [{r.rows}, {weight.c.rows}], contiguous rows")
+    ldo = max(out.stride(0), out.shape[1])
+    code, nbytes = _dtype_code(out, "out"), ws.numel() * ws.element_size()
+    with _on(q.device, stream, scales, offsets, weight.w, out, ws) as s:
+        if offsets is None:
+            _check(lib().mx_fp8_matmul(C.byref(r), C.byref(weight.c), out.data_ptr(), ldo, code, s, ws.data_ptr(),
+                                       nbytes))
+        else:
+            _check(lib().mx_fp8_grouped_matmul(C.byref(r), offsets.data_ptr(), C.byref(weight.c), out.data_ptr(), ldo,
+                                               code, s, ws.data_ptr(), nbytes))
+
+
+def fp8_matmul(q, scales, weight: Fp8Weight, out, ws, stream=None):
+    """out = (q, scales) times the transposed ``weight``; out float32 or bfloat16 [rows, weight rows]."""
+    _product(q, scales, None, weight, out, ws, stream)
+
+
+def fp8_grouped_matmul(q, scales, offsets, weight: Fp8Weight, out, ws, stream=None):
+    """The same with rows [offsets[e], offsets[e + 1]) against matrix e; offsets int32 [count + 1] on the device."""
+    _need(_is(offsets, "torch.int32") and offsets.is_contiguous() and offsets.numel() == weight.c.count + 1,
+          f"offsets must be contiguous int32 [{weight.c.count + 1}]")
+    _product(q, scales, offsets, weight, out, ws, stream)
+
+
+def fp8_moe_workspace_bytes(layer: Fp8Layer, T: int) -> int:
+    return lib().mx_fp8_moe_workspace_bytes(C.byref(layer.c), T)
+
+
+def fp8_moe_forward(x, topk_idx, topk_w, layer: Fp8Layer, out, ws, residual=None, stream=None):
+    """The block after its routing (mx_fp8_moe_forward): x, out and residual [T, D] of the layer's act_dtype,
+    topk_idx int32 and topk_w float32 [T, top_k], all contiguous."""
+    c = layer.c
+    T = x.shape[0]
+    shape = (T, c.gate.cols)
+    for name, t in (("x", x), ("out", out), ("residual", residual)):
+        _need(t is None or (tuple(t.shape) == shape and t.is_contiguous() and _dtype_code(t, name) == c.act_dtype),
+              f"{name} must be a contiguous {list(shape)} tensor of the layer's act_dtype")
+    _need(tuple(topk_idx.shape) == (T, c.top_k) and topk_idx.is_contiguous() and _is(topk_idx, "torch.int32"),
+          f"topk_idx must be contiguous int32 [{T}, {c.top_k}]")
+    _need(tuple(topk_w.shape) == (T, c.top_k) and topk_w.is_contiguous() and _is(topk_w, "torch.float32"),
+          f"topk_w must be contiguous float32 [{T}, {c.top_k}]")
+    with _on(x.device, stream, topk_idx, topk_w, out, ws, residual, layer) as s:
+        _check(lib().mx_fp8_moe_forward(x.data_ptr(), T, topk_idx.data_ptr(), topk_w.data_ptr(), C.byref(c),
+                                        None if residual is None else residual.data_ptr(), out.data_ptr(), s,
+                                        ws.data_ptr(), ws.numel() * ws.element_size()))

@@ -7,6 +7,7 @@
 // runs entirely on the host, before any CUDA call, so a rejected call touches
 // neither the device nor the outputs.
 #include "mx_moe.h"
+#include "mx_error.h"
 #include "mx_internal.h"
 
 #include <algorithm>
@@ -20,10 +21,10 @@
 using namespace mx;
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
 
-mx_status fail(mx_status s, const char *fmt, ...)
+mx_status mx::fail(mx_status s, const char *fmt, ...)
 {
     va_list ap;
     va_start(ap, fmt);
@@ -31,6 +32,8 @@ mx_status fail(mx_status s, const char *fmt, ...)
     va_end(ap);
     return s;
 }
+
+namespace {
 
 mx_status cuda_fail(cudaError_t e, const char *what)
 {

@@ -1,0 +1,131 @@
+// mx_fp8.cuh -- what the translation units of the FP8 block-scaled operators
+// share: argument blocks, launchers, and the device helpers of their kernels.
+//
+// Numbers: e4m3 values with one fp32 scale for each 128 columns of an
+// activation row and for each 128 x 128 block of a weight matrix.
+#pragma once
+
+#include "mx_common.cuh"
+#include "mx_internal.h"
+#include "mx_moe.h"
+
+
+namespace mx {
+namespace fp8 {
+
+constexpr int kBlk = 128;        // columns (and weight rows) that share a scale
+constexpr float kMaxE4M3 = 448.0f;
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: a block of zeros keeps a usable scale
+constexpr int kFewTokens = 64;   // largest T of the two-launch layer path (all tokens as one operand tile)
+
+__host__ __device__ constexpr int blocks(int n) { return (n + kBlk - 1) / kBlk; }
+__host__ __device__ constexpr int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
+
+// What a GEMM launch computes (see mx_fp8_gemm.cu).
+enum Mode {
+    kProduct = 0,  // out = rows x W^T, rows grouped by matrix (or one matrix)
+    kGateUp = 1,   // h = Q(act(rows Wg^T) * (rows Wu^T)), rows grouped by matrix
+    kFewGateUp = 2,  // the same for every active expert and the shared one, all tokens in each
+    kFewDown = 3     // out = residual + lambda * (sum over the active experts' and the shared expert's blocks)
+};
+
+struct GemmArgs {
+    CUtensorMap wa, wb;  // weights: (gate, up) or one matrix stack
+    CUtensorMap sa, sb;  // few tokens: the shared expert's
+    CUtensorMap xm;      // e4m3 operand rows (tokens)
+    int rows;            // operand rows (an upper bound when `offsets` is given)
+    int K, N, E;         // inner columns, weight rows per matrix, matrices
+    const int32_t *offsets;  // [E + 1] first row of each matrix's group, nullable: one group of all rows
+    const float *sx;         // operand scales: row r, block b at r * sx_r + b * sx_b
+    int64_t sx_r, sx_b;
+    const float *swa, *swb;  // weight scales [E][blocks(N)][blocks(K)]
+    const float *ssa, *ssb;  // few tokens: the shared expert's
+    void *out;               // kProduct, kFewDown
+    int64_t ldo;
+    int out_bf16;
+    uint8_t *h;          // kGateUp, kFewGateUp: e4m3 hidden
+    int64_t ldh;         // its row pitch (kGateUp)
+    float *hs;           // its scales
+    int64_t hs_ld;       // kGateUp: rows per block column of hs
+    int act;             // mx_activation
+    // few tokens
+    const int32_t *idx;  // [T][topk]
+    const float *wts;    // [T][topk]
+    int T, topk, IB, SB; // hidden blocks of a routed and of the shared expert
+    const void *residual;
+    float lam;
+    unsigned *err;
+    int xbox;            // rows of one operand copy
+    int stages, cl;      // ring depth, cluster size (split of the inner dimension)
+    int ncol_own;        // columns that one CTA of a cluster reduces, at most
+    int pdl;             // the launch may start before its predecessor has ended
+};
+
+cudaError_t launch_gemm(Mode mode, int nt, const GemmArgs &a, int grid, cudaStream_t s);
+// Dynamic shared memory of a launch with `stages` stages.
+size_t gemm_smem(Mode mode, int nt, int stages, int cl, int ncol_own);
+
+struct QuantArgs {
+    const void *x;       // [rows][cols]
+    int64_t rows, ldx;
+    int cols, bf16, pow2;
+    uint8_t *q;          // [rows][cols], row pitch ldq
+    int64_t ldq;
+    float *scales;       // row r, block b at r * s_r + b * s_b
+    int64_t s_r, s_b;
+    // copies of each row at the positions of its slots (nullable)
+    const int32_t *pos;  // [rows][topk], -1: none
+    int topk;
+    uint8_t *qr;         // row pitch ldq
+    float *sr;           // position p, block b at p + b * sr_b
+    int64_t sr_b;
+    int pdl;             // let the next launch start early
+};
+cudaError_t launch_quantize(const QuantArgs &a, cudaStream_t s);
+
+// Slots grouped by expert: offsets [E + 1] and pos [n] (-1 for an index outside
+// [0, E)).  counts and cursor: [E] scratch.  The order inside a group is not
+// fixed; no result depends on it.
+cudaError_t launch_group(const int32_t *idx, int n, int E, int32_t *counts, int32_t *cursor, int32_t *offsets,
+                         int32_t *pos, cudaStream_t s);
+
+struct CombineArgs {
+    const float *Y;      // [slots][D]
+    const float *Ys;     // [T][D], nullable
+    const int32_t *pos;  // [T][topk]
+    const float *wts;
+    const void *residual;
+    void *out;
+    int T, D, topk, bf16;
+    float lam;
+};
+cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s);
+
+// ------------------------------------------------------------ device helpers
+
+__device__ __forceinline__ float scale_of(float amax, int pow2)
+{
+    float s = __fdiv_rn(amax, kMaxE4M3);
+    s = s < kMinScale ? kMinScale : s;  // keeps a NaN
+    if (pow2 && s < INFINITY) {
+        const uint32_t b = __float_as_uint(s);
+        s = __uint_as_float((b + 0x7FFFFFu) & 0xFF800000u);
+    }
+    return s;
+}
+
+// Two floats to e4m3 (round to nearest even, saturating, NaN kept): lo in bits 0-7.
+__device__ __forceinline__ uint32_t e4m3_x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float load_act(const void *p, int64_t i, int bf16)
+{
+    return bf16 ? bf2f(__ldg(reinterpret_cast<const uint16_t *>(p) + i)) : __ldg(reinterpret_cast<const float *>(p) + i);
+}
+
+}  // namespace fp8
+}  // namespace mx

@@ -1,0 +1,589 @@
+// mx_fp8_api.cu -- the FP8 block-scaled entry points of include/mx_moe.h:
+// argument validation (all of it on the host, before any CUDA call), the
+// workspace plan, and the choice of tile, split and grid for each launch.
+#include "mx_error.h"
+#include "mx_fp8.cuh"
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+using namespace mx;
+using namespace mx::fp8;
+
+namespace {
+
+constexpr int kMaxCols = 1 << 20, kMaxRows = 1 << 28;
+constexpr size_t kErrBytes = 256;      // the workspace's error word
+constexpr int kSmem = 227 * 1024;      // shared memory of a CTA alone on its SM
+constexpr int kSmemHalf = 113 * 1024;  // of one of two
+
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+mx_status cuda_fail(cudaError_t e, const char *what)
+{
+    return fail(MX_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+int num_sms()
+{
+    static std::mutex mu;
+    static int cache[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return 148;
+    std::lock_guard<std::mutex> g(mu);
+    if (!cache[dev]) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+            n = 148;
+        cache[dev] = n;
+    }
+    return cache[dev];
+}
+
+// ---------------------------------------------------------------- validation
+
+mx_status check_matrix(const mx_fp8_matrix *m, const char *name)
+{
+    if (!m)
+        return fail(MX_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!m->w || !m->scales)
+        return fail(MX_ERR_INVALID_ARG, "%s has a NULL pointer", name);
+    if (m->rows < 1 || m->cols < 1 || m->rows > kMaxCols || m->cols > kMaxCols)
+        return fail(MX_ERR_UNSUPPORTED, "%s: shape [%d, %d] must be within [1, %d]", name, m->rows, m->cols, kMaxCols);
+    if (m->count < 1 || m->count > kMaxExperts)
+        return fail(MX_ERR_UNSUPPORTED, "%s: %d matrices, at most %d are supported", name, m->count, kMaxExperts);
+    if (m->ld < m->cols)
+        return fail(MX_ERR_INVALID_ARG, "%s: row pitch %lld is below its %d columns", name, (long long)m->ld, m->cols);
+    if (m->ld > 4 * (int64_t)kMaxCols)
+        return fail(MX_ERR_UNSUPPORTED, "%s: row pitch %lld is above %d", name, (long long)m->ld, 4 * kMaxCols);
+    if (!aligned(m->w, 16) || m->ld % 16)
+        return fail(MX_ERR_ALIGNMENT, "%s: address and row pitch must be multiples of 16 bytes", name);
+    if (!aligned(m->scales, 4))
+        return fail(MX_ERR_ALIGNMENT, "%s: scales must be 4-byte aligned", name);
+    return MX_OK;
+}
+
+mx_status check_rows(const mx_fp8_rows *r, const char *name, bool operand)
+{
+    if (!r)
+        return fail(MX_ERR_INVALID_ARG, "%s is NULL", name);
+    if (r->rows < 0 || r->rows > kMaxRows)
+        return fail(MX_ERR_INVALID_ARG, "%s: %d rows must be within [0, %d]", name, r->rows, kMaxRows);
+    if (r->cols < 1 || r->cols > kMaxCols)
+        return fail(MX_ERR_UNSUPPORTED, "%s: %d columns must be within [1, %d]", name, r->cols, kMaxCols);
+    if (r->ld < r->cols)
+        return fail(MX_ERR_INVALID_ARG, "%s: row pitch %lld is below its %d columns", name, (long long)r->ld, r->cols);
+    if (r->ld > ((int64_t)1 << 36))
+        return fail(MX_ERR_UNSUPPORTED, "%s: row pitch %lld is too large", name, (long long)r->ld);
+    if (r->scale_row < 0 || r->scale_block < 0)
+        return fail(MX_ERR_INVALID_ARG, "%s: negative scale strides", name);
+    if (r->rows == 0)
+        return MX_OK;
+    if (!r->q || !r->scales)
+        return fail(MX_ERR_INVALID_ARG, "%s has a NULL pointer", name);
+    if (operand && (!aligned(r->q, 16) || r->ld % 16))
+        return fail(MX_ERR_ALIGNMENT, "%s: address and row pitch must be multiples of 16 bytes", name);
+    if (!aligned(r->scales, 4))
+        return fail(MX_ERR_ALIGNMENT, "%s: scales must be 4-byte aligned", name);
+    return MX_OK;
+}
+
+mx_status check_dtype(int dtype, const char *name)
+{
+    if (dtype != MX_F32 && dtype != MX_BF16)
+        return fail(MX_ERR_INVALID_ARG, "%s %d is not MX_F32 or MX_BF16", name, dtype);
+    return MX_OK;
+}
+
+mx_status check_ws(const void *ws, size_t have, size_t need)
+{
+    if (!ws || have < need)
+        return fail(MX_ERR_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? have : (size_t)0, need);
+    if (!aligned(ws, 256))
+        return fail(MX_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    return MX_OK;
+}
+
+mx_status check_layer(const mx_fp8_layer *L)
+{
+    mx_status st;
+    if (!L)
+        return fail(MX_ERR_INVALID_ARG, "layer is NULL");
+    if ((st = check_matrix(&L->gate, "gate")) != MX_OK || (st = check_matrix(&L->up, "up")) != MX_OK ||
+        (st = check_matrix(&L->down, "down")) != MX_OK)
+        return st;
+    const int D = L->gate.cols, I = L->gate.rows, E = L->gate.count;
+    if (L->up.rows != I || L->up.cols != D || L->up.count != E || L->down.rows != D || L->down.cols != I ||
+        L->down.count != E)
+        return fail(MX_ERR_INVALID_ARG, "up must be %d x [%d, %d] and down %d x [%d, %d]", E, I, D, E, D, I);
+    if (L->shared_gate.w) {
+        if ((st = check_matrix(&L->shared_gate, "shared_gate")) != MX_OK ||
+            (st = check_matrix(&L->shared_up, "shared_up")) != MX_OK ||
+            (st = check_matrix(&L->shared_down, "shared_down")) != MX_OK)
+            return st;
+        const int S = L->shared_gate.rows;
+        if (L->shared_gate.cols != D || L->shared_gate.count != 1 || L->shared_up.rows != S ||
+            L->shared_up.cols != D || L->shared_up.count != 1 || L->shared_down.rows != D ||
+            L->shared_down.cols != S || L->shared_down.count != 1)
+            return fail(MX_ERR_INVALID_ARG, "the shared expert must be [%d, %d], [%d, %d] and [%d, %d]", S, D, S, D, D,
+                        S);
+    }
+    if (L->top_k < 1 || L->top_k > kMaxTopK)
+        return fail(MX_ERR_INVALID_ARG, "top_k %d must be in [1, %d]", L->top_k, kMaxTopK);
+    if ((st = check_dtype(L->act_dtype, "act_dtype")) != MX_OK)
+        return st;
+    if (L->activation != MX_GELU_TANH && L->activation != MX_SILU)
+        return fail(MX_ERR_INVALID_ARG, "activation %d is not MX_GELU_TANH or MX_SILU", L->activation);
+    return MX_OK;
+}
+
+// -------------------------------------------------------------- launch choice
+
+// Ring depth that fits `bytes` of shared memory, at most `want`.
+int fit_stages(Mode mode, int nt, int cl, int own, int bytes, int want)
+{
+    int s = std::min(want, 16);
+    while (s > 2 && gemm_smem(mode, nt, s, cl, own) > (size_t)bytes)
+        --s;
+    return s;
+}
+
+// Token tile for groups of about `n` rows: the smallest that holds one.
+int tile_for(double n, int most)
+{
+    int nt = 16;
+    while (nt < most && nt < n)
+        nt *= 2;
+    return nt;
+}
+
+mx_status weight_map(CUtensorMap *m, const mx_fp8_matrix &w)
+{
+    const cudaError_t e =
+        tma_map_bytes(m, w.w, TmaBytes{(uint64_t)w.cols, (uint64_t)w.rows, (uint64_t)w.count, (uint64_t)w.ld, 128});
+    return e == cudaSuccess ? MX_OK : cuda_fail(e, "tensor map of a weight");
+}
+
+mx_status rows_map(CUtensorMap *m, const void *q, int64_t rows, int64_t cols, int64_t ld, int box)
+{
+    const cudaError_t e =
+        tma_map_bytes(m, q, TmaBytes{(uint64_t)cols, (uint64_t)rows, 0, (uint64_t)ld, (uint32_t)box});
+    return e == cudaSuccess ? MX_OK : cuda_fail(e, "tensor map of the activations");
+}
+
+// One product launch over rows grouped by matrix (offsets NULL: one group).
+// `avg` is the expected size of a group.
+mx_status run_product(Mode mode, GemmArgs &g, const void *q, int64_t ldq, double avg, cudaStream_t s)
+{
+    const int sms = num_sms();
+    const int FT = blocks(g.N), KB = blocks(g.K), most = mode == kGateUp ? 128 : 256;
+    int nt = tile_for(g.offsets ? avg + 2 * std::sqrt(avg) : g.rows, most);
+    double tiles = g.offsets ? (double)g.E : std::ceil((double)g.rows / nt);
+    if (!g.offsets)
+        while (nt > 128 && tiles * FT < sms) {  // too few units to go round: smaller ones
+            nt /= 2;
+            tiles = std::ceil((double)g.rows / nt);
+        }
+    int cl = 1;
+    if (!g.offsets && nt <= 64 && mode == kProduct)
+        while (cl < 8 && tiles * FT * cl * 2 <= sms && KB / (cl * 2) >= 2)
+            cl *= 2;
+    g.cl = cl;
+    g.ncol_own = (std::min(nt, g.rows) + cl - 1) / cl;
+    g.xbox = std::min(nt, 64);
+    g.stages = fit_stages(mode, nt, cl, g.ncol_own, kSmem, std::max(2, KB));
+    mx_status st = rows_map(&g.xm, q, g.rows, g.K, ldq, g.xbox);
+    if (st != MX_OK)
+        return st;
+    int64_t units = g.offsets ? (int64_t)1 << 30 : (int64_t)tiles * FT;
+    const int grid = (int)std::min<int64_t>(sms / cl, units) * cl;
+    const cudaError_t e = launch_gemm(mode, nt, g, grid, s);
+    return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
+}
+
+mx_status product(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_matrix *w, void *out, int64_t ldo,
+                  int out_dtype, void *stream, void *ws, size_t ws_bytes)
+{
+    mx_status st;
+    if ((st = check_rows(x, "x", true)) != MX_OK || (st = check_matrix(w, "w")) != MX_OK ||
+        (st = check_dtype(out_dtype, "out_dtype")) != MX_OK)
+        return st;
+    if (x->cols != w->cols)
+        return fail(MX_ERR_INVALID_ARG, "x has %d columns, w has %d", x->cols, w->cols);
+    if (ldo < w->rows)
+        return fail(MX_ERR_INVALID_ARG, "output row pitch %lld is below its %d columns", (long long)ldo, w->rows);
+    if (x->rows == 0)
+        return MX_OK;
+    if (!out)
+        return fail(MX_ERR_INVALID_ARG, "out is NULL");
+    if (!aligned(out, out_dtype == MX_BF16 ? 2 : 4))
+        return fail(MX_ERR_ALIGNMENT, "out is misaligned");
+    if ((st = check_ws(ws, ws_bytes, kErrBytes)) != MX_OK)
+        return st;
+    GemmArgs g{};
+    g.rows = x->rows;
+    g.K = w->cols;
+    g.N = w->rows;
+    g.E = w->count;
+    g.offsets = offsets;
+    g.sx = x->scales;
+    g.sx_r = x->scale_row;
+    g.sx_b = x->scale_block;
+    g.swa = w->scales;
+    g.out = out;
+    g.ldo = ldo;
+    g.out_bf16 = out_dtype == MX_BF16;
+    g.err = static_cast<unsigned *>(ws);
+    if ((st = weight_map(&g.wa, *w)) != MX_OK)
+        return st;
+    return run_product(kProduct, g, x->q, x->ld, offsets ? (double)x->rows / w->count : x->rows,
+                       static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------------ the layer
+
+struct Plan {
+    // all paths: e4m3 activations and their scales [blocks(D)][T]
+    size_t xq, sx;
+    // up to kFewTokens tokens: hidden tiles [item][nt][128] and factors [item][nt]
+    size_t h, hs;
+    int nt, items;
+    // more: grouping, gathered rows, hidden rows, per-slot outputs
+    size_t counts, cursor, offsets, pos, xr, sr, hr, hrs, hsh, hshs, y, ys;
+    size_t total;
+};
+
+Plan make_plan(const mx_fp8_layer *L, int T)
+{
+    const int64_t D = L->gate.cols, I = L->gate.rows, E = L->gate.count, K = L->top_k;
+    const int64_t S = L->shared_gate.w ? L->shared_gate.rows : 0;
+    const int64_t IB = blocks((int)I), SB = blocks((int)S), DB = blocks((int)D), n = T * K;
+    Plan p{};
+    size_t o = kErrBytes;
+    auto take = [&](int64_t bytes) {
+        const size_t at = o;
+        o += up256((size_t)bytes);
+        return at;
+    };
+    p.xq = take(T * up16(D));
+    p.sx = take(DB * T * 4);
+    if (T <= kFewTokens) {
+        p.nt = tile_for(T, kFewTokens);
+        p.items = (int)(std::min(n, E) * IB + SB);
+        p.h = take((int64_t)p.items * p.nt * kBlk);
+        p.hs = take((int64_t)p.items * p.nt * 4);
+    } else {
+        p.counts = take(2 * E * 4);
+        p.cursor = p.counts + E * 4;
+        p.offsets = take((E + 1) * 4);
+        p.pos = take(n * 4);
+        p.xr = take(n * up16(D));
+        p.sr = take(DB * n * 4);
+        p.hr = take(n * IB * kBlk);
+        p.hrs = take(IB * n * 4);
+        p.hsh = take(T * SB * kBlk);
+        p.hshs = take(SB * T * 4);
+        p.y = take(n * D * 4);
+        p.ys = take(S ? T * D * 4 : 0);
+    }
+    p.total = o;
+    return p;
+}
+
+void matrices(GemmArgs &g, const mx_fp8_matrix &a, const mx_fp8_matrix *b)
+{
+    g.K = a.cols;
+    g.N = a.rows;
+    g.E = a.count;
+    g.swa = a.scales;
+    g.swb = b ? b->scales : nullptr;
+}
+
+// Up to kFewTokens tokens: quantise, then gate/up and down over the active
+// experts, each launched while its predecessor still runs so that its weights
+// are on their way when its operand is ready.
+mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, const mx_fp8_layer *L,
+                  const void *residual, void *out, cudaStream_t s, uint8_t *ws)
+{
+    const Plan p = make_plan(L, T);
+    const int D = L->gate.cols, I = L->gate.rows, E = L->gate.count, K = L->top_k, sms = num_sms();
+    const bool shared = L->shared_gate.w != nullptr;
+    const int IB = blocks(I), SB = shared ? blocks(L->shared_gate.rows) : 0;
+    mx_status st;
+    cudaError_t e;
+
+    QuantArgs q{};
+    q.x = x;
+    q.rows = T;
+    q.ldx = D;
+    q.cols = D;
+    q.bf16 = L->act_dtype == MX_BF16;
+    q.q = ws + p.xq;
+    q.ldq = up16(D);
+    q.scales = reinterpret_cast<float *>(ws + p.sx);
+    q.s_r = 1;
+    q.s_b = T;
+    q.pdl = 1;
+    if ((e = launch_quantize(q, s)) != cudaSuccess)
+        return cuda_fail(e, "FP8 quantisation");
+
+    GemmArgs g{};
+    matrices(g, L->gate, &L->up);
+    g.rows = T;
+    g.sx = q.scales;
+    g.sx_r = 1;
+    g.sx_b = T;
+    g.h = ws + p.h;
+    g.hs = reinterpret_cast<float *>(ws + p.hs);
+    g.act = L->activation;
+    g.idx = idx;
+    g.wts = wts;
+    g.T = T;
+    g.topk = K;
+    g.IB = IB;
+    g.SB = SB;
+    g.err = reinterpret_cast<unsigned *>(ws);
+    g.pdl = 1;
+    if ((st = weight_map(&g.wa, L->gate)) != MX_OK || (st = weight_map(&g.wb, L->up)) != MX_OK ||
+        (st = rows_map(&g.xm, ws + p.xq, T, D, up16(D), p.nt)) != MX_OK)
+        return st;
+    if (shared) {
+        g.ssa = L->shared_gate.scales;
+        g.ssb = L->shared_up.scales;
+        if ((st = weight_map(&g.sa, L->shared_gate)) != MX_OK || (st = weight_map(&g.sb, L->shared_up)) != MX_OK)
+            return st;
+    }
+    g.xbox = p.nt;
+    // experts that T tokens are expected to select, each on its own draw of K
+    const double active = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)K / E), (double)T));
+    const double units = active * IB + SB;
+    const int DB = blocks(D);
+    const int most = p.nt == 16 ? 8 : p.nt == 32 ? 4 : 2;
+    g.cl = 1;
+    while (g.cl < most && units * g.cl * 2 <= 2.0 * sms && DB / (g.cl * 2) >= 2)
+        g.cl *= 2;
+    g.ncol_own = (T + g.cl - 1) / g.cl;
+    const int per_sm = p.nt <= 32 ? 2 : 1;
+    const int smem = per_sm == 2 ? kSmemHalf : kSmem;
+    g.stages = fit_stages(kFewGateUp, p.nt, g.cl, g.ncol_own, smem, 16);
+    int grid = std::max(1, std::min(per_sm * sms / g.cl, p.items)) * g.cl;
+    if ((e = launch_gemm(kFewGateUp, p.nt, g, grid, s)) != cudaSuccess)
+        return cuda_fail(e, "FP8 gate/up");
+
+    GemmArgs d = g;
+    matrices(d, L->down, nullptr);
+    d.out = out;
+    d.ldo = D;
+    d.out_bf16 = L->act_dtype == MX_BF16;
+    d.residual = residual;
+    d.lam = L->layer_scalar;
+    d.pdl = 0;
+    if ((st = weight_map(&d.wa, L->down)) != MX_OK ||
+        (st = rows_map(&d.xm, ws + p.h, (int64_t)p.items * p.nt, kBlk, kBlk, p.nt)) != MX_OK)
+        return st;
+    if (shared) {
+        d.ssa = L->shared_down.scales;
+        if ((st = weight_map(&d.sa, L->shared_down)) != MX_OK)
+            return st;
+    }
+    const double items = active * IB + SB;
+    d.cl = 1;
+    while (d.cl < most && DB * d.cl * 2 <= 2 * sms && items / (d.cl * 2) >= 2)
+        d.cl *= 2;
+    d.ncol_own = (T + d.cl - 1) / d.cl;
+    d.stages = fit_stages(kFewDown, p.nt, d.cl, d.ncol_own, smem, 16);
+    grid = std::min(per_sm * sms / d.cl, DB) * d.cl;
+    if ((e = launch_gemm(kFewDown, p.nt, d, grid, s)) != cudaSuccess)
+        return cuda_fail(e, "FP8 down");
+    return MX_OK;
+}
+
+mx_status run_many(const void *x, int T, const int32_t *idx, const float *wts, const mx_fp8_layer *L,
+                   const void *residual, void *out, cudaStream_t s, uint8_t *ws)
+{
+    const Plan p = make_plan(L, T);
+    const int D = L->gate.cols, I = L->gate.rows, E = L->gate.count, K = L->top_k, n = T * K;
+    const bool shared = L->shared_gate.w != nullptr;
+    const int IB = blocks(I), S = shared ? L->shared_gate.rows : 0, SB = blocks(S);
+    auto f32 = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
+    auto i32 = [&](size_t o) { return reinterpret_cast<int32_t *>(ws + o); };
+    mx_status st;
+    cudaError_t e;
+
+    if ((e = launch_group(idx, n, E, i32(p.counts), i32(p.cursor), i32(p.offsets), i32(p.pos), s)) != cudaSuccess)
+        return cuda_fail(e, "grouping");
+    QuantArgs q{};
+    q.x = x;
+    q.rows = T;
+    q.ldx = D;
+    q.cols = D;
+    q.bf16 = L->act_dtype == MX_BF16;
+    q.q = shared ? ws + p.xq : nullptr;
+    q.ldq = up16(D);
+    q.scales = f32(p.sx);
+    q.s_r = 1;
+    q.s_b = T;
+    q.pos = i32(p.pos);
+    q.topk = K;
+    q.qr = ws + p.xr;
+    q.sr = f32(p.sr);
+    q.sr_b = n;
+    if ((e = launch_quantize(q, s)) != cudaSuccess)
+        return cuda_fail(e, "FP8 quantisation");
+
+    for (int sh = 0; sh < (shared ? 2 : 1); ++sh) {
+        const double avg = sh ? T : (double)n / E;
+        const mx_fp8_matrix &wg = sh ? L->shared_gate : L->gate, &wu = sh ? L->shared_up : L->up;
+        const mx_fp8_matrix &wd = sh ? L->shared_down : L->down;
+        const int rows = sh ? T : n, HB = sh ? SB : IB;
+        GemmArgs g{};
+        matrices(g, wg, &wu);
+        g.rows = rows;
+        g.offsets = sh ? nullptr : i32(p.offsets);
+        g.sx = f32(sh ? p.sx : p.sr);
+        g.sx_r = 1;
+        g.sx_b = rows;
+        g.h = ws + (sh ? p.hsh : p.hr);
+        g.ldh = (int64_t)HB * kBlk;
+        g.hs = f32(sh ? p.hshs : p.hrs);
+        g.hs_ld = rows;
+        g.act = L->activation;
+        g.err = reinterpret_cast<unsigned *>(ws);
+        if ((st = weight_map(&g.wa, wg)) != MX_OK || (st = weight_map(&g.wb, wu)) != MX_OK ||
+            (st = run_product(kGateUp, g, ws + (sh ? p.xq : p.xr), up16(D), avg, s)) != MX_OK)
+            return st;
+        GemmArgs d{};
+        matrices(d, wd, nullptr);
+        d.rows = rows;
+        d.offsets = g.offsets;
+        d.sx = g.hs;
+        d.sx_r = 1;
+        d.sx_b = rows;
+        d.out = ws + (sh ? p.ys : p.y);
+        d.ldo = D;
+        d.err = g.err;
+        if ((st = weight_map(&d.wa, wd)) != MX_OK || (st = run_product(kProduct, d, g.h, g.ldh, avg, s)) != MX_OK)
+            return st;
+    }
+
+    CombineArgs c{};
+    c.Y = f32(p.y);
+    c.Ys = shared ? f32(p.ys) : nullptr;
+    c.pos = i32(p.pos);
+    c.wts = wts;
+    c.residual = residual;
+    c.out = out;
+    c.T = T;
+    c.D = D;
+    c.topk = K;
+    c.bf16 = L->act_dtype == MX_BF16;
+    c.lam = L->layer_scalar;
+    if ((e = launch_combine(c, s)) != cudaSuccess)
+        return cuda_fail(e, "combine");
+    return MX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_fp8_quantize(const void *x, int64_t ldx, int dtype, int pow2, const mx_fp8_rows *out, void *stream)
+{
+    mx_status st;
+    if ((st = check_rows(out, "out", false)) != MX_OK || (st = check_dtype(dtype, "dtype")) != MX_OK)
+        return st;
+    if (pow2 != 0 && pow2 != 1)
+        return fail(MX_ERR_INVALID_ARG, "pow2 %d is not 0 or 1", pow2);
+    if (ldx < out->cols)
+        return fail(MX_ERR_INVALID_ARG, "input row pitch %lld is below its %d columns", (long long)ldx, out->cols);
+    if (out->rows == 0)
+        return MX_OK;
+    if (!x)
+        return fail(MX_ERR_INVALID_ARG, "x is NULL");
+    if (!aligned(x, dtype == MX_BF16 ? 2 : 4))
+        return fail(MX_ERR_ALIGNMENT, "x is misaligned");
+    QuantArgs q{};
+    q.x = x;
+    q.rows = out->rows;
+    q.ldx = ldx;
+    q.cols = out->cols;
+    q.bf16 = dtype == MX_BF16;
+    q.pow2 = pow2;
+    q.q = static_cast<uint8_t *>(out->q);
+    q.ldq = out->ld;
+    q.scales = out->scales;
+    q.s_r = out->scale_row;
+    q.s_b = out->scale_block;
+    const cudaError_t e = launch_quantize(q, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 quantisation");
+}
+
+size_t mx_fp8_matmul_workspace_bytes(const mx_fp8_matrix *w, int rows)
+{
+    return check_matrix(w, "w") == MX_OK && rows >= 0 ? kErrBytes : 0;
+}
+
+mx_status mx_fp8_matmul(const mx_fp8_rows *x, const mx_fp8_matrix *w, void *out, int64_t ldo, int out_dtype,
+                        void *stream, void *ws, size_t ws_bytes)
+{
+    if (w && w->count != 1)
+        return fail(MX_ERR_INVALID_ARG, "w holds %d matrices, one is wanted", w->count);
+    return product(x, nullptr, w, out, ldo, out_dtype, stream, ws, ws_bytes);
+}
+
+mx_status mx_fp8_grouped_matmul(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_matrix *w, void *out,
+                                int64_t ldo, int out_dtype, void *stream, void *ws, size_t ws_bytes)
+{
+    if (!offsets)
+        return fail(MX_ERR_INVALID_ARG, "offsets is NULL");
+    if (!aligned(offsets, 4))
+        return fail(MX_ERR_ALIGNMENT, "offsets must be 4-byte aligned");
+    return product(x, offsets, w, out, ldo, out_dtype, stream, ws, ws_bytes);
+}
+
+size_t mx_fp8_moe_workspace_bytes(const mx_fp8_layer *layer, int T_max)
+{
+    if (check_layer(layer) != MX_OK || T_max < 0 || (int64_t)T_max * layer->top_k > kMaxRows)
+        return 0;
+    const int t = std::max(T_max, 1);
+    size_t n = make_plan(layer, std::min(t, kFewTokens)).total;
+    if (t > kFewTokens)
+        n = std::max(n, make_plan(layer, t).total);
+    return n;
+}
+
+mx_status mx_fp8_moe_forward(const void *x, int T, const int32_t *topk_idx, const float *topk_w,
+                             const mx_fp8_layer *layer, const void *residual, void *out, void *stream, void *ws,
+                             size_t ws_bytes)
+{
+    mx_status st;
+    if ((st = check_layer(layer)) != MX_OK)
+        return st;
+    if (T < 0 || (int64_t)T * layer->top_k > kMaxRows)
+        return fail(MX_ERR_INVALID_ARG, "T = %d must be >= 0 and T * top_k <= %d", T, kMaxRows);
+    if (T == 0)
+        return MX_OK;
+    if (!x || !topk_idx || !topk_w || !out)
+        return fail(MX_ERR_INVALID_ARG, "x, topk_idx, topk_w and out must not be NULL");
+    if (!aligned(x, 16) || !aligned(out, 16) || !aligned(residual, 16) || !aligned(topk_idx, 4) || !aligned(topk_w, 4))
+        return fail(MX_ERR_ALIGNMENT, "x, out and residual must be 16-byte aligned, topk_idx and topk_w 4-byte");
+    if ((st = check_ws(ws, ws_bytes, make_plan(layer, T).total)) != MX_OK)
+        return st;
+    const size_t bytes = (size_t)T * layer->gate.cols * (layer->act_dtype == MX_BF16 ? 2 : 4);
+    const void *ins[2] = {x, residual};
+    for (const void *in : ins) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
+        if (in && a != b && a < b + bytes && b < a + bytes)
+            return fail(MX_ERR_INVALID_ARG, "out overlaps an input without being it");
+    }
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    return T <= kFewTokens ? run_few(x, T, topk_idx, topk_w, layer, residual, out, s, w)
+                           : run_many(x, T, topk_idx, topk_w, layer, residual, out, s, w);
+}
+
+}  // extern "C"

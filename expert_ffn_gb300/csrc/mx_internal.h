@@ -110,6 +110,14 @@ struct FfnMaps {
 };
 cudaError_t get_ffn_maps(const FfnArgs &a, FfnMaps *out);
 
+// A byte matrix (count 0), or a stack of them, as a map whose boxes are 128
+// bytes x box_rows rows, in the 128-byte swizzle; pitch a multiple of 16 bytes.
+struct TmaBytes {
+    uint64_t cols, rows, count, pitch;
+    uint32_t box_rows;
+};
+cudaError_t tma_map_bytes(CUtensorMap *m, const void *base, const TmaBytes &t);
+
 // Launch configuration of the routing kernel for T tokens.
 struct RouteLaunch {
     int TT, ET, GC, n_tt, n_et;

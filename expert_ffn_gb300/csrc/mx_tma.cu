@@ -75,6 +75,19 @@ int g_n = 0, g_next = 0;
 
 } // namespace
 
+cudaError_t tma_map_bytes(CUtensorMap *m, const void *base, const TmaBytes &t)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {t.cols, t.rows, t.count}, strides[2] = {t.pitch, t.pitch * t.rows};
+    const cuuint32_t box[3] = {128, t.box_rows, 1}, es[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, t.count ? 3 : 2, const_cast<void *>(base), dims, strides,
+                          box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t smem_optin(const void *k, size_t bytes)
 {
     if (bytes <= 48 * 1024)

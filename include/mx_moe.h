@@ -354,6 +354,116 @@ MX_API mx_status mx_moe_pack_down_sb(const mx_moe_layout *layout, const void *bl
 MX_API mx_status mx_moe_profile_enable(int on);
 MX_API mx_status mx_moe_profile_read(double *ms, int *launches, int reset);
 
+/* ------------------------------------------------------------------------
+ * FP8 block-scaled operators: the block's products for weights held as e4m3
+ * with one fp32 scale for each 128 x 128 block, and activations quantised to
+ * e4m3 with one fp32 scale for each row and 128 columns.
+ *
+ *   value of an activation   x[r][c] = q[r][c] * s[r][c / 128]
+ *   value of a weight        w[o][c] = q[o][c] * s[o / 128][c / 128]
+ *   product                  y[r][o] = sum_b (sx[r][b] * sw[o / 128][b]) *
+ *                                      sum_{c in block b} qx[r][c] qw[o][c]
+ * with every sum in fp32 and one rounding to the output type.  The last block
+ * of columns (and of weight rows) may be shorter than 128; any size from 1 on
+ * is accepted.  A result does not depend on the other rows of a call, nor on
+ * timing.
+ *
+ * All calls are asynchronous on `stream` (NULL: the legacy default stream) and
+ * run on the current device, which has to own every buffer.  They allocate
+ * nothing and may be captured into a CUDA graph.  `ws` is a device workspace
+ * of at least the size that the matching *_workspace_bytes call returns,
+ * 256-byte aligned, prepared by mx_moe_workspace_init; its first word is the
+ * error word that mx_moe_workspace_check reads.  Calls (and captured graphs)
+ * that share a workspace must be ordered on the GPU.
+ * ------------------------------------------------------------------------ */
+
+/* A stack of `count` quantised matrices [rows][cols]. */
+typedef struct {
+    const void *w;        /* e4m3, row pitch ld bytes, matrices rows * ld bytes apart; 16-byte aligned */
+    const float *scales;  /* [count][ceil(rows / 128)][ceil(cols / 128)]                            */
+    int32_t rows, cols, count;
+    int64_t ld;           /* multiple of 16, >= cols                                                */
+} mx_fp8_matrix;
+
+/* Quantised activations [rows][cols]. */
+typedef struct {
+    void *q;              /* e4m3, row pitch ld bytes; 16-byte aligned                               */
+    float *scales;        /* row r, block b at r * scale_row + b * scale_block (elements, >= 0); the
+                             products read them fastest with scale_row == 1                         */
+    int32_t rows, cols;
+    int64_t ld;           /* multiple of 16, >= cols (mx_fp8_quantize takes any ld >= cols)          */
+    int64_t scale_row, scale_block;
+} mx_fp8_rows;
+
+/*
+ * Quantise activations: for each block of 128 columns of a row, a = max |x|,
+ *   s = max(fl32(a / 448), 2^-126);  with pow2 the smallest power of two >= s;
+ *   q = e4m3(fl32(x / s)), round to nearest, ties to even.
+ * A block with a NaN or an infinity gets that as its scale and dequantises to
+ * NaN.
+ *   x      device [rows][cols] of `dtype` (mx_dtype), row pitch ldx elements
+ *   out    q [rows][cols] and scales; only those elements are written
+ */
+MX_API mx_status mx_fp8_quantize(const void *x, int64_t ldx, int dtype, int pow2, const mx_fp8_rows *out,
+                                 void *stream);
+
+/*
+ * out[r][o] = sum_c x[r][c] w[o][c], one matrix (w->count == 1).
+ *   out    device [x->rows][w->rows] of out_dtype (mx_dtype), row pitch ldo elements
+ */
+MX_API mx_status mx_fp8_matmul(const mx_fp8_rows *x, const mx_fp8_matrix *w, void *out, int64_t ldo, int out_dtype,
+                               void *stream, void *ws, size_t ws_bytes);
+
+/*
+ * The same for rows grouped by matrix (the experts' products): rows
+ * [offsets[e], offsets[e + 1]) meet matrix e.
+ *   offsets  device int32 [w->count + 1], non-decreasing, within [0, x->rows]
+ *            (an entry outside is read as the nearest bound, a decreasing pair
+ *            as an empty group); w->count <= 512.  Groups may be empty.
+ *   out      rows that belong to no group are left as they were
+ */
+MX_API mx_status mx_fp8_grouped_matmul(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_matrix *w,
+                                       void *out, int64_t ldo, int out_dtype, void *stream, void *ws,
+                                       size_t ws_bytes);
+
+/* Workspace bytes of the two calls above for up to `rows` rows (0 on an invalid matrix). */
+MX_API size_t mx_fp8_matmul_workspace_bytes(const mx_fp8_matrix *w, int rows);
+
+typedef enum { MX_GELU_TANH = 0, MX_SILU = 1 } mx_activation;
+
+/* One layer: n_experts = gate.count routed experts (gate and up [I][D], down
+ * [D][I]) and, unless shared_gate.w is NULL, a dense shared expert (gate and up
+ * [S][D], down [D][S], count 1). */
+typedef struct {
+    mx_fp8_matrix gate, up, down;
+    mx_fp8_matrix shared_gate, shared_up, shared_down;
+    int32_t top_k;        /* 1 <= top_k <= 32                       */
+    int32_t act_dtype;    /* mx_dtype of x, residual and out        */
+    int32_t activation;   /* mx_activation                          */
+    float layer_scalar;   /* lambda                                 */
+} mx_fp8_layer;
+
+/*
+ * The block after its routing, with FP8 weights.  Per token t:
+ *   xq = quantise(x_t)
+ *   expert(x) = Wd quantise( act(Wg xq) * (Wu xq) )
+ *   out[t] = residual[t] + layer_scalar * ( shared(x_t) + sum_k topk_w[t,k] * expert_{topk_idx[t,k]}(x_t) )
+ *   x, residual, out  device [T][D]; residual nullable; out may be x or
+ *            residual itself but may not overlap them otherwise
+ *   topk_idx  device int32 [T][top_k], topk_w device fp32 [T][top_k], as
+ *            mx_moe_route writes them.  An index outside [0, n_experts)
+ *            contributes nothing; one that a token repeats counts each time.
+ * Up to 64 tokens the layer runs as two GEMM launches over the experts that some
+ * token selected, each of whose weights are read once; above, as grouped
+ * products.
+ */
+MX_API mx_status mx_fp8_moe_forward(const void *x, int T, const int32_t *topk_idx, const float *topk_w,
+                                    const mx_fp8_layer *layer, const void *residual, void *out, void *stream,
+                                    void *ws, size_t ws_bytes);
+
+/* Workspace bytes of mx_fp8_moe_forward for up to T_max tokens (0 on an invalid layer). */
+MX_API size_t mx_fp8_moe_workspace_bytes(const mx_fp8_layer *layer, int T_max);
+
 /* Human-readable status and the last error of the calling thread. */
 MX_API const char *mx_status_string(mx_status s);
 MX_API const char *mx_last_error_string(void);
