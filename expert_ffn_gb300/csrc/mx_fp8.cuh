@@ -43,6 +43,7 @@ struct GemmArgs {
     void *out;               // kProduct, kFewDown
     int64_t ldo;
     int out_bf16;
+    int out_vec;         // 16 bytes of neighbouring outputs may be stored at once
     uint8_t *h;          // kGateUp, kFewGateUp: e4m3 hidden
     int64_t ldh;         // its row pitch (kGateUp)
     float *hs;           // its scales
@@ -57,13 +58,14 @@ struct GemmArgs {
     unsigned *err;
     int xbox;            // rows of one operand copy
     int stages, cl;      // ring depth, cluster size (split of the inner dimension)
-    int ncol_own;        // columns that one CTA of a cluster reduces, at most
     int pdl;             // the launch may start before its predecessor has ended
 };
 
 cudaError_t launch_gemm(Mode mode, int nt, const GemmArgs &a, int grid, cudaStream_t s);
-// Dynamic shared memory of a launch with `stages` stages.
-size_t gemm_smem(Mode mode, int nt, int stages, int cl, int ncol_own);
+// The same for many rows: kProduct in tiles of 128 tokens x bn (128, 256) weight rows, or kGateUp.
+cudaError_t launch_rows(Mode mode, int bn, const GemmArgs &a, int grid, cudaStream_t s);
+// Dynamic shared memory of a launch_gemm with `stages` stages.
+size_t gemm_smem(Mode mode, int nt, int stages);
 
 struct QuantArgs {
     const void *x;       // [rows][cols]

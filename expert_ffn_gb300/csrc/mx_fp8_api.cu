@@ -144,10 +144,10 @@ mx_status check_layer(const mx_fp8_layer *L)
 // -------------------------------------------------------------- launch choice
 
 // Ring depth that fits `bytes` of shared memory, at most `want`.
-int fit_stages(Mode mode, int nt, int cl, int own, int bytes, int want)
+int fit_stages(Mode mode, int nt, int bytes, int want)
 {
     int s = std::min(want, 16);
-    while (s > 2 && gemm_smem(mode, nt, s, cl, own) > (size_t)bytes)
+    while (s > 2 && gemm_smem(mode, nt, s) > (size_t)bytes)
         --s;
     return s;
 }
@@ -160,6 +160,9 @@ int tile_for(double n, int most)
         nt *= 2;
     return nt;
 }
+
+// Whether rows of `out` start at multiples of 16 bytes.
+bool vec16(const void *out, int64_t ldo, int bf16) { return aligned(out, 16) && ldo * (bf16 ? 2 : 4) % 16 == 0; }
 
 mx_status weight_map(CUtensorMap *m, const mx_fp8_matrix &w)
 {
@@ -176,32 +179,37 @@ mx_status rows_map(CUtensorMap *m, const void *q, int64_t rows, int64_t cols, in
 }
 
 // One product launch over rows grouped by matrix (offsets NULL: one group).
-// `avg` is the expected size of a group.
+// `avg` is the expected size of a group.  More than 64 rows a group: tokens on
+// the M side; fewer: on the N side, in a tile that holds most groups.
 mx_status run_product(Mode mode, GemmArgs &g, const void *q, int64_t ldq, double avg, cudaStream_t s)
 {
-    const int sms = num_sms();
-    const int FT = blocks(g.N), KB = blocks(g.K), most = mode == kGateUp ? 128 : 256;
-    int nt = tile_for(g.offsets ? avg + 2 * std::sqrt(avg) : g.rows, most);
-    double tiles = g.offsets ? (double)g.E : std::ceil((double)g.rows / nt);
-    if (!g.offsets)
-        while (nt > 128 && tiles * FT < sms) {  // too few units to go round: smaller ones
-            nt /= 2;
-            tiles = std::ceil((double)g.rows / nt);
-        }
-    int cl = 1;
-    if (!g.offsets && nt <= 64 && mode == kProduct)
-        while (cl < 8 && tiles * FT * cl * 2 <= sms && KB / (cl * 2) >= 2)
-            cl *= 2;
-    g.cl = cl;
-    g.ncol_own = (std::min(nt, g.rows) + cl - 1) / cl;
-    g.xbox = std::min(nt, 64);
-    g.stages = fit_stages(mode, nt, cl, g.ncol_own, kSmem, std::max(2, KB));
-    mx_status st = rows_map(&g.xm, q, g.rows, g.K, ldq, g.xbox);
-    if (st != MX_OK)
+    const int sms = num_sms(), FT = blocks(g.N), KB = blocks(g.K);
+    mx_status st;
+    cudaError_t e;
+    g.cl = 1;
+    if (avg > 32.0) {
+        const int64_t tiles = g.offsets ? g.E : (g.rows + 127) / 128;
+        // (narrower tiles when the wide ones would leave SMs idle)
+        const int bn = mode == kGateUp || tiles * ((g.N + 255) / 256) >= sms ? 256 : 128;
+        g.xbox = avg >= 96.0 ? 128 : 32;
+        if ((st = rows_map(&g.xm, q, g.rows, g.K, ldq, g.xbox)) != MX_OK)
+            return st;
+        const int ft = mode == kGateUp ? FT : (g.N + bn - 1) / bn;
+        const int64_t units = g.offsets ? ((int64_t)g.rows / 128 + g.E) * ft : tiles * ft;
+        e = launch_rows(mode, bn, g, (int)std::min<int64_t>(sms, units), s);
+        return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
+    }
+    const int nt = tile_for(g.offsets ? avg + 2 * std::sqrt(avg) : g.rows, 64);
+    const int64_t tiles = g.offsets ? g.E : (g.rows + nt - 1) / nt;
+    if (!g.offsets && mode == kProduct)
+        while (g.cl < 4 && tiles * FT * g.cl * 2 <= sms && KB / (g.cl * 2) >= 2)
+            g.cl *= 2;
+    g.xbox = nt;
+    g.stages = fit_stages(mode, nt, kSmem, std::max(2, KB));
+    if ((st = rows_map(&g.xm, q, g.rows, g.K, ldq, g.xbox)) != MX_OK)
         return st;
-    int64_t units = g.offsets ? (int64_t)1 << 30 : (int64_t)tiles * FT;
-    const int grid = (int)std::min<int64_t>(sms / cl, units) * cl;
-    const cudaError_t e = launch_gemm(mode, nt, g, grid, s);
+    const int64_t units = g.offsets ? ((int64_t)g.rows / nt + g.E) * FT : tiles * FT;
+    e = launch_gemm(mode, nt, g, (int)std::min<int64_t>(sms / g.cl, units) * g.cl, s);
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
 }
 
@@ -237,6 +245,7 @@ mx_status product(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_mat
     g.out = out;
     g.ldo = ldo;
     g.out_bf16 = out_dtype == MX_BF16;
+    g.out_vec = vec16(out, ldo, g.out_bf16);
     g.err = static_cast<unsigned *>(ws);
     if ((st = weight_map(&g.wa, *w)) != MX_OK)
         return st;
@@ -362,14 +371,13 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
     const double active = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)K / E), (double)T));
     const double units = active * IB + SB;
     const int DB = blocks(D);
-    const int most = p.nt == 16 ? 8 : p.nt == 32 ? 4 : 2;
+    const int most = 4;
     g.cl = 1;
     while (g.cl < most && units * g.cl * 2 <= 2.0 * sms && DB / (g.cl * 2) >= 2)
         g.cl *= 2;
-    g.ncol_own = (T + g.cl - 1) / g.cl;
     const int per_sm = p.nt <= 32 ? 2 : 1;
     const int smem = per_sm == 2 ? kSmemHalf : kSmem;
-    g.stages = fit_stages(kFewGateUp, p.nt, g.cl, g.ncol_own, smem, 16);
+    g.stages = fit_stages(kFewGateUp, p.nt, smem, 16);
     int grid = std::max(1, std::min(per_sm * sms / g.cl, p.items)) * g.cl;
     if ((e = launch_gemm(kFewGateUp, p.nt, g, grid, s)) != cudaSuccess)
         return cuda_fail(e, "FP8 gate/up");
@@ -379,6 +387,7 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
     d.out = out;
     d.ldo = D;
     d.out_bf16 = L->act_dtype == MX_BF16;
+    d.out_vec = vec16(out, D, d.out_bf16);
     d.residual = residual;
     d.lam = L->layer_scalar;
     d.pdl = 0;
@@ -394,8 +403,7 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
     d.cl = 1;
     while (d.cl < most && DB * d.cl * 2 <= 2 * sms && items / (d.cl * 2) >= 2)
         d.cl *= 2;
-    d.ncol_own = (T + d.cl - 1) / d.cl;
-    d.stages = fit_stages(kFewDown, p.nt, d.cl, d.ncol_own, smem, 16);
+    d.stages = fit_stages(kFewDown, p.nt, smem, 16);
     grid = std::min(per_sm * sms / d.cl, DB) * d.cl;
     if ((e = launch_gemm(kFewDown, p.nt, d, grid, s)) != cudaSuccess)
         return cuda_fail(e, "FP8 down");
@@ -465,6 +473,7 @@ mx_status run_many(const void *x, int T, const int32_t *idx, const float *wts, c
         d.sx_b = rows;
         d.out = ws + (sh ? p.ys : p.y);
         d.ldo = D;
+        d.out_vec = vec16(d.out, D, 0);
         d.err = g.err;
         if ((st = weight_map(&d.wa, wd)) != MX_OK || (st = run_product(kProduct, d, g.h, g.ldh, avg, s)) != MX_OK)
             return st;

@@ -21,13 +21,13 @@
 //              into a ring of TMEM buffers
 //   EW + 2     factors: sx * sw of a block for each token into a ring in shared
 //              memory, so that the summing warps read them as broadcast vectors
-// Few units: a cluster of `cl` CTAs splits the inner dimension; each CTA reduces
-// every cl-th token column over the others' partial sums, which they store into
-// its shared memory, in rank order, so the result does not depend on timing.
+// Few units: a cluster of `cl` CTAs splits the inner dimension; each CTA sums
+// every cl-th token column over the partial sums in all their shared memories, in
+// rank order, so the result does not depend on timing.
 //
 // Every wait is bounded: a wait that gives up sets the caller's error word and
 // ends the CTA's work.
-#include "mx_fp8.cuh"
+#include "mx_fp8_tc.cuh"
 
 namespace mx {
 namespace fp8 {
@@ -54,182 +54,27 @@ constexpr uint32_t tmem_cols(int mode, int nt)
 }
 constexpr uint32_t stage_bytes(int mode, int nt) { return n_mats(mode) * kTile + nt * 128; }
 
+// Token columns of one pass of the epilogue (per warpgroup).
+constexpr int pass_cols(int mode, int nt) { return nt > 64 ? (n_mats(mode) == 2 ? 16 : 32) : nt < 32 ? nt : 32; }
+
 // Dynamic shared memory after the ring (byte offsets from its end).
 struct Tail {
-    int fac, am, red, tab, bars, total;
+    int fac, stage, tab, bars, total;
 };
-__host__ __device__ constexpr Tail tail_of(int mode, int nt, int cl, int ncol_own)
+__host__ __device__ constexpr Tail tail_of(int mode, int nt)
 {
     Tail t{};
     int o = 0;
+    t.stage = o;  // sums on their way out: [warpgroup][matrix][column][128 rows] fp32
+    o += epi_warps(nt) / 4 * n_mats(mode) * pass_cols(mode, nt) * 512;
     t.fac = o;
     o += kFacRing * n_mats(mode) * nt * 4;
-    t.am = o;  // per-warp column maxima (two units) and reciprocal scales
-    if (n_mats(mode) == 2)
-        o += 3 * 4 * nt * 4;
-    t.red = o;  // partial sums of the other CTAs of the cluster
-    if (cl > 1)
-        o += cl * ncol_own * n_mats(mode) * 128 * 4;
     t.tab = o;  // expert tables
     o += (3 * kMaxExperts + 16) * 4;
     t.bars = o;
     o += 640;
     t.total = o;
     return t;
-}
-
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr)
-{
-    return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
-// e4m3 A and B (K-major), fp32 D, M = 128, N = n.
-__device__ __forceinline__ uint32_t idesc_e4m3(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
-
-__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
-                 : "memory");
-}
-
-__device__ __forceinline__ void umma_commit(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-#define MX_R16(r, o)                                                                                                \
-    "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), \
-        "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]),          \
-        "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])
-
-// 16 columns of this warp's 32 TMEM lanes; the wait is part of the statement, so
-// nothing that reads r can be scheduled before it.
-__device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
-                 "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : MX_R16(r, 0)
-                 : "r"(ta)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
-                 "[%32];\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-                 "%30,%31}, [%33];\n\ttcgen05.wait::ld.sync.aligned;"
-                 : MX_R16(r, 0), MX_R16(r, 16)
-                 : "r"(ta), "r"(tb)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-                 "%3}], [%4];" ::"r"(smem_u32(dst)),
-                 "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-                 "%3, %4}], [%5];" ::"r"(smem_u32(dst)),
-                 "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v)
-{
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-__device__ __forceinline__ void arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-
-// Bounded wait: false once this CTA has given up.
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool bwait(uint64_t *bar, uint32_t parity, unsigned *err, volatile int *abort)
-{
-    auto done = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (done())
-        return true;
-    const unsigned long long t0 = global_ns();
-    while (!done()) {
-        if (*abort)
-            return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
-            atomicOr(err, kErrTimeout);
-            *abort = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
-// The same by a whole warp: every lane gets one answer.
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool wwait(uint64_t *bar, uint32_t parity, unsigned *err, volatile int *abort)
-{
-    return __all_sync(0xFFFFFFFFu, bwait<CLUSTER>(bar, parity, err, abort));
-}
-
-// Barrier over `count` threads that tells each whether all of them passed true.
-__device__ __forceinline__ bool named_and(int id, int count, bool v)
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"(id), "r"(count), "r"((uint32_t)v)
-                 : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ float act_of(float g, int act)
-{
-    return act == MX_SILU ? __fdividef(g, 1.0f + __expf(-g)) : gelu_fast(g);
 }
 
 // A unit of work.
@@ -317,16 +162,13 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const int NS = a.stages, cl = a.cl;
     uint8_t *tail = ring + NS * kStage;
-    const Tail T = tail_of(MODE, NT, cl, a.ncol_own);
+    constexpr Tail T = tail_of(MODE, NT);
     float *fac = reinterpret_cast<float *>(tail + T.fac);
-    float *am = reinterpret_cast<float *>(tail + T.am);
-    float *red = reinterpret_cast<float *>(tail + T.red);
     int *tab = reinterpret_cast<int *>(tail + T.tab);
     uint64_t *full = reinterpret_cast<uint64_t *>(tail + T.bars), *empty = full + 16;
     uint64_t *tfull = empty + 16, *tempty = tfull + 4, *ffull = tempty + 4, *fempty = ffull + kFacRing;
-    uint64_t *rfull = fempty + kFacRing;  // one per lane quadrant: partial sums have come in (4), then may be
-                                          // overwritten (4)
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(rfull + 8);
+    uint64_t *rfull = fempty + kFacRing;  // cluster: every CTA has staged its sums; rfull + 1: has read them
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(rfull + 2);
     volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cl > 1 ? cluster_rank() : 0;
@@ -347,10 +189,8 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
             mbar_init(ffull + i, 1);
             mbar_init(fempty + i, EW);
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(rfull + i, cl > 1 ? cl - 1 : 1);
-            mbar_init(rfull + 4 + i, cl > 1 ? cl - 1 : 1);
-        }
+        mbar_init(rfull, cl);
+        mbar_init(rfull + 1, cl);
         *abort = 0;
         fence_mbar_init();
     }
@@ -393,35 +233,8 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
         w.n_units = MODE == kFewGateUp ? n * a.IB + a.SB : w.FT;
     } else {
         int *tt = tab, *lo = tab + kMaxExperts + 1, *len = lo + kMaxExperts;
-        if (warp == 0) {
-            int run = 0;
-            for (int e0 = 0; e0 < a.E; e0 += 32) {
-                const int e = e0 + lane;
-                int b = 0, c = 0;
-                if (e < a.E) {
-                    // a group outside the rows is cut to them
-                    b = a.offsets ? min(max(__ldg(a.offsets + e), 0), a.rows) : 0;
-                    const int d = a.offsets ? min(max(__ldg(a.offsets + e + 1), 0), a.rows) : a.rows;
-                    c = max(d - b, 0);
-                }
-                const int t = (c + NT - 1) / NT;
-                int incl = t;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                    if (lane >= o)
-                        incl += y;
-                }
-                if (e < a.E) {
-                    tt[e] = run + incl - t;
-                    lo[e] = b;
-                    len[e] = c;
-                }
-                run += __shfl_sync(0xFFFFFFFFu, incl, 31);
-            }
-            if (lane == 0)
-                tt[a.E] = run;
-        }
+        if (warp == 0)
+            group_table(a, NT, lane, tt, lo, len);
         w.tt = tt;
         w.lo = lo;
         w.len = len;
@@ -595,11 +408,14 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
         // -------------------------------------------------------------- sums
         const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t ta = tmem + ((uint32_t)quad << 21);
-        int b = 0, q = 0, parity = 0;
+        constexpr int GC = pass_cols(MODE, NT), GCH = GC / 16;  // columns and chunks of an epilogue pass
+        float *stage = reinterpret_cast<float *>(tail + T.stage) + wg * NMAT * GC * 128;
+        int b = 0, q = 0;
         uint32_t tph = 0, fph = 0, rph = 0;
         bool ok = true;
-        for (int u = w.first; u < w.n_units && ok; u += w.step, parity ^= 1) {
+        for (int u = w.first; u < w.n_units && ok; u += w.step) {
             const Unit U = unit_of<MODE, NT>(a, w, u);
+            const int nch = ((U.n + 15) / 16 + NWG - 1 - wg) / NWG;  // this warpgroup's chunks: every NWG-th
             uint64_t acc[NMAT][NCOL / 2];
 #pragma unroll
             for (int m = 0; m < NMAT; ++m)
@@ -612,37 +428,29 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
                     break;
                 }
                 fence_after();
-                const float *f = fac + q * NMAT * NT;
-                const uint32_t tb = ta + b * kCols;
+                const float4 *f = reinterpret_cast<const float4 *>(fac + q * NMAT * NT + wg * 16);
+                const uint32_t tb = ta + b * kCols + wg * 16;
+                // chunk by chunk, the next one's columns on their way while one is summed
+                uint32_t r[2][16];
+                if (nch > 0)
+                    tmem_ld16(tb, r[0]);
 #pragma unroll
-                for (int m = 0; m < NMAT; ++m) {
-                    auto fma16 = [&](int ch, const uint32_t *r) {
-                        const float4 *fv = reinterpret_cast<const float4 *>(f + m * NT + (ch * NWG + wg) * 16);
+                for (int i = 0; i < NCH * NMAT; ++i) {
+                    const int ch = i / NMAT, m = i % NMAT;
+                    if (ch < nch) {
+                        const int nx = i + 1;
+                        tmem_wait(r[i & 1]);
+                        if (nx < NCH * NMAT && nx / NMAT < nch)
+                            tmem_ld16(tb + (nx % NMAT) * NT + nx / NMAT * NWG * 16, r[nx & 1]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 v = fv[i];
-                            fma_f32x2(acc[m][ch * 8 + 2 * i],
-                                      pair_f32(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])),
-                                      pair_f32(v.x, v.y));
-                            fma_f32x2(acc[m][ch * 8 + 2 * i + 1],
-                                      pair_f32(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])),
-                                      pair_f32(v.z, v.w));
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 v = f[(m * NT + ch * NWG * 16) / 4 + j];
+                            const uint32_t *p = r[i & 1] + 4 * j;
+                            fma_f32x2(acc[m][ch * 8 + 2 * j],
+                                      pair_f32(__uint_as_float(p[0]), __uint_as_float(p[1])), pair_f32(v.x, v.y));
+                            fma_f32x2(acc[m][ch * 8 + 2 * j + 1],
+                                      pair_f32(__uint_as_float(p[2]), __uint_as_float(p[3])), pair_f32(v.z, v.w));
                         }
-                    };
-                    if (NCH >= 2) {
-#pragma unroll
-                        for (int ch = 0; ch + 1 < NCH; ch += 2) {
-                            if ((ch * NWG + wg) * 16 >= U.n)
-                                break;
-                            uint32_t r[32];
-                            tmem_ld16x2(tb + m * NT + (ch * NWG + wg) * 16, tb + m * NT + ((ch + 1) * NWG + wg) * 16, r);
-                            fma16(ch, r);
-                            fma16(ch + 1, r + 16);
-                        }
-                    } else {
-                        uint32_t r[16];
-                        tmem_ld16(tb + m * NT + wg * 16, r);
-                        fma16(0, r);
                     }
                 }
                 fence_before();
@@ -656,138 +464,129 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
                 if (++q == kFacRing)
                     q = 0, fph ^= 1;
             }
-            float v[NMAT][NCOL];
-#pragma unroll
-            for (int m = 0; m < NMAT; ++m)
-#pragma unroll
-                for (int i = 0; i < NCOL / 2; ++i)
-                    unpair_f32(acc[m][i], v[m][2 * i], v[m][2 * i + 1]);
-            // token column of this thread's i-th sum
-            auto col = [&](int i) { return ((i >> 4) * NWG + wg) * 16 + (i & 15); };
 
-            if (NWG == 1 && cl > 1) {
-                // The cluster's partial sums: column n belongs to CTA n % cl.
-                const int sh = 31 - __clz(cl), own = a.ncol_own;
-                if (u != w.first)
-                    ok = ok && wwait<true>(rfull + 4 + quad, rph ^ 1, a.err, abort);
+            // The sums leave in passes of GC columns through shared memory, where a
+            // warp takes a whole column (128 rows, four to a lane): its stores are
+            // contiguous, the largest |h| of a hidden block is one warp maximum, and
+            // the code stays small -- unrolled over the registers it ran at the rate
+            // of its instruction fetches (64 columns: 5 us for the stores alone).
 #pragma unroll
-                for (int i = 0; i < NCOL; ++i)
-                    if (i < U.n && (i & (cl - 1)) != (int)rank) {
+            for (int ps = 0; ps < NCH / GCH; ++ps) {
+                if (ps * GCH >= nch && cl == 1)
+                    break;
+                if (cl > 1 && (u != w.first || ps > 0))
+                    ok = ok && wwait<true>(rfull + 1, rph ^ 1, a.err, abort);
 #pragma unroll
-                        for (int m = 0; m < NMAT; ++m)
-                            st_cluster(mapa(smem_u32(red + ((rank * own + (i >> sh)) * NMAT + m) * 128 + row),
-                                            i & (cl - 1)),
-                                       v[m][i]);
+                for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+                    for (int j = 0; j < GC / 2; ++j) {
+                        float lo, hi;
+                        unpair_f32(acc[m][ps * GC / 2 + j], lo, hi);
+                        stage[(m * GC + 2 * j) * 128 + row] = lo;
+                        stage[(m * GC + 2 * j + 1) * 128 + row] = hi;
                     }
-                asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                __syncwarp();
-                if (lane < cl && lane != (int)rank)
-                    arrive_cluster(mapa(smem_u32(rfull + quad), lane));
-                ok = ok && wwait<true>(rfull + quad, rph, a.err, abort);
-#pragma unroll
-                for (int i = 0; i < NCOL; ++i)
-                    if (i < U.n && (i & (cl - 1)) == (int)rank) {
-#pragma unroll
-                        for (int m = 0; m < NMAT; ++m) {
-                            float sum = 0.0f;
-                            for (int r = 0; r < cl; ++r)
-                                sum += r == (int)rank ? v[m][i] : red[((r * own + (i >> sh)) * NMAT + m) * 128 + row];
-                            v[m][i] = sum;
-                        }
-                    }
-                __syncwarp();
-                if (lane < cl && lane != (int)rank)
-                    arrive_cluster(mapa(smem_u32(rfull + 4 + quad), lane));
-                rph ^= 1;
-            }
-            // (n % 1 == 0: without a cluster every column is this CTA's)
-            auto mine = [&](int n) { return n < U.n && (n & (cl - 1)) == (int)rank; };
-
-            if constexpr (NMAT == 2) {
-                // h = act(g) u, then e4m3 by the largest |h| of the tile's 128 hidden columns
-                float *am4 = am + (parity * NWG + wg) * 4 * NCOL, *rcp = am + 2 * 4 * NT + warp * NCOL;
-                uint32_t keep = 0;
-#pragma unroll
-                for (int i = 0; i < NCOL; ++i) {
-                    const float h = act_of(v[0][i], a.act) * v[1][i];
-                    v[0][i] = h;
-                    uint32_t m = 0;
-                    if (mine(col(i)))  // (the whole warp agrees)
-                        m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
-                    if ((i & 31) == lane)
-                        keep = m;
-                    if ((i & 31) == 31 || i == NCOL - 1) {
-                        const int at = (i & ~31) + lane;
-                        if (at < NCOL)
-                            am4[quad * NCOL + at] = __uint_as_float(keep);
-                    }
-                }
-                // (the four warps of a warpgroup give up together: none is left at the barrier)
+                if (cl > 1)
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                // (the four warps of a warpgroup give up together: none is left at a barrier)
                 __syncwarp();
                 ok = named_and(1 + wg, 128, ok);
                 if (!ok)
                     break;
+                if (cl > 1) {
+                    if (quad == 0 && lane < cl)
+                        arrive_cluster(mapa(smem_u32(rfull), lane));
+                    ok = wwait<true>(rfull, rph, a.err, abort);
+                }
+                // column n of the tile: CTA n % cl of the cluster
+                for (int j = quad; j < GC && ok; j += 4) {
+                    const int n = ((ps * GCH + (j >> 4)) * NWG + wg) * 16 + (j & 15);
+                    if (n >= U.n || (n & (cl - 1)) != (int)rank)
+                        continue;
+                    float4 v[NMAT];
 #pragma unroll
-                for (int j = 0; j < (NCOL + 31) / 32; ++j) {
-                    const int i = lane + 32 * j;
-                    if (i < NCOL) {
-                        const int n = col(i);
-                        uint32_t m = 0;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            m = max(m, __float_as_uint(am4[r * NCOL + i]));
-                        const float s = scale_of(__uint_as_float(m), 0);
-                        // (h by a reciprocal: it is a rounded sum, on no border between two e4m3 numbers)
-                        float inv = __frcp_rn(s), sc = s;
-                        if (MODE == kFewGateUp && U.e >= 0 && n < a.T) {
-                            // the routing weight joins the scale; a token that did not choose the expert adds nothing
-                            float wt = 0.0f;
-                            bool routed = false;
-                            for (int k = 0; k < a.topk; ++k)
-                                if (__ldg(a.idx + n * a.topk + k) == U.e) {
-                                    wt += __ldg(a.wts + n * a.topk + k);
-                                    routed = true;
-                                }
-                            sc = routed ? s * wt : 0.0f;
-                            inv = routed ? inv : 0.0f;
+                    for (int m = 0; m < NMAT; ++m) {
+                        const float4 *at = reinterpret_cast<const float4 *>(stage + (m * GC + j) * 128) + lane;
+                        if (cl == 1) {
+                            v[m] = *at;
+                        } else {
+                            v[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                            for (int r = 0; r < cl; ++r) {
+                                const float4 p = ld_cluster(mapa(smem_u32(at), r));
+                                v[m].x += p.x, v[m].y += p.y, v[m].z += p.z, v[m].w += p.w;
+                            }
                         }
-                        rcp[i] = inv;
-                        if (quad == 0 && mine(n))
+                    }
+                    if constexpr (NMAT == 2) {
+                        const float h[4] = {act_of(v[0].x, a.act) * v[NMAT - 1].x, act_of(v[0].y, a.act) * v[NMAT - 1].y,
+                                            act_of(v[0].z, a.act) * v[NMAT - 1].z, act_of(v[0].w, a.act) * v[NMAT - 1].w};
+                        uint32_t mx = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mx = max(mx, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+                        const float s = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, mx)), 0);
+                        // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
+                        const float inv = __frcp_rn(s);
+                        uint32_t e = e4m3_x2(h[0] * inv, h[1] * inv) | e4m3_x2(h[2] * inv, h[3] * inv) << 16;
+                        float sc = s;
+                        if (MODE == kFewGateUp && U.e >= 0) {
+                            // the routing weight joins the scale; a token that did not choose the expert adds nothing
+                            const int mine = lane < a.topk ? __ldg(a.idx + n * a.topk + lane) : -1;
+                            const float wt = mine == U.e ? __ldg(a.wts + n * a.topk + lane) : 0.0f;
+                            if (__any_sync(0xFFFFFFFFu, mine == U.e)) {
+                                float sum = wt;
+#pragma unroll
+                                for (int o = 16; o; o >>= 1)
+                                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                                sc = s * sum;
+                            } else {
+                                sc = 0.0f;
+                                e = 0;
+                            }
+                        }
+                        uint8_t *hp = MODE == kFewGateUp ? a.h + ((int64_t)U.item * NT + n) * 128
+                                                         : a.h + (int64_t)(U.tok0 + n) * a.ldh + U.f * kBlk;
+                        reinterpret_cast<uint32_t *>(hp)[lane] = e;
+                        if (lane == 0)
                             a.hs[MODE == kFewGateUp ? (int64_t)U.item * NT + n : (int64_t)U.f * a.hs_ld + U.tok0 + n] = sc;
+                    } else {
+                        const int o = U.f * kBlk + 4 * lane;
+                        const int64_t at = (int64_t)(U.tok0 + n) * a.ldo + o;
+                        float y[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                        if (MODE == kFewDown) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (o + i < a.N)
+                                    y[i] = fmaf(a.lam, y[i], a.residual ? load_act(a.residual, at + i, a.out_bf16) : 0.0f);
+                        }
+                        if (a.out_vec && o + 4 <= a.N) {
+                            if (a.out_bf16)
+                                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) =
+                                    make_uint2(f2bf(y[0]) | (uint32_t)f2bf(y[1]) << 16,
+                                               f2bf(y[2]) | (uint32_t)f2bf(y[3]) << 16);
+                            else
+                                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at) =
+                                    make_float4(y[0], y[1], y[2], y[3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (o + i < a.N) {
+                                    if (a.out_bf16)
+                                        reinterpret_cast<uint16_t *>(a.out)[at + i] = f2bf(y[i]);
+                                    else
+                                        reinterpret_cast<float *>(a.out)[at + i] = y[i];
+                                }
+                        }
                     }
                 }
                 __syncwarp();
-                uint8_t *h = a.h + (MODE == kFewGateUp ? (int64_t)U.item * NT * 128
-                                                       : (int64_t)U.tok0 * a.ldh + U.f * kBlk) + row;
-                const int64_t ld = MODE == kFewGateUp ? 128 : a.ldh;
-#pragma unroll
-                for (int i = 0; i < NCOL; i += 2) {
-                    const float r0 = rcp[i], r1 = rcp[i + 1];
-                    const uint32_t e = e4m3_x2(r0 != 0.0f ? v[0][i] * r0 : 0.0f, r1 != 0.0f ? v[0][i + 1] * r1 : 0.0f);
-                    if (mine(col(i)))
-                        h[col(i) * ld] = (uint8_t)e;
-                    if (mine(col(i + 1)))
-                        h[col(i + 1) * ld] = (uint8_t)(e >> 8);
-                }
-            } else {
+                ok = named_and(1 + wg, 128, ok);
                 if (!ok)
                     break;
-                const int o = U.f * kBlk + row;
-                if (o < a.N) {
-#pragma unroll
-                    for (int i = 0; i < NCOL; ++i) {
-                        const int n = col(i);
-                        if (!mine(n))
-                            continue;
-                        const int64_t at = (int64_t)(U.tok0 + n) * a.ldo + o;
-                        float y = v[0][i];
-                        if (MODE == kFewDown)
-                            y = fmaf(a.lam, y, a.residual ? load_act(a.residual, at, a.out_bf16) : 0.0f);
-                        if (a.out_bf16)
-                            reinterpret_cast<uint16_t *>(a.out)[at] = f2bf(y);
-                        else
-                            reinterpret_cast<float *>(a.out)[at] = y;
-                    }
+                if (cl > 1) {
+                    if (quad == 0 && lane < cl)
+                        arrive_cluster(mapa(smem_u32(rfull + 1), lane));
+                    rph ^= 1;
                 }
             }
         }
@@ -812,7 +611,7 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
 template <int MODE, int NT>
 cudaError_t launch_t(const GemmArgs &a, int grid, cudaStream_t s)
 {
-    const size_t smem = gemm_smem((Mode)MODE, NT, a.stages, a.cl, a.ncol_own);
+    const size_t smem = gemm_smem((Mode)MODE, NT, a.stages);
     cudaError_t e = smem_optin((const void *)gemm_kernel<MODE, NT>, smem);
     if (e != cudaSuccess)
         return e;
@@ -840,9 +639,9 @@ cudaError_t launch_t(const GemmArgs &a, int grid, cudaStream_t s)
 
 }  // namespace
 
-size_t gemm_smem(Mode mode, int nt, int stages, int cl, int ncol_own)
+size_t gemm_smem(Mode mode, int nt, int stages)
 {
-    return 1024 + (size_t)stages * stage_bytes(mode, nt) + tail_of(mode, nt, cl, ncol_own).total;
+    return 1024 + (size_t)stages * stage_bytes(mode, nt) + tail_of(mode, nt).total;
 }
 
 cudaError_t launch_gemm(Mode mode, int nt, const GemmArgs &a, int grid, cudaStream_t s)
@@ -853,12 +652,9 @@ cudaError_t launch_gemm(Mode mode, int nt, const GemmArgs &a, int grid, cudaStre
     MX_CASE(kProduct, 16);
     MX_CASE(kProduct, 32);
     MX_CASE(kProduct, 64);
-    MX_CASE(kProduct, 128);
-    MX_CASE(kProduct, 256);
     MX_CASE(kGateUp, 16);
     MX_CASE(kGateUp, 32);
     MX_CASE(kGateUp, 64);
-    MX_CASE(kGateUp, 128);
     MX_CASE(kFewGateUp, 16);
     MX_CASE(kFewGateUp, 32);
     MX_CASE(kFewGateUp, 64);
