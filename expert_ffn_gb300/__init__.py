@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct as _struct
 import threading
 
 from .build import LIB as LIB_PATH
@@ -122,9 +123,9 @@ def lib():
             L.mx_moe_workspace_check.argtypes = [P, P]
             L.mx_moe_profile_read.argtypes = [C.POINTER(C.c_double), C.POINTER(C.c_int), I32]
             I64 = C.c_int64
-            L.mx_fp8_quantize.argtypes = [P, I64, I32, I32, C.POINTER(Fp8Rows), P]
-            L.mx_fp8_matmul.argtypes = [C.POINTER(Fp8Rows), C.POINTER(Fp8Matrix), P, I64, I32, P, P, SZ]
-            L.mx_fp8_grouped_matmul.argtypes = [C.POINTER(Fp8Rows), P, C.POINTER(Fp8Matrix), P, I64, I32, P, P, SZ]
+            L.mx_fp8_quantize.argtypes = [P, I64, I32, I32, P, P]  # (P: an Fp8Rows, by reference or packed)
+            L.mx_fp8_matmul.argtypes = [P, C.POINTER(Fp8Matrix), P, I64, I32, P, P, SZ]
+            L.mx_fp8_grouped_matmul.argtypes = [P, P, C.POINTER(Fp8Matrix), P, I64, I32, P, P, SZ]
             L.mx_fp8_matmul_workspace_bytes.argtypes = [C.POINTER(Fp8Matrix), I32]
             L.mx_fp8_matmul_workspace_bytes.restype = SZ
             L.mx_fp8_moe_forward.argtypes = [P, I32, P, P, C.POINTER(Fp8LayerStruct), P, P, P, P, SZ]
@@ -358,20 +359,35 @@ def profile_read(reset: bool = True) -> dict:
 #
 # Tensors carry their own shapes and strides here, so these calls check them: a
 # wrong one raises MxError(-1) like a wrong argument of the library.  Work goes
-# to `stream`, by default the current stream of the tensors' device.
+# to `stream`, by default the current stream of the tensors' device.  A call for
+# a single token runs for a few microseconds on the GPU, so the marshalling
+# keeps to cheap operations: the row descriptor is packed bytes, devices are
+# compared by index.
 
-_DTYPES = None  # torch dtype -> mx_dtype, filled on first use
+_ROWS = _struct.Struct("@PPiiqqq")  # Fp8Rows
+_t = None  # names of torch, filled on first use
 
 
-def _dtype_code(t, name):
-    global _DTYPES
-    if _DTYPES is None:
+class _Torch:
+    def __init__(self):
         import torch
-        _DTYPES = {torch.float32: MX_F32, torch.bfloat16: MX_BF16}
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise MxError(-1, f"{name} must be float32 or bfloat16, not {t.dtype}")
-    return code
+        self.f8, self.f32, self.i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+        self.codes = {torch.float32: MX_F32, torch.bfloat16: MX_BF16}
+        self.sizes = {MX_F32: 4, MX_BF16: 2}
+        self.device = torch.cuda.device
+        self.current_device = torch.cuda.current_device
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+        L = lib()
+        self.quantize, self.matmul, self.grouped = L.mx_fp8_quantize, L.mx_fp8_matmul, L.mx_fp8_grouped_matmul
+        self.moe = L.mx_fp8_moe_forward
+
+
+def _torch():
+    global _t
+    if _t is None:
+        _t = _Torch()
+    return _t
 
 
 def _need(ok, msg):
@@ -379,56 +395,59 @@ def _need(ok, msg):
         raise MxError(-1, msg)
 
 
-def _is(t, dtype):
-    return str(t.dtype) == dtype
+def _dtype_code(t, name):
+    code = _torch().codes.get(t.dtype)
+    if code is None:
+        raise MxError(-1, f"{name} must be float32 or bfloat16, not {t.dtype}")
+    return code
 
 
-class _on:
-    """The device of the call's tensors made current, and its stream handle."""
-
-    def __init__(self, device, stream, *others):
-        import torch
-        _need(device.type == "cuda", "tensors must be on a CUDA device")
-        for t in others:
-            _need(t is None or t.device == device, f"all tensors must be on {device}")
-        self.guard = None
-        if torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-        self.stream = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream_handle(stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on(dev, stream, fn, *args):
+    """fn(*args, ...) with the tensors' device current; {stream} stands for the stream handle."""
+    if dev < 0:
+        raise MxError(-1, "tensors must be on a CUDA device")
+    t = _t
+    handle = t.stream(dev) if stream is None else _stream_handle(stream)
+    args = [handle if a is _on else a for a in args]
+    if t.current_device() == dev:
+        status = fn(*args)
+    else:
+        with t.device(dev):
+            status = fn(*args)
+    if status:
+        _check(status)
 
 
 def _fp8_matrix(w, scales, name):
-    _need(_is(w, "torch.float8_e4m3fn") and w.dim() in (2, 3), f"{name} must be float8_e4m3fn [count,] rows, cols")
+    t = _torch()
+    _need(w.dtype is t.f8 and w.dim() in (2, 3), f"{name} must be float8_e4m3fn [count,] rows, cols")
     rows, cols = w.shape[-2:]
     count = w.shape[0] if w.dim() == 3 else 1
     ld = w.stride(-2) if rows > 1 else -(-max(cols, w.stride(-2)) // 16) * 16
     _need(w.stride(-1) == 1 or cols == 1, f"{name} must have contiguous rows")
     _need(count == 1 or w.stride(0) == rows * ld, f"{name}: the matrices must follow one another")
     want = (-(-rows // 128), -(-cols // 128))
-    _need(_is(scales, "torch.float32") and scales.is_contiguous() and tuple(scales.shape[-2:]) == want
+    _need(scales.dtype is t.f32 and scales.is_contiguous() and tuple(scales.shape[-2:]) == want
           and scales.numel() == count * want[0] * want[1],
           f"{name}: scales must be contiguous float32 [{count}, {want[0]}, {want[1]}]")
     _need(scales.device == w.device, f"{name}: scales must be on {w.device}")
     return Fp8Matrix(w.data_ptr(), scales.data_ptr(), rows, cols, count, ld)
 
 
-def _fp8_rows(q, scales):
-    _need(q.dim() == 2 and _is(q, "torch.float8_e4m3fn"), "q must be float8_e4m3fn [rows, cols]")
+def _fp8_rows(t, q, scales, operand):
+    """Packed Fp8Rows of a pair of tensors."""
+    if q.dtype is not t.f8 or q.dim() != 2:
+        raise MxError(-1, "q must be float8_e4m3fn [rows, cols]")
     rows, cols = q.shape
-    _need(q.stride(1) == 1 or cols == 1, "q must have contiguous rows")
-    _need(scales.dim() == 2 and _is(scales, "torch.float32") and scales.shape[0] == rows
-          and scales.shape[1] == -(-cols // 128), f"scales must be float32 [{rows}, {-(-cols // 128)}]")
-    ld = q.stride(0) if rows > 1 else -(-max(cols, q.stride(0)) // 16) * 16
-    return Fp8Rows(q.data_ptr(), scales.data_ptr(), rows, cols, ld, scales.stride(0), scales.stride(1))
+    ld, one = q.stride()
+    sr, sb = scales.stride() if scales.dim() == 2 else (0, 0)
+    if scales.dtype is not t.f32 or scales.shape != (rows, -(-cols // 128)):
+        raise MxError(-1, f"scales must be float32 [{rows}, {-(-cols // 128)}]")
+    if one != 1 and cols > 1:
+        raise MxError(-1, "q must have contiguous rows")
+    if rows <= 1:  # (the stride of a single row means nothing)
+        ld = -(-cols // 16) * 16 if operand else cols
+    return _ROWS.pack(q.data_ptr(), scales.data_ptr(), rows, cols, ld, sr, sb)
 
 
 class Fp8Weight:
@@ -439,6 +458,7 @@ class Fp8Weight:
     def __init__(self, w, scales):
         self.w, self.scales = w, scales
         self.c = _fp8_matrix(w, scales, "w")
+        self.ref, self.rows, self.count, self.dev = C.byref(self.c), self.c.rows, self.c.count, w.get_device()
 
 
 class Fp8Layer:
@@ -455,71 +475,84 @@ class Fp8Layer:
             _need(pair[0].device == gate[0].device, f"{name} must be on {gate[0].device}")
         c.top_k, c.act_dtype, c.activation, c.layer_scalar = top_k, act_dtype, activation, layer_scalar
         self.c = c
-        self.device = gate[0].device
+        self.ref, self.dev, self.d_model, self.top_k = C.byref(c), gate[0].get_device(), c.gate.cols, top_k
+        self.dtype = {v: k for k, v in _torch().codes.items()}.get(act_dtype)
 
 
 def fp8_quantize(x, q, scales, pow2=False, stream=None):
     """Quantise the rows of ``x`` (float32 or bfloat16 [rows, cols]) into ``q`` (float8_e4m3fn) and ``scales``
     (float32 [rows, ceil(cols / 128)], any strides; ``empty(blocks, rows).t()`` suits the products best)."""
-    _need(x.dim() == 2 and x.shape == q.shape and (x.stride(1) == 1 or x.shape[1] == 1),
-          "x and q must have the same shape, x contiguous rows")
-    r = _fp8_rows(q, scales)
-    if x.shape[0] > 1:
-        r.ld = q.stride(0)
-    with _on(x.device, stream, q, scales) as s:
-        _check(lib().mx_fp8_quantize(x.data_ptr(), max(x.stride(0), x.shape[1]), _dtype_code(x, "x"), int(pow2),
-                                     C.byref(r), s))
+    t = _t or _torch()
+    r = _fp8_rows(t, q, scales, False)
+    shape = x.shape
+    if shape != q.shape:
+        raise MxError(-1, "x and q must have the same shape")
+    ldx, one = x.stride()
+    if one != 1 and shape[1] > 1:
+        raise MxError(-1, "x must have contiguous rows")
+    dev = x.get_device()
+    if q.get_device() != dev or scales.get_device() != dev:
+        raise MxError(-1, "all tensors must be on one device")
+    _on(dev, stream, t.quantize, x.data_ptr(), ldx if shape[0] > 1 else shape[1], _dtype_code(x, "x"), 1 if pow2 else 0, r, _on)
 
 
 def fp8_matmul_workspace_bytes(weight: Fp8Weight, rows: int) -> int:
-    return lib().mx_fp8_matmul_workspace_bytes(C.byref(weight.c), rows)
+    return lib().mx_fp8_matmul_workspace_bytes(weight.ref, rows)
 
 
-def _product(q, scales, offsets, weight, out, ws, stream):
-    r = _fp8_rows(q, scales)
-    _need(out.dim() == 2 and out.shape[0] == r.rows and out.shape[1] == weight.c.rows
-          and (out.stride(1) == 1 or out.shape[1] == 1), f"out must be [{r.rows}, {weight.c.rows}], contiguous rows")
-    ldo = max(out.stride(0), out.shape[1])
-    code, nbytes = _dtype_code(out, "out"), ws.numel() * ws.element_size()
-    with _on(q.device, stream, scales, offsets, weight.w, out, ws) as s:
-        if offsets is None:
-            _check(lib().mx_fp8_matmul(C.byref(r), C.byref(weight.c), out.data_ptr(), ldo, code, s, ws.data_ptr(),
-                                       nbytes))
-        else:
-            _check(lib().mx_fp8_grouped_matmul(C.byref(r), offsets.data_ptr(), C.byref(weight.c), out.data_ptr(), ldo,
-                                               code, s, ws.data_ptr(), nbytes))
+def _out_pitch(q, weight, out, ws, scales):
+    dev = weight.dev
+    if (q.get_device() != dev or out.get_device() != dev or ws.get_device() != dev or scales.get_device() != dev):
+        raise MxError(-1, "all tensors must be on one device")
+    ldo, one = out.stride() if out.dim() == 2 else (0, 0)
+    n = weight.rows
+    if out.shape != (q.shape[0], n) or (one != 1 and n > 1):
+        raise MxError(-1, f"out must be [{q.shape[0]}, {n}] with contiguous rows")
+    return ldo if q.shape[0] > 1 else n
 
 
 def fp8_matmul(q, scales, weight: Fp8Weight, out, ws, stream=None):
-    """out = (q, scales) times the transposed ``weight``; out float32 or bfloat16 [rows, weight rows]."""
-    _product(q, scales, None, weight, out, ws, stream)
+    """out = (q, scales) times the transposed ``weight``; out float32 or bfloat16 [rows, weight rows]; ws a
+    uint8 workspace of fp8_matmul_workspace_bytes, prepared by workspace_init."""
+    t = _t or _torch()
+    r = _fp8_rows(t, q, scales, True)
+    ldo = _out_pitch(q, weight, out, ws, scales)
+    _on(weight.dev, stream, t.matmul, r, weight.ref, out.data_ptr(), ldo, _dtype_code(out, "out"), _on, ws.data_ptr(),
+        ws.nbytes)
 
 
 def fp8_grouped_matmul(q, scales, offsets, weight: Fp8Weight, out, ws, stream=None):
     """The same with rows [offsets[e], offsets[e + 1]) against matrix e; offsets int32 [count + 1] on the device."""
-    _need(_is(offsets, "torch.int32") and offsets.is_contiguous() and offsets.numel() == weight.c.count + 1,
-          f"offsets must be contiguous int32 [{weight.c.count + 1}]")
-    _product(q, scales, offsets, weight, out, ws, stream)
+    t = _t or _torch()
+    r = _fp8_rows(t, q, scales, True)
+    ldo = _out_pitch(q, weight, out, ws, scales)
+    if (offsets.dtype is not t.i32 or offsets.shape != (weight.count + 1,) or not offsets.is_contiguous()
+            or offsets.get_device() != weight.dev):
+        raise MxError(-1, f"offsets must be contiguous int32 [{weight.count + 1}] on the weight's device")
+    _on(weight.dev, stream, t.grouped, r, offsets.data_ptr(), weight.ref, out.data_ptr(), ldo, _dtype_code(out, "out"), _on,
+        ws.data_ptr(), ws.nbytes)
 
 
 def fp8_moe_workspace_bytes(layer: Fp8Layer, T: int) -> int:
-    return lib().mx_fp8_moe_workspace_bytes(C.byref(layer.c), T)
+    return lib().mx_fp8_moe_workspace_bytes(layer.ref, T)
 
 
 def fp8_moe_forward(x, topk_idx, topk_w, layer: Fp8Layer, out, ws, residual=None, stream=None):
     """The block after its routing (mx_fp8_moe_forward): x, out and residual [T, D] of the layer's act_dtype,
-    topk_idx int32 and topk_w float32 [T, top_k], all contiguous."""
-    c = layer.c
-    T = x.shape[0]
-    shape = (T, c.gate.cols)
-    for name, t in (("x", x), ("out", out), ("residual", residual)):
-        _need(t is None or (tuple(t.shape) == shape and t.is_contiguous() and _dtype_code(t, name) == c.act_dtype),
-              f"{name} must be a contiguous {list(shape)} tensor of the layer's act_dtype")
-    _need(tuple(topk_idx.shape) == (T, c.top_k) and topk_idx.is_contiguous() and _is(topk_idx, "torch.int32"),
-          f"topk_idx must be contiguous int32 [{T}, {c.top_k}]")
-    _need(tuple(topk_w.shape) == (T, c.top_k) and topk_w.is_contiguous() and _is(topk_w, "torch.float32"),
-          f"topk_w must be contiguous float32 [{T}, {c.top_k}]")
-    with _on(x.device, stream, topk_idx, topk_w, out, ws, residual, layer) as s:
-        _check(lib().mx_fp8_moe_forward(x.data_ptr(), T, topk_idx.data_ptr(), topk_w.data_ptr(), C.byref(c),
-                                        None if residual is None else residual.data_ptr(), out.data_ptr(), s,
-                                        ws.data_ptr(), ws.numel() * ws.element_size()))
+    topk_idx int32 and topk_w float32 [T, top_k], all contiguous; ws a uint8 workspace of
+    fp8_moe_workspace_bytes, prepared by workspace_init."""
+    t = _t or _torch()
+    dev, shape = layer.dev, x.shape
+    T = shape[0]
+    for a in (x, out) if residual is None else (x, out, residual):
+        if a.dtype is not layer.dtype or a.shape != (T, layer.d_model) or not a.is_contiguous() or a.get_device() != dev:
+            raise MxError(-1, f"x, out and residual must be contiguous [T, {layer.d_model}] tensors of the layer's "
+                              "act_dtype on its device")
+    k = (T, layer.top_k)
+    if (topk_idx.dtype is not t.i32 or topk_idx.shape != k or not topk_idx.is_contiguous() or topk_w.dtype is not t.f32
+            or topk_w.shape != k or not topk_w.is_contiguous()):
+        raise MxError(-1, f"topk_idx and topk_w must be contiguous int32 and float32 [{T}, {layer.top_k}]")
+    if topk_idx.get_device() != dev or topk_w.get_device() != dev or ws.get_device() != dev:
+        raise MxError(-1, "all tensors must be on one device")
+    _on(dev, stream, t.moe, x.data_ptr(), T, topk_idx.data_ptr(), topk_w.data_ptr(), layer.ref,
+        None if residual is None else residual.data_ptr(), out.data_ptr(), _on, ws.data_ptr(), ws.nbytes)

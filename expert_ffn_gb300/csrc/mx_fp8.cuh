@@ -67,6 +67,38 @@ cudaError_t launch_rows(Mode mode, int bn, const GemmArgs &a, int grid, cudaStre
 // Dynamic shared memory of a launch_gemm with `stages` stages.
 size_t gemm_smem(Mode mode, int nt, int stages);
 
+// One to eight rows (mx_fp8_gemv.cu).
+constexpr int kGemvRows = 8;
+struct GemvArgs {
+    int T, K, N;  // rows, inner columns, weight rows (the layer: K = d_model)
+    // product
+    const uint8_t *q;
+    int64_t ldq;
+    const float *sx;
+    int64_t sx_r, sx_b;
+    const uint8_t *w;
+    int64_t ldw;
+    const float *sw;
+    int64_t ldo;
+    int out_bf16;
+    void *out;
+    // layer: x [T][K], routed gate / up / down stacks, the shared expert's (S 0: none)
+    const void *x;
+    int bf16, act, topk, E, I, S;
+    const int32_t *idx;
+    const float *wts;
+    const uint8_t *w_gate, *w_up, *w_down, *sw_gate, *sw_up, *sw_down;
+    int64_t ld_gate, ld_up, ld_down, ld_sgate, ld_sup, ld_sdown;
+    const float *s_gate, *s_up, *s_down, *ss_gate, *ss_up, *ss_down;
+    uint8_t *h8;         // hidden [block][8][128] e4m3 and its factors [block][8]
+    float *hf;
+    const void *residual;
+    float lam;
+};
+cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s);
+cudaError_t launch_gemv_moe(const GemvArgs &a, cudaStream_t s);
+size_t gemv_gate_up_smem(int T, int D);
+
 struct QuantArgs {
     const void *x;       // [rows][cols]
     int64_t rows, ldx;

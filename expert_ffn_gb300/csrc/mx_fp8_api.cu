@@ -232,6 +232,25 @@ mx_status product(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_mat
         return fail(MX_ERR_ALIGNMENT, "out is misaligned");
     if ((st = check_ws(ws, ws_bytes, kErrBytes)) != MX_OK)
         return st;
+    if (!offsets && x->rows <= kGemvRows) {
+        GemvArgs v{};
+        v.T = x->rows;
+        v.K = w->cols;
+        v.N = w->rows;
+        v.q = static_cast<const uint8_t *>(x->q);
+        v.ldq = x->ld;
+        v.sx = x->scales;
+        v.sx_r = x->scale_row;
+        v.sx_b = x->scale_block;
+        v.w = static_cast<const uint8_t *>(w->w);
+        v.ldw = w->ld;
+        v.sw = w->scales;
+        v.out = out;
+        v.ldo = ldo;
+        v.out_bf16 = out_dtype == MX_BF16;
+        const cudaError_t e = launch_gemv(v, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
+    }
     GemmArgs g{};
     g.rows = x->rows;
     g.K = w->cols;
@@ -260,6 +279,7 @@ struct Plan {
     size_t xq, sx;
     // up to kFewTokens tokens: hidden tiles [item][nt][128] and factors [item][nt]
     size_t h, hs;
+    size_t h8, hf;  // up to kGemvRows: the same for the two-launch form, 8 to a block
     int nt, items;
     // more: grouping, gathered rows, hidden rows, per-slot outputs
     size_t counts, cursor, offsets, pos, xr, sr, hr, hrs, hsh, hshs, y, ys;
@@ -285,6 +305,9 @@ Plan make_plan(const mx_fp8_layer *L, int T)
         p.items = (int)(std::min(n, E) * IB + SB);
         p.h = take((int64_t)p.items * p.nt * kBlk);
         p.hs = take((int64_t)p.items * p.nt * 4);
+        const int64_t gemv_items = (T == 1 ? K : std::min(n, E)) * IB + SB;
+        p.h8 = take(T <= kGemvRows ? gemv_items * kGemvRows * kBlk : 0);
+        p.hf = take(T <= kGemvRows ? gemv_items * kGemvRows * 4 : 0);
     } else {
         p.counts = take(2 * E * 4);
         p.cursor = p.counts + E * 4;
@@ -310,6 +333,41 @@ void matrices(GemmArgs &g, const mx_fp8_matrix &a, const mx_fp8_matrix *b)
     g.E = a.count;
     g.swa = a.scales;
     g.swb = b ? b->scales : nullptr;
+}
+
+// Up to kGemvRows tokens: two launches that read the weights into registers.
+mx_status run_gemv(const void *x, int T, const int32_t *idx, const float *wts, const mx_fp8_layer *L,
+                   const void *residual, void *out, cudaStream_t s, uint8_t *ws)
+{
+    auto bytes = [](const mx_fp8_matrix &m) { return static_cast<const uint8_t *>(m.w); };
+    GemvArgs v{};
+    v.T = T;
+    v.K = L->gate.cols;
+    v.x = x;
+    v.bf16 = L->act_dtype == MX_BF16;
+    v.act = L->activation;
+    v.topk = L->top_k;
+    v.E = L->gate.count;
+    v.I = L->gate.rows;
+    v.idx = idx;
+    v.wts = wts;
+    v.w_gate = bytes(L->gate), v.w_up = bytes(L->up), v.w_down = bytes(L->down);
+    v.ld_gate = L->gate.ld, v.ld_up = L->up.ld, v.ld_down = L->down.ld;
+    v.s_gate = L->gate.scales, v.s_up = L->up.scales, v.s_down = L->down.scales;
+    if (L->shared_gate.w) {
+        v.S = L->shared_gate.rows;
+        v.sw_gate = bytes(L->shared_gate), v.sw_up = bytes(L->shared_up), v.sw_down = bytes(L->shared_down);
+        v.ld_sgate = L->shared_gate.ld, v.ld_sup = L->shared_up.ld, v.ld_sdown = L->shared_down.ld;
+        v.ss_gate = L->shared_gate.scales, v.ss_up = L->shared_up.scales, v.ss_down = L->shared_down.scales;
+    }
+    const Plan p = make_plan(L, T);
+    v.h8 = ws + p.h8;
+    v.hf = reinterpret_cast<float *>(ws + p.hf);
+    v.out = out;
+    v.residual = residual;
+    v.lam = L->layer_scalar;
+    const cudaError_t e = launch_gemv_moe(v, s);
+    return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 layer");
 }
 
 // Up to kFewTokens tokens: quantise, then gate/up and down over the active
@@ -559,7 +617,9 @@ size_t mx_fp8_moe_workspace_bytes(const mx_fp8_layer *layer, int T_max)
     if (check_layer(layer) != MX_OK || T_max < 0 || (int64_t)T_max * layer->top_k > kMaxRows)
         return 0;
     const int t = std::max(T_max, 1);
-    size_t n = make_plan(layer, std::min(t, kFewTokens)).total;
+    // (for any number of tokens up to t: each form grows with them)
+    size_t n = std::max(make_plan(layer, std::min(t, kGemvRows)).total, make_plan(layer, 1).total);
+    n = std::max(n, make_plan(layer, std::min(t, kFewTokens)).total);
     if (t > kFewTokens)
         n = std::max(n, make_plan(layer, t).total);
     return n;
@@ -591,6 +651,9 @@ mx_status mx_fp8_moe_forward(const void *x, int T, const int32_t *topk_idx, cons
     }
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t *w = static_cast<uint8_t *>(ws);
+    // (a slice of x has to fit the shared memory of four CTAs to an SM)
+    if (T <= kGemvRows && gemv_gate_up_smem(T, layer->gate.cols) <= 48 * 1024)
+        return run_gemv(x, T, topk_idx, topk_w, layer, residual, out, s, w);
     return T <= kFewTokens ? run_few(x, T, topk_idx, topk_w, layer, residual, out, s, w)
                            : run_many(x, T, topk_idx, topk_w, layer, residual, out, s, w);
 }

@@ -1,0 +1,544 @@
+// mx_fp8_gemv.cu -- the FP8 products for one to eight rows, and the MoE layer of
+// as many tokens in two launches.
+//
+// These read every weight once and do next to nothing with it, so what counts is
+// that all SMs have loads in flight from the first moment to the last, and how
+// long the chain before and behind them is.  A tile of 16 weight rows is one CTA
+// (or several: no persistence, the scheduler evens them out); its warps split the
+// inner dimension.  A lane loads 16-byte pieces of rows straight into the operand
+// registers of mma.sync m16n8k32 (e4m3): four lanes cover 64 consecutive bytes of
+// a row, and since any order of k serves a dot product, the four words of a piece
+// are used as they come, against the tokens' bytes in the same order.  No shared
+// memory, barrier or tensor memory stands between HBM and the MMA; through the
+// tcgen05 kernel the 2112 x 2816 product of one row took 7.7 us, most of it set-up,
+// pipeline fill and cluster reduction.  The MMA's eight columns are the tokens.
+//
+// The layer: gate/up quantises its slice of x in each warp while the weights are
+// under way, and leaves the hidden blocks in e4m3; down sums over all active
+// experts and the shared one in a fixed order, so no scratch output and no third
+// launch are needed.  Its first weights are requested before the gate/up launch has
+// ended.
+#include "mx_fp8.cuh"
+
+namespace mx {
+namespace fp8 {
+
+namespace {
+
+constexpr int kN = 8;  // MMA columns: tokens
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The bytes of v below `n` of 16 (n may be negative or above).
+__device__ __forceinline__ uint4 keep_bytes(uint4 v, int n)
+{
+    auto m = [n](uint32_t w, int at) {
+        const int k = n - at;
+        return k >= 4 ? w : k <= 0 ? 0u : w & ((1u << (8 * k)) - 1u);
+    };
+    return make_uint4(m(v.x, 0), m(v.y, 4), m(v.z, 8), m(v.w, 12));
+}
+
+// One matrix tile of 16 rows as a lane sees it: its two rows.
+struct Rows2 {
+    const uint8_t *r0, *r1;
+};
+
+__device__ __forceinline__ Rows2 rows_of(const uint8_t *w, int64_t ld, int row0, int n, int lane)
+{
+    const int g = row0 + (lane >> 2);
+    return Rows2{w + (int64_t)min(g, n - 1) * ld, w + (int64_t)min(g + 8, n - 1) * ld};
+}
+
+// Block b (128 columns) of both rows: words 0-3 of each half of 64 columns.
+struct Piece {
+    uint4 a[2], c[2];
+};
+
+__device__ __forceinline__ Piece load_block(const Rows2 &r, int b, int cols, int lane)
+{
+    Piece p;
+    const int o = b * kBlk + (lane & 3) * 16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int k = o + 64 * j;
+        p.a[j] = p.c[j] = make_uint4(0, 0, 0, 0);
+        if (k < cols) {  // (a row's last 16 bytes are its own: the pitch is a multiple of 16)
+            p.a[j] = ld_stream_u4(r.r0 + k);
+            p.c[j] = ld_stream_u4(r.r1 + k);
+        }
+    }
+    return p;
+}
+
+// What lies behind the last column is not the caller's data: make it zero.
+__device__ __forceinline__ void trim(Piece &p, int b, int cols, int lane)
+{
+    if ((b + 1) * kBlk <= cols)
+        return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int n = cols - (b * kBlk + (lane & 3) * 16 + 64 * j);
+        p.a[j] = keep_bytes(p.a[j], n);
+        p.c[j] = keep_bytes(p.c[j], n);
+    }
+}
+
+// acc += (block's product) * (sx of columns 2 tig, 2 tig + 1) * sw
+__device__ __forceinline__ void add_block(float (&acc)[4], const Piece &p, const uint4 (&x)[2], float f0, float f1)
+{
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        mma_e4m3(d, p.a[j].x, p.c[j].x, p.a[j].y, p.c[j].y, x[j].x, x[j].y);
+        mma_e4m3(d, p.a[j].z, p.c[j].z, p.a[j].w, p.c[j].w, x[j].z, x[j].w);
+    }
+    acc[0] = fmaf(d[0], f0, acc[0]);
+    acc[1] = fmaf(d[1], f1, acc[1]);
+    acc[2] = fmaf(d[2], f0, acc[2]);
+    acc[3] = fmaf(d[3], f1, acc[3]);
+}
+
+// A warp's sums [16 rows][8 tokens] to its place in `part`.
+__device__ __forceinline__ void put_sums(float *part, const float (&acc)[4], int lane)
+{
+    const int g = lane >> 2, c = 2 * (lane & 3);
+    *reinterpret_cast<float2 *>(part + g * kN + c) = make_float2(acc[0], acc[1]);
+    *reinterpret_cast<float2 *>(part + (g + 8) * kN + c) = make_float2(acc[2], acc[3]);
+}
+
+// Quantise 128 values of a token (four to a lane) into `q`; every lane gets the scale.
+__device__ __forceinline__ float quantize128(const float (&v)[4], uint8_t *q, int lane)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    const float s = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)), 0);
+    reinterpret_cast<uint32_t *>(q)[lane] =
+        e4m3_x2(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s)) | e4m3_x2(__fdiv_rn(v[2], s), __fdiv_rn(v[3], s)) << 16;
+    return s;
+}
+
+// ------------------------------------------------------------------- product
+
+constexpr int kMmWarps = 8, kMmBatch = 4;
+
+__global__ void __launch_bounds__(kMmWarps * 32, 2) gemv_kernel(const GemvArgs a)
+{
+    __shared__ __align__(16) float part[kMmWarps][16 * kN];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row0 = blockIdx.x * 16, KB = blocks(a.K);
+    const Rows2 r = rows_of(a.w, a.ldw, row0, a.N, lane);
+    const int b0 = KB * warp / kMmWarps, b1 = KB * (warp + 1) / kMmWarps;
+    const float *sw = a.sw + (int64_t)(row0 / kBlk) * KB;
+    const int n = min(lane >> 2, a.T - 1), c0 = min(2 * (lane & 3), a.T - 1), c1 = min(2 * (lane & 3) + 1, a.T - 1);
+    const uint8_t *xr = a.q + n * a.ldq;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = b0; b < b1; b += kMmBatch) {
+        Piece p[kMmBatch];
+        uint4 x[kMmBatch][2];
+        float f0[kMmBatch], f1[kMmBatch], s[kMmBatch];
+#pragma unroll
+        for (int i = 0; i < kMmBatch; ++i)
+            if (b + i < b1)
+                p[i] = load_block(r, b + i, a.K, lane);
+#pragma unroll
+        for (int i = 0; i < kMmBatch; ++i)
+            if (b + i < b1) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int k = (b + i) * kBlk + (lane & 3) * 16 + 64 * j;
+                    x[i][j] = k < a.K ? ldg_u4(xr + k) : make_uint4(0, 0, 0, 0);
+                }
+                s[i] = __ldg(sw + b + i);
+                f0[i] = __ldg(a.sx + c0 * a.sx_r + (b + i) * a.sx_b);
+                f1[i] = __ldg(a.sx + c1 * a.sx_r + (b + i) * a.sx_b);
+            }
+#pragma unroll
+        for (int i = 0; i < kMmBatch; ++i)
+            if (b + i < b1) {
+                trim(p[i], b + i, a.K, lane);
+                if ((b + i + 1) * kBlk > a.K)  // (nor are a row of x's last bytes)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        x[i][j] = keep_bytes(x[i][j], a.K - ((b + i) * kBlk + (lane & 3) * 16 + 64 * j));
+                add_block(acc, p[i], x[i], f0[i] * s[i], f1[i] * s[i]);
+            }
+    }
+    put_sums(part[warp], acc, lane);
+    __syncthreads();
+    const int t = threadIdx.x >> 4, o = threadIdx.x & 15;
+    if (t < a.T && row0 + o < a.N) {
+        float y = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kMmWarps; ++k)
+            y += part[k][o * kN + t];
+        const int64_t at = t * a.ldo + row0 + o;
+        if (a.out_bf16)
+            reinterpret_cast<uint16_t *>(a.out)[at] = f2bf(y);
+        else
+            reinterpret_cast<float *>(a.out)[at] = y;
+    }
+}
+
+// --------------------------------------------------------------------- layer
+
+// Active experts of up to kN tokens.  One token: its slots as they are (an
+// expert may come twice, an index may be none of the experts).  More: each
+// expert once, ascending.  All threads of the CTA; list[] and mask[] are shared.
+__device__ __forceinline__ int active_list(const GemvArgs &a, int *list, uint32_t *mask)
+{
+    const int tid = threadIdx.x, n = a.T * a.topk;
+    if (a.T == 1) {
+        for (int s = tid; s < n; s += blockDim.x)
+            list[s] = __ldg(a.idx + s);
+        __syncthreads();
+        return n;
+    }
+    if (tid < kMaxExperts / 32)
+        mask[tid] = 0;
+    __syncthreads();
+    for (int s = tid; s < n; s += blockDim.x) {
+        const int e = __ldg(a.idx + s);
+        if (e >= 0 && e < a.E)
+            atomicOr(mask + (e >> 5), 1u << (e & 31));
+    }
+    __syncthreads();
+    int total = 0;
+    for (int i = 0; i < kMaxExperts / 32; ++i)
+        total += __popc(mask[i]);
+    for (int e = tid; e < a.E; e += blockDim.x)
+        if (mask[e >> 5] >> (e & 31) & 1) {
+            int at = __popc(mask[e >> 5] & ((1u << (e & 31)) - 1));
+            for (int i = 0; i < e >> 5; ++i)
+                at += __popc(mask[i]);
+            list[at] = e;
+        }
+    __syncthreads();
+    return total;
+}
+
+// Four neighbouring values of an activation row, zeros from column n on.
+__device__ __forceinline__ void load4(const void *p, int64_t row, int c, int n, int bf16, float (&v)[4])
+{
+    if (c + 4 <= n && n % 4 == 0) {
+        if (bf16) {
+            const uint2 r = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + row * n + c));
+            v[0] = __uint_as_float(r.x << 16), v[1] = __uint_as_float(r.x & 0xFFFF0000u);
+            v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xFFFF0000u);
+        } else {
+            const float4 r = __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + row * n + c));
+            v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = c + i < n ? load_act(p, row * n + c + i, bf16) : 0.0f;
+    }
+}
+
+constexpr int kGuWarps = 4, kGuDepth = 2, kGuCluster = kBlk / 16;
+
+// Hidden blocks: h8[block][token][128] in e4m3 and their factors (scale times
+// routing weight); block = the shared expert's, then (active expert, block).  A CTA
+// has 16 hidden rows, gate and up; the eight CTAs of a block form a cluster and
+// tell each other their largest |h|.
+__global__ void __launch_bounds__(kGuWarps * 32, 4) gemv_gate_up(const GemvArgs a)
+{
+    extern __shared__ __align__(16) uint8_t xs[];  // [warp][token][pitch]: the warp's slice of x, e4m3
+    __shared__ __align__(16) float part[kGuWarps][2][16 * kN];
+    __shared__ float am[kGuCluster][kN];
+    __shared__ int list[kMaxTopK * kN];
+    __shared__ uint32_t mask[kMaxExperts / 32];
+    pdl_trigger();
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // (this CTA runs: its memory may be written)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int KB = blocks(a.K), SB = blocks(a.S), IB = blocks(a.I);
+    const int rank = blockIdx.x % kGuCluster, blk = blockIdx.x / kGuCluster;
+    int e = -1, f = blk, rows = a.S;  // (the shared expert's blocks come first: they wait for no index)
+    const uint8_t *wg = a.sw_gate, *wu = a.sw_up;
+    const float *sg = a.ss_gate, *su = a.ss_up;
+    int64_t lg = a.ld_sgate, lu = a.ld_sup;
+    if (blk >= SB) {
+        const int n = active_list(a, list, mask), i = (blk - SB) / IB;
+        if (i >= n)
+            return;
+        e = list[i];
+        if (e < 0 || e >= a.E)
+            return;
+        f = blk - SB - i * IB;
+        rows = a.I;
+        wg = a.w_gate + (int64_t)e * a.I * a.ld_gate;
+        wu = a.w_up + (int64_t)e * a.I * a.ld_up;
+        lg = a.ld_gate;
+        lu = a.ld_up;
+        sg = a.s_gate + (int64_t)e * IB * KB;
+        su = a.s_up + (int64_t)e * IB * KB;
+    }
+    const int row0 = f * kBlk + rank * 16;
+    sg += (int64_t)f * KB;
+    su += (int64_t)f * KB;
+    if (row0 < rows) {
+        const Rows2 rg = rows_of(wg, lg, row0, rows, lane), ru = rows_of(wu, lu, row0, rows, lane);
+        const int b0 = KB * warp / kGuWarps, b1 = KB * (warp + 1) / kGuWarps;
+        const int slice = (KB + kGuWarps - 1) / kGuWarps, pitch = slice * kBlk + 64;
+        uint8_t *x = xs + warp * a.T * pitch;
+        float *fx = reinterpret_cast<float *>(xs + kGuWarps * a.T * pitch) + warp * slice * kN;  // [block][token]
+        float ag[4] = {0.0f, 0.0f, 0.0f, 0.0f}, au[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // kGuDepth blocks of both matrices are under way at any time
+        Piece pg[kGuDepth], pu[kGuDepth];
+        float s0[kGuDepth], s1[kGuDepth];
+        auto load = [&](int i, int b) {
+            pg[i] = load_block(rg, b, a.K, lane);
+            pu[i] = load_block(ru, b, a.K, lane);
+            s0[i] = __ldg(sg + b);
+            s1[i] = __ldg(su + b);
+        };
+#pragma unroll
+        for (int i = 0; i < kGuDepth; ++i)
+            if (b0 + i < b1)
+                load(i, b0 + i);
+        // x's slice, behind the first requests for weights, four blocks' loads at a time
+        const int n = (b1 - b0) * a.T;
+        for (int q = 0; q < n; q += 4) {
+            float v[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (q + i < n) {
+                    const int k = a.T == 1 ? q + i : (q + i) / a.T;
+                    load4(a.x, q + i - k * a.T, (b0 + k) * kBlk + 4 * lane, a.K, a.bf16, v[i]);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (q + i < n) {
+                    const int k = a.T == 1 ? q + i : (q + i) / a.T, t = q + i - k * a.T;
+                    const float s = quantize128(v[i], x + t * pitch + k * kBlk, lane);
+                    if (lane == 0)
+                        fx[k * kN + t] = s;
+                }
+        }
+        __syncwarp();
+        const uint8_t *xb = x + min(lane >> 2, a.T - 1) * pitch + (lane & 3) * 16;
+        const float *fb = fx + 2 * (lane & 3);
+        for (int b = b0; b < b1; b += kGuDepth)
+#pragma unroll
+            for (int i = 0; i < kGuDepth; ++i)
+                if (b + i < b1) {
+                    const uint4 xv[2] = {*reinterpret_cast<const uint4 *>(xb), *reinterpret_cast<const uint4 *>(xb + 64)};
+                    const float2 fv = *reinterpret_cast<const float2 *>(fb);
+                    xb += kBlk;
+                    fb += kN;
+                    trim(pg[i], b + i, a.K, lane);
+                    trim(pu[i], b + i, a.K, lane);
+                    add_block(ag, pg[i], xv, fv.x * s0[i], fv.y * s0[i]);
+                    add_block(au, pu[i], xv, fv.x * s1[i], fv.y * s1[i]);
+                    if (b + i + kGuDepth < b1)
+                        load(i, b + i + kGuDepth);
+                }
+        put_sums(part[warp][0], ag, lane);
+        put_sums(part[warp][1], au, lane);
+    }
+    __syncthreads();
+    const int t = threadIdx.x >> 4, r = threadIdx.x & 15;
+    float h = 0.0f;
+    if (row0 + r < rows && t < a.T) {
+        float g = 0.0f, v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kGuWarps; ++k) {
+            g += part[k][0][r * kN + t];
+            v += part[k][1][r * kN + t];
+        }
+        h = (a.act == MX_SILU ? __fdividef(g, 1.0f + __expf(-g)) : gelu_fast(g)) * v;
+    }
+    uint32_t m = __float_as_uint(h) & 0x7FFFFFFFu;
+#pragma unroll
+    for (int o = 8; o; o >>= 1)
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+    if (r < kGuCluster) {
+        uint32_t at;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&am[rank][t])), "r"(r));
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(m) : "memory");
+    }
+    // (the other CTAs' maxima come with the barrier; none writes here after it)
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    if (t >= a.T)
+        return;
+    m = 0;
+#pragma unroll
+    for (int k = 0; k < kGuCluster; ++k)
+        m = max(m, __float_as_uint(am[k][t]));
+    const float s = scale_of(__uint_as_float(m), 0);
+    // The routing weight joins the scale; a token that did not choose the expert adds nothing.
+    float wt = 1.0f;
+    bool in = true;
+    if (e >= 0 && a.T == 1) {
+        wt = __ldg(a.wts + (blk - SB) / IB);
+    } else if (e >= 0) {
+        wt = 0.0f;
+        in = false;
+        for (int k = 0; k < a.topk; ++k)
+            if (__ldg(a.idx + t * a.topk + k) == e) {
+                wt += __ldg(a.wts + t * a.topk + k);
+                in = true;
+            }
+    }
+    // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
+    a.h8[((int64_t)blk * kN + t) * kBlk + rank * 16 + r] = in ? (uint8_t)e4m3_x2(h * __frcp_rn(s), 0.0f) : 0;
+    if (rank == 0 && r == 0)
+        a.hf[(int64_t)blk * kN + t] = in ? s * wt : 0.0f;
+}
+
+constexpr int kDnWarps = 8, kDnDepth = 3;
+
+// 16 output columns of every token: all hidden blocks of the shared expert and
+// of the active experts, split over the warps in order.
+__global__ void __launch_bounds__(kDnWarps * 32, 2) gemv_down(const GemvArgs a)
+{
+    __shared__ __align__(16) float part[kDnWarps][16 * kN];
+    __shared__ int list[kMaxTopK * kN];
+    __shared__ uint32_t mask[kMaxExperts / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int IB = blocks(a.I), SB = blocks(a.S), DB = blocks(a.K);
+    const int row0 = blockIdx.x * 16;
+    const int n_act = active_list(a, list, mask), items = SB + n_act * IB;
+    const int b0 = (int)((int64_t)items * warp / kDnWarps), b1 = (int)((int64_t)items * (warp + 1) / kDnWarps);
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    // the next item to request: its expert's place in the list (-1: shared), block and rows
+    int lj = b0 < SB ? -1 : (b0 - SB) / IB, lc = b0 < SB ? b0 : (b0 - SB) - lj * IB;
+    Rows2 lr;
+    const float *ls;
+    bool lok;
+    auto locate = [&]() {
+        const int e = lj < 0 ? 0 : lj < n_act ? list[lj] : -1;
+        lok = e >= 0 && (lj < 0 || e < a.E);
+        if (!lok)
+            return;
+        lr = lj < 0 ? rows_of(a.sw_down, a.ld_sdown, row0, a.K, lane)
+                    : rows_of(a.w_down + (int64_t)e * a.K * a.ld_down, a.ld_down, row0, a.K, lane);
+        ls = lj < 0 ? a.ss_down + (int64_t)(row0 / kBlk) * SB : a.s_down + ((int64_t)e * DB + row0 / kBlk) * IB;
+    };
+    Piece p[kDnDepth];
+    float sw[kDnDepth];
+    int left[kDnDepth];  // columns from the block's first to the matrix's last; 0: no expert
+    auto load = [&](int i) {
+        const int cols = lj < 0 ? a.S : a.I;
+        left[i] = 0;
+        if (lok) {
+            left[i] = cols - lc * kBlk;
+            p[i] = load_block(lr, lc, cols, lane);
+            sw[i] = __ldg(ls + lc);
+        }
+        if (++lc == (lj < 0 ? SB : IB)) {
+            lc = 0;
+            ++lj;
+            locate();
+        }
+    };
+    locate();
+#pragma unroll
+    for (int i = 0; i < kDnDepth; ++i)
+        if (b0 + i < b1)
+            load(i);
+    pdl_wait();  // the hidden blocks, behind the first requests for weights
+    // (written by the launch before: not through the read-only path)
+    const uint8_t *xb = a.h8 + ((int64_t)b0 * kN + min(lane >> 2, a.T - 1)) * kBlk + (lane & 3) * 16;
+    const float *fb = a.hf + (int64_t)b0 * kN + 2 * (lane & 3);
+    for (int b = b0; b < b1; b += kDnDepth) {
+        uint4 x[kDnDepth][2];
+        float2 f[kDnDepth];
+#pragma unroll
+        for (int i = 0; i < kDnDepth; ++i)
+            if (b + i < b1 && left[i]) {
+                x[i][0] = *reinterpret_cast<const uint4 *>(xb + i * kN * kBlk);
+                x[i][1] = *reinterpret_cast<const uint4 *>(xb + i * kN * kBlk + 64);
+                f[i] = *reinterpret_cast<const float2 *>(fb + i * kN);
+            }
+        xb += kDnDepth * kN * kBlk;
+        fb += kDnDepth * kN;
+#pragma unroll
+        for (int i = 0; i < kDnDepth; ++i)
+            if (b + i < b1) {
+                if (left[i]) {
+                    if (left[i] < kBlk) {  // what lies behind the last column is nobody's: neither operand's
+                        const int at = (lane & 3) * 16;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            p[i].a[j] = keep_bytes(p[i].a[j], left[i] - at - 64 * j);
+                            p[i].c[j] = keep_bytes(p[i].c[j], left[i] - at - 64 * j);
+                            x[i][j] = keep_bytes(x[i][j], left[i] - at - 64 * j);
+                        }
+                    }
+                    add_block(acc, p[i], x[i], f[i].x * sw[i], f[i].y * sw[i]);
+                }
+                if (b + i + kDnDepth < b1)
+                    load(i);
+            }
+    }
+    put_sums(part[warp], acc, lane);
+    __syncthreads();
+    const int t = threadIdx.x >> 4, o = threadIdx.x & 15;
+    if (t < a.T && row0 + o < a.K) {
+        float y = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kDnWarps; ++k)
+            y += part[k][o * kN + t];
+        const int64_t at = (int64_t)t * a.K + row0 + o;
+        y = fmaf(a.lam, y, a.residual ? load_act(a.residual, at, a.bf16) : 0.0f);
+        if (a.bf16)
+            reinterpret_cast<uint16_t *>(a.out)[at] = f2bf(y);
+        else
+            reinterpret_cast<float *>(a.out)[at] = y;
+    }
+}
+
+}  // namespace
+
+size_t gemv_gate_up_smem(int T, int D)
+{
+    const int slice = (blocks(D) + kGuWarps - 1) / kGuWarps;
+    return (size_t)kGuWarps * (T * (slice * kBlk + 64) + slice * kN * 4);
+}
+
+cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s)
+{
+    gemv_kernel<<<(a.N + 15) / 16, kMmWarps * 32, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gemv_moe(const GemvArgs &a, cudaStream_t s)
+{
+    const size_t smem = gemv_gate_up_smem(a.T, a.K);
+    cudaError_t e = smem_optin((const void *)gemv_gate_up, smem);
+    if (e != cudaSuccess)
+        return e;
+    const int most = a.T == 1 ? a.topk : (a.T * a.topk < a.E ? a.T * a.topk : a.E);
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute at;
+    c.gridDim = dim3((blocks(a.S) + most * blocks(a.I)) * kGuCluster);
+    c.blockDim = dim3(kGuWarps * 32);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {kGuCluster, 1, 1};
+    c.attrs = &at;
+    c.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&c, gemv_gate_up, a)) != cudaSuccess)
+        return e;
+    c.gridDim = dim3((a.K + 15) / 16);
+    c.blockDim = dim3(kDnWarps * 32);
+    c.dynamicSmemBytes = 0;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&c, gemv_down, a);
+}
+
+}  // namespace fp8
+}  // namespace mx
