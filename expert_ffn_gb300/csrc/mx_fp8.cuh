@@ -103,6 +103,7 @@ struct QuantArgs {
     const void *x;       // [rows][cols]
     int64_t rows, ldx;
     int cols, bf16, pow2;
+    int vec;             // (set by the launch) rows start at multiples of 16 bytes
     uint8_t *q;          // [rows][cols], row pitch ldq
     int64_t ldq;
     float *scales;       // row r, block b at r * s_r + b * s_b
@@ -137,23 +138,81 @@ cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s);
 
 // ------------------------------------------------------------ device helpers
 
-__device__ __forceinline__ float scale_of(float amax, int pow2)
-{
-    float s = __fdiv_rn(amax, kMaxE4M3);
-    s = s < kMinScale ? kMinScale : s;  // keeps a NaN
-    if (pow2 && s < INFINITY) {
-        const uint32_t b = __float_as_uint(s);
-        s = __uint_as_float((b + 0x7FFFFFu) & 0xFF800000u);
-    }
-    return s;
-}
-
 // Two floats to e4m3 (round to nearest even, saturating, NaN kept): lo in bits 0-7.
 __device__ __forceinline__ uint32_t e4m3_x2(float lo, float hi)
 {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// The scale of a block whose largest magnitude is amax (a NaN stays one), by CUDA's
+// division.  Not inlined: the compiler would otherwise run it beside the fast form
+// below for every block and choose afterwards.
+static __device__ __noinline__ float scale_any(float amax, int pow2)
+{
+    float s = __fdiv_rn(amax, kMaxE4M3);
+    s = s < kMinScale ? kMinScale : s;
+    if (pow2 && s < INFINITY)
+        s = __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0xFF800000u);
+    return s;
+}
+
+static __device__ __noinline__ float divide_any(float x, float s) { return __fdiv_rn(x, s); }
+
+// Magnitudes whose quotients the fast forms round correctly: 2^-80 to 2^100.
+__device__ __forceinline__ bool plain_range(float amax) { return amax >= 8.271806e-25f && amax <= 1.2676506e30f; }
+
+// Correctly rounded x / s for many x and one s.  Markstein's theorem (IBM J. Res.
+// Dev. 34, 1990): with r the correctly rounded 1 / s and q = fl(x r), fl(q + fl(x -
+// q s) r) is the correctly rounded quotient as long as nothing leaves the normal
+// range (a quotient below 2^-11 quantises to 0 either way).  Three instructions a
+// value, or a pair of them, instead of a dozen; equal to CUDA's division on 8e9
+// random and bf16 pairs, and for the scale on every amax.
+__device__ __forceinline__ float divide_fast(float x, float s, float r)
+{
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
+}
+
+__device__ __forceinline__ float scale_of(float amax, int pow2)
+{
+    if (!plain_range(amax))
+        return scale_any(amax, pow2);
+    const float s = divide_fast(amax, kMaxE4M3, 1.0f / kMaxE4M3);
+    return pow2 ? __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0xFF800000u) : s;
+}
+
+// Quantise pairs of values of a block whose largest magnitude has the bits `amax`:
+// e[j] = two e4m3 bytes.  Returns the scale.
+template <int N>
+__device__ __forceinline__ float quantize_pairs(const uint64_t (&p)[N], uint32_t amax, int pow2, uint32_t (&e)[N])
+{
+    const float top = __uint_as_float(amax), s = scale_of(top, pow2);
+    if (plain_range(top)) {
+        const float r = __frcp_rn(s);
+        const uint64_t r2 = pair_f32(r, r), ns2 = pair_f32(-s, -s);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            uint64_t q = mul_f32x2(p[j], r2), rem = p[j];
+            fma_f32x2(rem, q, ns2);
+            fma_f32x2(q, rem, r2);
+            float lo, hi;
+            unpair_f32(q, lo, hi);
+            e[j] = e4m3_x2(lo, hi);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            e[j] = 0;  // (a block of zeros, as padding has them)
+            if (top != 0.0f) {
+                float lo, hi;
+                unpair_f32(p[j], lo, hi);
+                e[j] = e4m3_x2(divide_any(lo, s), divide_any(hi, s));
+            }
+        }
+    }
+    return s;
 }
 
 __device__ __forceinline__ float load_act(const void *p, int64_t i, int bf16)

@@ -120,9 +120,10 @@ __device__ __forceinline__ float quantize128(const float (&v)[4], uint8_t *q, in
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    const float s = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)), 0);
-    reinterpret_cast<uint32_t *>(q)[lane] =
-        e4m3_x2(__fdiv_rn(v[0], s), __fdiv_rn(v[1], s)) | e4m3_x2(__fdiv_rn(v[2], s), __fdiv_rn(v[3], s)) << 16;
+    const uint64_t p[2] = {pair_f32(v[0], v[1]), pair_f32(v[2], v[3])};
+    uint32_t e[2];
+    const float s = quantize_pairs(p, __reduce_max_sync(0xFFFFFFFFu, m), 0, e);
+    reinterpret_cast<uint32_t *>(q)[lane] = e[0] | e[1] << 16;
     return s;
 }
 

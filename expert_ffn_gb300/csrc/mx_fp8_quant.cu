@@ -15,103 +15,186 @@ namespace {
 // integers and keep a NaN or an infinity: such a block gets a NaN or infinite
 // scale and dequantises to NaN instead of to plausible numbers.
 //
-// Half a warp per (row, block): 16 lanes of 8 columns.  A CTA covers kRows rows
-// of one block column, so the scales of a block column, which the products read
-// along the rows, leave in whole sectors.
-constexpr int kRows = 32, kThreads = 256;
+// Half a warp per (row, block): 16 lanes of 8 columns.  A CTA of 16 half-warps
+// walks down one block column, 16 neighbouring rows at a time, so the scales of a
+// block column, which the products read along the rows, leave in whole sectors, and
+// its addresses advance by constants; neighbouring CTAs have neighbouring block
+// columns.  The bound is HBM (3 bytes a bf16 value), but only if a row of 128 takes
+// few instructions: quotients go two to an instruction, the maximum of bf16 values
+// is taken on pairs, the next three loads are under way, and CUDA's division, which
+// made this 250 instructions instead of 90, is left to blocks of extreme magnitude.
+constexpr int kThreads = 256, kHalves = kThreads / 16, kAhead = 3;
 
-template <bool VEC>
-__device__ __forceinline__ void load8(const QuantArgs &a, int64_t row, int c0, float (&v)[8])
+// Eight values as they were loaded.
+template <bool BF16>
+struct Raw {
+    uint4 r[BF16 ? 1 : 2];
+};
+
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_raw(const void *x, int64_t at)
 {
+    Raw<BF16> v;
+    if (BF16) {
+        v.r[0] = ldg_u4(reinterpret_cast<const uint16_t *>(x) + at);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = 0.0f;
-    if (row >= a.rows)
-        return;
-    const int64_t at = row * a.ldx + c0;
-    if (VEC && c0 + 8 <= a.cols) {
-        if (a.bf16) {
-            const uint4 r = ldg_u4(reinterpret_cast<const uint16_t *>(a.x) + at);
-            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+            v.r[i] = ldg_u4(reinterpret_cast<const float *>(x) + at + 4 * i);
+    }
+    return v;
+}
+
+// Of a ragged or misaligned block: column by column, zeros behind the last.
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_slow(const void *x, int64_t at, int n)
+{
+    uint32_t w[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = __uint_as_float(w[j] << 16);
-                v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int j = 0; j < 8; ++j) {
+        w[j] = 0;
+        if (j < n)
+            w[j] = BF16 ? __ldg(reinterpret_cast<const uint16_t *>(x) + at + j)
+                        : __ldg(reinterpret_cast<const uint32_t *>(x) + at + j);
+    }
+    Raw<BF16> v;
+    if (BF16) {
+        v.r[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    } else {
+        v.r[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        v.r[BF16 ? 0 : 1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Bits of the largest magnitude among the 16 lanes' values.
+__device__ __forceinline__ uint32_t largest(const Raw<true> &v)
+{
+    const uint4 r = v.r[0];
+    uint32_t m = max_u16x2(max_u16x2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu), max_u16x2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
+#pragma unroll
+    for (int o = 8; o; o >>= 1)
+        m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    return max(m & 0xFFFF0000u, m << 16);
+}
+
+__device__ __forceinline__ uint32_t largest(const Raw<false> &v)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        m = max(max(max(m, v.r[i].x & 0x7FFFFFFFu), max(v.r[i].y & 0x7FFFFFFFu, v.r[i].z & 0x7FFFFFFFu)),
+                v.r[i].w & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 8; o; o >>= 1)
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    return m;
+}
+
+// Values 2 j and 2 j + 1.
+__device__ __forceinline__ uint64_t pair_of(const Raw<true> &v, int j)
+{
+    const uint32_t w = j == 0 ? v.r[0].x : j == 1 ? v.r[0].y : j == 2 ? v.r[0].z : v.r[0].w;
+    return pair_f32(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint64_t pair_of(const Raw<false> &v, int j)
+{
+    const uint4 r = v.r[j >> 1];
+    return (j & 1) ? pair_f32(__uint_as_float(r.z), __uint_as_float(r.w)) : pair_f32(__uint_as_float(r.x), __uint_as_float(r.y));
+}
+
+__device__ __forceinline__ void store8(uint8_t *q, int n, bool vec, uint2 w)
+{
+    if (vec) {
+        *reinterpret_cast<uint2 *>(q) = w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n)
+                q[j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+    }
+}
+
+template <bool BF16, bool FULL>
+__device__ __forceinline__ void quantize_column(const QuantArgs &a, int b, int64_t row, int64_t dr)
+{
+    const int l = threadIdx.x & 15, c = b * kBlk + 8 * l, n = a.cols - c;
+    const int64_t dx = dr * a.ldx, dq = dr * a.ldq, ds = dr * a.s_r;
+    int64_t xp = row * a.ldx + c, prow = row;
+    uint8_t *qp = a.q + row * a.ldq + c;
+    float *sp = a.scales + row * a.s_r + b * a.s_b;
+    // (a half-warp whose row is behind the last still takes part in the warp's shuffles)
+    auto fetch = [&]() {
+        Raw<BF16> v{};
+        if (prow < a.rows)
+            v = FULL ? load_raw<BF16>(a.x, xp) : load_slow<BF16>(a.x, xp, n);
+        xp += dx;
+        prow += dr;
+        return v;
+    };
+    Raw<BF16> v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        v[i] = fetch();
+    for (int64_t first = row - (threadIdx.x >> 4); first < a.rows;) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (first >= a.rows)
+                break;
+            const Raw<BF16> x = v[i];
+            v[i] = fetch();
+            uint64_t p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                p[j] = pair_of(x, j);
+            uint32_t e[4];
+            const float s = quantize_pairs(p, largest(x), a.pow2, e);
+            const uint2 q = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+            if (row < a.rows) {
+                if (a.q) {
+                    store8(qp, n, FULL, q);
+                    if (l == 0)
+                        *sp = s;
+                }
+                if (a.pos)
+                    for (int k = 0; k < a.topk; ++k) {
+                        const int to = __ldg(a.pos + row * a.topk + k);
+                        if (to < 0)
+                            continue;
+                        store8(a.qr + (int64_t)to * a.ldq + c, n, FULL, q);
+                        if (l == 0)
+                            a.sr[to + b * a.sr_b] = s;
+                    }
             }
-        } else {
-            const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.x) + at);
-            const float4 r0 = __ldg(p), r1 = __ldg(p + 1);
-            v[0] = r0.x, v[1] = r0.y, v[2] = r0.z, v[3] = r0.w;
-            v[4] = r1.x, v[5] = r1.y, v[6] = r1.z, v[7] = r1.w;
+            qp += dq;
+            sp += ds;
+            row += dr;
+            first += dr;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j < a.cols)
-                v[j] = load_act(a.x, at + j, a.bf16);
     }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store8(uint8_t *q, int64_t at, int c0, int cols, uint2 w)
-{
-    if (VEC && c0 + 8 <= cols) {
-        *reinterpret_cast<uint2 *>(q + at) = w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j < cols)
-                q[at + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-    }
-}
-
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
+// gridDim.x: a multiple of the block columns.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 4) quantize_kernel(const QuantArgs a)
 {
     if (a.pdl)
         pdl_trigger();
-    const int tid = threadIdx.x, hw = tid >> 4, l = tid & 15;
-    const int b = blockIdx.y;
-    const int64_t row0 = (int64_t)blockIdx.x * kRows + hw;
-    const int c0 = b * kBlk + 8 * l;
-    constexpr int kPer = kRows / (kThreads / 16);
-    float v[kPer][8];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        load8<VEC>(a, row0 + i * (kThreads / 16), c0, v[i]);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int64_t row = row0 + i * (kThreads / 16);
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = 8; o; o >>= 1)
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (row >= a.rows)
-            continue;
-        const float s = scale_of(__uint_as_float(m), a.pow2);
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = e4m3_x2(__fdiv_rn(v[i][2 * j], s), __fdiv_rn(v[i][2 * j + 1], s));
-        const uint2 q = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-        if (a.q) {
-            store8<VEC>(a.q, row * a.ldq + c0, c0, a.cols, q);
-            if (l == 0)
-                a.scales[row * a.s_r + b * a.s_b] = s;
-        }
-        if (a.pos)
-            for (int k = 0; k < a.topk; ++k) {
-                const int p = __ldg(a.pos + row * a.topk + k);
-                if (p < 0)
-                    continue;
-                store8<VEC>(a.qr, (int64_t)p * a.ldq + c0, c0, a.cols, q);
-                if (l == 0)
-                    a.sr[p + b * a.sr_b] = s;
-            }
-    }
+    const unsigned nb = blocks(a.cols), part = blockIdx.x / nb;
+    const int b = blockIdx.x - part * nb;
+    const int64_t row = (int64_t)part * kHalves + (threadIdx.x >> 4), dr = (int64_t)(gridDim.x / nb) * kHalves;
+    if (a.vec && (b + 1) * kBlk <= a.cols)
+        quantize_column<BF16, true>(a, b, row, dr);
+    else
+        quantize_column<BF16, false>(a, b, row, dr);
 }
 
 // ------------------------------------------------------------------ grouping
@@ -238,13 +321,16 @@ cudaError_t launch_quantize(const QuantArgs &a, cudaStream_t s)
     if (a.rows == 0)
         return cudaSuccess;
     const size_t es = a.bf16 ? 2 : 4;
-    const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ldx * es) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(a.q) % 8 == 0 && a.ldq % 8 == 0;
-    const dim3 grid((unsigned)((a.rows + kRows - 1) / kRows), blocks(a.cols));
-    if (vec)
-        quantize_kernel<true><<<grid, kThreads, 0, s>>>(a);
+    QuantArgs v = a;
+    v.vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ldx * es) % 16 == 0 &&
+            reinterpret_cast<uintptr_t>(a.q) % 8 == 0 && a.ldq % 8 == 0;
+    // four CTAs to an SM, in whole rows of block columns
+    const int64_t groups = (a.rows + kHalves - 1) / kHalves, nb = blocks(a.cols), want = 4 * 152 / nb;
+    const unsigned grid = (unsigned)((want < 1 ? 1 : want < groups ? want : groups) * nb);
+    if (a.bf16)
+        quantize_kernel<true><<<grid, kThreads, 0, s>>>(v);
     else
-        quantize_kernel<false><<<grid, kThreads, 0, s>>>(a);
+        quantize_kernel<false><<<grid, kThreads, 0, s>>>(v);
     return cudaGetLastError();
 }
 
