@@ -29,6 +29,9 @@ enum Mode {
     kFewDown = 3     // out = residual + lambda * (sum over the active experts' and the shared expert's blocks)
 };
 
+// Types of a product's results; kOutF16: scaled rows, with a factor for each 64 columns.
+enum OutKind { kOutF32 = 0, kOutBf16 = 1, kOutF16 = 2 };
+
 struct GemmArgs {
     CUtensorMap wa, wb;  // weights: (gate, up) or one matrix stack
     CUtensorMap sa, sb;  // few tokens: the shared expert's
@@ -42,8 +45,10 @@ struct GemmArgs {
     const float *ssa, *ssb;  // few tokens: the shared expert's
     void *out;               // kProduct, kFewDown
     int64_t ldo;
-    int out_bf16;
+    int out_kind;        // OutKind
     int out_vec;         // 16 bytes of neighbouring outputs may be stored at once
+    float *out_scale;    // kOutF16: a row's factor for each 64 columns
+    int64_t out_scale_ld;
     uint8_t *h;          // kGateUp, kFewGateUp: e4m3 hidden
     int64_t ldh;         // its row pitch (kGateUp)
     float *hs;           // its scales
@@ -62,8 +67,34 @@ struct GemmArgs {
 };
 
 cudaError_t launch_gemm(Mode mode, int nt, const GemmArgs &a, int grid, cudaStream_t s);
-// The same for many rows: kProduct in tiles of 128 tokens x bn (128, 256) weight rows, or kGateUp.
-cudaError_t launch_rows(Mode mode, int bn, const GemmArgs &a, int grid, cudaStream_t s);
+// The same for many rows (mx_fp8_rows.cu): one or two products, or gate/up
+// products, in one launch.
+struct RowsProblem {
+    CUtensorMap wa, wb, xm;
+    int rows, K, N, E;       // rows 0: no second problem
+    const int32_t *offsets;  // first problem only; nullable: one group of all rows
+    const float *sx;
+    int64_t sx_r, sx_b;
+    const float *swa, *swb;
+    void *out;               // kProduct
+    int64_t ldo;
+    int out_kind, out_vec;
+    float *out_scale;        // kOutF16: a row's factor for each 64 columns
+    int64_t out_scale_ld;
+    uint8_t *h;              // kGateUp
+    int64_t ldh;
+    float *hs;
+    int64_t hs_ld;
+    int xbox;
+};
+struct RowsArgs {
+    RowsProblem p[2];
+    int act;
+    unsigned *err;
+};
+// Tiles of 128 tokens x bn (128, 256; kGateUp: 256) weight rows.
+cudaError_t launch_rows(Mode mode, int bn, const RowsArgs &a, int grid, cudaStream_t s);
+
 // Dynamic shared memory of a launch_gemm with `stages` stages.
 size_t gemm_smem(Mode mode, int nt, int stages);
 
@@ -125,8 +156,10 @@ cudaError_t launch_group(const int32_t *idx, int n, int E, int32_t *counts, int3
                          int32_t *pos, cudaStream_t s);
 
 struct CombineArgs {
-    const float *Y;      // [slots][D]
-    const float *Ys;     // [T][D], nullable
+    const void *Y;       // [slots][D] fp32, or FP16 with a factor for each 64 columns
+    const float *Yf;     // [slots][ceil(D / 64)], nullable: fp32
+    const void *Ys;      // [T][D], nullable
+    const float *Ysf;
     const int32_t *pos;  // [T][topk]
     const float *wts;
     const void *residual;

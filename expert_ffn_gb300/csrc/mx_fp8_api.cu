@@ -178,29 +178,43 @@ mx_status rows_map(CUtensorMap *m, const void *q, int64_t rows, int64_t cols, in
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "tensor map of the activations");
 }
 
-// One product launch over rows grouped by matrix (offsets NULL: one group).
-// `avg` is the expected size of a group.  More than 64 rows a group: tokens on
-// the M side; fewer: on the N side, in a tile that holds most groups.
+// Rows of a group from which on the tokens take the MMA's M side (mx_fp8_rows.cu).
+bool many_rows(bool grouped, double avg) { return grouped ? avg > 24.0 : avg > 64.0; }
+
+// One launch of one or two products by mx_fp8_rows.cu; p[i].xm is encoded here from
+// its rows at q[i].
+mx_status run_rows(Mode mode, RowsArgs &g, const void *const *q, const int64_t *ldq, const double *avg, cudaStream_t s)
+{
+    const int sms = num_sms();
+    mx_status st;
+    double wide = 0;  // tiles of 128 x 256
+    for (int i = 0; i < 2; ++i) {
+        RowsProblem &p = g.p[i];
+        if (p.rows == 0)
+            continue;
+        // (a group that is expected to have `avg` rows)
+        const double tiles = !p.offsets ? (p.rows + 127) / 128 : p.E * (avg[i] <= 100 ? 1.0 : avg[i] / 128 + 0.5);
+        wide += tiles * (mode == kGateUp ? blocks(p.N) : (p.N + 255) / 256);
+        p.xbox = avg[i] >= 96.0 ? 128 : 32;
+        if ((st = rows_map(&p.xm, q[i], p.rows, p.K, ldq[i], p.xbox)) != MX_OK)
+            return st;
+    }
+    // (narrower tiles when the wide ones would leave SMs idle)
+    const int bn = mode == kGateUp || wide >= sms ? 256 : 128;
+    const cudaError_t e = launch_rows(mode, bn, g, sms, s);
+    return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
+}
+
+// One product launch by mx_fp8_gemm.cu over rows grouped by matrix (offsets NULL: one
+// group); `avg` is the expected size of a group.  Tokens take the MMA's N side, in a
+// tile that holds most groups.
 mx_status run_product(Mode mode, GemmArgs &g, const void *q, int64_t ldq, double avg, cudaStream_t s)
 {
     const int sms = num_sms(), FT = blocks(g.N), KB = blocks(g.K);
-    mx_status st;
-    cudaError_t e;
-    g.cl = 1;
-    if (avg > 32.0) {
-        const int64_t tiles = g.offsets ? g.E : (g.rows + 127) / 128;
-        // (narrower tiles when the wide ones would leave SMs idle)
-        const int bn = mode == kGateUp || tiles * ((g.N + 255) / 256) >= sms ? 256 : 128;
-        g.xbox = avg >= 96.0 ? 128 : 32;
-        if ((st = rows_map(&g.xm, q, g.rows, g.K, ldq, g.xbox)) != MX_OK)
-            return st;
-        const int ft = mode == kGateUp ? FT : (g.N + bn - 1) / bn;
-        const int64_t units = g.offsets ? ((int64_t)g.rows / 128 + g.E) * ft : tiles * ft;
-        e = launch_rows(mode, bn, g, (int)std::min<int64_t>(sms, units), s);
-        return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
-    }
     const int nt = tile_for(g.offsets ? avg + 2 * std::sqrt(avg) : g.rows, 64);
     const int64_t tiles = g.offsets ? g.E : (g.rows + nt - 1) / nt;
+    mx_status st;
+    g.cl = 1;
     if (!g.offsets && mode == kProduct)
         while (g.cl < 4 && tiles * FT * g.cl * 2 <= sms && KB / (g.cl * 2) >= 2)
             g.cl *= 2;
@@ -209,7 +223,7 @@ mx_status run_product(Mode mode, GemmArgs &g, const void *q, int64_t ldq, double
     if ((st = rows_map(&g.xm, q, g.rows, g.K, ldq, g.xbox)) != MX_OK)
         return st;
     const int64_t units = g.offsets ? ((int64_t)g.rows / nt + g.E) * FT : tiles * FT;
-    e = launch_gemm(mode, nt, g, (int)std::min<int64_t>(sms / g.cl, units) * g.cl, s);
+    const cudaError_t e = launch_gemm(mode, nt, g, (int)std::min<int64_t>(sms / g.cl, units) * g.cl, s);
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
 }
 
@@ -251,6 +265,29 @@ mx_status product(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_mat
         const cudaError_t e = launch_gemv(v, static_cast<cudaStream_t>(stream));
         return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
     }
+    const double avg = offsets ? (double)x->rows / w->count : x->rows;
+    if (many_rows(offsets, avg)) {
+        RowsArgs r{};
+        RowsProblem &p = r.p[0];
+        p.rows = x->rows;
+        p.K = w->cols;
+        p.N = w->rows;
+        p.E = w->count;
+        p.offsets = offsets;
+        p.sx = x->scales;
+        p.sx_r = x->scale_row;
+        p.sx_b = x->scale_block;
+        p.swa = w->scales;
+        p.out = out;
+        p.ldo = ldo;
+        p.out_kind = out_dtype == MX_BF16 ? kOutBf16 : kOutF32;
+        p.out_vec = vec16(out, ldo, out_dtype == MX_BF16);
+        r.err = static_cast<unsigned *>(ws);
+        if ((st = weight_map(&p.wa, *w)) != MX_OK)
+            return st;
+        const void *q[1] = {x->q};
+        return run_rows(kProduct, r, q, &x->ld, &avg, static_cast<cudaStream_t>(stream));
+    }
     GemmArgs g{};
     g.rows = x->rows;
     g.K = w->cols;
@@ -263,13 +300,12 @@ mx_status product(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_mat
     g.swa = w->scales;
     g.out = out;
     g.ldo = ldo;
-    g.out_bf16 = out_dtype == MX_BF16;
-    g.out_vec = vec16(out, ldo, g.out_bf16);
+    g.out_kind = out_dtype == MX_BF16 ? kOutBf16 : kOutF32;
+    g.out_vec = vec16(out, ldo, out_dtype == MX_BF16);
     g.err = static_cast<unsigned *>(ws);
     if ((st = weight_map(&g.wa, *w)) != MX_OK)
         return st;
-    return run_product(kProduct, g, x->q, x->ld, offsets ? (double)x->rows / w->count : x->rows,
-                       static_cast<cudaStream_t>(stream));
+    return run_product(kProduct, g, x->q, x->ld, avg, static_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ the layer
@@ -282,7 +318,7 @@ struct Plan {
     size_t h8, hf;  // up to kGemvRows: the same for the two-launch form, 8 to a block
     int nt, items;
     // more: grouping, gathered rows, hidden rows, per-slot outputs
-    size_t counts, cursor, offsets, pos, xr, sr, hr, hrs, hsh, hshs, y, ys;
+    size_t counts, cursor, offsets, pos, xr, sr, hr, hrs, hsh, hshs, y, ys, yf, ysf;
     size_t total;
 };
 
@@ -319,8 +355,12 @@ Plan make_plan(const mx_fp8_layer *L, int T)
         p.hrs = take(IB * n * 4);
         p.hsh = take(T * SB * kBlk);
         p.hshs = take(SB * T * 4);
-        p.y = take(n * D * 4);
-        p.ys = take(S ? T * D * 4 : 0);
+        // (FP16 with a factor for each 64 columns under a bf16 result, else fp32)
+        const int es = L->act_dtype == MX_BF16 ? 2 : 4;
+        p.y = take(n * D * es);
+        p.ys = take(S ? T * D * es : 0);
+        p.yf = take(es == 2 ? n * ((D + 63) / 64) * 4 : 0);
+        p.ysf = take(es == 2 && S ? T * ((D + 63) / 64) * 4 : 0);
     }
     p.total = o;
     return p;
@@ -444,8 +484,8 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
     matrices(d, L->down, nullptr);
     d.out = out;
     d.ldo = D;
-    d.out_bf16 = L->act_dtype == MX_BF16;
-    d.out_vec = vec16(out, D, d.out_bf16);
+    d.out_kind = L->act_dtype == MX_BF16 ? kOutBf16 : kOutF32;
+    d.out_vec = vec16(out, D, L->act_dtype == MX_BF16);
     d.residual = residual;
     d.lam = L->layer_scalar;
     d.pdl = 0;
@@ -501,45 +541,97 @@ mx_status run_many(const void *x, int T, const int32_t *idx, const float *wts, c
     if ((e = launch_quantize(q, s)) != cudaSuccess)
         return cuda_fail(e, "FP8 quantisation");
 
+    // The routed and the shared expert's products: together when the tokens of a group
+    // are many, else one after the other.
+    const double avg[2] = {(double)n / E, (double)T};
+    const bool together = many_rows(true, avg[0]), half = L->act_dtype == MX_BF16;
+    const int64_t ldx[2] = {up16(D), up16(D)}, ldh[2] = {(int64_t)IB * kBlk, (int64_t)SB * kBlk};
+    const void *xq[2] = {ws + p.xr, ws + p.xq}, *hq[2] = {ws + p.hr, ws + p.hsh};
+    RowsArgs gu{}, dn{};
+    gu.act = L->activation;
+    gu.err = dn.err = reinterpret_cast<unsigned *>(ws);
     for (int sh = 0; sh < (shared ? 2 : 1); ++sh) {
-        const double avg = sh ? T : (double)n / E;
         const mx_fp8_matrix &wg = sh ? L->shared_gate : L->gate, &wu = sh ? L->shared_up : L->up;
         const mx_fp8_matrix &wd = sh ? L->shared_down : L->down;
-        const int rows = sh ? T : n, HB = sh ? SB : IB;
-        GemmArgs g{};
-        matrices(g, wg, &wu);
-        g.rows = rows;
-        g.offsets = sh ? nullptr : i32(p.offsets);
+        RowsProblem &g = gu.p[sh], &d = dn.p[sh];
+        g.rows = d.rows = sh ? T : n;
+        g.offsets = d.offsets = sh ? nullptr : i32(p.offsets);
+        g.K = D;
+        g.N = wg.rows;
+        g.E = d.E = wg.count;
         g.sx = f32(sh ? p.sx : p.sr);
-        g.sx_r = 1;
-        g.sx_b = rows;
+        g.sx_r = d.sx_r = 1;
+        g.sx_b = d.sx_b = g.rows;
+        g.swa = wg.scales;
+        g.swb = wu.scales;
         g.h = ws + (sh ? p.hsh : p.hr);
-        g.ldh = (int64_t)HB * kBlk;
+        g.ldh = ldh[sh];
         g.hs = f32(sh ? p.hshs : p.hrs);
-        g.hs_ld = rows;
-        g.act = L->activation;
-        g.err = reinterpret_cast<unsigned *>(ws);
-        if ((st = weight_map(&g.wa, wg)) != MX_OK || (st = weight_map(&g.wb, wu)) != MX_OK ||
-            (st = run_product(kGateUp, g, ws + (sh ? p.xq : p.xr), up16(D), avg, s)) != MX_OK)
-            return st;
-        GemmArgs d{};
-        matrices(d, wd, nullptr);
-        d.rows = rows;
-        d.offsets = g.offsets;
+        g.hs_ld = g.rows;
+        d.K = wd.cols;
+        d.N = D;
         d.sx = g.hs;
-        d.sx_r = 1;
-        d.sx_b = rows;
+        d.swa = wd.scales;
         d.out = ws + (sh ? p.ys : p.y);
         d.ldo = D;
-        d.out_vec = vec16(d.out, D, 0);
-        d.err = g.err;
-        if ((st = weight_map(&d.wa, wd)) != MX_OK || (st = run_product(kProduct, d, g.h, g.ldh, avg, s)) != MX_OK)
+        d.out_kind = half ? kOutF16 : kOutF32;
+        d.out_vec = vec16(d.out, D, half);
+        d.out_scale = f32(sh ? p.ysf : p.yf);
+        d.out_scale_ld = (D + 63) / 64;
+        if ((st = weight_map(&g.wa, wg)) != MX_OK || (st = weight_map(&g.wb, wu)) != MX_OK ||
+            (st = weight_map(&d.wa, wd)) != MX_OK)
             return st;
+    }
+    if (together) {
+        if ((st = run_rows(kGateUp, gu, xq, ldx, avg, s)) != MX_OK || (st = run_rows(kProduct, dn, hq, ldh, avg, s)) != MX_OK)
+            return st;
+    } else {
+        // few tokens to an expert: the routed part on the N side
+        GemmArgs g{}, d{};
+        const RowsProblem &pg = gu.p[0], &pd = dn.p[0];
+        g.rows = d.rows = n;
+        g.offsets = d.offsets = pg.offsets;
+        g.wa = pg.wa, g.wb = pg.wb, d.wa = pd.wa;
+        matrices(g, L->gate, &L->up);
+        matrices(d, L->down, nullptr);
+        g.sx = pg.sx, d.sx = pd.sx;
+        g.sx_r = d.sx_r = 1;
+        g.sx_b = d.sx_b = n;
+        g.h = pg.h;
+        g.ldh = pg.ldh;
+        g.hs = pg.hs;
+        g.hs_ld = n;
+        g.act = L->activation;
+        g.err = d.err = gu.err;
+        d.out = pd.out;
+        d.ldo = D;
+        d.out_kind = pd.out_kind;
+        d.out_vec = pd.out_vec;
+        d.out_scale = pd.out_scale;
+        d.out_scale_ld = pd.out_scale_ld;
+        if ((st = run_product(kGateUp, g, xq[0], ldx[0], avg[0], s)) != MX_OK)
+            return st;
+        if (shared) {
+            gu.p[0] = gu.p[1];
+            gu.p[1] = RowsProblem{};
+            if ((st = run_rows(kGateUp, gu, xq + 1, ldx + 1, avg + 1, s)) != MX_OK)
+                return st;
+        }
+        if ((st = run_product(kProduct, d, hq[0], ldh[0], avg[0], s)) != MX_OK)
+            return st;
+        if (shared) {
+            dn.p[0] = dn.p[1];
+            dn.p[1] = RowsProblem{};
+            if ((st = run_rows(kProduct, dn, hq + 1, ldh + 1, avg + 1, s)) != MX_OK)
+                return st;
+        }
     }
 
     CombineArgs c{};
-    c.Y = f32(p.y);
-    c.Ys = shared ? f32(p.ys) : nullptr;
+    c.Y = ws + p.y;
+    c.Yf = half ? f32(p.yf) : nullptr;
+    c.Ys = shared ? ws + p.ys : nullptr;
+    c.Ysf = half ? f32(p.ysf) : nullptr;
     c.pos = i32(p.pos);
     c.wts = wts;
     c.residual = residual;

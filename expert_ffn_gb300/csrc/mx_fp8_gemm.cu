@@ -29,6 +29,8 @@
 // ends the CTA's work.
 #include "mx_fp8_tc.cuh"
 
+#include <cuda_fp16.h>
+
 namespace mx {
 namespace fp8 {
 
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
     } else {
         int *tt = tab, *lo = tab + kMaxExperts + 1, *len = lo + kMaxExperts;
         if (warp == 0)
-            group_table(a, NT, lane, tt, lo, len);
+            group_table(a.offsets, a.E, a.rows, NT, lane, tt, lo, len);
         w.tt = tt;
         w.lo = lo;
         w.len = len;
@@ -258,7 +260,9 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
 
     if (warp == EW) {
         // ------------------------------------------------------ TMA producer
-        if (lane == 0) {
+        {
+            // (the whole warp walks the loop and one elected lane issues: behind `lane == 0` the
+            // compiler issues each copy, or MMA, in a loop over lanes)
             auto weights = [&](const Unit &U, int kb, int s) {
                 uint8_t *st = ring + s * kStage;
                 int e, c;
@@ -284,8 +288,11 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
                 for (int u = w.first; u < w.n_units && early < NS; u += w.step) {
                     const Unit U = unit_of<MODE, NT>(a, w, u);
                     for (int kb = w.kb0; kb < w.kb1 && early < NS; ++kb, ++early) {
-                        mbar_arrive_expect_tx(full + early, bytes(U));
-                        weights(U, kb, early);
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(full + early, bytes(U));
+                            weights(U, kb, early);
+                        }
+                        __syncwarp();
                     }
                 }
                 pdl_wait();
@@ -295,13 +302,16 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
             for (int u = w.first; u < w.n_units; u += w.step) {
                 const Unit U = unit_of<MODE, NT>(a, w, u);
                 for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    if (it >= early) {
-                        if (!bwait(empty + s, ph, a.err, abort))
-                            goto produced;
-                        mbar_arrive_expect_tx(full + s, bytes(U));
-                        weights(U, kb, s);
+                    if (it >= early && !wwait(empty + s, ph, a.err, abort))
+                        goto produced;
+                    if (elect_one()) {
+                        if (it >= early) {
+                            mbar_arrive_expect_tx(full + s, bytes(U));
+                            weights(U, kb, s);
+                        }
+                        tokens(U, kb, s);
                     }
-                    tokens(U, kb, s);
+                    __syncwarp();
                     if (++s == NS)
                         s = 0, ph ^= 1;
                 }
@@ -310,27 +320,30 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
     produced:;
     } else if (warp == EW + 1) {
         // --------------------------------------------------------------- MMA
-        if (lane == 0) {
+        {
             int s = 0, b = 0;
             uint32_t ph = 0, tph = 1;
             for (int u = w.first; u < w.n_units; u += w.step) {
                 const Unit U = unit_of<MODE, NT>(a, w, u);
                 const uint32_t idesc = idesc_e4m3((U.n + 15) & ~15);
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (!bwait(tempty + b, tph, a.err, abort) || !bwait(full + s, ph, a.err, abort))
+                    if (!wwait(tempty + b, tph, a.err, abort) || !wwait(full + s, ph, a.err, abort))
                         goto issued;
                     fence_after();
                     const uint32_t st = smem_u32(ring + s * kStage);
                     const uint64_t xd = sw128_desc(st + NMAT * kTile);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int m = 0; m < NMAT; ++m) {
-                        const uint64_t wd = sw128_desc(st + m * kTile);
+                        for (int m = 0; m < NMAT; ++m) {
+                            const uint64_t wd = sw128_desc(st + m * kTile);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_f8(tmem + b * kCols + m * NT, wd + 2 * k, xd + 2 * k, idesc, k > 0);
+                            for (int k = 0; k < 4; ++k)
+                                umma_f8(tmem + b * kCols + m * NT, wd + 2 * k, xd + 2 * k, idesc, k > 0);
+                        }
+                        umma_commit(empty + s);
+                        umma_commit(tfull + b);
                     }
-                    umma_commit(empty + s);
-                    umma_commit(tfull + b);
+                    __syncwarp();
                     if (++s == NS)
                         s = 0, ph ^= 1;
                     if (++b == NB)
@@ -439,17 +452,15 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
                     const int ch = i / NMAT, m = i % NMAT;
                     if (ch < nch) {
                         const int nx = i + 1;
-                        tmem_wait(r[i & 1]);
+                        tmem_wait();
                         if (nx < NCH * NMAT && nx / NMAT < nch)
                             tmem_ld16(tb + (nx % NMAT) * NT + nx / NMAT * NWG * 16, r[nx & 1]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float4 v = f[(m * NT + ch * NWG * 16) / 4 + j];
                             const uint32_t *p = r[i & 1] + 4 * j;
-                            fma_f32x2(acc[m][ch * 8 + 2 * j],
-                                      pair_f32(__uint_as_float(p[0]), __uint_as_float(p[1])), pair_f32(v.x, v.y));
-                            fma_f32x2(acc[m][ch * 8 + 2 * j + 1],
-                                      pair_f32(__uint_as_float(p[2]), __uint_as_float(p[3])), pair_f32(v.z, v.w));
+                            fma_after(acc[m][ch * 8 + 2 * j], p[0], p[1], pair_f32(v.x, v.y));
+                            fma_after(acc[m][ch * 8 + 2 * j + 1], p[2], p[3], pair_f32(v.z, v.w));
                         }
                     }
                 }
@@ -557,13 +568,35 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 if (o + i < a.N)
-                                    y[i] = fmaf(a.lam, y[i], a.residual ? load_act(a.residual, at + i, a.out_bf16) : 0.0f);
+                                    y[i] = fmaf(a.lam, y[i],
+                                                a.residual ? load_act(a.residual, at + i, a.out_kind == kOutBf16) : 0.0f);
                         }
+                        if (MODE == kProduct && a.out_kind == kOutF16) {
+                            // FP16 of y 2^-k with 2^k beside it, as in mx_fp8_rows.cu; half a warp has 64 columns
+                            uint32_t mx = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mx = max(mx, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+#pragma unroll
+                            for (int d = 8; d; d >>= 1)
+                                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+                            const int ex = (int)(mx >> 23);
+                            const int k = ex < 30 || ex > 240 ? 0 : ex - (127 + 14);
+                            const float down = __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                y[i] *= down;
+                            if ((lane & 15) == 0 && o < a.N)
+                                a.out_scale[(int64_t)(U.tok0 + n) * a.out_scale_ld + 2 * U.f + (lane >> 4)] =
+                                    __uint_as_float((uint32_t)(127 + k) << 23);
+                        }
+                        auto two = [&](float v) -> uint32_t {
+                            return a.out_kind == kOutF16 ? __half_as_ushort(__float2half_rn(v)) : f2bf(v);
+                        };
                         if (a.out_vec && o + 4 <= a.N) {
-                            if (a.out_bf16)
+                            if (a.out_kind != kOutF32)
                                 *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) =
-                                    make_uint2(f2bf(y[0]) | (uint32_t)f2bf(y[1]) << 16,
-                                               f2bf(y[2]) | (uint32_t)f2bf(y[3]) << 16);
+                                    make_uint2(two(y[0]) | two(y[1]) << 16, two(y[2]) | two(y[3]) << 16);
                             else
                                 *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at) =
                                     make_float4(y[0], y[1], y[2], y[3]);
@@ -571,8 +604,8 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 if (o + i < a.N) {
-                                    if (a.out_bf16)
-                                        reinterpret_cast<uint16_t *>(a.out)[at + i] = f2bf(y[i]);
+                                    if (a.out_kind != kOutF32)
+                                        reinterpret_cast<uint16_t *>(a.out)[at + i] = (uint16_t)two(y[i]);
                                     else
                                         reinterpret_cast<float *>(a.out)[at + i] = y[i];
                                 }

@@ -3,6 +3,8 @@
 // weighted sum of the experts' rows.
 #include "mx_fp8.cuh"
 
+#include <cuda_fp16.h>
+
 namespace mx {
 namespace fp8 {
 
@@ -271,8 +273,9 @@ __global__ void __launch_bounds__(512) group_scatter(const int32_t *__restrict__
 
 // ------------------------------------------------------------------- combine
 
-// out[t] = residual + lambda * (Ys[t] + sum_k w_k Y[pos[t,k]]), k ascending.
-// One thread per four columns.
+// out[t] = residual + lambda * (Ys[t] + sum_k w_k Y[pos[t,k]]), k ascending, in fp32.
+// One thread per four columns, all of a token's rows requested before the first is used.
+template <bool HALF>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a)
 {
     const int t = blockIdx.y;
@@ -280,37 +283,85 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a)
     if (d >= a.D)
         return;
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int n = min(4, a.D - d);
+    const int n = min(4, a.D - d), nb = (a.D + 63) / 64, blk = d / 64;
     const bool vec = (a.D & 3) == 0;
-    auto add = [&](const float *row, float w) {
-        if (vec) {
-            const float4 y = __ldg(reinterpret_cast<const float4 *>(row + d));
-            acc[0] = fmaf(w, y.x, acc[0]), acc[1] = fmaf(w, y.y, acc[1]);
-            acc[2] = fmaf(w, y.z, acc[2]), acc[3] = fmaf(w, y.w, acc[3]);
-        } else {
+    auto load = [&](const void *y, int64_t row, float (&v)[4]) {
+        if (HALF) {
+            const uint16_t *p = static_cast<const uint16_t *>(y) + row * a.D + d;
+            uint32_t h[4] = {0, 0, 0, 0};
+            if (vec) {
+                const uint2 r = __ldg(reinterpret_cast<const uint2 *>(p));
+                h[0] = r.x & 0xFFFF, h[1] = r.x >> 16, h[2] = r.y & 0xFFFF, h[3] = r.y >> 16;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    h[j] = j < n ? __ldg(p + j) : 0;
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j < n)
-                    acc[j] = fmaf(w, __ldg(row + d + j), acc[j]);
+                v[j] = __half2float(__ushort_as_half((unsigned short)h[j]));
+        } else {
+            const float *p = static_cast<const float *>(y) + row * a.D + d;
+            if (vec) {
+                const float4 r = __ldg(reinterpret_cast<const float4 *>(p));
+                v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = j < n ? __ldg(p + j) : 0.0f;
+            }
         }
     };
-    for (int k = 0; k < a.topk; ++k) {
-        const int p = __ldg(a.pos + (int64_t)t * a.topk + k);
-        if (p >= 0)
-            add(a.Y + (int64_t)p * a.D, __ldg(a.wts + (int64_t)t * a.topk + k));
-    }
-    if (a.Ys)
-        add(a.Ys + (int64_t)t * a.D, 1.0f);
-    const int64_t at = (int64_t)t * a.D + d;
+    constexpr int kStep = 4;
+    for (int k0 = 0; k0 < a.topk; k0 += kStep) {
+        float v[kStep][4], w[kStep];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j >= n)
-            break;
-        const float v = fmaf(a.lam, acc[j], a.residual ? load_act(a.residual, at + j, a.bf16) : 0.0f);
-        if (a.bf16)
-            reinterpret_cast<uint16_t *>(a.out)[at + j] = f2bf(v);
-        else
-            reinterpret_cast<float *>(a.out)[at + j] = v;
+        for (int i = 0; i < kStep; ++i) {
+            const int p = k0 + i < a.topk ? __ldg(a.pos + (int64_t)t * a.topk + k0 + i) : -1;
+            w[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[i][j] = 0.0f;  // (a slot without an expert: nothing)
+            if (p >= 0) {
+                w[i] = __ldg(a.wts + (int64_t)t * a.topk + k0 + i);
+                if (HALF)
+                    w[i] *= __ldg(a.Yf + (int64_t)p * nb + blk);
+                load(a.Y, p, v[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[j] = fmaf(w[i], v[i][j], acc[j]);
+    }
+    if (a.Ys) {
+        float v[4];
+        load(a.Ys, t, v);
+        const float f = HALF ? __ldg(a.Ysf + (int64_t)t * nb + blk) : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[j] = fmaf(f, v[j], acc[j]);
+    }
+    const int64_t at = (int64_t)t * a.D + d;
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        y[j] = j < n ? fmaf(a.lam, acc[j], a.residual ? load_act(a.residual, at + j, a.bf16) : 0.0f) : 0.0f;
+    if (vec && a.bf16) {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+            make_uint2(f2bf(y[0]) | (uint32_t)f2bf(y[1]) << 16, f2bf(y[2]) | (uint32_t)f2bf(y[3]) << 16);
+    } else if (vec) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < n) {
+                if (a.bf16)
+                    static_cast<uint16_t *>(a.out)[at + j] = f2bf(y[j]);
+                else
+                    static_cast<float *>(a.out)[at + j] = y[j];
+            }
     }
 }
 
@@ -358,12 +409,18 @@ cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s)
         b.T = a.T - t0 < 65535 ? a.T - t0 : 65535;
         b.pos += (int64_t)t0 * a.topk;
         b.wts += (int64_t)t0 * a.topk;
-        if (b.Ys)
-            b.Ys += (int64_t)t0 * a.D;
+        if (b.Ys) {
+            b.Ys = (const char *)b.Ys + (int64_t)t0 * a.D * (b.Yf ? 2 : 4);
+            b.Ysf += b.Yf ? (int64_t)t0 * ((a.D + 63) / 64) : 0;
+        }
         if (b.residual)
             b.residual = (const char *)b.residual + (int64_t)t0 * a.D * es;
         b.out = (char *)b.out + (int64_t)t0 * a.D * es;
-        combine_kernel<<<dim3((a.D + 1023) / 1024, b.T), 256, 0, s>>>(b);
+        const dim3 grid((a.D + 1023) / 1024, b.T);
+        if (b.Yf)
+            combine_kernel<true><<<grid, 256, 0, s>>>(b);
+        else
+            combine_kernel<false><<<grid, 256, 0, s>>>(b);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess)
             return e;

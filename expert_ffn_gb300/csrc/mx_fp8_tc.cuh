@@ -23,6 +23,14 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
                  : "memory");
 }
 
+// One lane of the converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void umma_commit(uint64_t *bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -37,10 +45,6 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
         "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]), "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]),          \
         "=r"(r[o + 13]), "=r"(r[o + 14]), "=r"(r[o + 15])
 
-#define MX_W16(r)                                                                                                   \
-    "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),      \
-        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-
 // Request 16 columns of this warp's 32 TMEM lanes; r holds them after tmem_wait.
 __device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16])
 {
@@ -51,11 +55,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16])
                  : "memory");
 }
 
-// Wait for the requested columns.  r is an operand, so that nothing which reads it
-// can be scheduled before the wait.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
+// Wait for the requested columns.
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// d += (lo, hi) * f, a pair of columns.  Volatile, so that it stays behind the wait for
+// lo and hi; with the registers as operands of the wait instead, the compiler moved
+// each of them once or twice (1.5 moves an FMA).
+__device__ __forceinline__ void fma_after(uint64_t &d, uint32_t lo, uint32_t hi, uint64_t f)
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : MX_W16(r)::"memory");
+    asm volatile("{\n\t.reg .b64 p;\n\tmov.b64 p, {%1, %2};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}"
+                 : "+l"(d)
+                 : "r"(lo), "r"(hi), "l"(f));
 }
 
 __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar)
@@ -167,15 +177,16 @@ __device__ __forceinline__ float act_of(float g, int act)
 // Row groups of the matrices as token tiles of `nt` rows (one warp): tile offsets
 // tt[E + 1], first rows lo[E], lengths len[E].  A group outside the rows is cut
 // to them.
-__device__ __forceinline__ void group_table(const GemmArgs &a, int nt, int lane, int *tt, int *lo, int *len)
+__device__ __forceinline__ void group_table(const int32_t *offsets, int E, int rows, int nt, int lane, int *tt, int *lo,
+                                            int *len)
 {
     int run = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
+    for (int e0 = 0; e0 < E; e0 += 32) {
         const int e = e0 + lane;
         int b = 0, c = 0;
-        if (e < a.E) {
-            b = a.offsets ? min(max(__ldg(a.offsets + e), 0), a.rows) : 0;
-            const int d = a.offsets ? min(max(__ldg(a.offsets + e + 1), 0), a.rows) : a.rows;
+        if (e < E) {
+            b = offsets ? min(max(__ldg(offsets + e), 0), rows) : 0;
+            const int d = offsets ? min(max(__ldg(offsets + e + 1), 0), rows) : rows;
             c = max(d - b, 0);
         }
         const int t = (c + nt - 1) / nt;
@@ -186,7 +197,7 @@ __device__ __forceinline__ void group_table(const GemmArgs &a, int nt, int lane,
             if (lane >= o)
                 incl += y;
         }
-        if (e < a.E) {
+        if (e < E) {
             tt[e] = run + incl - t;
             lo[e] = b;
             len[e] = c;
@@ -194,7 +205,7 @@ __device__ __forceinline__ void group_table(const GemmArgs &a, int nt, int lane,
         run += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
     if (lane == 0)
-        tt[a.E] = run;
+        tt[E] = run;
 }
 
 }  // namespace fp8

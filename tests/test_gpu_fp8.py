@@ -172,7 +172,7 @@ def test_quantize_extreme_values(dtype):
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 2112, 2816), (2, 130, 16), (16, 128, 128), (17, 127, 129), (5, 4096, 700),
                                    (33, 257, 1037), (64, 704, 384), (65, 300, 2816), (129, 129, 640), (300, 1000, 256),
-                                   (1000, 520, 333)])
+                                   (1000, 520, 333), (2999, 2600, 333)])
 def test_matmul(m, n, k, out):
     import torch
     q, s = make_rows(m, k, 1, row_major=m % 2 == 1, spare=m % 3)
@@ -211,11 +211,12 @@ GROUPS = {
     "gaps": [0, 5, 0, 0, 300, 1, 0],
     "ragged": [17, 33, 129, 2, 64, 65, 16],
     "empty": [0, 0, 0],
+    "many": [700, 0, 129, 300, 5, 256, 257, 900],
 }
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
-@pytest.mark.parametrize("n,k", [(129, 272), (704, 640), (40, 1037)])
+@pytest.mark.parametrize("n,k", [(129, 272), (704, 640), (40, 1037), (2600, 400)])
 @pytest.mark.parametrize("groups", sorted(GROUPS))
 def test_grouped(groups, n, k, out):
     import torch
@@ -350,6 +351,8 @@ CASES = [  # T, E, K, D, I, S, act, dtype, residual
     (200, 8, 2, 336, 100, 0, mx.MX_SILU, "f32", False),
     (513, 60, 6, 272, 256, 130, mx.MX_SILU, "bf16", False),
     (700, 4, 3, 512, 384, 512, mx.MX_GELU_TANH, "f32", True),
+    (1500, 8, 2, 700, 520, 1100, mx.MX_SILU, "bf16", True),
+    (900, 4, 2, 2048, 1040, 0, mx.MX_GELU_TANH, "f32", False),
 ]
 
 
