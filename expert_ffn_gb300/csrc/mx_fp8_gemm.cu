@@ -172,7 +172,7 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
     uint64_t *rfull = fempty + kFacRing;  // cluster: every CTA has staged its sums; rfull + 1: has read them
     uint32_t *tslot = reinterpret_cast<uint32_t *>(rfull + 2);
     volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const uint32_t rank = cl > 1 ? cluster_rank() : 0;
     constexpr int kThreads = (EW + 3) * 32;
 
@@ -332,18 +332,10 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
                     fence_after();
                     const uint32_t st = smem_u32(ring + s * kStage);
                     const uint64_t xd = sw128_desc(st + NMAT * kTile);
-                    if (elect_one()) {
 #pragma unroll
-                        for (int m = 0; m < NMAT; ++m) {
-                            const uint64_t wd = sw128_desc(st + m * kTile);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                umma_f8(tmem + b * kCols + m * NT, wd + 2 * k, xd + 2 * k, idesc, k > 0);
-                        }
-                        umma_commit(empty + s);
-                        umma_commit(tfull + b);
-                    }
-                    __syncwarp();
+                    for (int m = 0; m < NMAT; ++m)
+                        umma_block(tmem + b * kCols + m * NT, sw128_desc(st + m * kTile), xd, idesc);
+                    umma_commit2(empty + s, tfull + b);
                     if (++s == NS)
                         s = 0, ph ^= 1;
                     if (++b == NB)

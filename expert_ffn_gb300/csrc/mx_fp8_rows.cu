@@ -16,9 +16,12 @@
 //         running sums of its token in registers (232 after setmaxnreg)
 //   8     TMA producer: token and weight tiles (SWIZZLE_128B)
 //   9     MMA: four tcgen05.mma (K = 32) a block, two TMEM buffers of BN columns
-//   10    factors: sx * sw of a block for each token (and 128 weight rows) into a ring
-//         in shared memory; loaded by the summing threads themselves they cost 560
-//         cycles of waiting in every block
+//   10    factors: sx * sw of a block for each token (and 128 weight rows) into shared
+//         memory, beside the TMEM buffer; loaded by the summing threads themselves they
+//         cost 560 cycles of waiting in every block
+// A barrier or a load of shared memory takes 100 to 300 cycles while an MMA reads its
+// operands there (15 to 30 without), so a buffer has one barrier for its products and
+// its factors, and one for its release.
 // Results pass through 2 KB of shared memory a warp, 64 bytes of each of its 32
 // rows at a time, so that they leave in 16-byte pieces of whole sectors.
 //
@@ -33,7 +36,6 @@ namespace {
 
 constexpr int kSumWarps = 8, kWarps = 12, kThreads = kWarps * 32;
 constexpr uint32_t kTile = 128 * 128;
-constexpr int kFac = 8;  // blocks of factors in flight
 
 constexpr int kAcc = 2;  // TMEM buffers of BN columns
 
@@ -52,8 +54,8 @@ __host__ __device__ constexpr RowTail row_tail()
     o += kSumWarps * 2048;
     t.am = o;  // largest hidden value of each token in each half of the columns
     o += 2 * 128 * 4;
-    t.fac = o;  // [block of the ring][half or matrix][token]
-    o += kFac * 2 * 128 * 4;
+    t.fac = o;  // [buffer][half or matrix][token]
+    o += kAcc * 2 * 128 * 4;
     t.tab = o;
     o += (3 * kMaxExperts + 16) * 4;
     t.bars = o;
@@ -157,10 +159,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     float *fac = reinterpret_cast<float *>(tail + RT.fac);
     int *tab = reinterpret_cast<int *>(tail + RT.tab);
     uint64_t *full = reinterpret_cast<uint64_t *>(tail + RT.bars), *empty = full + 12;
-    uint64_t *tfull = empty + 12, *tempty = tfull + kAcc, *ffull = tempty + kAcc, *fempty = ffull + kFac;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(fempty + kFac);
+    uint64_t *tfull = empty + 12, *tempty = tfull + kAcc;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(tempty + kAcc);
     volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -168,12 +170,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < kAcc; ++i) {
-            mbar_init(tfull + i, 1);
+            mbar_init(tfull + i, 2);  // products, factors
             mbar_init(tempty + i, kSumWarps);
-        }
-        for (int i = 0; i < kFac; ++i) {
-            mbar_init(ffull + i, 1);
-            mbar_init(fempty + i, kSumWarps);
         }
         *abort = 0;
         fence_mbar_init();
@@ -205,8 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     if (warp >= kSumWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         // (TMA and MMA: the whole warp walks the loop and one elected lane issues.  Behind `lane ==
-        // 0` the compiler does not know that one lane is left and issues each copy or MMA in a
-        // loop over lanes: 150 cycles an MMA.)
+        // 0` the compiler does not know that one lane is left and issues each in a loop over lanes.)
         if (warp == 8) {
             // -------------------------------------------------- TMA producer
             int s = 0;
@@ -245,19 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             for (int u = blockIdx.x; u < w.n; u += gridDim.x) {
                 const int KB = blocks(a.p[tile_at(a, w, u).p].K);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!wwait(tempty + b, tph, a.err, abort) || !wwait(full + s, ph, a.err, abort))
+                    if (!wwait(full + s, ph, a.err, abort) || !wwait(tempty + b, tph, a.err, abort))
                         goto issued;
                     fence_after();
                     const uint32_t st = smem_u32(ring + s * kStage);
                     const uint64_t xd = sw128_desc(st), wd = sw128_desc(st + kTile);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_f8(tmem + b * BN, xd + 2 * k, wd + 2 * k, idesc, k > 0);
-                        umma_commit(tfull + b);
-                        umma_commit(empty + s);
-                    }
-                    __syncwarp();
+                    umma_block(tmem + b * BN, xd, wd, idesc);
+                    umma_commit2(tfull + b, empty + s);
                     if (++b == kAcc)
                         b = 0, tph ^= 1;
                     if (++s == NS)
@@ -268,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         } else if (warp == 10) {
             // ------------------------------------------------------- factors
             constexpr int BATCH = 2;
-            int q = 0;
+            int b = 0;
             uint32_t ph = 1;
             bool ok = true;
             for (int u = blockIdx.x; u < w.n && ok; u += gridDim.x) {
@@ -298,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     for (int i = 0; i < BATCH; ++i) {
                         if (kb0 + i >= KB)
                             break;
-                        ok &= wwait(fempty + q, ph, a.err, abort);
-                        float *o = fac + q * 256 + lane;
+                        ok &= wwait(tempty + b, ph, a.err, abort);
+                        float *o = fac + b * 256 + lane;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             o[32 * j] = x[i][j] * w0[i];
@@ -307,9 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                         }
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive(ffull + q);
-                        if (++q == kFac)
-                            q = 0, ph ^= 1;
+                            mbar_arrive(tfull + b);
+                        if (++b == kAcc)
+                            b = 0, ph ^= 1;
                     }
                 }
             }
@@ -320,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t ta = tmem + ((uint32_t)quad << 21);
         uint4 *mine = reinterpret_cast<uint4 *>(tail + RT.out + warp * 2048);
-        int b = 0, q = 0;
-        uint32_t tph = 0, fph = 0;
+        int b = 0;
+        uint32_t tph = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < w.n && ok; u += gridDim.x) {
             const Tile T = tile_at(a, w, u);
@@ -343,38 +334,27 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 if (++b == kAcc)
                     b = 0, tph ^= 1;
             };
-            auto used = [&]() {
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(fempty + q);
-                if (++q == kFac)
-                    q = 0, fph ^= 1;
-            };
             if (!live)
                 for (int kb = 0; kb < KB; ++kb) {
-                    ok &= bwait(ffull + q, fph, a.err, abort);
-                    used();
                     ok &= bwait(tfull + b, tph, a.err, abort);
                     release();
                 }
             else
                 for (int kb = 0; kb < KB; ++kb) {
-                    ok &= bwait(ffull + q, fph, a.err, abort);
-                    const float f[2] = {fac[q * 256 + row], fac[q * 256 + 128 + row]};
-                    used();
                     ok &= bwait(tfull + b, tph, a.err, abort);
                     fence_after();
                     // 64 columns of each half of the buffer, 32 at a time
                     const uint32_t tb = ta + b * BN + wg * 64;
                     uint32_t r[2][32];
                     tmem_get32(tb, r[0]);
+                    const float f[2] = {fac[b * 256 + row], fac[b * 256 + 128 + row]};
 #pragma unroll
                     for (int h = 0; h < 2 * NSUB; ++h) {
                         tmem_wait();
                         if (h + 1 < 2 * NSUB)
                             tmem_get32(tb + ((h + 1) >> 1) * 128 + ((h + 1) & 1) * 32, r[(h + 1) & 1]);
                         else
-                            release();  // (the columns are in registers)
+                            release();  // (the columns and the factors are in registers)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             fma_behind(acc[h * 32 + i], r[h & 1][i], f[h >> 1]);

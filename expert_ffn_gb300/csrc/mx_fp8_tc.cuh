@@ -15,11 +15,21 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr)
 // e4m3 A and B (K-major), fp32 D, M = 128, N = n.
 __device__ __forceinline__ uint32_t idesc_e4m3(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
 
-__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// D = A B^T over a block of 128 columns: four MMAs of K = 32, the first of which
+// overwrites D.  By one elected lane of a converged warp.  In one statement, with the
+// election inside: as four statements behind a branch on it they took 200 cycles an
+// MMA to issue, whatever N; so they take the 128 that N = 256 needs.
+__device__ __forceinline__ void umma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+                 "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+                 "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+                 "elect.sync _|q, 0xffffffff;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, !p;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, p;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, p;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc)
                  : "memory");
 }
 
@@ -31,11 +41,18 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-__device__ __forceinline__ void umma_commit(uint64_t *bar)
+// Arrive on both barriers when the MMAs issued so far are done (one elected lane).
+__device__ __forceinline__ void umma_commit2(uint64_t *x, uint64_t *y)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(smem_u32(x)),
+                 "r"(smem_u32(y))
                  : "memory");
 }
+
+// The warp's index, known to the compiler to be the same in all its lanes.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0); }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
