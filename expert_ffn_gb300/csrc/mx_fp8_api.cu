@@ -469,14 +469,15 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
     const double active = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)K / E), (double)T));
     const double units = active * IB + SB;
     const int DB = blocks(D);
-    const int most = 4;
+    // A cluster holds one unit, whose columns it reduces in one pass.
+    const int most = p.nt <= 32 ? 4 : 1;
     g.cl = 1;
     while (g.cl < most && units * g.cl * 2 <= 2.0 * sms && DB / (g.cl * 2) >= 2)
         g.cl *= 2;
     const int per_sm = p.nt <= 32 ? 2 : 1;
     const int smem = per_sm == 2 ? kSmemHalf : kSmem;
     g.stages = fit_stages(kFewGateUp, p.nt, smem, 16);
-    int grid = std::max(1, std::min(per_sm * sms / g.cl, p.items)) * g.cl;
+    int grid = g.cl > 1 ? p.items * g.cl : std::max(1, std::min(per_sm * sms, p.items));
     if ((e = launch_gemm(kFewGateUp, p.nt, g, grid, s)) != cudaSuccess)
         return cuda_fail(e, "FP8 gate/up");
 
@@ -499,10 +500,10 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
     }
     const double items = active * IB + SB;
     d.cl = 1;
-    while (d.cl < most && DB * d.cl * 2 <= 2 * sms && items / (d.cl * 2) >= 2)
+    while (d.cl < (p.nt <= 64 ? 4 : 1) && DB * d.cl * 2 <= 2 * sms && items / (d.cl * 2) >= 2)
         d.cl *= 2;
     d.stages = fit_stages(kFewDown, p.nt, smem, 16);
-    grid = std::min(per_sm * sms / d.cl, DB) * d.cl;
+    grid = d.cl > 1 ? DB * d.cl : std::min(per_sm * sms, DB);
     if ((e = launch_gemm(kFewDown, p.nt, d, grid, s)) != cudaSuccess)
         return cuda_fail(e, "FP8 down");
     return MX_OK;

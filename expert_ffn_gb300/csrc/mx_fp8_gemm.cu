@@ -7,23 +7,21 @@
 // in fp32 by CUDA cores, which keep the running sums in registers.  The weights
 // take the M side of the MMA (128 rows = one block of weight scales, so the
 // weight scale is one number per MMA tile and block) and the tokens its N side
-// (16 to 256): a single token then costs the smallest N, a group of tokens is
+// (16 to 64): a single token then costs the smallest N, a group of tokens is
 // padded to 16 rather than to 128, and weights stream from HBM straight into
 // the MMA's operand layout without passing through a thread.
 //
 // A CTA walks units (128 weight rows x one token tile, or what Mode says).  Warps:
-//   0 .. EW-1  sums: tcgen05.ld of a block's products (lane quadrant = warp % 4;
-//              with EW = 8 two warpgroups take alternate chunks of 16 tokens),
-//              packed two-lane FMA by the block's factors, and the epilogue
-//   EW         TMA producer: weight tiles 128 x 128 bytes and token tiles
-//              (SWIZZLE_128B) into a ring of stages
-//   EW + 1     MMA: one lane issues four tcgen05.mma (K = 32) per matrix and block
-//              into a ring of TMEM buffers
-//   EW + 2     factors: sx * sw of a block for each token into a ring in shared
-//              memory, so that the summing warps read them as broadcast vectors
-// Few units: a cluster of `cl` CTAs splits the inner dimension; each CTA sums
-// every cl-th token column over the partial sums in all their shared memories, in
-// rank order, so the result does not depend on timing.
+//   0-3  sums: tcgen05.ld of a block's products (lane quadrant = warp % 4), packed
+//        two-lane FMA by the block's factors, and the epilogue
+//   4    TMA producer: weight tiles 128 x 128 bytes and token tiles (SWIZZLE_128B)
+//        into a ring of stages
+//   5    MMA: four tcgen05.mma (K = 32) per matrix and block into a ring of TMEM buffers
+//   6    factors: sx * sw of a block for each token into a ring in shared memory, so that
+//        the summing warps read them as broadcast vectors
+// Few units: a cluster of `cl` CTAs splits the inner dimension of one unit; each CTA
+// sums every cl-th token column over the partial sums in all their shared memories,
+// in rank order, so the result does not depend on timing.
 //
 // Every wait is bounded: a wait that gives up sets the caller's error word and
 // ends the CTA's work.
@@ -39,13 +37,13 @@ namespace {
 constexpr uint32_t kTile = 128 * 128;  // bytes of one weight tile
 constexpr int kFacRing = 8;            // blocks of factors in flight
 
-constexpr int epi_warps(int nt) { return nt > 64 ? 8 : 4; }
+constexpr int kSumWarps = 4, kThreads = (kSumWarps + 3) * 32;
 constexpr int n_mats(int mode) { return mode == kGateUp || mode == kFewGateUp ? 2 : 1; }
-// TMEM buffers: at most 256 columns up to 64 tokens (two CTAs of an SM share 512).
+// TMEM buffers: at most 256 columns (two CTAs of an SM share 512).
 constexpr int n_acc(int mode, int nt)
 {
-    const int cols = n_mats(mode) * nt, lim = nt > 64 ? 512 : 256;
-    return lim / cols > 4 ? 4 : lim / cols;
+    const int cols = n_mats(mode) * nt;
+    return 256 / cols > 4 ? 4 : 256 / cols;
 }
 constexpr uint32_t tmem_cols(int mode, int nt)
 {
@@ -56,8 +54,8 @@ constexpr uint32_t tmem_cols(int mode, int nt)
 }
 constexpr uint32_t stage_bytes(int mode, int nt) { return n_mats(mode) * kTile + nt * 128; }
 
-// Token columns of one pass of the epilogue (per warpgroup).
-constexpr int pass_cols(int mode, int nt) { return nt > 64 ? (n_mats(mode) == 2 ? 16 : 32) : nt < 32 ? nt : 32; }
+// Token columns of one pass of the epilogue.
+constexpr int pass_cols(int mode, int nt) { return n_mats(mode) * nt > 64 ? 32 : nt; }
 
 // Dynamic shared memory after the ring (byte offsets from its end).
 struct Tail {
@@ -67,8 +65,8 @@ __host__ __device__ constexpr Tail tail_of(int mode, int nt)
 {
     Tail t{};
     int o = 0;
-    t.stage = o;  // sums on their way out: [warpgroup][matrix][column][128 rows] fp32
-    o += epi_warps(nt) / 4 * n_mats(mode) * pass_cols(mode, nt) * 512;
+    t.stage = o;  // sums on their way out: [matrix][column][128 rows] fp32
+    o += n_mats(mode) * pass_cols(mode, nt) * 512;
     t.fac = o;
     o += kFacRing * n_mats(mode) * nt * 4;
     t.tab = o;  // expert tables
@@ -152,11 +150,100 @@ __device__ __forceinline__ void tile_of(const GemmArgs &a, const Walk &w, const 
     }
 }
 
+// Results of token column n of a unit: 128 weight rows, four to a lane.
 template <int MODE, int NT>
-__global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) gemm_kernel(const __grid_constant__ GemmArgs a)
+__device__ __forceinline__ void emit(const GemmArgs &a, const Unit &U, int n, const float4 (&v)[n_mats(MODE)], int lane)
 {
-    constexpr int NMAT = n_mats(MODE), EW = epi_warps(NT), NWG = EW / 4, NB = n_acc(MODE, NT);
-    constexpr int NCH = NT / 16 / NWG, NCOL = NCH * 16;  // chunks and columns of a summing thread
+    constexpr int NMAT = n_mats(MODE);
+    if constexpr (NMAT == 2) {
+        const float h[4] = {act_of(v[0].x, a.act) * v[NMAT - 1].x, act_of(v[0].y, a.act) * v[NMAT - 1].y,
+                            act_of(v[0].z, a.act) * v[NMAT - 1].z, act_of(v[0].w, a.act) * v[NMAT - 1].w};
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mx = max(mx, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+        const float s = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, mx)), 0);
+        // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
+        const float inv = __frcp_rn(s);
+        uint32_t e = e4m3_x2(h[0] * inv, h[1] * inv) | e4m3_x2(h[2] * inv, h[3] * inv) << 16;
+        float sc = s;
+        if (MODE == kFewGateUp && U.e >= 0) {
+            // the routing weight joins the scale; a token that did not choose the expert adds nothing
+            const int mine = lane < a.topk ? __ldg(a.idx + n * a.topk + lane) : -1;
+            const float wt = mine == U.e ? __ldg(a.wts + n * a.topk + lane) : 0.0f;
+            if (__any_sync(0xFFFFFFFFu, mine == U.e)) {
+                float sum = wt;
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                sc = s * sum;
+            } else {
+                sc = 0.0f;
+                e = 0;
+            }
+        }
+        uint8_t *hp = MODE == kFewGateUp ? a.h + ((int64_t)U.item * NT + n) * 128
+                                         : a.h + (int64_t)(U.tok0 + n) * a.ldh + U.f * kBlk;
+        reinterpret_cast<uint32_t *>(hp)[lane] = e;
+        if (lane == 0)
+            a.hs[MODE == kFewGateUp ? (int64_t)U.item * NT + n : (int64_t)U.f * a.hs_ld + U.tok0 + n] = sc;
+    } else {
+        const int o = U.f * kBlk + 4 * lane;
+        const int64_t at = (int64_t)(U.tok0 + n) * a.ldo + o;
+        float y[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+        if (MODE == kFewDown) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (o + i < a.N)
+                    y[i] = fmaf(a.lam, y[i],
+                                a.residual ? load_act(a.residual, at + i, a.out_kind == kOutBf16) : 0.0f);
+        }
+        if (MODE == kProduct && a.out_kind == kOutF16) {
+            // FP16 of y 2^-k with 2^k beside it, as in mx_fp8_rows.cu; half a warp has 64 columns
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mx = max(mx, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int d = 8; d; d >>= 1)
+                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+            const int ex = (int)(mx >> 23);
+            const int k = ex < 30 || ex > 240 ? 0 : ex - (127 + 14);
+            const float down = __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                y[i] *= down;
+            if ((lane & 15) == 0 && o < a.N)
+                a.out_scale[(int64_t)(U.tok0 + n) * a.out_scale_ld + 2 * U.f + (lane >> 4)] =
+                    __uint_as_float((uint32_t)(127 + k) << 23);
+        }
+        auto two = [&](float v) -> uint32_t {
+            return a.out_kind == kOutF16 ? __half_as_ushort(__float2half_rn(v)) : f2bf(v);
+        };
+        if (a.out_vec && o + 4 <= a.N) {
+            if (a.out_kind != kOutF32)
+                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) =
+                    make_uint2(two(y[0]) | two(y[1]) << 16, two(y[2]) | two(y[3]) << 16);
+            else
+                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at) =
+                    make_float4(y[0], y[1], y[2], y[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (o + i < a.N) {
+                    if (a.out_kind != kOutF32)
+                        reinterpret_cast<uint16_t *>(a.out)[at + i] = (uint16_t)two(y[i]);
+                    else
+                        reinterpret_cast<float *>(a.out)[at + i] = y[i];
+                }
+        }
+    }
+}
+
+template <int MODE, int NT>
+__global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const __grid_constant__ GemmArgs a)
+{
+    constexpr int NMAT = n_mats(MODE), EW = kSumWarps, NB = n_acc(MODE, NT), NCH = NT / 16;
     constexpr uint32_t kStage = stage_bytes(MODE, NT), kCols = NMAT * NT, kTmem = tmem_cols(MODE, NT);
     constexpr bool FEW = MODE == kFewGateUp || MODE == kFewDown;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -165,16 +252,16 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
     const int NS = a.stages, cl = a.cl;
     uint8_t *tail = ring + NS * kStage;
     constexpr Tail T = tail_of(MODE, NT);
+    constexpr int GC = pass_cols(MODE, NT);
+    float *stage = reinterpret_cast<float *>(tail + T.stage);
     float *fac = reinterpret_cast<float *>(tail + T.fac);
     int *tab = reinterpret_cast<int *>(tail + T.tab);
     uint64_t *full = reinterpret_cast<uint64_t *>(tail + T.bars), *empty = full + 16;
     uint64_t *tfull = empty + 16, *tempty = tfull + 4, *ffull = tempty + 4, *fempty = ffull + kFacRing;
-    uint64_t *rfull = fempty + kFacRing;  // cluster: every CTA has staged its sums; rfull + 1: has read them
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(rfull + 2);
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(fempty + kFacRing);
     volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const uint32_t rank = cl > 1 ? cluster_rank() : 0;
-    constexpr int kThreads = (EW + 3) * 32;
 
     if (a.pdl)
         pdl_trigger();
@@ -191,8 +278,6 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
             mbar_init(ffull + i, 1);
             mbar_init(fempty + i, EW);
         }
-        mbar_init(rfull, cl);
-        mbar_init(rfull + 1, cl);
         *abort = 0;
         fence_mbar_init();
     }
@@ -411,34 +496,30 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
         }
     } else {
         // -------------------------------------------------------------- sums
-        const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-        const uint32_t ta = tmem + ((uint32_t)quad << 21);
-        constexpr int GC = pass_cols(MODE, NT), GCH = GC / 16;  // columns and chunks of an epilogue pass
-        float *stage = reinterpret_cast<float *>(tail + T.stage) + wg * NMAT * GC * 128;
+        const int row = warp * 32 + lane;
+        const uint32_t ta = tmem + ((uint32_t)warp << 21);
         int b = 0, q = 0;
-        uint32_t tph = 0, fph = 0, rph = 0;
+        uint32_t tph = 0, fph = 0;
         bool ok = true;
         for (int u = w.first; u < w.n_units && ok; u += w.step) {
             const Unit U = unit_of<MODE, NT>(a, w, u);
-            const int nch = ((U.n + 15) / 16 + NWG - 1 - wg) / NWG;  // this warpgroup's chunks: every NWG-th
-            uint64_t acc[NMAT][NCOL / 2];
+            const int nch = (U.n + 15) / 16;
+            uint64_t acc[NMAT][NT / 2];
 #pragma unroll
             for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-                for (int i = 0; i < NCOL / 2; ++i)
+                for (int i = 0; i < NT / 2; ++i)
                     acc[m][i] = 0;
+            // (a wait that gave up does not leave the loop early: the sums stay in place)
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                if (!wwait(ffull + q, fph, a.err, abort) || !wwait(tfull + b, tph, a.err, abort)) {
-                    ok = false;
-                    break;
-                }
+                ok &= bwait(ffull + q, fph, a.err, abort);
+                ok &= bwait(tfull + b, tph, a.err, abort);
                 fence_after();
-                const float4 *f = reinterpret_cast<const float4 *>(fac + q * NMAT * NT + wg * 16);
-                const uint32_t tb = ta + b * kCols + wg * 16;
+                const float4 *f = reinterpret_cast<const float4 *>(fac + q * NMAT * NT);
+                const uint32_t tb = ta + b * kCols;
                 // chunk by chunk, the next one's columns on their way while one is summed
                 uint32_t r[2][16];
-                if (nch > 0)
-                    tmem_ld16(tb, r[0]);
+                tmem_ld16(tb, r[0]);
 #pragma unroll
                 for (int i = 0; i < NCH * NMAT; ++i) {
                     const int ch = i / NMAT, m = i % NMAT;
@@ -446,10 +527,10 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
                         const int nx = i + 1;
                         tmem_wait();
                         if (nx < NCH * NMAT && nx / NMAT < nch)
-                            tmem_ld16(tb + (nx % NMAT) * NT + nx / NMAT * NWG * 16, r[nx & 1]);
+                            tmem_ld16(tb + (nx % NMAT) * NT + nx / NMAT * 16, r[nx & 1]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float4 v = f[(m * NT + ch * NWG * 16) / 4 + j];
+                            const float4 v = f[(m * NT + ch * 16) / 4 + j];
                             const uint32_t *p = r[i & 1] + 4 * j;
                             fma_after(acc[m][ch * 8 + 2 * j], p[0], p[1], pair_f32(v.x, v.y));
                             fma_after(acc[m][ch * 8 + 2 * j + 1], p[2], p[3], pair_f32(v.z, v.w));
@@ -467,6 +548,7 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
                 if (++q == kFacRing)
                     q = 0, fph ^= 1;
             }
+            ok = __all_sync(0xFFFFFFFFu, ok);
 
             // The sums leave in passes of GC columns through shared memory, where a
             // warp takes a whole column (128 rows, four to a lane): its stores are
@@ -474,11 +556,9 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
             // the code stays small -- unrolled over the registers it ran at the rate
             // of its instruction fetches (64 columns: 5 us for the stores alone).
 #pragma unroll
-            for (int ps = 0; ps < NCH / GCH; ++ps) {
-                if (ps * GCH >= nch && cl == 1)
+            for (int ps = 0; ps < NT / GC; ++ps) {
+                if (ps * GC >= U.n)
                     break;
-                if (cl > 1 && (u != w.first || ps > 0))
-                    ok = ok && wwait<true>(rfull + 1, rph ^ 1, a.err, abort);
 #pragma unroll
                 for (int m = 0; m < NMAT; ++m)
 #pragma unroll
@@ -489,130 +569,45 @@ __global__ void __launch_bounds__((epi_warps(NT) + 3) * 32, NT <= 32 ? 2 : 1) ge
                         stage[(m * GC + 2 * j + 1) * 128 + row] = hi;
                     }
                 if (cl > 1)
-                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                // (the four warps of a warpgroup give up together: none is left at a barrier)
+                    break;  // (one unit and one pass: the rest follows the cluster's barrier)
+                // (the four warps give up together: none is left at a barrier)
                 __syncwarp();
-                ok = named_and(1 + wg, 128, ok);
+                ok = named_and(1, 128, ok);
                 if (!ok)
                     break;
-                if (cl > 1) {
-                    if (quad == 0 && lane < cl)
-                        arrive_cluster(mapa(smem_u32(rfull), lane));
-                    ok = wwait<true>(rfull, rph, a.err, abort);
-                }
-                // column n of the tile: CTA n % cl of the cluster
-                for (int j = quad; j < GC && ok; j += 4) {
-                    const int n = ((ps * GCH + (j >> 4)) * NWG + wg) * 16 + (j & 15);
-                    if (n >= U.n || (n & (cl - 1)) != (int)rank)
-                        continue;
+                for (int j = warp; j < GC && ps * GC + j < U.n; j += 4) {
                     float4 v[NMAT];
 #pragma unroll
-                    for (int m = 0; m < NMAT; ++m) {
-                        const float4 *at = reinterpret_cast<const float4 *>(stage + (m * GC + j) * 128) + lane;
-                        if (cl == 1) {
-                            v[m] = *at;
-                        } else {
-                            v[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                            for (int r = 0; r < cl; ++r) {
-                                const float4 p = ld_cluster(mapa(smem_u32(at), r));
-                                v[m].x += p.x, v[m].y += p.y, v[m].z += p.z, v[m].w += p.w;
-                            }
-                        }
-                    }
-                    if constexpr (NMAT == 2) {
-                        const float h[4] = {act_of(v[0].x, a.act) * v[NMAT - 1].x, act_of(v[0].y, a.act) * v[NMAT - 1].y,
-                                            act_of(v[0].z, a.act) * v[NMAT - 1].z, act_of(v[0].w, a.act) * v[NMAT - 1].w};
-                        uint32_t mx = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mx = max(mx, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-                        const float s = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, mx)), 0);
-                        // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
-                        const float inv = __frcp_rn(s);
-                        uint32_t e = e4m3_x2(h[0] * inv, h[1] * inv) | e4m3_x2(h[2] * inv, h[3] * inv) << 16;
-                        float sc = s;
-                        if (MODE == kFewGateUp && U.e >= 0) {
-                            // the routing weight joins the scale; a token that did not choose the expert adds nothing
-                            const int mine = lane < a.topk ? __ldg(a.idx + n * a.topk + lane) : -1;
-                            const float wt = mine == U.e ? __ldg(a.wts + n * a.topk + lane) : 0.0f;
-                            if (__any_sync(0xFFFFFFFFu, mine == U.e)) {
-                                float sum = wt;
-#pragma unroll
-                                for (int o = 16; o; o >>= 1)
-                                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                                sc = s * sum;
-                            } else {
-                                sc = 0.0f;
-                                e = 0;
-                            }
-                        }
-                        uint8_t *hp = MODE == kFewGateUp ? a.h + ((int64_t)U.item * NT + n) * 128
-                                                         : a.h + (int64_t)(U.tok0 + n) * a.ldh + U.f * kBlk;
-                        reinterpret_cast<uint32_t *>(hp)[lane] = e;
-                        if (lane == 0)
-                            a.hs[MODE == kFewGateUp ? (int64_t)U.item * NT + n : (int64_t)U.f * a.hs_ld + U.tok0 + n] = sc;
-                    } else {
-                        const int o = U.f * kBlk + 4 * lane;
-                        const int64_t at = (int64_t)(U.tok0 + n) * a.ldo + o;
-                        float y[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-                        if (MODE == kFewDown) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (o + i < a.N)
-                                    y[i] = fmaf(a.lam, y[i],
-                                                a.residual ? load_act(a.residual, at + i, a.out_kind == kOutBf16) : 0.0f);
-                        }
-                        if (MODE == kProduct && a.out_kind == kOutF16) {
-                            // FP16 of y 2^-k with 2^k beside it, as in mx_fp8_rows.cu; half a warp has 64 columns
-                            uint32_t mx = 0;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mx = max(mx, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-#pragma unroll
-                            for (int d = 8; d; d >>= 1)
-                                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-                            const int ex = (int)(mx >> 23);
-                            const int k = ex < 30 || ex > 240 ? 0 : ex - (127 + 14);
-                            const float down = __uint_as_float((uint32_t)(127 - k) << 23);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                y[i] *= down;
-                            if ((lane & 15) == 0 && o < a.N)
-                                a.out_scale[(int64_t)(U.tok0 + n) * a.out_scale_ld + 2 * U.f + (lane >> 4)] =
-                                    __uint_as_float((uint32_t)(127 + k) << 23);
-                        }
-                        auto two = [&](float v) -> uint32_t {
-                            return a.out_kind == kOutF16 ? __half_as_ushort(__float2half_rn(v)) : f2bf(v);
-                        };
-                        if (a.out_vec && o + 4 <= a.N) {
-                            if (a.out_kind != kOutF32)
-                                *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) =
-                                    make_uint2(two(y[0]) | two(y[1]) << 16, two(y[2]) | two(y[3]) << 16);
-                            else
-                                *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at) =
-                                    make_float4(y[0], y[1], y[2], y[3]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (o + i < a.N) {
-                                    if (a.out_kind != kOutF32)
-                                        reinterpret_cast<uint16_t *>(a.out)[at + i] = (uint16_t)two(y[i]);
-                                    else
-                                        reinterpret_cast<float *>(a.out)[at + i] = y[i];
-                                }
-                        }
-                    }
+                    for (int m = 0; m < NMAT; ++m)
+                        v[m] = reinterpret_cast<const float4 *>(stage + (m * GC + j) * 128)[lane];
+                    emit<MODE, NT>(a, U, ps * GC + j, v, lane);
                 }
                 __syncwarp();
-                ok = named_and(1 + wg, 128, ok);
+                ok = named_and(1, 128, ok);
                 if (!ok)
                     break;
-                if (cl > 1) {
-                    if (quad == 0 && lane < cl)
-                        arrive_cluster(mapa(smem_u32(rfull + 1), lane));
-                    rph ^= 1;
+            }
+        }
+    }
+    if (cl > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp < kSumWarps && w.first < w.n_units && !*abort) {
+            const Unit U = unit_of<MODE, NT>(a, w, w.first);
+            // column n of the tile: CTA n % cl of the cluster, over all ranks in order
+            for (int n = rank + cl * warp; n < U.n; n += cl * 4) {
+                float4 v[NMAT];
+#pragma unroll
+                for (int m = 0; m < NMAT; ++m) {
+                    const uint32_t at = smem_u32(stage + (m * GC + n) * 128 + 4 * lane);
+                    v[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                    for (int r = 0; r < cl; ++r) {
+                        const float4 p = ld_cluster(mapa(at, r));
+                        v[m].x += p.x, v[m].y += p.y, v[m].z += p.z, v[m].w += p.w;
+                    }
                 }
+                emit<MODE, NT>(a, U, n, v, lane);
             }
         }
     }
@@ -642,7 +637,7 @@ cudaError_t launch_t(const GemmArgs &a, int grid, cudaStream_t s)
         return e;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(grid);
-    c.blockDim = dim3((epi_warps(NT) + 3) * 32);
+    c.blockDim = dim3(kThreads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
     cudaLaunchAttribute at[2];
