@@ -22,8 +22,8 @@
 // A barrier or a load of shared memory takes 100 to 300 cycles while an MMA reads its
 // operands there (15 to 30 without), so a buffer has one barrier for its products and
 // its factors, and one for its release.
-// Results pass through 2 KB of shared memory a warp, 64 bytes of each of its 32
-// rows at a time, so that they leave in 16-byte pieces of whole sectors.
+// Results pass through 2 KB of shared memory a warp, 16 of its 32 rows at a time, so
+// that they leave as whole lines.
 //
 // A launch may hold two problems, the routed experts' and the shared expert's: the
 // first is bound by HBM, the second by the tensor cores, and their tiles alternate.
@@ -130,6 +130,9 @@ __device__ __forceinline__ void fma_behind(float &d, uint32_t v, float f)
 // 16-byte piece c (0..3) of row r in a warp's 2 KB: 32 rows of 64 bytes, pieces
 // rotated so that neither a row per lane nor four lanes per row conflict.
 __device__ __forceinline__ int piece(int r, int c) { return r * 4 + (c ^ ((r >> 1) & 3)); }
+
+// The same for 16 rows of 128 bytes.
+__device__ __forceinline__ int line_piece(int r, int c) { return r * 8 + (c ^ (r & 7)); }
 
 __device__ __forceinline__ uint32_t bf16_x2(float lo, float hi)
 {
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 for (int kb = 0; kb < KB; ++kb) {
                     ok &= bwait(tfull + b, tph, a.err, abort);
                     fence_after();
-                    // 64 columns of each half of the buffer, 32 at a time
+                    // 64 columns of each half of the buffer, 32 at a time, the next 32 on their way
                     const uint32_t tb = ta + b * BN + wg * 64;
                     uint32_t r[2][32];
                     tmem_get32(tb, r[0]);
@@ -429,64 +432,70 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                                 __uint_as_float((uint32_t)(127 + k) << 23);
                     }
                 }
-                // passes of 64 bytes a row: 32 two-byte or 16 four-byte columns
-                char *base = static_cast<char *>(P.out) +
-                             ((int64_t)(tok0 + quad * 32 + (lane >> 2)) * P.ldo + o0 + (lane & 3) * per) * es;
-                const int64_t rstep = 8 * P.ldo * es;
-                const int rows = n - quad * 32 - (lane >> 2);  // this lane's rows: 0, 8, 16, 24 below it
-                auto flush = [&](int c0) {
+                // Passes of 16 rows x 128 bytes (64 two-byte or 32 four-byte columns): whole lines leave.
+                const int prow = lane >> 3, col = (lane & 7) * per;  // this lane's row of four, and column
+                char *base = static_cast<char *>(P.out) + ((int64_t)(tok0 + quad * 32 + prow) * P.ldo + o0 + col) * es;
+                const int64_t rstep = 4 * P.ldo * es;
+                // rows r0 .. r0 + 15, columns c0 on; x: this lane's row, eight pieces of 16 bytes
+                auto pass = [&](int r0, int c0, auto &&x) {
+                    if ((lane >> 4) == (r0 >> 4))
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            mine[line_piece(lane & 15, c)] = x(c);
                     __syncwarp();
-                    const int o = o0 + c0 + (lane & 3) * per;
+                    const int o = o0 + c0 + col, rows = n - quad * 32 - r0 - prow;  // (rows 0, 4, 8, 12 below it)
+                    char *to = base + (r0 >> 2) * rstep + c0 * es;
                     if (P.out_vec && o + per <= P.N) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (8 * i < rows)
-                                *reinterpret_cast<uint4 *>(base + i * rstep + c0 * es) =
-                                    mine[piece(i * 8 + (lane >> 2), lane & 3)];
+                            if (4 * i < rows)
+                                *reinterpret_cast<uint4 *>(to + i * rstep) = mine[line_piece(4 * i + prow, lane & 7)];
                     } else {
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 v = mine[piece(i * 8 + (lane >> 2), lane & 3)];
-                            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                            char *p = base + i * rstep + c0 * es;
-                            if (8 * i >= rows)
-                                continue;
+                        for (int i = 0; i < 4 && 4 * i < rows; ++i) {
+                            const uint4 v = mine[line_piece(4 * i + prow, lane & 7)];
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            char *p = to + i * rstep;
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
                                 if (k >= per || o + k >= P.N)
                                     break;
                                 if (es == 2)
-                                    reinterpret_cast<uint16_t *>(p)[k] = (uint16_t)(x[k >> 1] >> (16 * (k & 1)));
+                                    reinterpret_cast<uint16_t *>(p)[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
                                 else
-                                    reinterpret_cast<uint32_t *>(p)[k] = x[k & 3];
+                                    reinterpret_cast<uint32_t *>(p)[k] = w[k & 3];
                             }
                         }
                     }
                     __syncwarp();
                 };
-                if (P.out_kind != kOutF32) {
-                    const bool half = P.out_kind == kOutF16;
 #pragma unroll
-                    for (int p = 0; p < NC / 32; ++p) {
+                for (int j = 0; j < NSUB; ++j) {
+                    const float *y = acc + 64 * j;
+                    if (P.out_kind == kOutF32) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float *y = acc + 32 * p + 8 * c;
-                            uint32_t x[4];
+                        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                x[i] = half ? f16_x2(y[2 * i], y[2 * i + 1]) : bf16_x2(y[2 * i], y[2 * i + 1]);
-                            mine[piece(lane, c)] = make_uint4(x[0], x[1], x[2], x[3]);
+                            for (int r0 = 0; r0 < 32; r0 += 16)
+                                pass(r0, 128 * j + 32 * q, [&](int c) {
+                                    const float *z = y + 32 * q + 4 * c;
+                                    return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]),
+                                                      __float_as_uint(z[3]));
+                                });
+                    } else {
+                        uint32_t h[32];
+                        if (P.out_kind == kOutF16) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                h[i] = f16_x2(y[2 * i], y[2 * i + 1]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                h[i] = bf16_x2(y[2 * i], y[2 * i + 1]);
                         }
-                        flush((p >> 1) * 128 + (p & 1) * 32);
-                    }
-                } else {
 #pragma unroll
-                    for (int p = 0; p < NC / 16; ++p) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            mine[piece(lane, c)] =
-                                make_uint4(__float_as_uint(acc[16 * p + 4 * c]), __float_as_uint(acc[16 * p + 4 * c + 1]),
-                                           __float_as_uint(acc[16 * p + 4 * c + 2]), __float_as_uint(acc[16 * p + 4 * c + 3]));
-                        flush((p >> 2) * 128 + (p & 3) * 16);
+                        for (int r0 = 0; r0 < 32; r0 += 16)
+                            pass(r0, 128 * j,
+                                 [&](int c) { return make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]); });
                     }
                 }
             }
