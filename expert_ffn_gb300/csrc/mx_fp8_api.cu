@@ -199,8 +199,9 @@ mx_status run_rows(Mode mode, RowsArgs &g, const void *const *q, const int64_t *
         if ((st = rows_map(&p.xm, q[i], p.rows, p.K, ldq[i], p.xbox)) != MX_OK)
             return st;
     }
-    // (narrower tiles when the wide ones would leave SMs idle)
-    const int bn = mode == kGateUp || wide >= sms ? 256 : 128;
+    // (narrower tiles when the wide ones would leave SMs idle; a factor for each 64 columns
+    // wants a thread to have them)
+    const int bn = mode == kGateUp || g.p[0].out_kind == kOutF16 || wide >= sms ? 256 : 128;
     const cudaError_t e = launch_rows(mode, bn, g, sms, s);
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
 }

@@ -121,12 +121,6 @@ __device__ __forceinline__ void tmem_get32(uint32_t ta, uint32_t (&r)[32])
                  : "memory");
 }
 
-// d += v * f.  Volatile, so that it stays behind the wait for v.
-__device__ __forceinline__ void fma_behind(float &d, uint32_t v, float f)
-{
-    asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(d) : "f"(__uint_as_float(v)), "f"(f));
-}
-
 // 16-byte piece c (0..3) of row r in a warp's 2 KB: 32 rows of 64 bytes, pieces
 // rotated so that neither a row per lane nor four lanes per row conflict.
 __device__ __forceinline__ int piece(int r, int c) { return r * 4 + (c ^ ((r >> 1) & 3)); }
@@ -323,10 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             const int KB = blocks(P.K);
             const int n = T.n, tok0 = T.tok0;
             const bool live = quad * 32 < n;  // (a warp without tokens only releases the buffers)
-            float acc[NC];
+            uint64_t acc2[NC / 2];
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                acc[i] = 0.0f;
+            for (int i = 0; i < NC / 2; ++i)
+                acc2[i] = 0;
             // (a warp without tokens has a loop of its own, and a wait that gave up does not leave
             // the loop early: either made the compiler copy the sums in every block)
             auto release = [&]() {
@@ -358,12 +352,17 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                             tmem_get32(tb + ((h + 1) >> 1) * 128 + ((h + 1) & 1) * 32, r[(h + 1) & 1]);
                         else
                             release();  // (the columns and the factors are in registers)
+                        const uint64_t ff = pair_f32(f[h >> 1], f[h >> 1]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            fma_behind(acc[h * 32 + i], r[h & 1][i], f[h >> 1]);
+                        for (int i = 0; i < 16; ++i)
+                            fma_after(acc2[h * 16 + i], r[h & 1][2 * i], r[h & 1][2 * i + 1], ff);
                     }
                 }
             ok = __all_sync(0xFFFFFFFFu, ok);
+            float acc[NC];
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i)
+                unpair_f32(acc2[i], acc[2 * i], acc[2 * i + 1]);
 
             if constexpr (MODE == kGateUp) {
                 uint32_t m = 0;
