@@ -375,7 +375,7 @@ class _Torch:
         self.codes = {torch.float32: MX_F32, torch.bfloat16: MX_BF16}
         self.sizes = {MX_F32: 4, MX_BF16: 2}
         self.device = torch.cuda.device
-        self.current_device = torch.cuda.current_device
+        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda i: torch.cuda.current_stream(i).cuda_stream)
         L = lib()
@@ -402,20 +402,24 @@ def _dtype_code(t, name):
     return code
 
 
-def _on(dev, stream, fn, *args):
-    """fn(*args, ...) with the tensors' device current; {stream} stands for the stream handle."""
+def _on(dev, fn, *args):
+    """fn(*args) with the tensors' device current."""
     if dev < 0:
         raise MxError(-1, "tensors must be on a CUDA device")
-    t = _t
-    handle = t.stream(dev) if stream is None else _stream_handle(stream)
-    args = [handle if a is _on else a for a in args]
-    if t.current_device() == dev:
+    if _t.current_device() == dev:
         status = fn(*args)
     else:
-        with t.device(dev):
+        with _t.device(dev):
             status = fn(*args)
     if status:
         _check(status)
+
+
+def _stream_on(dev, stream):
+    """The handle of `stream`, by default of the device's current one."""
+    if stream is None:
+        return _t.stream(dev) if dev >= 0 else None
+    return _stream_handle(stream)
 
 
 def _fp8_matrix(w, scales, name):
@@ -434,20 +438,22 @@ def _fp8_matrix(w, scales, name):
     return Fp8Matrix(w.data_ptr(), scales.data_ptr(), rows, cols, count, ld)
 
 
-def _fp8_rows(t, q, scales, operand):
-    """Packed Fp8Rows of a pair of tensors."""
-    if q.dtype is not t.f8 or q.dim() != 2:
-        raise MxError(-1, "q must be float8_e4m3fn [rows, cols]")
-    rows, cols = q.shape
-    ld, one = q.stride()
-    sr, sb = scales.stride() if scales.dim() == 2 else (0, 0)
-    if scales.dtype is not t.f32 or scales.shape != (rows, -(-cols // 128)):
-        raise MxError(-1, f"scales must be float32 [{rows}, {-(-cols // 128)}]")
-    if one != 1 and cols > 1:
-        raise MxError(-1, "q must have contiguous rows")
+def _fp8_rows(t, q, scales, dev, operand):
+    """(rows, columns, packed Fp8Rows) of a pair of tensors."""
+    if q.dtype is not t.f8 or scales.dtype is not t.f32:
+        raise MxError(-1, "q must be float8_e4m3fn, scales float32")
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
+        raise MxError(-1, "q must be [rows, cols] with contiguous rows")
+    rows, cols = shape
+    if scales.shape != (rows, (cols + 127) // 128):
+        raise MxError(-1, f"scales must be [{rows}, {(cols + 127) // 128}]")
+    if q.get_device() != dev or scales.get_device() != dev:
+        raise MxError(-1, "all tensors must be on one device")
+    ld = strides[0]
     if rows <= 1:  # (the stride of a single row means nothing)
-        ld = -(-cols // 16) * 16 if operand else cols
-    return _ROWS.pack(q.data_ptr(), scales.data_ptr(), rows, cols, ld, sr, sb)
+        ld = (cols + 15) // 16 * 16 if operand else cols
+    return rows, cols, _ROWS.pack(q.data_ptr(), scales.data_ptr(), rows, cols, ld, *scales.stride())
 
 
 class Fp8Weight:
@@ -483,54 +489,51 @@ def fp8_quantize(x, q, scales, pow2=False, stream=None):
     """Quantise the rows of ``x`` (float32 or bfloat16 [rows, cols]) into ``q`` (float8_e4m3fn) and ``scales``
     (float32 [rows, ceil(cols / 128)], any strides; ``empty(blocks, rows).t()`` suits the products best)."""
     t = _t or _torch()
-    r = _fp8_rows(t, q, scales, False)
-    shape = x.shape
-    if shape != q.shape:
-        raise MxError(-1, "x and q must have the same shape")
-    ldx, one = x.stride()
-    if one != 1 and shape[1] > 1:
-        raise MxError(-1, "x must have contiguous rows")
     dev = x.get_device()
-    if q.get_device() != dev or scales.get_device() != dev:
-        raise MxError(-1, "all tensors must be on one device")
-    _on(dev, stream, t.quantize, x.data_ptr(), ldx if shape[0] > 1 else shape[1], _dtype_code(x, "x"), 1 if pow2 else 0, r, _on)
+    rows, cols, r = _fp8_rows(t, q, scales, dev, False)
+    ldx, one = x.stride() if x.dim() == 2 else (0, 0)
+    if x.shape != (rows, cols) or (one != 1 and cols > 1):
+        raise MxError(-1, f"x must be [{rows}, {cols}] with contiguous rows")
+    _on(dev, t.quantize, x.data_ptr(), ldx if rows > 1 else cols, _dtype_code(x, "x"), 1 if pow2 else 0, r,
+        _stream_on(dev, stream))
 
 
 def fp8_matmul_workspace_bytes(weight: Fp8Weight, rows: int) -> int:
     return lib().mx_fp8_matmul_workspace_bytes(weight.ref, rows)
 
 
-def _out_pitch(q, weight, out, ws, scales):
-    dev = weight.dev
-    if (q.get_device() != dev or out.get_device() != dev or ws.get_device() != dev or scales.get_device() != dev):
+def _out_pitch(rows, weight, out, ws):
+    if out.get_device() != weight.dev or ws.get_device() != weight.dev:
         raise MxError(-1, "all tensors must be on one device")
-    ldo, one = out.stride() if out.dim() == 2 else (0, 0)
     n = weight.rows
-    if out.shape != (q.shape[0], n) or (one != 1 and n > 1):
-        raise MxError(-1, f"out must be [{q.shape[0]}, {n}] with contiguous rows")
-    return ldo if q.shape[0] > 1 else n
+    ldo, one = out.stride() if out.dim() == 2 else (0, 0)
+    if out.shape != (rows, n) or (one != 1 and n > 1):
+        raise MxError(-1, f"out must be [{rows}, {n}] with contiguous rows")
+    return ldo if rows > 1 else n
 
 
 def fp8_matmul(q, scales, weight: Fp8Weight, out, ws, stream=None):
     """out = (q, scales) times the transposed ``weight``; out float32 or bfloat16 [rows, weight rows]; ws a
     uint8 workspace of fp8_matmul_workspace_bytes, prepared by workspace_init."""
     t = _t or _torch()
-    r = _fp8_rows(t, q, scales, True)
-    ldo = _out_pitch(q, weight, out, ws, scales)
-    _on(weight.dev, stream, t.matmul, r, weight.ref, out.data_ptr(), ldo, _dtype_code(out, "out"), _on, ws.data_ptr(),
-        ws.nbytes)
+    dev = weight.dev
+    rows, _, r = _fp8_rows(t, q, scales, dev, True)
+    ldo = _out_pitch(rows, weight, out, ws)
+    _on(dev, t.matmul, r, weight.ref, out.data_ptr(), ldo, _dtype_code(out, "out"), _stream_on(dev, stream),
+        ws.data_ptr(), ws.nbytes)
 
 
 def fp8_grouped_matmul(q, scales, offsets, weight: Fp8Weight, out, ws, stream=None):
     """The same with rows [offsets[e], offsets[e + 1]) against matrix e; offsets int32 [count + 1] on the device."""
     t = _t or _torch()
-    r = _fp8_rows(t, q, scales, True)
-    ldo = _out_pitch(q, weight, out, ws, scales)
+    dev = weight.dev
+    rows, _, r = _fp8_rows(t, q, scales, dev, True)
+    ldo = _out_pitch(rows, weight, out, ws)
     if (offsets.dtype is not t.i32 or offsets.shape != (weight.count + 1,) or not offsets.is_contiguous()
-            or offsets.get_device() != weight.dev):
+            or offsets.get_device() != dev):
         raise MxError(-1, f"offsets must be contiguous int32 [{weight.count + 1}] on the weight's device")
-    _on(weight.dev, stream, t.grouped, r, offsets.data_ptr(), weight.ref, out.data_ptr(), ldo, _dtype_code(out, "out"), _on,
-        ws.data_ptr(), ws.nbytes)
+    _on(dev, t.grouped, r, offsets.data_ptr(), weight.ref, out.data_ptr(), ldo, _dtype_code(out, "out"),
+        _stream_on(dev, stream), ws.data_ptr(), ws.nbytes)
 
 
 def fp8_moe_workspace_bytes(layer: Fp8Layer, T: int) -> int:
@@ -554,5 +557,6 @@ def fp8_moe_forward(x, topk_idx, topk_w, layer: Fp8Layer, out, ws, residual=None
         raise MxError(-1, f"topk_idx and topk_w must be contiguous int32 and float32 [{T}, {layer.top_k}]")
     if topk_idx.get_device() != dev or topk_w.get_device() != dev or ws.get_device() != dev:
         raise MxError(-1, "all tensors must be on one device")
-    _on(dev, stream, t.moe, x.data_ptr(), T, topk_idx.data_ptr(), topk_w.data_ptr(), layer.ref,
-        None if residual is None else residual.data_ptr(), out.data_ptr(), _on, ws.data_ptr(), ws.nbytes)
+    _on(dev, t.moe, x.data_ptr(), T, topk_idx.data_ptr(), topk_w.data_ptr(), layer.ref,
+        None if residual is None else residual.data_ptr(), out.data_ptr(), _stream_on(dev, stream), ws.data_ptr(),
+        ws.nbytes)
