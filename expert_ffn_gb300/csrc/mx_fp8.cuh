@@ -21,7 +21,8 @@ constexpr int kFewTokens = 64;   // largest T of the two-launch layer path (all 
 __host__ __device__ constexpr int blocks(int n) { return (n + kBlk - 1) / kBlk; }
 __host__ __device__ constexpr int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
-// What a GEMM launch computes (see mx_fp8_gemm.cu).
+// What a launch computes: kProduct in mx_fp8_gemm.cu and mx_fp8_rows.cu, kGateUp in
+// the second, the others in the first.
 enum Mode {
     kProduct = 0,  // out = rows x W^T, rows grouped by matrix (or one matrix)
     kGateUp = 1,   // h = Q(act(rows Wg^T) * (rows Wu^T)), rows grouped by matrix
@@ -45,14 +46,10 @@ struct GemmArgs {
     const float *ssa, *ssb;  // few tokens: the shared expert's
     void *out;               // kProduct, kFewDown
     int64_t ldo;
-    int out_kind;        // OutKind
+    int out_kind;        // kOutF32 or kOutBf16
     int out_vec;         // 16 bytes of neighbouring outputs may be stored at once
-    float *out_scale;    // kOutF16: a row's factor for each 64 columns
-    int64_t out_scale_ld;
-    uint8_t *h;          // kGateUp, kFewGateUp: e4m3 hidden
-    int64_t ldh;         // its row pitch (kGateUp)
-    float *hs;           // its scales
-    int64_t hs_ld;       // kGateUp: rows per block column of hs
+    uint8_t *h;          // kFewGateUp: e4m3 hidden tiles
+    float *hs;           // their factors
     int act;             // mx_activation
     // few tokens
     const int32_t *idx;  // [T][topk]
@@ -67,6 +64,7 @@ struct GemmArgs {
 };
 
 cudaError_t launch_gemm(Mode mode, int nt, const GemmArgs &a, int grid, cudaStream_t s);
+
 // The same for many rows (mx_fp8_rows.cu): one or two products, or gate/up
 // products, in one launch.
 struct RowsProblem {
@@ -147,7 +145,7 @@ struct QuantArgs {
     int64_t sr_b;
     int pdl;             // let the next launch start early
 };
-cudaError_t launch_quantize(const QuantArgs &a, cudaStream_t s);
+cudaError_t launch_quantize(const QuantArgs &a, int sms, cudaStream_t s);
 
 // Slots grouped by expert: offsets [E + 1] and pos [n] (-1 for an index outside
 // [0, E)).  counts and cursor: [E] scratch.  The order inside a group is not

@@ -179,7 +179,20 @@ mx_status rows_map(CUtensorMap *m, const void *q, int64_t rows, int64_t cols, in
 }
 
 // Rows of a group from which on the tokens take the MMA's M side (mx_fp8_rows.cu).
-bool many_rows(bool grouped, double avg) { return grouped ? avg > 24.0 : avg > 64.0; }
+// The two sides' times cross there: 128 matrices [2112, 2816] with a quarter, one, eight
+// and 24 rows each 33 | 72 | 119 | 126 us on the N side and 33 | 76 | 119 | 123 on the M
+// side, and when a few matrices have most of the rows 24 | 55 | 120 | 139 and 27 | 60 |
+// 112 | 129.  One matrix: 64 rows fill one tile of the N side.
+bool many_rows(bool grouped, double avg) { return avg > (grouped ? 6.0 : 64.0); }
+
+// CTAs that share the `items` inner blocks of each of `units` units, out of `ctas` that
+// run at once; they form a cluster.  More than `most` gain nothing over whole clusters
+// left waiting (clusters of eight with an SM to a CTA: a GPC holds one or two).
+int split_of(int64_t units, double items, int ctas, int most)
+{
+    const int64_t n = std::min<int64_t>(units <= 8 ? 8 : most, ctas / units);
+    return items < 8 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(n, (int64_t)(items / 2)));
+}
 
 // One launch of one or two products by mx_fp8_rows.cu; p[i].xm is encoded here from
 // its rows at q[i].
@@ -209,22 +222,21 @@ mx_status run_rows(Mode mode, RowsArgs &g, const void *const *q, const int64_t *
 // One product launch by mx_fp8_gemm.cu over rows grouped by matrix (offsets NULL: one
 // group); `avg` is the expected size of a group.  Tokens take the MMA's N side, in a
 // tile that holds most groups.
-mx_status run_product(Mode mode, GemmArgs &g, const void *q, int64_t ldq, double avg, cudaStream_t s)
+mx_status run_product(GemmArgs &g, const void *q, int64_t ldq, double avg, cudaStream_t s)
 {
     const int sms = num_sms(), FT = blocks(g.N), KB = blocks(g.K);
     const int nt = tile_for(g.offsets ? avg + 2 * std::sqrt(avg) : g.rows, 64);
     const int64_t tiles = g.offsets ? g.E : (g.rows + nt - 1) / nt;
     mx_status st;
-    g.cl = 1;
-    if (!g.offsets && mode == kProduct)
-        while (g.cl < 4 && tiles * FT * g.cl * 2 <= sms && KB / (g.cl * 2) >= 2)
-            g.cl *= 2;
+    // (64 x 4096 x 4096: 15.5 us whole, 12.5 in two, 9.5 in four or more; 64 x 704 x 2816
+    // 12.8, 7.9 in four, 6.9 in eight)
+    g.cl = g.offsets ? 1 : split_of(tiles * FT, KB, sms, 4);
     g.xbox = nt;
-    g.stages = fit_stages(mode, nt, kSmem, std::max(2, KB));
+    g.stages = fit_stages(kProduct, nt, kSmem, std::max(2, KB));
     if ((st = rows_map(&g.xm, q, g.rows, g.K, ldq, g.xbox)) != MX_OK)
         return st;
     const int64_t units = g.offsets ? ((int64_t)g.rows / nt + g.E) * FT : tiles * FT;
-    const cudaError_t e = launch_gemm(mode, nt, g, (int)std::min<int64_t>(sms / g.cl, units) * g.cl, s);
+    const cudaError_t e = launch_gemm(kProduct, nt, g, (int)std::min<int64_t>(sms / g.cl, units) * g.cl, s);
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
 }
 
@@ -306,7 +318,7 @@ mx_status product(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_mat
     g.err = static_cast<unsigned *>(ws);
     if ((st = weight_map(&g.wa, *w)) != MX_OK)
         return st;
-    return run_product(kProduct, g, x->q, x->ld, avg, static_cast<cudaStream_t>(stream));
+    return run_product(g, x->q, x->ld, avg, static_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ the layer
@@ -436,7 +448,7 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
     q.s_r = 1;
     q.s_b = T;
     q.pdl = 1;
-    if ((e = launch_quantize(q, s)) != cudaSuccess)
+    if ((e = launch_quantize(q, num_sms(), s)) != cudaSuccess)
         return cuda_fail(e, "FP8 quantisation");
 
     GemmArgs g{};
@@ -468,18 +480,11 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
     g.xbox = p.nt;
     // experts that T tokens are expected to select, each on its own draw of K
     const double active = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)K / E), (double)T));
-    const double units = active * IB + SB;
     const int DB = blocks(D);
-    // A cluster holds one unit, whose columns it reduces in one pass.
-    const int most = p.nt <= 32 ? 4 : 1;
+    // (one CTA to an SM with all its memory for loads in flight)
     g.cl = 1;
-    while (g.cl < most && units * g.cl * 2 <= 2.0 * sms && DB / (g.cl * 2) >= 2)
-        g.cl *= 2;
-    const int per_sm = p.nt <= 32 ? 2 : 1;
-    const int smem = per_sm == 2 ? kSmemHalf : kSmem;
-    g.stages = fit_stages(kFewGateUp, p.nt, smem, 16);
-    int grid = g.cl > 1 ? p.items * g.cl : std::max(1, std::min(per_sm * sms, p.items));
-    if ((e = launch_gemm(kFewGateUp, p.nt, g, grid, s)) != cudaSuccess)
+    g.stages = fit_stages(kFewGateUp, p.nt, kSmem, 16);
+    if ((e = launch_gemm(kFewGateUp, p.nt, g, std::max(1, std::min(sms, p.items)), s)) != cudaSuccess)
         return cuda_fail(e, "FP8 gate/up");
 
     GemmArgs d = g;
@@ -500,11 +505,14 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
             return st;
     }
     const double items = active * IB + SB;
-    d.cl = 1;
-    while (d.cl < (p.nt <= 64 ? 4 : 1) && DB * d.cl * 2 <= 2 * sms && items / (d.cl * 2) >= 2)
-        d.cl *= 2;
-    d.stages = fit_stages(kFewDown, p.nt, smem, 16);
-    grid = d.cl > 1 ? DB * d.cl : std::min(per_sm * sms, DB);
+    // Two CTAs to an SM take more blocks than SMs: 12, 31 tokens of top-8 of 128 experts
+    // (d_model 2816, 22 units) in four 91, 148 us for the layer, in eight 78, 123; 256
+    // experts with d_model 4096 in four 178, 339, in six 172, 317, in eight 194, 315.
+    // A tile of 64 tokens wants an SM: 60 tokens in four 174 us, in six 155, in eight 184.
+    const bool two = p.nt <= 32;
+    d.cl = two ? split_of(DB, items, sms * 4 / 3, 8) : split_of(DB, items, sms, 6);
+    d.stages = fit_stages(kFewDown, p.nt, two ? kSmemHalf : kSmem, 16);
+    const int grid = d.cl > 1 ? DB * d.cl : std::min(two ? 2 * sms : sms, DB);
     if ((e = launch_gemm(kFewDown, p.nt, d, grid, s)) != cudaSuccess)
         return cuda_fail(e, "FP8 down");
     return MX_OK;
@@ -540,13 +548,14 @@ mx_status run_many(const void *x, int T, const int32_t *idx, const float *wts, c
     q.qr = ws + p.xr;
     q.sr = f32(p.sr);
     q.sr_b = n;
-    if ((e = launch_quantize(q, s)) != cudaSuccess)
+    if ((e = launch_quantize(q, num_sms(), s)) != cudaSuccess)
         return cuda_fail(e, "FP8 quantisation");
 
-    // The routed and the shared expert's products: together when the tokens of a group
-    // are many, else one after the other.
+    // The routed and the shared expert's products in one launch each, tokens on the M side
+    // whatever their number to an expert: 100 tokens of top-8 of 128 experts 175 us, on the
+    // N side and the shared expert by itself 179; when a few experts have most of them 87 and 117.
     const double avg[2] = {(double)n / E, (double)T};
-    const bool together = many_rows(true, avg[0]), half = L->act_dtype == MX_BF16;
+    const bool half = L->act_dtype == MX_BF16;
     const int64_t ldx[2] = {up16(D), up16(D)}, ldh[2] = {(int64_t)IB * kBlk, (int64_t)SB * kBlk};
     const void *xq[2] = {ws + p.xr, ws + p.xq}, *hq[2] = {ws + p.hr, ws + p.hsh};
     RowsArgs gu{}, dn{};
@@ -584,50 +593,8 @@ mx_status run_many(const void *x, int T, const int32_t *idx, const float *wts, c
             (st = weight_map(&d.wa, wd)) != MX_OK)
             return st;
     }
-    if (together) {
-        if ((st = run_rows(kGateUp, gu, xq, ldx, avg, s)) != MX_OK || (st = run_rows(kProduct, dn, hq, ldh, avg, s)) != MX_OK)
-            return st;
-    } else {
-        // few tokens to an expert: the routed part on the N side
-        GemmArgs g{}, d{};
-        const RowsProblem &pg = gu.p[0], &pd = dn.p[0];
-        g.rows = d.rows = n;
-        g.offsets = d.offsets = pg.offsets;
-        g.wa = pg.wa, g.wb = pg.wb, d.wa = pd.wa;
-        matrices(g, L->gate, &L->up);
-        matrices(d, L->down, nullptr);
-        g.sx = pg.sx, d.sx = pd.sx;
-        g.sx_r = d.sx_r = 1;
-        g.sx_b = d.sx_b = n;
-        g.h = pg.h;
-        g.ldh = pg.ldh;
-        g.hs = pg.hs;
-        g.hs_ld = n;
-        g.act = L->activation;
-        g.err = d.err = gu.err;
-        d.out = pd.out;
-        d.ldo = D;
-        d.out_kind = pd.out_kind;
-        d.out_vec = pd.out_vec;
-        d.out_scale = pd.out_scale;
-        d.out_scale_ld = pd.out_scale_ld;
-        if ((st = run_product(kGateUp, g, xq[0], ldx[0], avg[0], s)) != MX_OK)
-            return st;
-        if (shared) {
-            gu.p[0] = gu.p[1];
-            gu.p[1] = RowsProblem{};
-            if ((st = run_rows(kGateUp, gu, xq + 1, ldx + 1, avg + 1, s)) != MX_OK)
-                return st;
-        }
-        if ((st = run_product(kProduct, d, hq[0], ldh[0], avg[0], s)) != MX_OK)
-            return st;
-        if (shared) {
-            dn.p[0] = dn.p[1];
-            dn.p[1] = RowsProblem{};
-            if ((st = run_rows(kProduct, dn, hq + 1, ldh + 1, avg + 1, s)) != MX_OK)
-                return st;
-        }
-    }
+    if ((st = run_rows(kGateUp, gu, xq, ldx, avg, s)) != MX_OK || (st = run_rows(kProduct, dn, hq, ldh, avg, s)) != MX_OK)
+        return st;
 
     CombineArgs c{};
     c.Y = ws + p.y;
@@ -679,7 +646,7 @@ mx_status mx_fp8_quantize(const void *x, int64_t ldx, int dtype, int pow2, const
     q.scales = out->scales;
     q.s_r = out->scale_row;
     q.s_b = out->scale_block;
-    const cudaError_t e = launch_quantize(q, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_quantize(q, num_sms(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 quantisation");
 }
 

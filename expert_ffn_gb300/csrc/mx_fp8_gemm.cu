@@ -27,8 +27,6 @@
 // ends the CTA's work.
 #include "mx_fp8_tc.cuh"
 
-#include <cuda_fp16.h>
-
 namespace mx {
 namespace fp8 {
 
@@ -38,7 +36,7 @@ constexpr uint32_t kTile = 128 * 128;  // bytes of one weight tile
 constexpr int kFacRing = 8;            // blocks of factors in flight
 
 constexpr int kSumWarps = 4, kThreads = (kSumWarps + 3) * 32;
-constexpr int n_mats(int mode) { return mode == kGateUp || mode == kFewGateUp ? 2 : 1; }
+constexpr int n_mats(int mode) { return mode == kFewGateUp ? 2 : 1; }
 // TMEM buffers: at most 256 columns (two CTAs of an SM share 512).
 constexpr int n_acc(int mode, int nt)
 {
@@ -54,8 +52,15 @@ constexpr uint32_t tmem_cols(int mode, int nt)
 }
 constexpr uint32_t stage_bytes(int mode, int nt) { return n_mats(mode) * kTile + nt * 128; }
 
-// Token columns of one pass of the epilogue.
-constexpr int pass_cols(int mode, int nt) { return n_mats(mode) * nt > 64 ? 32 : nt; }
+// Token columns of one pass of the epilogue.  (A cluster, whose one unit is done by
+// then, leaves all its columns in the ring instead.)
+constexpr int pass_cols(int mode, int nt)
+{
+    return mode == kFewDown ? 16 : n_mats(mode) * nt > 64 ? 32 : nt;
+}
+
+// CTAs that share an SM.
+constexpr int per_sm(int mode, int nt) { return mode == kFewDown && nt <= 32 ? 2 : 1; }
 
 // Dynamic shared memory after the ring (byte offsets from its end).
 struct Tail {
@@ -69,8 +74,9 @@ __host__ __device__ constexpr Tail tail_of(int mode, int nt)
     o += n_mats(mode) * pass_cols(mode, nt) * 512;
     t.fac = o;
     o += kFacRing * n_mats(mode) * nt * 4;
-    t.tab = o;  // expert tables
-    o += (3 * kMaxExperts + 16) * 4;
+    t.tab = o;  // expert tables; few tokens: active experts, their bits, routing indices and weights
+    o += mode == kFewGateUp || mode == kFewDown ? (kMaxExperts + kMaxExperts / 32 + 2 * nt * kMaxTopK) * 4
+                                                : (3 * kMaxExperts + 16) * 4;
     t.bars = o;
     o += 640;
     t.total = o;
@@ -92,13 +98,15 @@ struct Walk {
     int FT, n_act;
     const int *tt, *lo, *len;  // by tokens: token-tile offsets [E + 1], group starts and lengths [E]
     const int *act;            // few tokens: active experts
+    const int *idx;            // their routing: [T][topk] experts and weights
+    const float *wts;
 };
 
 template <int MODE, int NT>
 __device__ __forceinline__ Unit unit_of(const GemmArgs &a, const Walk &w, int u)
 {
     Unit U{};
-    if (MODE == kProduct || MODE == kGateUp) {
+    if (MODE == kProduct) {
         const int tile = u / w.FT;
         U.f = u - tile * w.FT;
         int lo = 0, hi = a.E;
@@ -152,41 +160,43 @@ __device__ __forceinline__ void tile_of(const GemmArgs &a, const Walk &w, const 
 
 // Results of token column n of a unit: 128 weight rows, four to a lane.
 template <int MODE, int NT>
-__device__ __forceinline__ void emit(const GemmArgs &a, const Unit &U, int n, const float4 (&v)[n_mats(MODE)], int lane)
+__device__ __forceinline__ void emit(const GemmArgs &a, const Walk &w, const Unit &U, int n,
+                                     const float4 (&v)[n_mats(MODE)], int lane)
 {
     constexpr int NMAT = n_mats(MODE);
     if constexpr (NMAT == 2) {
-        const float h[4] = {act_of(v[0].x, a.act) * v[NMAT - 1].x, act_of(v[0].y, a.act) * v[NMAT - 1].y,
-                            act_of(v[0].z, a.act) * v[NMAT - 1].z, act_of(v[0].w, a.act) * v[NMAT - 1].w};
-        uint32_t mx = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            mx = max(mx, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-        const float s = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, mx)), 0);
-        // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
-        const float inv = __frcp_rn(s);
-        uint32_t e = e4m3_x2(h[0] * inv, h[1] * inv) | e4m3_x2(h[2] * inv, h[3] * inv) << 16;
-        float sc = s;
-        if (MODE == kFewGateUp && U.e >= 0) {
-            // the routing weight joins the scale; a token that did not choose the expert adds nothing
-            const int mine = lane < a.topk ? __ldg(a.idx + n * a.topk + lane) : -1;
-            const float wt = mine == U.e ? __ldg(a.wts + n * a.topk + lane) : 0.0f;
-            if (__any_sync(0xFFFFFFFFu, mine == U.e)) {
-                float sum = wt;
+        // few tokens: the routing weight joins the scale; a token that did not choose the
+        // expert adds nothing (most do not: found out first)
+        float wt = 1.0f;
+        bool in = true;
+        if (U.e >= 0) {
+            const bool mine = lane < a.topk && w.idx[n * a.topk + lane] == U.e;
+            wt = mine ? w.wts[n * a.topk + lane] : 0.0f;
+            in = __any_sync(0xFFFFFFFFu, mine);
+        }
+        uint32_t e = 0;
+        float sc = 0.0f;
+        if (in) {
+            if (U.e >= 0)
 #pragma unroll
                 for (int o = 16; o; o >>= 1)
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                sc = s * sum;
-            } else {
-                sc = 0.0f;
-                e = 0;
-            }
+                    wt += __shfl_xor_sync(0xFFFFFFFFu, wt, o);
+            const float h[4] = {act_of(v[0].x, a.act) * v[NMAT - 1].x, act_of(v[0].y, a.act) * v[NMAT - 1].y,
+                                act_of(v[0].z, a.act) * v[NMAT - 1].z, act_of(v[0].w, a.act) * v[NMAT - 1].w};
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mx = max(mx, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+            const float s = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, mx)), 0);
+            // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
+            const float inv = __frcp_rn(s);
+            e = e4m3_x2(h[0] * inv, h[1] * inv) | e4m3_x2(h[2] * inv, h[3] * inv) << 16;
+            sc = s * wt;
         }
-        uint8_t *hp = MODE == kFewGateUp ? a.h + ((int64_t)U.item * NT + n) * 128
-                                         : a.h + (int64_t)(U.tok0 + n) * a.ldh + U.f * kBlk;
-        reinterpret_cast<uint32_t *>(hp)[lane] = e;
+        const int64_t at = (int64_t)U.item * NT + n;
+        reinterpret_cast<uint32_t *>(a.h + at * kBlk)[lane] = e;
         if (lane == 0)
-            a.hs[MODE == kFewGateUp ? (int64_t)U.item * NT + n : (int64_t)U.f * a.hs_ld + U.tok0 + n] = sc;
+            a.hs[at] = sc;
     } else {
         const int o = U.f * kBlk + 4 * lane;
         const int64_t at = (int64_t)(U.tok0 + n) * a.ldo + o;
@@ -198,32 +208,10 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Unit &U, int n, co
                     y[i] = fmaf(a.lam, y[i],
                                 a.residual ? load_act(a.residual, at + i, a.out_kind == kOutBf16) : 0.0f);
         }
-        if (MODE == kProduct && a.out_kind == kOutF16) {
-            // FP16 of y 2^-k with 2^k beside it, as in mx_fp8_rows.cu; half a warp has 64 columns
-            uint32_t mx = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                mx = max(mx, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-#pragma unroll
-            for (int d = 8; d; d >>= 1)
-                mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-            const int ex = (int)(mx >> 23);
-            const int k = ex < 30 || ex > 240 ? 0 : ex - (127 + 14);
-            const float down = __uint_as_float((uint32_t)(127 - k) << 23);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y[i] *= down;
-            if ((lane & 15) == 0 && o < a.N)
-                a.out_scale[(int64_t)(U.tok0 + n) * a.out_scale_ld + 2 * U.f + (lane >> 4)] =
-                    __uint_as_float((uint32_t)(127 + k) << 23);
-        }
-        auto two = [&](float v) -> uint32_t {
-            return a.out_kind == kOutF16 ? __half_as_ushort(__float2half_rn(v)) : f2bf(v);
-        };
         if (a.out_vec && o + 4 <= a.N) {
-            if (a.out_kind != kOutF32)
+            if (a.out_kind == kOutBf16)
                 *reinterpret_cast<uint2 *>(reinterpret_cast<uint16_t *>(a.out) + at) =
-                    make_uint2(two(y[0]) | two(y[1]) << 16, two(y[2]) | two(y[3]) << 16);
+                    make_uint2(f2bf(y[0]) | (uint32_t)f2bf(y[1]) << 16, f2bf(y[2]) | (uint32_t)f2bf(y[3]) << 16);
             else
                 *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at) =
                     make_float4(y[0], y[1], y[2], y[3]);
@@ -231,8 +219,8 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Unit &U, int n, co
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (o + i < a.N) {
-                    if (a.out_kind != kOutF32)
-                        reinterpret_cast<uint16_t *>(a.out)[at + i] = (uint16_t)two(y[i]);
+                    if (a.out_kind == kOutBf16)
+                        reinterpret_cast<uint16_t *>(a.out)[at + i] = f2bf(y[i]);
                     else
                         reinterpret_cast<float *>(a.out)[at + i] = y[i];
                 }
@@ -241,7 +229,7 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Unit &U, int n, co
 }
 
 template <int MODE, int NT>
-__global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const __grid_constant__ GemmArgs a)
+__global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const __grid_constant__ GemmArgs a)
 {
     constexpr int NMAT = n_mats(MODE), EW = kSumWarps, NB = n_acc(MODE, NT), NCH = NT / 16;
     constexpr uint32_t kStage = stage_bytes(MODE, NT), kCols = NMAT * NT, kTmem = tmem_cols(MODE, NT);
@@ -253,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const 
     uint8_t *tail = ring + NS * kStage;
     constexpr Tail T = tail_of(MODE, NT);
     constexpr int GC = pass_cols(MODE, NT);
-    float *stage = reinterpret_cast<float *>(tail + T.stage);
+    float *stage = reinterpret_cast<float *>(cl > 1 ? ring : tail + T.stage);
     float *fac = reinterpret_cast<float *>(tail + T.fac);
     int *tab = reinterpret_cast<int *>(tail + T.tab);
     uint64_t *full = reinterpret_cast<uint64_t *>(tail + T.bars), *empty = full + 16;
@@ -295,12 +283,17 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const 
     if (FEW) {
         // active experts: a bit each, then their list in ascending order
         uint32_t *mask = reinterpret_cast<uint32_t *>(tab + kMaxExperts);
-        int *act = tab;
+        int *act = tab, *idx = tab + kMaxExperts + kMaxExperts / 32;
+        float *wts = reinterpret_cast<float *>(idx + NT * kMaxTopK);
         if (tid < kMaxExperts / 32)
             mask[tid] = 0;
         __syncthreads();
         for (int s = tid; s < a.T * a.topk; s += kThreads) {
             const int e = __ldg(a.idx + s);
+            if (MODE == kFewGateUp) {
+                idx[s] = e;
+                wts[s] = __ldg(a.wts + s);
+            }
             if (e >= 0 && e < a.E)
                 atomicOr(mask + (e >> 5), 1u << (e & 31));
         }
@@ -317,6 +310,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const 
             }
         w.n_act = n;
         w.act = act;
+        w.idx = idx;
+        w.wts = wts;
         w.n_units = MODE == kFewGateUp ? n * a.IB + a.SB : w.FT;
     } else {
         int *tt = tab, *lo = tab + kMaxExperts + 1, *len = lo + kMaxExperts;
@@ -555,6 +550,18 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const 
             // contiguous, the largest |h| of a hidden block is one warp maximum, and
             // the code stays small -- unrolled over the registers it ran at the rate
             // of its instruction fetches (64 columns: 5 us for the stores alone).
+            if (cl > 1) {  // one unit: the rest follows the cluster's barrier
+#pragma unroll
+                for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+                    for (int j = 0; j < NT / 2; ++j) {
+                        float lo, hi;
+                        unpair_f32(acc[m][j], lo, hi);
+                        stage[(m * NT + 2 * j) * 128 + row] = lo;
+                        stage[(m * NT + 2 * j + 1) * 128 + row] = hi;
+                    }
+                break;
+            }
 #pragma unroll
             for (int ps = 0; ps < NT / GC; ++ps) {
                 if (ps * GC >= U.n)
@@ -568,8 +575,6 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const 
                         stage[(m * GC + 2 * j) * 128 + row] = lo;
                         stage[(m * GC + 2 * j + 1) * 128 + row] = hi;
                     }
-                if (cl > 1)
-                    break;  // (one unit and one pass: the rest follows the cluster's barrier)
                 // (the four warps give up together: none is left at a barrier)
                 __syncwarp();
                 ok = named_and(1, 128, ok);
@@ -580,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const 
 #pragma unroll
                     for (int m = 0; m < NMAT; ++m)
                         v[m] = reinterpret_cast<const float4 *>(stage + (m * GC + j) * 128)[lane];
-                    emit<MODE, NT>(a, U, ps * GC + j, v, lane);
+                    emit<MODE, NT>(a, w, U, ps * GC + j, v, lane);
                 }
                 __syncwarp();
                 ok = named_and(1, 128, ok);
@@ -599,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const 
                 float4 v[NMAT];
 #pragma unroll
                 for (int m = 0; m < NMAT; ++m) {
-                    const uint32_t at = smem_u32(stage + (m * GC + n) * 128 + 4 * lane);
+                    const uint32_t at = smem_u32(stage + (m * NT + n) * 128 + 4 * lane);
                     v[m] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
                     for (int r = 0; r < cl; ++r) {
@@ -607,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 32 ? 2 : 1) gemm_kernel(const 
                         v[m].x += p.x, v[m].y += p.y, v[m].z += p.z, v[m].w += p.w;
                     }
                 }
-                emit<MODE, NT>(a, U, n, v, lane);
+                emit<MODE, NT>(a, w, U, n, v, lane);
             }
         }
     }
@@ -672,9 +677,6 @@ cudaError_t launch_gemm(Mode mode, int nt, const GemmArgs &a, int grid, cudaStre
     MX_CASE(kProduct, 16);
     MX_CASE(kProduct, 32);
     MX_CASE(kProduct, 64);
-    MX_CASE(kGateUp, 16);
-    MX_CASE(kGateUp, 32);
-    MX_CASE(kGateUp, 64);
     MX_CASE(kFewGateUp, 16);
     MX_CASE(kFewGateUp, 32);
     MX_CASE(kFewGateUp, 64);

@@ -201,7 +201,57 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) quantize_kernel(const 
 
 // ------------------------------------------------------------------ grouping
 
-constexpr int kGrp = 1024;  // slots per block
+constexpr int kGrp = 1024;     // slots per block
+constexpr int kGrpOne = 4096;  // slots that one block groups by itself
+
+// Up to kGrpOne slots: counted, scanned and ranked in shared memory by one block (three
+// launches for more: 64 tokens of top-8 then cost 5 us more).
+__global__ void __launch_bounds__(1024) group_one(const int32_t *__restrict__ idx, int n, int E, int32_t *offsets,
+                                                  int32_t *pos)
+{
+    __shared__ int h[kMaxExperts], wsum[kMaxExperts / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid < kMaxExperts)
+        h[tid] = 0;
+    __syncthreads();
+    int e[kGrpOne / 1024], r[kGrpOne / 1024];
+#pragma unroll
+    for (int i = 0; i < kGrpOne / 1024; ++i) {
+        const int s = i * 1024 + tid;
+        e[i] = s < n ? __ldg(idx + s) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kGrpOne / 1024; ++i)
+        r[i] = e[i] >= 0 && e[i] < E ? atomicAdd(&h[e[i]], 1) : -1;
+    __syncthreads();
+    const int c = tid < kMaxExperts ? h[tid] : 0;
+    int incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o)
+            incl += y;
+    }
+    if (tid < kMaxExperts && lane == 31)
+        wsum[warp] = incl;
+    __syncthreads();
+    if (tid < kMaxExperts) {
+        for (int w = 0; w < warp; ++w)
+            incl += wsum[w];
+        h[tid] = incl - c;
+        if (tid < E)
+            offsets[tid] = incl - c;
+        if (tid == E - 1)
+            offsets[E] = incl;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGrpOne / 1024; ++i) {
+        const int s = i * 1024 + tid;
+        if (s < n)
+            pos[s] = r[i] < 0 ? -1 : h[e[i]] + r[i];
+    }
+}
 
 __global__ void __launch_bounds__(256) group_count(const int32_t *__restrict__ idx, int n, int E, int32_t *counts)
 {
@@ -274,24 +324,19 @@ __global__ void __launch_bounds__(512) group_scatter(const int32_t *__restrict__
 // ------------------------------------------------------------------- combine
 
 // out[t] = residual + lambda * (Ys[t] + sum_k w_k Y[pos[t,k]]), k ascending, in fp32.
-// A thread has 16 bytes of each row; the positions of eight slots are read at once and
-// then the eight rows, so that a thread waits for memory twice and not twice a slot
-// (148 us at 4096 tokens top-8 with d_model 4096 when it took four slots at a time and
-// half the bytes; HBM needs 45).
+// A thread has 16 bytes of each row.  The positions of eight slots are read at once, then
+// their rows and factors, a slot without an expert reading the first row and leaving it
+// out: behind a test for each slot its load waited for the one before.
 template <bool HALF>
-__global__ void __launch_bounds__(256, 4) combine_kernel(const CombineArgs a)
+__global__ void __launch_bounds__(256, 3) combine_kernel(const CombineArgs a)
 {
     constexpr int C = HALF ? 8 : 4, kStep = 8;
-    const int t = blockIdx.y;
     const int d = (blockIdx.x * 256 + threadIdx.x) * C;
     if (d >= a.D)
         return;
     const int n = min(C, a.D - d), nb = (a.D + 63) / 64, blk = d / 64;
     const bool vec = a.D % C == 0;
     float acc[C];
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-        acc[j] = 0.0f;
     auto load = [&](const void *y, int64_t row) -> uint4 {
         if (vec)
             return ld_stream_u4(static_cast<const char *>(y) + (row * a.D + d) * (HALF ? 2 : 4));
@@ -313,35 +358,45 @@ __global__ void __launch_bounds__(256, 4) combine_kernel(const CombineArgs a)
             acc[j] = fmaf(w, v, acc[j]);
         }
     };
-    const int32_t *pos = a.pos + (int64_t)t * a.topk;
-    const float *wts = a.wts + (int64_t)t * a.topk;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+        acc[j] = 0.0f;
+    const int64_t t = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
+    if (t >= a.T)
+        return;
+    const int32_t *pos = a.pos + t * a.topk;
+    const float *wts = a.wts + t * a.topk;
     uint4 shared = make_uint4(0, 0, 0, 0);
     float fs = 0.0f;
     if (a.Ys) {
         shared = load(a.Ys, t);
-        fs = HALF ? __ldg(a.Ysf + (int64_t)t * nb + blk) : 1.0f;
+        fs = HALF ? __ldg(a.Ysf + t * nb + blk) : 1.0f;
     }
     for (int k0 = 0; k0 < a.topk; k0 += kStep) {
         int p[kStep];
         uint4 y[kStep];
-        float w[kStep];
+        float w[kStep], f[kStep];
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+            const int k = min(k0 + i, a.topk - 1);
+            p[i] = __ldg(pos + k);
+            w[i] = __ldg(wts + k);
+        }
 #pragma unroll
         for (int i = 0; i < kStep; ++i)
-            p[i] = k0 + i < a.topk ? __ldg(pos + k0 + i) : -1;
-#pragma unroll
-        for (int i = 0; i < kStep; ++i)
-            if (p[i] >= 0) {  // (a slot without an expert: nothing)
-                y[i] = load(a.Y, p[i]);
-                w[i] = __ldg(wts + k0 + i) * (HALF ? __ldg(a.Yf + (int64_t)p[i] * nb + blk) : 1.0f);
+            if (k0 + i < a.topk) {  // (the same for the whole grid)
+                const int64_t row = max(p[i], 0);
+                y[i] = load(a.Y, row);
+                f[i] = HALF ? __ldg(a.Yf + row * nb + blk) : 1.0f;
             }
 #pragma unroll
         for (int i = 0; i < kStep; ++i)
-            if (p[i] >= 0)
-                add(y[i], w[i]);
+            if (k0 + i < a.topk && p[i] >= 0)
+                add(y[i], w[i] * f[i]);
     }
     if (a.Ys)
         add(shared, fs);
-    const int64_t at = (int64_t)t * a.D + d;
+    const int64_t at = t * a.D + d;
 #pragma unroll
     for (int j = 0; j < C; ++j)
         acc[j] = j < n ? fmaf(a.lam, acc[j], a.residual ? load_act(a.residual, at + j, a.bf16) : 0.0f) : 0.0f;
@@ -367,7 +422,7 @@ __global__ void __launch_bounds__(256, 4) combine_kernel(const CombineArgs a)
 
 }  // namespace
 
-cudaError_t launch_quantize(const QuantArgs &a, cudaStream_t s)
+cudaError_t launch_quantize(const QuantArgs &a, int sms, cudaStream_t s)
 {
     if (a.rows == 0)
         return cudaSuccess;
@@ -376,7 +431,7 @@ cudaError_t launch_quantize(const QuantArgs &a, cudaStream_t s)
     v.vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ldx * es) % 16 == 0 &&
             reinterpret_cast<uintptr_t>(a.q) % 8 == 0 && a.ldq % 8 == 0;
     // four CTAs to an SM, in whole rows of block columns
-    const int64_t groups = (a.rows + kHalves - 1) / kHalves, nb = blocks(a.cols), want = 4 * 152 / nb;
+    const int64_t groups = (a.rows + kHalves - 1) / kHalves, nb = blocks(a.cols), want = 4 * sms / nb;
     const unsigned grid = (unsigned)((want < 1 ? 1 : want < groups ? want : groups) * nb);
     if (a.bf16)
         quantize_kernel<true><<<grid, kThreads, 0, s>>>(v);
@@ -389,6 +444,10 @@ cudaError_t launch_group(const int32_t *idx, int n, int E, int32_t *counts, int3
                          int32_t *pos, cudaStream_t s)
 {
     cudaError_t e;
+    if (n <= kGrpOne) {
+        group_one<<<1, 1024, 0, s>>>(idx, n, E, offsets, pos);
+        return cudaGetLastError();
+    }
     // counts and cursor are neighbours
     if ((e = cudaMemsetAsync(counts, 0, (size_t)(cursor + E - counts) * 4, s)) != cudaSuccess)
         return e;
@@ -402,31 +461,13 @@ cudaError_t launch_group(const int32_t *idx, int n, int E, int32_t *counts, int3
 
 cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s)
 {
-    // (tokens on the y axis: at most 65535 per launch)
-    for (int t0 = 0; t0 < a.T; t0 += 65535) {
-        CombineArgs b = a;
-        const size_t es = a.bf16 ? 2 : 4;
-        b.T = a.T - t0 < 65535 ? a.T - t0 : 65535;
-        b.pos += (int64_t)t0 * a.topk;
-        b.wts += (int64_t)t0 * a.topk;
-        if (b.Ys) {
-            b.Ys = (const char *)b.Ys + (int64_t)t0 * a.D * (b.Yf ? 2 : 4);
-            b.Ysf += b.Yf ? (int64_t)t0 * ((a.D + 63) / 64) : 0;
-        }
-        if (b.residual)
-            b.residual = (const char *)b.residual + (int64_t)t0 * a.D * es;
-        b.out = (char *)b.out + (int64_t)t0 * a.D * es;
-        const int per = 256 * (b.Yf ? 8 : 4);
-        const dim3 grid((a.D + per - 1) / per, b.T);
-        if (b.Yf)
-            combine_kernel<true><<<grid, 256, 0, s>>>(b);
-        else
-            combine_kernel<false><<<grid, 256, 0, s>>>(b);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess)
-            return e;
-    }
-    return cudaSuccess;
+    const int per = 256 * (a.Yf ? 8 : 4), ny = a.T < 32768 ? a.T : 32768;
+    const dim3 grid((a.D + per - 1) / per, ny, (a.T + ny - 1) / ny);
+    if (a.Yf)
+        combine_kernel<true><<<grid, 256, 0, s>>>(a);
+    else
+        combine_kernel<false><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace fp8

@@ -130,32 +130,13 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr)
     return v;
 }
 
-__device__ __forceinline__ void arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-
 // Bounded wait: false once this CTA has given up.
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool bwait(uint64_t *bar, uint32_t parity, unsigned *err, volatile int *abort)
 {
-    auto done = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (done())
+    if (mbar_try_wait(bar, parity))
         return true;
     const unsigned long long t0 = global_ns();
-    while (!done()) {
+    while (!mbar_try_wait(bar, parity)) {
         if (*abort)
             return false;
         if (global_ns() - t0 > kWaitLimitNs) {
@@ -168,10 +149,9 @@ __device__ __forceinline__ bool bwait(uint64_t *bar, uint32_t parity, unsigned *
 }
 
 // The same by a whole warp: every lane gets one answer.
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool wwait(uint64_t *bar, uint32_t parity, unsigned *err, volatile int *abort)
 {
-    return __all_sync(0xFFFFFFFFu, bwait<CLUSTER>(bar, parity, err, abort));
+    return __all_sync(0xFFFFFFFFu, bwait(bar, parity, err, abort));
 }
 
 // Barrier over `count` threads that tells each whether all of them passed true.
