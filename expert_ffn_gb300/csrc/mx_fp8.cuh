@@ -111,7 +111,7 @@ struct GemvArgs {
     int64_t ldo;
     int out_bf16;
     void *out;
-    // layer: x [T][K], routed gate / up / down stacks, the shared expert's (S 0: none)
+    // layer (T 1): x [K], routed gate / up / down stacks, the shared expert's (S 0: none)
     const void *x;
     int bf16, act, topk, E, I, S;
     const int32_t *idx;
@@ -119,14 +119,13 @@ struct GemvArgs {
     const uint8_t *w_gate, *w_up, *w_down, *sw_gate, *sw_up, *sw_down;
     int64_t ld_gate, ld_up, ld_down, ld_sgate, ld_sup, ld_sdown;
     const float *s_gate, *s_up, *s_down, *ss_gate, *ss_up, *ss_down;
-    uint8_t *h8;         // hidden [block][8][128] e4m3 and its factors [block][8]
+    uint8_t *h8;         // hidden [block][128] e4m3 and its factors [block]
     float *hf;
     const void *residual;
     float lam;
 };
 cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s);
 cudaError_t launch_gemv_moe(const GemvArgs &a, cudaStream_t s);
-size_t gemv_gate_up_smem(int T, int D);
 
 struct QuantArgs {
     const void *x;       // [rows][cols]

@@ -259,7 +259,10 @@ mx_status product(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_mat
         return fail(MX_ERR_ALIGNMENT, "out is misaligned");
     if ((st = check_ws(ws, ws_bytes, kErrBytes)) != MX_OK)
         return st;
-    if (!offsets && x->rows <= kGemvRows) {
+    // Weights straight into registers while they are few: one and eight rows by 2112 x 2816
+    // take 3.6, 3.9 us (the tcgen05 kernel 5.8, 5.9), by 4096 x 4096 6.4, 6.9 (6.9, 7.4), by
+    // 14336 x 4096 17.8, 19.1 (13.7, 13.9).
+    if (!offsets && x->rows <= kGemvRows && (int64_t)w->rows * w->cols <= 1 << 25) {
         GemvArgs v{};
         v.T = x->rows;
         v.K = w->cols;
@@ -328,7 +331,7 @@ struct Plan {
     size_t xq, sx;
     // up to kFewTokens tokens: hidden tiles [item][nt][128] and factors [item][nt]
     size_t h, hs;
-    size_t h8, hf;  // up to kGemvRows: the same for the two-launch form, 8 to a block
+    size_t h8, hf;  // one token: the same for the two-launch form, by slot
     int nt, items;
     // more: grouping, gathered rows, hidden rows, per-slot outputs
     size_t counts, cursor, offsets, pos, xr, sr, hr, hrs, hsh, hshs, y, ys, yf, ysf;
@@ -354,9 +357,9 @@ Plan make_plan(const mx_fp8_layer *L, int T)
         p.items = (int)(std::min(n, E) * IB + SB);
         p.h = take((int64_t)p.items * p.nt * kBlk);
         p.hs = take((int64_t)p.items * p.nt * 4);
-        const int64_t gemv_items = (T == 1 ? K : std::min(n, E)) * IB + SB;
-        p.h8 = take(T <= kGemvRows ? gemv_items * kGemvRows * kBlk : 0);
-        p.hf = take(T <= kGemvRows ? gemv_items * kGemvRows * 4 : 0);
+        const int64_t slots = T == 1 ? K * IB + SB : 0;
+        p.h8 = take(slots * kBlk);
+        p.hf = take(slots * 4);
     } else {
         p.counts = take(2 * E * 4);
         p.cursor = p.counts + E * 4;
@@ -388,13 +391,21 @@ void matrices(GemmArgs &g, const mx_fp8_matrix &a, const mx_fp8_matrix *b)
     g.swb = b ? b->scales : nullptr;
 }
 
-// Up to kGemvRows tokens: two launches that read the weights into registers.
-mx_status run_gemv(const void *x, int T, const int32_t *idx, const float *wts, const mx_fp8_layer *L,
+// One token by two launches (mx_fp8_gemv.cu), when all CTAs of the first run at once: with
+// d_model 4096, 520 to 580 CTAs take 19 to 25 us and the few-token form 22 to 29; eight
+// experts' 14336 hidden rows, 1792 CTAs, 67 and 61.
+bool one_token(const mx_fp8_layer *L, int T)
+{
+    const int64_t units = L->top_k * (int64_t)blocks(L->gate.rows) + (L->shared_gate.w ? blocks(L->shared_gate.rows) : 0);
+    return T == 1 && units * (kBlk / 16) <= 4 * num_sms() && L->gate.cols <= 32768;
+}
+
+mx_status run_gemv(const void *x, const int32_t *idx, const float *wts, const mx_fp8_layer *L,
                    const void *residual, void *out, cudaStream_t s, uint8_t *ws)
 {
     auto bytes = [](const mx_fp8_matrix &m) { return static_cast<const uint8_t *>(m.w); };
     GemvArgs v{};
-    v.T = T;
+    v.T = 1;
     v.K = L->gate.cols;
     v.x = x;
     v.bf16 = L->act_dtype == MX_BF16;
@@ -413,7 +424,7 @@ mx_status run_gemv(const void *x, int T, const int32_t *idx, const float *wts, c
         v.ld_sgate = L->shared_gate.ld, v.ld_sup = L->shared_up.ld, v.ld_sdown = L->shared_down.ld;
         v.ss_gate = L->shared_gate.scales, v.ss_up = L->shared_up.scales, v.ss_down = L->shared_down.scales;
     }
-    const Plan p = make_plan(L, T);
+    const Plan p = make_plan(L, 1);
     v.h8 = ws + p.h8;
     v.hf = reinterpret_cast<float *>(ws + p.hf);
     v.out = out;
@@ -679,8 +690,7 @@ size_t mx_fp8_moe_workspace_bytes(const mx_fp8_layer *layer, int T_max)
         return 0;
     const int t = std::max(T_max, 1);
     // (for any number of tokens up to t: each form grows with them)
-    size_t n = std::max(make_plan(layer, std::min(t, kGemvRows)).total, make_plan(layer, 1).total);
-    n = std::max(n, make_plan(layer, std::min(t, kFewTokens)).total);
+    size_t n = std::max(make_plan(layer, 1).total, make_plan(layer, std::min(t, kFewTokens)).total);
     if (t > kFewTokens)
         n = std::max(n, make_plan(layer, t).total);
     return n;
@@ -712,9 +722,8 @@ mx_status mx_fp8_moe_forward(const void *x, int T, const int32_t *topk_idx, cons
     }
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t *w = static_cast<uint8_t *>(ws);
-    // (a slice of x has to fit the shared memory of four CTAs to an SM)
-    if (T <= kGemvRows && gemv_gate_up_smem(T, layer->gate.cols) <= 48 * 1024)
-        return run_gemv(x, T, topk_idx, topk_w, layer, residual, out, s, w);
+    if (one_token(layer, T))
+        return run_gemv(x, topk_idx, topk_w, layer, residual, out, s, w);
     return T <= kFewTokens ? run_few(x, T, topk_idx, topk_w, layer, residual, out, s, w)
                            : run_many(x, T, topk_idx, topk_w, layer, residual, out, s, w);
 }

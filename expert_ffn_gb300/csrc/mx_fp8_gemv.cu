@@ -13,11 +13,12 @@
 // tcgen05 kernel the 2112 x 2816 product of one row took 7.7 us, most of it set-up,
 // pipeline fill and cluster reduction.  The MMA's eight columns are the tokens.
 //
-// The layer: gate/up quantises its slice of x in each warp while the weights are
-// under way, and leaves the hidden blocks in e4m3; down sums over all active
-// experts and the shared one in a fixed order, so no scratch output and no third
-// launch are needed.  Its first weights are requested before the gate/up launch has
-// ended.
+// The layer, of one token: gate/up quantises its slice of x in each warp while the
+// weights are under way, and leaves the hidden blocks in e4m3; down sums over all slots
+// and the shared expert in a fixed order, so no scratch output and no third launch are
+// needed.  Its first weights are requested before the gate/up launch has ended.  Two
+// tokens and more are faster by mx_fp8_gemm.cu (128 experts, top-8: 2 tokens 27 us and 44
+// here, 8 tokens 62 and 316, where the same expert's blocks made long chains).
 #include "mx_fp8.cuh"
 
 namespace mx {
@@ -73,6 +74,30 @@ __device__ __forceinline__ Piece load_block(const Rows2 &r, int b, int cols, int
             p.a[j] = ld_stream_u4(r.r0 + k);
             p.c[j] = ld_stream_u4(r.r1 + k);
         }
+    }
+    return p;
+}
+
+// The same into four 16-byte places of shared memory, `gap` apart, asynchronously; a
+// piece behind the last column is left out.
+__device__ __forceinline__ void copy_block(uint8_t *to, int gap, const Rows2 &r, int b, int cols, int lane)
+{
+    const int o = b * kBlk + (lane & 3) * 16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (o + 64 * j < cols) {
+            cp_async16(to + 2 * j * gap, r.r0 + o + 64 * j);
+            cp_async16(to + (2 * j + 1) * gap, r.r1 + o + 64 * j);
+        }
+}
+
+__device__ __forceinline__ Piece copied(const uint8_t *from, int gap)
+{
+    Piece p;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        p.a[j] = *reinterpret_cast<const uint4 *>(from + 2 * j * gap);
+        p.c[j] = *reinterpret_cast<const uint4 *>(from + (2 * j + 1) * gap);
     }
     return p;
 }
@@ -191,90 +216,88 @@ __global__ void __launch_bounds__(kMmWarps * 32, 2) gemv_kernel(const GemvArgs a
 
 // --------------------------------------------------------------------- layer
 
-// Active experts of up to kN tokens.  One token: its slots as they are (an
-// expert may come twice, an index may be none of the experts).  More: each
-// expert once, ascending.  All threads of the CTA; list[] and mask[] are shared.
-__device__ __forceinline__ int active_list(const GemvArgs &a, int *list, uint32_t *mask)
+// Four neighbouring values of the token, as they lie in memory: nothing here
+// waits for them.  A lane behind the last column reads the last four.
+__device__ __forceinline__ uint4 load4(const void *p, int c, int n, int bf16)
 {
-    const int tid = threadIdx.x, n = a.T * a.topk;
-    if (a.T == 1) {
-        for (int s = tid; s < n; s += blockDim.x)
-            list[s] = __ldg(a.idx + s);
-        __syncthreads();
-        return n;
-    }
-    if (tid < kMaxExperts / 32)
-        mask[tid] = 0;
-    __syncthreads();
-    for (int s = tid; s < n; s += blockDim.x) {
-        const int e = __ldg(a.idx + s);
-        if (e >= 0 && e < a.E)
-            atomicOr(mask + (e >> 5), 1u << (e & 31));
-    }
-    __syncthreads();
-    int total = 0;
-    for (int i = 0; i < kMaxExperts / 32; ++i)
-        total += __popc(mask[i]);
-    for (int e = tid; e < a.E; e += blockDim.x)
-        if (mask[e >> 5] >> (e & 31) & 1) {
-            int at = __popc(mask[e >> 5] & ((1u << (e & 31)) - 1));
-            for (int i = 0; i < e >> 5; ++i)
-                at += __popc(mask[i]);
-            list[at] = e;
-        }
-    __syncthreads();
-    return total;
-}
-
-// Four neighbouring values of an activation row, zeros from column n on.
-__device__ __forceinline__ void load4(const void *p, int64_t row, int c, int n, int bf16, float (&v)[4])
-{
-    if (c + 4 <= n && n % 4 == 0) {
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (n % 4 == 0) {
+        const int k = min(c, n - 4);
         if (bf16) {
-            const uint2 r = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + row * n + c));
-            v[0] = __uint_as_float(r.x << 16), v[1] = __uint_as_float(r.x & 0xFFFF0000u);
-            v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xFFFF0000u);
+            const uint2 h = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const uint16_t *>(p) + k));
+            r.x = h.x, r.y = h.y;
         } else {
-            const float4 r = __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p) + row * n + c));
-            v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+            r = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(p) + k));
         }
     } else {
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = c + i < n ? load_act(p, row * n + c + i, bf16) : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+            const int k = min(c + i, n - 1);
+            w[i] = bf16 ? __ldg(reinterpret_cast<const uint16_t *>(p) + k) : __ldg(reinterpret_cast<const uint32_t *>(p) + k);
+        }
+        r = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    return r;
 }
 
-constexpr int kGuWarps = 4, kGuDepth = 2, kGuCluster = kBlk / 16;
+// Their numbers, zeros from column n on.
+__device__ __forceinline__ void values4(const uint4 &r, int c, int n, int bf16, float (&v)[4])
+{
+    uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    if (bf16) {
+        const bool pairs = n % 4 == 0;
+        w[3] = pairs ? r.y & 0xFFFF0000u : r.w << 16;
+        w[2] = pairs ? r.y << 16 : r.z << 16;
+        w[1] = pairs ? r.x & 0xFFFF0000u : r.y << 16;
+        w[0] = r.x << 16;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = c + i < n ? __uint_as_float(w[i]) : 0.0f;
+}
 
-// Hidden blocks: h8[block][token][128] in e4m3 and their factors (scale times
-// routing weight); block = the shared expert's, then (active expert, block).  A CTA
-// has 16 hidden rows, gate and up; the eight CTAs of a block form a cluster and
-// tell each other their largest |h|.
+constexpr int kGuWarps = 4, kGuDepth = 3, kGuX = 6, kGuCluster = kBlk / 16, kGuGap = kGuWarps * 32 * 16;
+constexpr int kGuRing = kGuDepth * 8 * kGuGap;  // bytes: [kGuDepth][gate, up][4][thread] pieces under way
+
+// Hidden blocks: h8[block][128] in e4m3 and their factors (scale times routing weight);
+// block = the shared expert's, then (slot, block): an expert may come twice, an index may
+// be none of the experts.  A CTA has 16 hidden rows, gate and up; the eight CTAs of a
+// block form a cluster and tell each other their largest |h|.  Weights go through shared
+// memory asynchronously, each lane's pieces to its own places: in registers two blocks a
+// warp could be under way, and the token's loads came behind them (the launch took 13.5 us
+// and not 11).
 __global__ void __launch_bounds__(kGuWarps * 32, 4) gemv_gate_up(const GemvArgs a)
 {
-    extern __shared__ __align__(16) uint8_t xs[];  // [warp][token][pitch]: the warp's slice of x, e4m3
-    __shared__ __align__(16) float part[kGuWarps][2][16 * kN];
-    __shared__ float am[kGuCluster][kN];
-    __shared__ int list[kMaxTopK * kN];
-    __shared__ uint32_t mask[kMaxExperts / 32];
+    extern __shared__ __align__(16) uint8_t gu[];
+    // a warp's sums, in its own first two places of the ring when all has been read
+    auto part = [&](int w, int m) { return reinterpret_cast<float *>(gu + m * kGuGap + w * 512); };
+    __shared__ float am[kGuCluster];
     pdl_trigger();
     asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // (this CTA runs: its memory may be written)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int KB = blocks(a.K), SB = blocks(a.S), IB = blocks(a.I);
     const int rank = blockIdx.x % kGuCluster, blk = blockIdx.x / kGuCluster;
-    int e = -1, f = blk, rows = a.S;  // (the shared expert's blocks come first: they wait for no index)
+    const int slot = blk < SB ? -1 : (blk - SB) / IB;
+    const int e = slot < 0 ? -1 : __ldg(a.idx + slot);
+    // the warp's slice of x: its first kGuX blocks' loads before those of weights
+    const int b0 = KB * warp / kGuWarps, b1 = KB * (warp + 1) / kGuWarps, nx = b1 - b0;
+    uint4 raw[kGuX];
+    auto load_x = [&](int q) {
+#pragma unroll
+        for (int i = 0; i < kGuX; ++i)
+            raw[i] = load4(a.x, (b0 + min(q + i, nx - 1)) * kBlk + 4 * lane, a.K, a.bf16);
+    };
+    if (nx > 0)
+        load_x(0);
+    int f = blk, rows = a.S;
     const uint8_t *wg = a.sw_gate, *wu = a.sw_up;
     const float *sg = a.ss_gate, *su = a.ss_up;
     int64_t lg = a.ld_sgate, lu = a.ld_sup;
-    if (blk >= SB) {
-        const int n = active_list(a, list, mask), i = (blk - SB) / IB;
-        if (i >= n)
-            return;
-        e = list[i];
+    if (slot >= 0) {
         if (e < 0 || e >= a.E)
             return;
-        f = blk - SB - i * IB;
+        f = blk - SB - slot * IB;
         rows = a.I;
         wg = a.w_gate + (int64_t)e * a.I * a.ld_gate;
         wu = a.w_up + (int64_t)e * a.I * a.ld_up;
@@ -288,137 +311,117 @@ __global__ void __launch_bounds__(kGuWarps * 32, 4) gemv_gate_up(const GemvArgs 
     su += (int64_t)f * KB;
     if (row0 < rows) {
         const Rows2 rg = rows_of(wg, lg, row0, rows, lane), ru = rows_of(wu, lu, row0, rows, lane);
-        const int b0 = KB * warp / kGuWarps, b1 = KB * (warp + 1) / kGuWarps;
-        const int slice = (KB + kGuWarps - 1) / kGuWarps, pitch = slice * kBlk + 64;
-        uint8_t *x = xs + warp * a.T * pitch;
-        float *fx = reinterpret_cast<float *>(xs + kGuWarps * a.T * pitch) + warp * slice * kN;  // [block][token]
+        // behind the ring the slices of x, e4m3, and their scales
+        const int slice = (KB + kGuWarps - 1) / kGuWarps;
+        uint8_t *x = gu + kGuRing + warp * slice * kBlk;
+        float *fx = reinterpret_cast<float *>(gu + kGuRing + kGuWarps * slice * kBlk) + warp * slice;
         float ag[4] = {0.0f, 0.0f, 0.0f, 0.0f}, au[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         // kGuDepth blocks of both matrices are under way at any time
-        Piece pg[kGuDepth], pu[kGuDepth];
+        uint8_t *mine = gu + threadIdx.x * 16;
         float s0[kGuDepth], s1[kGuDepth];
         auto load = [&](int i, int b) {
-            pg[i] = load_block(rg, b, a.K, lane);
-            pu[i] = load_block(ru, b, a.K, lane);
+            copy_block(mine + 8 * i * kGuGap, kGuGap, rg, b, a.K, lane);
+            copy_block(mine + (8 * i + 4) * kGuGap, kGuGap, ru, b, a.K, lane);
             s0[i] = __ldg(sg + b);
             s1[i] = __ldg(su + b);
         };
 #pragma unroll
-        for (int i = 0; i < kGuDepth; ++i)
+        for (int i = 0; i < kGuDepth; ++i) {
             if (b0 + i < b1)
                 load(i, b0 + i);
-        // x's slice, behind the first requests for weights, four blocks' loads at a time
-        const int n = (b1 - b0) * a.T;
-        for (int q = 0; q < n; q += 4) {
-            float v[4][4];
+            cp_async_commit();
+        }
+        for (int q = 0; q < nx; q += kGuX) {
+            if (q)
+                load_x(q);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (q + i < n) {
-                    const int k = a.T == 1 ? q + i : (q + i) / a.T;
-                    load4(a.x, q + i - k * a.T, (b0 + k) * kBlk + 4 * lane, a.K, a.bf16, v[i]);
-                }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (q + i < n) {
-                    const int k = a.T == 1 ? q + i : (q + i) / a.T, t = q + i - k * a.T;
-                    const float s = quantize128(v[i], x + t * pitch + k * kBlk, lane);
+            for (int i = 0; i < kGuX; ++i)
+                if (q + i < nx) {
+                    float v[4];
+                    values4(raw[i], (b0 + q + i) * kBlk + 4 * lane, a.K, a.bf16, v);
+                    const float s = quantize128(v, x + (q + i) * kBlk, lane);
                     if (lane == 0)
-                        fx[k * kN + t] = s;
+                        fx[q + i] = s;
                 }
         }
         __syncwarp();
-        const uint8_t *xb = x + min(lane >> 2, a.T - 1) * pitch + (lane & 3) * 16;
-        const float *fb = fx + 2 * (lane & 3);
+        const uint8_t *xb = x + (lane & 3) * 16;  // (all eight columns of the MMA: the token)
         for (int b = b0; b < b1; b += kGuDepth)
 #pragma unroll
             for (int i = 0; i < kGuDepth; ++i)
                 if (b + i < b1) {
                     const uint4 xv[2] = {*reinterpret_cast<const uint4 *>(xb), *reinterpret_cast<const uint4 *>(xb + 64)};
-                    const float2 fv = *reinterpret_cast<const float2 *>(fb);
+                    const float fv = fx[b + i - b0];
                     xb += kBlk;
-                    fb += kN;
-                    trim(pg[i], b + i, a.K, lane);
-                    trim(pu[i], b + i, a.K, lane);
-                    add_block(ag, pg[i], xv, fv.x * s0[i], fv.y * s0[i]);
-                    add_block(au, pu[i], xv, fv.x * s1[i], fv.y * s1[i]);
+                    cp_async_wait<kGuDepth - 1>();
+                    Piece pg = copied(mine + 8 * i * kGuGap, kGuGap), pu = copied(mine + (8 * i + 4) * kGuGap, kGuGap);
+                    trim(pg, b + i, a.K, lane);
+                    trim(pu, b + i, a.K, lane);
+                    add_block(ag, pg, xv, fv * s0[i], fv * s0[i]);
+                    add_block(au, pu, xv, fv * s1[i], fv * s1[i]);
                     if (b + i + kGuDepth < b1)
                         load(i, b + i + kGuDepth);
+                    cp_async_commit();
                 }
-        put_sums(part[warp][0], ag, lane);
-        put_sums(part[warp][1], au, lane);
+        __syncwarp();
+        put_sums(part(warp, 0), ag, lane);
+        put_sums(part(warp, 1), au, lane);
     }
     __syncthreads();
-    const int t = threadIdx.x >> 4, r = threadIdx.x & 15;
+    const int r = threadIdx.x;  // the CTA's hidden row, of the first 16 threads
     float h = 0.0f;
-    if (row0 + r < rows && t < a.T) {
+    if (r < 16 && row0 + r < rows) {
         float g = 0.0f, v = 0.0f;
 #pragma unroll
         for (int k = 0; k < kGuWarps; ++k) {
-            g += part[k][0][r * kN + t];
-            v += part[k][1][r * kN + t];
+            g += part(k, 0)[r * kN];
+            v += part(k, 1)[r * kN];
         }
         h = (a.act == MX_SILU ? __fdividef(g, 1.0f + __expf(-g)) : gelu_fast(g)) * v;
     }
-    uint32_t m = __float_as_uint(h) & 0x7FFFFFFFu;
-#pragma unroll
-    for (int o = 8; o; o >>= 1)
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
     asm volatile("barrier.cluster.wait;" ::: "memory");
     if (r < kGuCluster) {
         uint32_t at;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&am[rank][t])), "r"(r));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&am[rank])), "r"(r));
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(m) : "memory");
     }
     // (the other CTAs' maxima come with the barrier; none writes here after it)
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-    if (t >= a.T)
+    if (r >= 16)
         return;
     m = 0;
 #pragma unroll
     for (int k = 0; k < kGuCluster; ++k)
-        m = max(m, __float_as_uint(am[k][t]));
+        m = max(m, __float_as_uint(am[k]));
     const float s = scale_of(__uint_as_float(m), 0);
-    // The routing weight joins the scale; a token that did not choose the expert adds nothing.
-    float wt = 1.0f;
-    bool in = true;
-    if (e >= 0 && a.T == 1) {
-        wt = __ldg(a.wts + (blk - SB) / IB);
-    } else if (e >= 0) {
-        wt = 0.0f;
-        in = false;
-        for (int k = 0; k < a.topk; ++k)
-            if (__ldg(a.idx + t * a.topk + k) == e) {
-                wt += __ldg(a.wts + t * a.topk + k);
-                in = true;
-            }
-    }
     // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
-    a.h8[((int64_t)blk * kN + t) * kBlk + rank * 16 + r] = in ? (uint8_t)e4m3_x2(h * __frcp_rn(s), 0.0f) : 0;
-    if (rank == 0 && r == 0)
-        a.hf[(int64_t)blk * kN + t] = in ? s * wt : 0.0f;
+    a.h8[(int64_t)blk * kBlk + rank * 16 + r] = (uint8_t)e4m3_x2(h * __frcp_rn(s), 0.0f);
+    if (rank == 0 && r == 0)  // (the routing weight joins the scale)
+        a.hf[blk] = slot < 0 ? s : s * __ldg(a.wts + slot);
 }
 
-constexpr int kDnWarps = 8, kDnDepth = 3;
+constexpr int kDnWarps = 8, kDnDepth = 6, kDnX = 3, kDnGap = kDnWarps * 32 * 16;
 
-// 16 output columns of every token: all hidden blocks of the shared expert and
-// of the active experts, split over the warps in order.
+// 16 output columns: all hidden blocks of the shared expert and of the slots, split over
+// the warps in order.
 __global__ void __launch_bounds__(kDnWarps * 32, 2) gemv_down(const GemvArgs a)
 {
+    extern __shared__ __align__(16) uint8_t dn[];  // [kDnDepth][4][thread] pieces under way
     __shared__ __align__(16) float part[kDnWarps][16 * kN];
-    __shared__ int list[kMaxTopK * kN];
-    __shared__ uint32_t mask[kMaxExperts / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int IB = blocks(a.I), SB = blocks(a.S), DB = blocks(a.K);
     const int row0 = blockIdx.x * 16;
-    const int n_act = active_list(a, list, mask), items = SB + n_act * IB;
+    const int items = SB + a.topk * IB;
     const int b0 = (int)((int64_t)items * warp / kDnWarps), b1 = (int)((int64_t)items * (warp + 1) / kDnWarps);
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    // the next item to request: its expert's place in the list (-1: shared), block and rows
+    // the next item to request: its slot (-1: the shared expert), block and rows
     int lj = b0 < SB ? -1 : (b0 - SB) / IB, lc = b0 < SB ? b0 : (b0 - SB) - lj * IB;
     Rows2 lr;
     const float *ls;
     bool lok;
     auto locate = [&]() {
-        const int e = lj < 0 ? 0 : lj < n_act ? list[lj] : -1;
+        const int e = lj < 0 ? 0 : lj < a.topk ? __ldg(a.idx + lj) : -1;
         lok = e >= 0 && (lj < 0 || e < a.E);
         if (!lok)
             return;
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(kDnWarps * 32, 2) gemv_down(const GemvArgs a)
                     : rows_of(a.w_down + (int64_t)e * a.K * a.ld_down, a.ld_down, row0, a.K, lane);
         ls = lj < 0 ? a.ss_down + (int64_t)(row0 / kBlk) * SB : a.s_down + ((int64_t)e * DB + row0 / kBlk) * IB;
     };
-    Piece p[kDnDepth];
+    uint8_t *mine = dn + threadIdx.x * 16;
     float sw[kDnDepth];
     int left[kDnDepth];  // columns from the block's first to the matrix's last; 0: no expert
     auto load = [&](int i) {
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(kDnWarps * 32, 2) gemv_down(const GemvArgs a)
         left[i] = 0;
         if (lok) {
             left[i] = cols - lc * kBlk;
-            p[i] = load_block(lr, lc, cols, lane);
+            copy_block(mine + 4 * i * kDnGap, kDnGap, lr, lc, cols, lane);
             sw[i] = __ldg(ls + lc);
         }
         if (++lc == (lj < 0 ? SB : IB)) {
@@ -445,54 +448,63 @@ __global__ void __launch_bounds__(kDnWarps * 32, 2) gemv_down(const GemvArgs a)
     };
     locate();
 #pragma unroll
-    for (int i = 0; i < kDnDepth; ++i)
+    for (int i = 0; i < kDnDepth; ++i) {
         if (b0 + i < b1)
             load(i);
+        cp_async_commit();
+    }
+    const int o = threadIdx.x, at = row0 + o;
+    const bool writes = o < 16 && at < a.K;
+    const float res = writes && a.residual ? load_act(a.residual, at, a.bf16) : 0.0f;
     pdl_wait();  // the hidden blocks, behind the first requests for weights
     // (written by the launch before: not through the read-only path)
-    const uint8_t *xb = a.h8 + ((int64_t)b0 * kN + min(lane >> 2, a.T - 1)) * kBlk + (lane & 3) * 16;
-    const float *fb = a.hf + (int64_t)b0 * kN + 2 * (lane & 3);
+    const uint8_t *xb = a.h8 + (int64_t)b0 * kBlk + (lane & 3) * 16;
+    const float *fb = a.hf + b0;
+    uint4 x[kDnX][2];
+    float f[kDnX];
+    auto hidden = [&](int i, int item) {
+        const int at = min(item, items - 1) - b0;  // (behind the warp's last: read, not used)
+        x[i][0] = *reinterpret_cast<const uint4 *>(xb + (int64_t)at * kBlk);
+        x[i][1] = *reinterpret_cast<const uint4 *>(xb + (int64_t)at * kBlk + 64);
+        f[i] = fb[at];
+    };
+    if (b0 < b1)
+#pragma unroll
+        for (int i = 0; i < kDnX; ++i)
+            hidden(i, b0 + i);
     for (int b = b0; b < b1; b += kDnDepth) {
-        uint4 x[kDnDepth][2];
-        float2 f[kDnDepth];
 #pragma unroll
-        for (int i = 0; i < kDnDepth; ++i)
-            if (b + i < b1 && left[i]) {
-                x[i][0] = *reinterpret_cast<const uint4 *>(xb + i * kN * kBlk);
-                x[i][1] = *reinterpret_cast<const uint4 *>(xb + i * kN * kBlk + 64);
-                f[i] = *reinterpret_cast<const float2 *>(fb + i * kN);
-            }
-        xb += kDnDepth * kN * kBlk;
-        fb += kDnDepth * kN;
-#pragma unroll
-        for (int i = 0; i < kDnDepth; ++i)
+        for (int i = 0; i < kDnDepth; ++i) {
             if (b + i < b1) {
+                cp_async_wait<kDnDepth - 1>();
                 if (left[i]) {
+                    Piece p = copied(mine + 4 * i * kDnGap, kDnGap);
                     if (left[i] < kBlk) {  // what lies behind the last column is nobody's: neither operand's
                         const int at = (lane & 3) * 16;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            p[i].a[j] = keep_bytes(p[i].a[j], left[i] - at - 64 * j);
-                            p[i].c[j] = keep_bytes(p[i].c[j], left[i] - at - 64 * j);
-                            x[i][j] = keep_bytes(x[i][j], left[i] - at - 64 * j);
+                            p.a[j] = keep_bytes(p.a[j], left[i] - at - 64 * j);
+                            p.c[j] = keep_bytes(p.c[j], left[i] - at - 64 * j);
+                            x[i % kDnX][j] = keep_bytes(x[i % kDnX][j], left[i] - at - 64 * j);
                         }
                     }
-                    add_block(acc, p[i], x[i], f[i].x * sw[i], f[i].y * sw[i]);
+                    add_block(acc, p, x[i % kDnX], f[i % kDnX] * sw[i], f[i % kDnX] * sw[i]);
                 }
+                hidden(i % kDnX, b + i + kDnX);
                 if (b + i + kDnDepth < b1)
                     load(i);
+                cp_async_commit();
             }
+        }
     }
     put_sums(part[warp], acc, lane);
     __syncthreads();
-    const int t = threadIdx.x >> 4, o = threadIdx.x & 15;
-    if (t < a.T && row0 + o < a.K) {
+    if (writes) {
         float y = 0.0f;
 #pragma unroll
         for (int k = 0; k < kDnWarps; ++k)
-            y += part[k][o * kN + t];
-        const int64_t at = (int64_t)t * a.K + row0 + o;
-        y = fmaf(a.lam, y, a.residual ? load_act(a.residual, at, a.bf16) : 0.0f);
+            y += part[k][o * kN];
+        y = fmaf(a.lam, y, res);
         if (a.bf16)
             reinterpret_cast<uint16_t *>(a.out)[at] = f2bf(y);
         else
@@ -502,12 +514,6 @@ __global__ void __launch_bounds__(kDnWarps * 32, 2) gemv_down(const GemvArgs a)
 
 }  // namespace
 
-size_t gemv_gate_up_smem(int T, int D)
-{
-    const int slice = (blocks(D) + kGuWarps - 1) / kGuWarps;
-    return (size_t)kGuWarps * (T * (slice * kBlk + 64) + slice * kN * 4);
-}
-
 cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s)
 {
     gemv_kernel<<<(a.N + 15) / 16, kMmWarps * 32, 0, s>>>(a);
@@ -516,14 +522,13 @@ cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s)
 
 cudaError_t launch_gemv_moe(const GemvArgs &a, cudaStream_t s)
 {
-    const size_t smem = gemv_gate_up_smem(a.T, a.K);
+    const size_t smem = kGuRing + kGuWarps * ((blocks(a.K) + kGuWarps - 1) / kGuWarps) * (kBlk + 4);
     cudaError_t e = smem_optin((const void *)gemv_gate_up, smem);
     if (e != cudaSuccess)
         return e;
-    const int most = a.T == 1 ? a.topk : (a.T * a.topk < a.E ? a.T * a.topk : a.E);
     cudaLaunchConfig_t c{};
     cudaLaunchAttribute at;
-    c.gridDim = dim3((blocks(a.S) + most * blocks(a.I)) * kGuCluster);
+    c.gridDim = dim3((blocks(a.S) + a.topk * blocks(a.I)) * kGuCluster);
     c.blockDim = dim3(kGuWarps * 32);
     c.dynamicSmemBytes = smem;
     c.stream = s;
@@ -535,7 +540,9 @@ cudaError_t launch_gemv_moe(const GemvArgs &a, cudaStream_t s)
         return e;
     c.gridDim = dim3((a.K + 15) / 16);
     c.blockDim = dim3(kDnWarps * 32);
-    c.dynamicSmemBytes = 0;
+    c.dynamicSmemBytes = kDnDepth * 4 * kDnGap;
+    if ((e = smem_optin((const void *)gemv_down, c.dynamicSmemBytes)) != cudaSuccess)
+        return e;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     return cudaLaunchKernelEx(&c, gemv_down, a);
