@@ -203,6 +203,33 @@ def test_matmul_keeps_non_finite_rows_apart():
     check_product(out[keep], rows_value(q, s)[keep], weight_value(w[0], ws[0]), 512)
 
 
+@pytest.mark.parametrize("m", [1, 7])
+def test_matmul_few_rows_of_a_large_matrix(m):
+    import torch
+    n, k = 8200, 4104  # above the 32 MB from which few rows change kernels
+    q, s = make_rows(m, k, 31)
+    w, ws = make_weight(1, n, k, 32)
+    out = torch.full((m, n), 7.0, device="cuda")
+    work = workspace(256)
+    mx.fp8_matmul(q, s, mx.Fp8Weight(w[0], ws[0]), out, work)
+    mx.workspace_check(work, torch.cuda.current_stream())
+    check_product(out, rows_value(q, s), weight_value(w[0], ws[0]), k)
+
+
+@pytest.mark.parametrize("m", [1, 9, 40, 64])
+@pytest.mark.parametrize("n,k", [(100, 1100), (1024, 2100), (1300, 1024), (3000, 1030)])
+def test_matmul_split_over_clusters(m, n, k):
+    """Inner blocks over clusters of eight, four and two, and not at all."""
+    import torch
+    q, s = make_rows(m, k, 33)
+    w, ws = make_weight(1, n, k, 34)
+    out = torch.full((m, n), 7.0, device="cuda", dtype=torch.bfloat16)
+    work = workspace(256)
+    mx.fp8_matmul(q, s, mx.Fp8Weight(w[0], ws[0]), out, work)
+    mx.workspace_check(work, torch.cuda.current_stream())
+    check_product(out, rows_value(q, s), weight_value(w[0], ws[0]), k)
+
+
 # ---------------------------------------------------------------- grouped
 
 GROUPS = {
@@ -375,6 +402,49 @@ def test_moe_forward(case):
     assert torch.equal(out, again)
 
 
+# Every split of the inner blocks over a cluster (by d_model and the tile of tokens), one token with more hidden
+# blocks than run at once, many slots, many experts to a token, the smallest layers.
+MORE = [
+    (1, 40, 32, 300, 130, 0, mx.MX_SILU, "f32", False),
+    (1, 4, 4, 512, 2560, 0, mx.MX_GELU_TANH, "bf16", True),
+    (1, 2, 1, 5, 3, 0, mx.MX_SILU, "f32", True),
+    (1, 16, 8, 1022, 144, 72, mx.MX_SILU, "bf16", True),
+    (3, 2, 2, 1, 1, 1, mx.MX_GELU_TANH, "f32", False),
+    (8, 128, 8, 2816, 320, 256, mx.MX_SILU, "bf16", True),
+    (9, 40, 32, 300, 130, 50, mx.MX_GELU_TANH, "bf16", False),
+    (10, 4, 2, 4096, 640, 0, mx.MX_SILU, "bf16", False),
+    (20, 4, 2, 5120, 640, 128, mx.MX_GELU_TANH, "f32", True),
+    (30, 6, 3, 8192, 512, 0, mx.MX_SILU, "bf16", False),
+    (12, 4, 2, 13056, 512, 0, mx.MX_GELU_TANH, "f32", False),
+    (50, 4, 2, 2816, 640, 0, mx.MX_SILU, "bf16", True),
+    (50, 4, 2, 4096, 640, 64, mx.MX_SILU, "f32", True),
+    (64, 6, 3, 8192, 512, 0, mx.MX_GELU_TANH, "bf16", False),
+    (40, 4, 2, 20000, 256, 0, mx.MX_SILU, "bf16", False),
+    (70, 2, 1, 5, 3, 2, mx.MX_SILU, "f32", True),
+    (120, 40, 12, 272, 128, 0, mx.MX_SILU, "bf16", False),
+    (1100, 16, 4, 256, 128, 64, mx.MX_GELU_TANH, "bf16", True),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MORE)), ids=[f"T{c[0]}_E{c[1]}_K{c[2]}_D{c[3]}" for c in MORE])
+def test_moe_forward_splits_and_limits(case):
+    import torch
+    T, E, K, D, I, S, act, dtype, res = MORE[case]
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    layer, ws, sh = make_layer(E, D, I, S, 120 + case, K, act, dtype)
+    x = torch.randn(T, D, device="cuda", generator=gen(140 + case)).to(dt)
+    residual = torch.randn(T, D, device="cuda", generator=gen(160 + case)).to(dt) if res else None
+    idx, wts = routing(T, E, K, 180 + case)
+    n = mx.fp8_moe_workspace_bytes(layer, T)
+    work = workspace(n + 4096)
+    work[n:] = 0x5A  # (what lies behind the workspace is not this call's)
+    out = torch.full((T, D), 7.0, device="cuda", dtype=dt)
+    mx.fp8_moe_forward(x, idx, wts, layer, out, work[:n], residual=residual)
+    mx.workspace_check(work, torch.cuda.current_stream())
+    check_layer(out, x, idx, wts, ws, sh, act, 0.5, residual, K)
+    assert (work[n:] == 0x5A).all()
+
+
 @pytest.mark.parametrize("T", [1, 6, 40, 90])
 def test_moe_odd_routings(T):
     """Indices outside the experts add nothing, repeated ones count twice, a token may have no expert at all, one
@@ -436,8 +506,87 @@ def test_moe_in_place_and_other_stream(T):
     check_layer(buf, x2 * 2, idx, wts, ws, sh, mx.MX_GELU_TANH, 0.5, x2 * 2, K)
 
 
+@pytest.mark.parametrize("T", [4, 40, 90])
+def test_moe_non_finite_tokens_stay_apart(T):
+    """A NaN or an infinity in a token makes that token's output NaN and leaves the others' bits as they were."""
+    import torch
+    E, K, D, I, S = 6, 3, 384, 160, 128
+    layer, _, _ = make_layer(E, D, I, S, 45, K, mx.MX_GELU_TANH, "bf16")
+    x = torch.randn(T, D, device="cuda", generator=gen(46)).bfloat16()
+    idx, wts = routing(T, E, K, 47)
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, T))
+    clean, out = torch.empty_like(x), torch.empty_like(x)
+    mx.fp8_moe_forward(x, idx, wts, layer, clean, work)
+    x[1, 5], x[T - 1, 300] = math.nan, -math.inf
+    mx.fp8_moe_forward(x, idx, wts, layer, out, work)
+    assert out[1].isnan().all() and out[T - 1].isnan().all()
+    keep = [t for t in range(T) if t not in (1, T - 1)]
+    assert torch.equal(out[keep], clean[keep]) and clean.isfinite().all()
+
+
+@pytest.mark.parametrize("T", [1, 20, 90])
+def test_two_calls_at_once(T):
+    """Two streams with a workspace each, call upon call, give what one alone gives."""
+    import torch
+    E, K, D, I, S = 16, 4, 1024, 256, 128
+    layer, _, _ = make_layer(E, D, I, S, 35, K, mx.MX_SILU, "bf16")
+    n = mx.fp8_moe_workspace_bytes(layer, T)
+    runs = []
+    for i in range(2):
+        x = torch.randn(T, D, device="cuda", generator=gen(36 + i)).bfloat16()
+        idx, wts = routing(T, E, K, 38 + i)
+        alone = torch.empty_like(x)
+        mx.fp8_moe_forward(x, idx, wts, layer, alone, workspace(n))
+        runs.append((x, idx, wts, alone, workspace(n), torch.cuda.Stream(), [torch.zeros_like(x) for _ in range(8)]))
+    torch.cuda.synchronize()
+    for j in range(8):
+        for x, idx, wts, _, work, stream, outs in runs:
+            mx.fp8_moe_forward(x, idx, wts, layer, outs[j], work, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, _, alone, work, stream, outs in runs:
+        mx.workspace_check(work, stream)
+        assert all(torch.equal(o, alone) for o in outs)
+
+
+def test_captured_quantize_and_products():
+    """A graph of quantiser, product and grouped product follows its buffers' new values and offsets."""
+    import torch
+    x = torch.randn(30, 512, device="cuda", generator=gen(41)).bfloat16()
+    q, s = torch.empty(30, 512, device="cuda", dtype=torch.float8_e4m3fn), torch.empty(4, 30, device="cuda").t()
+    w, ws = make_weight(3, 200, 512, 42)
+    one, all_ = mx.Fp8Weight(w[0], ws[0]), mx.Fp8Weight(w, ws)
+    offsets = torch.tensor([0, 10, 10, 30], dtype=torch.int32, device="cuda")
+    out, grp, work = torch.empty(30, 200, device="cuda"), torch.full((30, 200), 7.0, device="cuda"), workspace(256)
+
+    def run():
+        mx.fp8_quantize(x, q, s)
+        mx.fp8_matmul(q, s, one, out, work)
+        mx.fp8_grouped_matmul(q, s, offsets, all_, grp, work)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            run()
+    torch.cuda.synchronize()
+    x.copy_(torch.randn(30, 512, device="cuda", generator=gen(43)))
+    offsets.copy_(torch.tensor([2, 2, 19, 25], dtype=torch.int32))  # (rows 0, 1 and 25 on belong to nobody)
+    grp.fill_(7.0)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    v = rows_value(*ref_quantize(x.double()))
+    check_product(out, v, weight_value(w[0], ws[0]), 512)
+    check_product(grp[2:19], v[2:19], weight_value(w[1], ws[1]), 512)
+    check_product(grp[19:25], v[19:25], weight_value(w[2], ws[2]), 512)
+    assert (grp[:2] == 7.0).all() and (grp[25:] == 7.0).all()
+
+
 def test_moe_tokens_do_not_depend_on_their_batch():
-    """A token's output is the same bits alone and in a batch of up to 64."""
+    """A token's output alone is its output in a batch of 64, up to hidden values next to a border of e4m3."""
     import torch
     E, K, D, I, S = 16, 4, 640, 256, 128
     layer, _, _ = make_layer(E, D, I, S, 13, K, mx.MX_SILU, "f32")
