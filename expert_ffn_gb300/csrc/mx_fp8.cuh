@@ -58,7 +58,6 @@ struct GemmArgs {
     const void *residual;
     float lam;
     unsigned *err;
-    int xbox;            // rows of one operand copy
     int stages, cl;      // ring depth, cluster size (split of the inner dimension)
     int pdl;             // the launch may start before its predecessor has ended
 };
@@ -83,13 +82,14 @@ struct RowsProblem {
     int64_t ldh;
     float *hs;
     int64_t hs_ld;
-    int xbox;
 };
 struct RowsArgs {
     RowsProblem p[2];
     int act;
     unsigned *err;
 };
+constexpr int kRowsBox = 32;  // token rows of one copy (32, 64 and 128 measured alike)
+
 // Tiles of 128 tokens x bn (128, 256; kGateUp: 256) weight rows.
 cudaError_t launch_rows(Mode mode, int bn, const RowsArgs &a, int grid, cudaStream_t s);
 

@@ -208,13 +208,13 @@ mx_status run_rows(Mode mode, RowsArgs &g, const void *const *q, const int64_t *
         // (a group that is expected to have `avg` rows)
         const double tiles = !p.offsets ? (p.rows + 127) / 128 : p.E * (avg[i] <= 100 ? 1.0 : avg[i] / 128 + 0.5);
         wide += tiles * (mode == kGateUp ? blocks(p.N) : (p.N + 255) / 256);
-        p.xbox = avg[i] >= 96.0 ? 128 : 32;
-        if ((st = rows_map(&p.xm, q[i], p.rows, p.K, ldq[i], p.xbox)) != MX_OK)
+        if ((st = rows_map(&p.xm, q[i], p.rows, p.K, ldq[i], kRowsBox)) != MX_OK)
             return st;
     }
-    // (narrower tiles when the wide ones would leave SMs idle; a factor for each 64 columns
-    // wants a thread to have them)
-    const int bn = mode == kGateUp || g.p[0].out_kind == kOutF16 || wide >= sms ? 256 : 128;
+    // Narrower tiles while each finds an SM of its own: 256 x 4096 x 4096, 64 of them, 12.8 us
+    // and by wide ones 16.7; 600 rows, 160 or 80, 21.5 and 17.9.  (A factor for each 64 columns
+    // wants a thread to have them.)
+    const int bn = mode == kGateUp || g.p[0].out_kind == kOutF16 || 2 * wide > sms ? 256 : 128;
     const cudaError_t e = launch_rows(mode, bn, g, sms, s);
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
 }
@@ -231,9 +231,8 @@ mx_status run_product(GemmArgs &g, const void *q, int64_t ldq, double avg, cudaS
     // (64 x 4096 x 4096: 15.5 us whole, 12.5 in two, 9.5 in four or more; 64 x 704 x 2816
     // 12.8, 7.9 in four, 6.9 in eight)
     g.cl = g.offsets ? 1 : split_of(tiles * FT, KB, sms, 4);
-    g.xbox = nt;
     g.stages = fit_stages(kProduct, nt, kSmem, std::max(2, KB));
-    if ((st = rows_map(&g.xm, q, g.rows, g.K, ldq, g.xbox)) != MX_OK)
+    if ((st = rows_map(&g.xm, q, g.rows, g.K, ldq, nt)) != MX_OK)
         return st;
     const int64_t units = g.offsets ? ((int64_t)g.rows / nt + g.E) * FT : tiles * FT;
     const cudaError_t e = launch_gemm(kProduct, nt, g, (int)std::min<int64_t>(sms / g.cl, units) * g.cl, s);
@@ -488,7 +487,6 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
         if ((st = weight_map(&g.sa, L->shared_gate)) != MX_OK || (st = weight_map(&g.sb, L->shared_up)) != MX_OK)
             return st;
     }
-    g.xbox = p.nt;
     // experts that T tokens are expected to select, each on its own draw of K
     const double active = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)K / E), (double)T));
     const int DB = blocks(D);

@@ -23,6 +23,13 @@
 // sums every cl-th token column over the partial sums in all their shared memories,
 // in rank order, so the result does not depend on timing.
 //
+// What bounds it: an MMA of 128 weight rows takes 129 cycles whatever its N up to 256, so
+// an SM streams 32 bytes of weights a cycle, 1.5 times its share of HBM: few tokens are
+// bound by HBM where there are enough units, and by the chain (launch, tables, pipeline
+// fill, cluster) where there are not.  64 x 4096 x 4096 takes 8.5 us (HBM 2.6, as a chain
+// about 6); the layer of 31 tokens of top-8 of 128 experts 48 us, of which the first 5 pass
+// before the quantised tokens are there, 20 in gate/up and 13 in down and its cluster.
+//
 // Every wait is bounded: a wait that gives up sets the caller's error word and
 // ends the CTA's work.
 #include "mx_fp8_tc.cuh"
@@ -357,19 +364,16 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
                 if (MODE == kFewDown)
                     tma_2d(st, &a.xm, 0, kb * NT, full + s);
                 else
-                    for (int r = 0; r < U.n; r += a.xbox)
-                        tma_2d(st + r * 128, &a.xm, kb * kBlk, U.tok0 + r, full + s);
+                    tma_2d(st, &a.xm, kb * kBlk, U.tok0, full + s);
             };
-            auto bytes = [&](const Unit &U) -> uint32_t {
-                return NMAT * kTile + (MODE == kFewDown ? NT : (U.n + a.xbox - 1) / a.xbox * a.xbox) * 128;
-            };
+            constexpr uint32_t bytes = NMAT * kTile + NT * 128;
             int early = 0;  // stages whose weights were requested before the launch's inputs were complete
             if (FEW) {
                 for (int u = w.first; u < w.n_units && early < NS; u += w.step) {
                     const Unit U = unit_of<MODE, NT>(a, w, u);
                     for (int kb = w.kb0; kb < w.kb1 && early < NS; ++kb, ++early) {
                         if (elect_one()) {
-                            mbar_arrive_expect_tx(full + early, bytes(U));
+                            mbar_arrive_expect_tx(full + early, bytes);
                             weights(U, kb, early);
                         }
                         __syncwarp();
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
                         goto produced;
                     if (elect_one()) {
                         if (it >= early) {
-                            mbar_arrive_expect_tx(full + s, bytes(U));
+                            mbar_arrive_expect_tx(full + s, bytes);
                             weights(U, kb, s);
                         }
                         tokens(U, kb, s);

@@ -27,6 +27,15 @@
 //
 // A launch may hold two problems, the routed experts' and the shared expert's: the
 // first is bound by HBM, the second by the tensor cores, and their tiles alternate.
+//
+// What bounds it: a block of 128 x 256 x 128 takes the tensor core 516 cycles (four MMAs,
+// 129 each, where N = 256 comes at the price of N = 16) and the summing warps about 640,
+// two sums to an FMA instruction; a tile's end costs them some 4000.  4096 x 4096 x 4096
+// takes 58 us, 2.35 PFLOP/s (without the sums 46, without the results 53); 32768 rows of
+// 256 experts x 1024 x 4096 211 us, 6.0 TB/s; gate/up and down of 4096 tokens of top-8
+// of those, with a shared expert of 4096, 480 and 330 us.  Tried and slower: a CTA pair (141 us
+// at 4096^3: each block's hand-over crosses the pair), 128 columns a tile in four buffers
+// (104 us), sixteen summing warps (66 us).
 #include "mx_fp8_tc.cuh"
 
 namespace mx {
@@ -208,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             for (int u = blockIdx.x; u < w.n; u += gridDim.x) {
                 const Tile T = tile_at(a, w, u);
                 const RowsProblem &P = a.p[T.p];
-                const int KB = blocks(P.K), xr = (T.n + P.xbox - 1) / P.xbox * P.xbox;
+                const int KB = blocks(P.K), xr = (T.n + kRowsBox - 1) / kRowsBox * kRowsBox;
                 const int row0 = MODE == kGateUp ? T.f * kBlk : T.f * BN;
                 // (rows of the second half behind the matrix: no copy, their columns are not stored)
                 const bool two = NSUB == 2 && (MODE == kGateUp || row0 + 128 < P.N);
@@ -218,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     uint8_t *st = ring + s * kStage;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(full + s, xr * 128 + (two ? 2 : 1) * kTile);
-                        for (int r = 0; r < T.n; r += P.xbox)
+                        for (int r = 0; r < T.n; r += kRowsBox)
                             tma_2d(st + r * 128, &P.xm, kb * kBlk, T.tok0 + r, full + s);
                         tma_3d(st + kTile, &P.wa, kb * kBlk, row0, T.e, full + s);
                         if (two)

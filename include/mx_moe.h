@@ -365,8 +365,8 @@ MX_API mx_status mx_moe_profile_read(double *ms, int *launches, int reset);
  *                                      sum_{c in block b} qx[r][c] qw[o][c]
  * with every sum in fp32 and one rounding to the output type.  The last block
  * of columns (and of weight rows) may be shorter than 128; any size from 1 on
- * is accepted.  A result does not depend on the other rows of a call, nor on
- * timing.
+ * is accepted.  A result does not depend on the values of the call's other rows,
+ * nor on timing; the order of its sums goes by the call's sizes.
  *
  * All calls are asynchronous on `stream` (NULL: the legacy default stream) and
  * run on the current device, which has to own every buffer.  They allocate
@@ -382,7 +382,8 @@ typedef struct {
     const void *w;        /* e4m3, row pitch ld bytes, matrices rows * ld bytes apart; 16-byte aligned */
     const float *scales;  /* [count][ceil(rows / 128)][ceil(cols / 128)]                            */
     int32_t rows, cols, count;
-    int64_t ld;           /* multiple of 16, >= cols                                                */
+    int64_t ld;           /* multiple of 16, >= cols; a row's bytes up to the next multiple of 16 from
+                             cols on are read, but not used                                         */
 } mx_fp8_matrix;
 
 /* Quantised activations [rows][cols]. */
@@ -391,7 +392,8 @@ typedef struct {
     float *scales;        /* row r, block b at r * scale_row + b * scale_block (elements, >= 0); the
                              products read them fastest with scale_row == 1                         */
     int32_t rows, cols;
-    int64_t ld;           /* multiple of 16, >= cols (mx_fp8_quantize takes any ld >= cols)          */
+    int64_t ld;           /* multiple of 16, >= cols (mx_fp8_quantize takes any ld >= cols); bytes
+                             behind cols as in mx_fp8_matrix, the last row's too                    */
     int64_t scale_row, scale_block;
 } mx_fp8_rows;
 
@@ -453,9 +455,9 @@ typedef struct {
  *   topk_idx  device int32 [T][top_k], topk_w device fp32 [T][top_k], as
  *            mx_moe_route writes them.  An index outside [0, n_experts)
  *            contributes nothing; one that a token repeats counts each time.
- * Up to 64 tokens the layer runs as two GEMM launches over the experts that some
- * token selected, each of whose weights are read once; above, as grouped
- * products.
+ * Up to 64 tokens the layer reads each selected expert's weights once: one token in
+ * two launches, more in three.  Above, it runs as grouped products over the experts'
+ * rows.
  */
 MX_API mx_status mx_fp8_moe_forward(const void *x, int T, const int32_t *topk_idx, const float *topk_w,
                                     const mx_fp8_layer *layer, const void *residual, void *out, void *stream,
