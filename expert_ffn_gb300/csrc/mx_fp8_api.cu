@@ -178,13 +178,6 @@ mx_status rows_map(CUtensorMap *m, const void *q, int64_t rows, int64_t cols, in
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "tensor map of the activations");
 }
 
-// Rows of a group from which on the tokens take the MMA's M side (mx_fp8_rows.cu).
-// The two sides' times cross there: 128 matrices [2112, 2816] with a quarter, one, eight
-// and 24 rows each 33 | 72 | 119 | 126 us on the N side and 33 | 76 | 119 | 123 on the M
-// side, and when a few matrices have most of the rows 24 | 55 | 120 | 139 and 27 | 60 |
-// 112 | 129.  One matrix: 64 rows fill one tile of the N side.
-bool many_rows(bool grouped, double avg) { return avg > (grouped ? 6.0 : 64.0); }
-
 // CTAs that share the `items` inner blocks of each of `units` units, out of `ctas` that
 // run at once; they form a cluster.  More than `most` gain nothing over whole clusters
 // left waiting (clusters of eight with an SM to a CTA: a GPC holds one or two).
@@ -192,6 +185,23 @@ int split_of(int64_t units, double items, int ctas, int most)
 {
     const int64_t n = std::min<int64_t>(units <= 8 ? 8 : most, ctas / units);
     return items < 8 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(n, (int64_t)(items / 2)));
+}
+
+// Rows of a group from which on the tokens take the MMA's M side (mx_fp8_rows.cu).
+// The two sides' times cross there: 128 matrices [2112, 2816] with a quarter, one, eight
+// and 24 rows each 33 | 72 | 119 | 126 us on the N side and 33 | 76 | 119 | 123 on the M
+// side, and when a few matrices have most of the rows 24 | 55 | 120 | 139 and 27 | 60 |
+// 112 | 129.
+constexpr double kManyRows = 6.0;
+
+// One matrix: the N side up to a tile of 64 rows, and for more as long as clusters can
+// split its units: 128 x 2112 x 2816 in four 8.0 us (M side 9.9), 256 x 1024 x 4096 in four
+// 8.7 (12.1), 128 x 4096 x 14336 in two 25.7 (38.4); but 192 x 2112 x 2816 in two 11.0 (9.9).
+bool many_rows(int rows, const mx_fp8_matrix &w)
+{
+    const int KB = blocks(w.cols);
+    const int cl = split_of((int64_t)((rows + 63) / 64) * blocks(w.rows), KB, num_sms(), 4);
+    return rows > 64 && cl < (KB >= 32 ? 2 : 3);
 }
 
 // One launch of one or two products by mx_fp8_rows.cu; p[i].xm is encoded here from
@@ -281,7 +291,7 @@ mx_status product(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_mat
         return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP8 product");
     }
     const double avg = offsets ? (double)x->rows / w->count : x->rows;
-    if (many_rows(offsets, avg)) {
+    if (offsets ? avg > kManyRows : many_rows(x->rows, *w)) {
         RowsArgs r{};
         RowsProblem &p = r.p[0];
         p.rows = x->rows;

@@ -374,7 +374,8 @@ MX_API mx_status mx_moe_profile_read(double *ms, int *launches, int reset);
  * of at least the size that the matching *_workspace_bytes call returns,
  * 256-byte aligned, prepared by mx_moe_workspace_init; its first word is the
  * error word that mx_moe_workspace_check reads.  Calls (and captured graphs)
- * that share a workspace must be ordered on the GPU.
+ * that share a workspace must be ordered on the GPU.  A call's outputs overlap none of
+ * its other buffers unless the call says so.
  * ------------------------------------------------------------------------ */
 
 /* A stack of `count` quantised matrices [rows][cols]. */
