@@ -453,7 +453,25 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     __syncwarp();
                     const int o = o0 + c0 + col, rows = n - quad * 32 - r0 - prow;  // (rows 0, 4, 8, 12 below it)
                     char *to = base + (r0 >> 2) * rstep + c0 * es;
-                    if (P.out_vec && o + per <= P.N) {
+                    if (!P.out_vec) {
+                        // a row at a time, one word of it to a lane
+                        const int left = P.N - o0 - c0, nr = n - quad * 32 - r0, c = lane * 4 / es;
+                        const uint32_t *word = reinterpret_cast<const uint32_t *>(mine);
+                        char *p = static_cast<char *>(P.out) + ((int64_t)(tok0 + quad * 32 + r0) * P.ldo + o0 + c0 + c) * es;
+#pragma unroll 8
+                        for (int i = 0; i < 16; ++i, p += P.ldo * es) {
+                            const uint32_t v = word[line_piece(i, lane >> 2) * 4 + (lane & 3)];
+                            if (i < nr && c < left) {
+                                if (es == 4) {
+                                    *reinterpret_cast<uint32_t *>(p) = v;
+                                } else {
+                                    reinterpret_cast<uint16_t *>(p)[0] = (uint16_t)v;
+                                    if (c + 1 < left)
+                                        reinterpret_cast<uint16_t *>(p)[1] = (uint16_t)(v >> 16);
+                                }
+                            }
+                        }
+                    } else if (o + per <= P.N) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (4 * i < rows)
