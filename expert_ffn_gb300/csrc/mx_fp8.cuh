@@ -9,14 +9,13 @@
 #include "mx_internal.h"
 #include "mx_moe.h"
 
-
 namespace mx {
 namespace fp8 {
 
 constexpr int kBlk = 128;        // columns (and weight rows) that share a scale
 constexpr float kMaxE4M3 = 448.0f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: a block of zeros keeps a usable scale
-constexpr int kFewTokens = 64;   // largest T of the two-launch layer path (all tokens as one operand tile)
+constexpr int kFewTokens = 64;   // largest T of the layer's few-token form (all tokens as one operand tile)
 
 __host__ __device__ constexpr int blocks(int n) { return (n + kBlk - 1) / kBlk; }
 __host__ __device__ constexpr int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
@@ -59,7 +58,7 @@ struct GemmArgs {
     float lam;
     unsigned *err;
     int stages, cl;      // ring depth, cluster size (split of the inner dimension)
-    int pdl;             // the launch may start before its predecessor has ended
+    int pdl;             // lets the next launch start before this one has ended
 };
 
 cudaError_t launch_gemm(Mode mode, int nt, const GemmArgs &a, int grid, cudaStream_t s);

@@ -152,8 +152,8 @@ int fit_stages(Mode mode, int nt, int bytes, int want)
     return s;
 }
 
-// Token tile for groups of about `n` rows: the smallest that holds one.
-int tile_for(double n, int most)
+// Token tile for `n` rows: the smallest that holds them.
+int tile_for(int n, int most)
 {
     int nt = 16;
     while (nt < most && nt < n)
@@ -191,8 +191,9 @@ int split_of(int64_t units, double items, int ctas, int most)
 // The two sides' times cross there: 128 matrices [2112, 2816] with a quarter, one, eight
 // and 24 rows each 33 | 72 | 119 | 126 us on the N side and 33 | 76 | 119 | 123 on the M
 // side, and when a few matrices have most of the rows 24 | 55 | 120 | 139 and 27 | 60 |
-// 112 | 129.
-constexpr double kManyRows = 6.0;
+// 112 | 129.  Four rows to a matrix: evenly 158 us (N) and 163 (M) for 256 matrices [1024,
+// 4096], all of them to one 33 and 19; two rows: 139 and 143, 20 and 19.
+constexpr double kManyRows = 3.0;
 
 // One matrix: the N side up to a tile of 64 rows, and for more as long as clusters can
 // split its units: 128 x 2112 x 2816 in four 8.0 us (M side 9.9), 256 x 1024 x 4096 in four
@@ -230,12 +231,12 @@ mx_status run_rows(Mode mode, RowsArgs &g, const void *const *q, const int64_t *
 }
 
 // One product launch by mx_fp8_gemm.cu over rows grouped by matrix (offsets NULL: one
-// group); `avg` is the expected size of a group.  Tokens take the MMA's N side, in a
-// tile that holds most groups.
-mx_status run_product(GemmArgs &g, const void *q, int64_t ldq, double avg, cudaStream_t s)
+// group).  Tokens take the MMA's N side, in a tile that holds them, of 64 at most; groups,
+// of kManyRows on average at most, in tiles of 16.
+mx_status run_product(GemmArgs &g, const void *q, int64_t ldq, cudaStream_t s)
 {
     const int sms = num_sms(), FT = blocks(g.N), KB = blocks(g.K);
-    const int nt = tile_for(g.offsets ? avg + 2 * std::sqrt(avg) : g.rows, 64);
+    const int nt = g.offsets ? 16 : tile_for(g.rows, 64);
     const int64_t tiles = g.offsets ? g.E : (g.rows + nt - 1) / nt;
     mx_status st;
     // (64 x 4096 x 4096: 15.5 us whole, 12.5 in two, 9.5 in four or more; 64 x 704 x 2816
@@ -330,7 +331,7 @@ mx_status product(const mx_fp8_rows *x, const int32_t *offsets, const mx_fp8_mat
     g.err = static_cast<unsigned *>(ws);
     if ((st = weight_map(&g.wa, *w)) != MX_OK)
         return st;
-    return run_product(g, x->q, x->ld, avg, static_cast<cudaStream_t>(stream));
+    return run_product(g, x->q, x->ld, static_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ the layer
@@ -400,9 +401,9 @@ void matrices(GemmArgs &g, const mx_fp8_matrix &a, const mx_fp8_matrix *b)
     g.swb = b ? b->scales : nullptr;
 }
 
-// One token by two launches (mx_fp8_gemv.cu), when all CTAs of the first run at once: with
-// d_model 4096, 520 to 580 CTAs take 19 to 25 us and the few-token form 22 to 29; eight
-// experts' 14336 hidden rows, 1792 CTAs, 67 and 61.
+// One token by two launches (mx_fp8_gemv.cu), when all CTAs of the first run at once: 520
+// CTAs (d_model 2816) take 18.6 us and the few-token form 21.7, 576 (4096) 24.5 and 29; two
+// experts of 14336 hidden rows, 1792 CTAs, 67 and 61.
 bool one_token(const mx_fp8_layer *L, int T)
 {
     const int64_t units = L->top_k * (int64_t)blocks(L->gate.rows) + (L->shared_gate.w ? blocks(L->shared_gate.rows) : 0);
