@@ -404,6 +404,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
     produced:;
     } else if (warp == EW + 1) {
         // --------------------------------------------------------------- MMA
+        if (FEW)
+            pdl_wait();  // (the launch before is not on this one's bounded waits' time)
         {
             int s = 0, b = 0;
             uint32_t ph = 0, tph = 1;
@@ -495,6 +497,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
         }
     } else {
         // -------------------------------------------------------------- sums
+        if (FEW)
+            pdl_wait();
         const int row = warp * 32 + lane;
         const uint32_t ta = tmem + ((uint32_t)warp << 21);
         int b = 0, q = 0;
