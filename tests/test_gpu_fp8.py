@@ -239,6 +239,8 @@ GROUPS = {
     "ragged": [17, 33, 129, 2, 64, 65, 16],
     "empty": [0, 0, 0],
     "many": [700, 0, 129, 300, 5, 256, 257, 900],
+    "few": [1, 0, 3, 2, 0, 0, 18, 0, 1, 0, 0, 2],
+    "sparse": [0] * 60 + [4, 33] + [0] * 40 + [1],
 }
 
 
@@ -277,6 +279,27 @@ def test_grouped_offsets_outside_the_rows():
     check_product(buf[9:], x[9:], weight_value(w[3], ws[3]), 256)
     check_product(buf[6:9], x[6:9], weight_value(w[2], ws[2]), 256)
     check_product(buf[:2], x[:2], weight_value(w[0], ws[0]), 256)
+
+
+def test_grouped_few_rows_between_others():
+    """Few rows to a matrix: those before the first group and behind the last are left alone, bad offsets are cut."""
+    import torch
+    q, s = make_rows(22, 400, 51)
+    w, ws = make_weight(9, 300, 400, 52)
+    weight, work, x = mx.Fp8Weight(w, ws), workspace(256), rows_value(q, s)
+    buf = torch.full((22, 300), 7.0, device="cuda")
+    offsets = torch.tensor([2, 2, 5, 5, 5, 9, 9, 9, 9, 19], dtype=torch.int32, device="cuda")
+    mx.fp8_grouped_matmul(q, s, offsets, weight, buf, work)
+    for e, lo, hi in ((1, 2, 5), (4, 5, 9), (8, 9, 19)):
+        check_product(buf[lo:hi], x[lo:hi], weight_value(w[e], ws[e]), 400)
+    assert (buf[:2] == 7.0).all() and (buf[19:] == 7.0).all()
+    offsets.copy_(torch.tensor([-7, 4, 1, 4, 4, 4, 4, 4, 10, 1 << 30], dtype=torch.int32))
+    mx.fp8_grouped_matmul(q, s, offsets, weight, buf, work)
+    mx.workspace_check(work, torch.cuda.current_stream())
+    # groups [0, 4), (4, 1): empty, [1, 4) over the first's rows, [4, 10), [10, 22)
+    check_product(buf[:1], x[:1], weight_value(w[0], ws[0]), 400)
+    check_product(buf[4:10], x[4:10], weight_value(w[7], ws[7]), 400)
+    check_product(buf[10:], x[10:], weight_value(w[8], ws[8]), 400)
 
 
 # ------------------------------------------------------------------ layer
@@ -522,6 +545,24 @@ def test_moe_non_finite_tokens_stay_apart(T):
     assert out[1].isnan().all() and out[T - 1].isnan().all()
     keep = [t for t in range(T) if t not in (1, T - 1)]
     assert torch.equal(out[keep], clean[keep]) and clean.isfinite().all()
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_moe_non_finite_single_token(value):
+    """One token with a NaN or an infinity: NaN throughout, and nothing of it in the workspace's next call."""
+    import torch
+    E, K, D, I, S = 6, 3, 384, 160, 128
+    layer, _, _ = make_layer(E, D, I, S, 45, K, mx.MX_SILU, "f32")
+    x = torch.randn(1, D, device="cuda", generator=gen(48))
+    idx, wts = routing(1, E, K, 49)
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, 1))
+    clean, out, again = (torch.empty_like(x) for _ in range(3))
+    mx.fp8_moe_forward(x, idx, wts, layer, clean, work)
+    bad = x.clone()
+    bad[0, 200] = value
+    mx.fp8_moe_forward(bad, idx, wts, layer, out, work)
+    mx.fp8_moe_forward(x, idx, wts, layer, again, work)
+    assert out.isnan().all() and clean.isfinite().all() and torch.equal(again, clean)
 
 
 @pytest.mark.parametrize("T", [1, 20, 90])
