@@ -420,17 +420,17 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 const int o0 = T.f * BN + wg * 64;
                 const int es = P.out_kind == kOutF32 ? 4 : 2, per = 16 / es;
                 if (P.out_kind == kOutF16) {
-                    // FP16 of y 2^-k, k such that the row's largest of 64 columns is below 2^15, and 2^k
-                    // beside it: 11 significant bits, enough under a bf16 result, at half the bytes
+                    // FP16 of y 2^-k, k such that the row's largest finite of 64 columns is below 2^15, and
+                    // 2^k beside it: 11 significant bits, enough under a bf16 result, at half the bytes.
+                    // (2^-112 counts as the smallest: 2^k and 2^-k stay normal.)  The maximum is taken on the
+                    // bits one exponent up, where infinities and NaN, which keep themselves, are negative.
 #pragma unroll
                     for (int j = 0; j < NSUB; ++j) {
-                        uint32_t m = 0;
+                        int m = 16 << 23;
 #pragma unroll
                         for (int i = 0; i < 64; ++i)
-                            m = max(m, __float_as_uint(acc[j * 64 + i]) & 0x7FFFFFFFu);
-                        // (zeros, subnormals, infinities and NaN as they are)
-                        const int ex = (int)(m >> 23);
-                        const int k = ex < 30 || ex > 240 ? 0 : ex - (127 + 14);
+                            m = max(m, (int)((__float_as_uint(acc[j * 64 + i]) & 0x7FFFFFFFu) + (1u << 23)));
+                        const int k = (m >> 23) - 1 - (127 + 14);
                         const float down = __uint_as_float((uint32_t)(127 - k) << 23);
 #pragma unroll
                         for (int i = 0; i < 64; ++i)

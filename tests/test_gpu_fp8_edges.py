@@ -1,0 +1,72 @@
+"""FP8 block-scaled operators at the ends of their number ranges: magnitudes, non-finite weights, signs of zero,
+borders of e4m3, and what a token's result may depend on.  Tolerances and definitions are those of test_gpu_fp8."""
+from __future__ import annotations
+
+import math
+
+import pytest
+
+import expert_ffn_gb300 as mx
+from tests.test_gpu_fp8 import (check_layer, gen, make_layer, make_rows, make_weight, nb, ref_quantize, ref_scale, routing,
+                                rows_value, weight_value, workspace)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------- magnitudes of a layer's results
+
+def scaled_layer(power, D=320, I=160, E=6, K=3, act=mx.MX_SILU, dtype="bf16", seed=210):
+    """A layer whose down scales, and so its results, are 2^power times the usual ones."""
+    layer, ws, _ = make_layer(E, D, I, 0, seed, K, act, dtype)
+    ws[2][1].mul_(2.0 ** power)
+    return layer, ws
+
+
+@pytest.mark.parametrize("T", [1, 40, 90])
+@pytest.mark.parametrize("power", [-100, 60, 114, 118])
+def test_moe_results_of_any_magnitude(T, power):
+    """Results near either end of the type's range keep their precision, whatever the number of tokens."""
+    import torch
+    layer, ws = scaled_layer(power)
+    x = torch.randn(T, 320, device="cuda", generator=gen(211)).bfloat16()
+    idx, wts = routing(T, 6, 3, 212)
+    out = torch.empty_like(x)
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, T))
+    mx.fp8_moe_forward(x, idx, wts, layer, out, work)
+    mx.workspace_check(work, torch.cuda.current_stream())
+    assert out.isfinite().all()
+    check_layer(out, x, idx, wts, ws, None, mx.MX_SILU, 0.5, None, 3)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("T", [1, 40, 90])
+def test_moe_non_finite_output_column_keeps_to_itself(T, value):
+    """An output column that is NaN or infinite leaves its neighbours as they are, also when they are large."""
+    import torch
+    layer, ws = scaled_layer(40)
+    x = torch.randn(T, 320, device="cuda", generator=gen(213)).bfloat16()
+    idx, wts = routing(T, 6, 3, 214)
+    out = torch.empty_like(x)
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, T))
+    w = ws[2][0].view(torch.uint8)
+    if math.isnan(value):
+        w[:, 70] = 0x7F  # e4m3's NaN in a row of every down matrix
+        mx.fp8_moe_forward(x, idx, wts, layer, out, work)
+        hit = slice(70, 71)
+        assert out[:, hit].isnan().all()
+    else:
+        ws[2][1][:, 1] = math.inf  # scales of a block of rows: 128 columns of the results
+        mx.fp8_moe_forward(x, idx, wts, layer, out, work)
+        hit = slice(128, 256)
+        assert not out[:, hit].isfinite().any()
+    w[:, 70] = 0
+    ws[2][1][:, 1] = 0.0
+    out[:, hit] = 0.0
+    clean = torch.empty_like(x)
+    mx.fp8_moe_forward(x, idx, wts, layer, clean, work)
+    clean[:, hit] = 0.0
+    if not math.isnan(value):
+        clean[:, 70] = out[:, 70]  # (this row was set to zero for the second call alone)
+    else:
+        clean[:, 128:256] = out[:, 128:256]
+    assert torch.equal(out, clean)
