@@ -41,6 +41,8 @@ namespace {
 
 constexpr uint32_t kTile = 128 * 128;  // bytes of one weight tile
 constexpr int kFacRing = 8;            // blocks of factors in flight
+// Few tokens: the factor of a hidden block of an expert that the token did not choose.
+constexpr uint32_t kNotChosen = 0x80000000u;  // -0; a chosen one's has 0 added, which makes a -0 of it +0
 
 constexpr int kSumWarps = 4, kThreads = (kSumWarps + 3) * 32;
 constexpr int n_mats(int mode) { return mode == kFewGateUp ? 2 : 1; }
@@ -173,7 +175,7 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Walk &w, const Uni
     constexpr int NMAT = n_mats(MODE);
     if constexpr (NMAT == 2) {
         // few tokens: the routing weight joins the scale; a token that did not choose the
-        // expert adds nothing (most do not: found out first)
+        // expert (most do not: found out first) has zeros and is marked
         float wt = 1.0f;
         bool in = true;
         if (U.e >= 0) {
@@ -182,7 +184,7 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Walk &w, const Uni
             in = __any_sync(0xFFFFFFFFu, mine);
         }
         uint32_t e = 0;
-        float sc = 0.0f;
+        float sc = __uint_as_float(kNotChosen);
         if (in) {
             if (U.e >= 0)
 #pragma unroll
@@ -198,7 +200,7 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Walk &w, const Uni
             // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
             const float inv = __frcp_rn(s);
             e = e4m3_x2(h[0] * inv, h[1] * inv) | e4m3_x2(h[2] * inv, h[3] * inv) << 16;
-            sc = s * wt;
+            sc = s * wt + 0.0f;
         }
         const int64_t at = (int64_t)U.item * NT + n;
         reinterpret_cast<uint32_t *>(a.h + at * kBlk)[lane] = e;
@@ -235,6 +237,101 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Walk &w, const Uni
     }
 }
 
+// Down of few tokens once more, for a unit with a NaN or an infinity in its sums: block by
+// block, each column with the experts that its token chose alone.  (The weights of an expert
+// meet the other tokens' zeros too, and zero times a NaN, or a factor of zero times an infinite
+// scale, is NaN.)  Columns that were right come out the same, bit for bit.  Apart from the
+// kernel's loops, where every instruction counts: with a predicate for each column 64 tokens of
+// top-8 of 128 experts took 189 us instead of 153, with a test in the factors alone 31 tokens
+// 127 instead of 115; looking at the first column's sums at the unit's end costs 0.4 us at most.
+// Leaves the sums [column][128 rows] in `stage`, of a cluster, or as results.  `bars`: three
+// barriers; parity: that of the next wait for them, which is returned.
+template <int NT>
+__device__ __noinline__ uint32_t redo_down(const GemmArgs &a, int f, int kb0, int kb1, const int *act, int n_act,
+                                           uint8_t *ring, float *stage, uint64_t *bars, uint32_t parity,
+                                           uint32_t tmem, volatile int *abort)
+{
+    constexpr int GC = pass_cols(kFewDown, NT);
+    Walk w{};
+    w.kb0 = kb0;
+    w.kb1 = kb1;
+    w.act = act;
+    w.n_act = n_act;
+    w.FT = blocks(a.N);
+    const Unit U = unit_of<kFewDown, NT>(a, w, f);
+    const int warp = warp_index(), lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane;
+    float acc[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        acc[n] = 0.0f;
+    for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        int e, c;
+        tile_of<kFewDown>(a, w, U, kb, e, c);
+        if (warp == kSumWarps) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bars, kTile + NT * 128);
+                tma_3d(ring, e < 0 ? &a.sa : &a.wa, c * kBlk, U.f * kBlk, e < 0 ? 0 : e, bars);
+                tma_2d(ring + kTile, &a.xm, 0, kb * NT, bars);
+            }
+            __syncwarp();
+        }
+        bool ok = wwait(bars, parity, a.err, abort);
+        if (warp == kSumWarps + 1 && ok) {
+            umma_block(tmem, sw128_desc(smem_u32(ring)), sw128_desc(smem_u32(ring + kTile)),
+                       idesc_e4m3((U.n + 15) & ~15));
+            umma_commit2(bars + 1, bars + 2);
+        }
+        ok = ok && wwait(bars + 1, parity, a.err, abort);
+        fence_after();
+        if (warp < kSumWarps && ok) {
+            const float sw = e < 0 ? __ldg(a.ssa + (int64_t)U.f * a.SB + c)
+                                   : __ldg(a.swa + ((int64_t)e * w.FT + U.f) * a.IB + c);
+#pragma unroll
+            for (int ch = 0; ch < NT / 16; ++ch) {
+                uint32_t r[16];
+                tmem_ld16(tmem + ((uint32_t)warp << 21) + ch * 16, r);
+                tmem_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int n = ch * 16 + j;
+                    const float x = n < U.n ? a.hs[(int64_t)kb * NT + n] : __uint_as_float(kNotChosen);
+                    if (__float_as_uint(x) != kNotChosen)
+                        acc[n] = fmaf(tmem_value(r[j]), x * sw + 0.0f, acc[n]);
+                }
+            }
+        }
+        fence_before();
+        parity ^= 1;
+        if (!__syncthreads_and(ok))
+            return parity;
+        fence_after();
+    }
+    if (a.cl > 1) {
+        if (warp < kSumWarps)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                stage[n * 128 + row] = acc[n];
+        return parity;
+    }
+#pragma unroll
+    for (int ps = 0; ps < NT / GC; ++ps) {
+        if (ps * GC >= U.n)
+            break;
+        if (warp < kSumWarps)
+#pragma unroll
+            for (int j = 0; j < GC; ++j)
+                stage[j * 128 + row] = acc[ps * GC + j];
+        __syncthreads();
+        if (warp < kSumWarps)
+            for (int j = warp; j < GC && ps * GC + j < U.n; j += 4) {
+                const float4 v[1] = {reinterpret_cast<const float4 *>(stage + j * 128)[lane]};
+                emit<kFewDown, NT>(a, w, U, ps * GC + j, v, lane);
+            }
+        __syncthreads();
+    }
+    return parity;
+}
+
 template <int MODE, int NT>
 __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const __grid_constant__ GemmArgs a)
 {
@@ -255,6 +352,9 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
     uint64_t *tfull = empty + 16, *tempty = tfull + 4, *ffull = tempty + 4, *fempty = ffull + kFacRing;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(fempty + kFacRing);
     volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
+    volatile uint64_t *redo = reinterpret_cast<volatile uint64_t *>(tslot + 2);  // kFewDown: units to do again
+    uint32_t *any_redo = tslot + 4;                                              // some of the cluster's
+    uint64_t *rbars = reinterpret_cast<uint64_t *>(tslot + 6);                   // and the barriers of that
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const uint32_t rank = cl > 1 ? cluster_rank() : 0;
 
@@ -273,6 +373,11 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
             mbar_init(ffull + i, 1);
             mbar_init(fempty + i, EW);
         }
+        if (MODE == kFewDown)
+            for (int i = 0; i < 3; ++i)
+                mbar_init(rbars + i, 1);
+        *redo = 0;
+        *any_redo = 0;
         *abort = 0;
         fence_mbar_init();
     }
@@ -504,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
         int b = 0, q = 0;
         uint32_t tph = 0, fph = 0;
         bool ok = true;
-        for (int u = w.first; u < w.n_units && ok; u += w.step) {
+        for (int u = w.first, k = 0; u < w.n_units && ok; u += w.step, ++k) {
             const Unit U = unit_of<MODE, NT>(a, w, u);
             const int nch = (U.n + 15) / 16;
             uint64_t acc[NMAT][NT / 2];
@@ -552,6 +657,27 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
                     q = 0, fph ^= 1;
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
+            if (MODE == kFewDown) {
+                // a NaN in a row's weights, or an infinite scale of theirs, is in the sums of every
+                // column, the first as well
+                float first, second;
+                unpair_f32(acc[0][0], first, second);
+                const bool good = __all_sync(0xFFFFFFFFu, fabsf(first) < INFINITY);
+                if (cl > 1) {
+                    if (!good) {
+                        *redo = 1;
+                        if (lane < cl)
+                            asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(mapa(smem_u32(any_redo), lane))
+                                         : "memory");
+                    }
+                } else if (!named_and(1, 128, good)) {
+                    if (tid == 0)
+                        *redo = *redo | 1ull << k;  // (54 units to a CTA at most)
+                    __syncwarp();
+                    ok = named_and(1, 128, ok);  // (the four warps give up together)
+                    continue;
+                }
+            }
 
             // The sums leave in passes of GC columns through shared memory, where a
             // warp takes a whole column (128 rows, four to a lane): its stores are
@@ -602,9 +728,28 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
             }
         }
     }
+    auto do_again = [&]() {
+        if constexpr (MODE == kFewDown) {
+            fence_after();
+            const uint64_t todo = *abort ? 0 : *redo;
+            uint32_t parity = 0;
+            for (int u = w.first, k = 0; u < w.n_units && !*abort; u += w.step, ++k)
+                if (todo >> k & 1)
+                    parity = redo_down<NT>(a, u, w.kb0, w.kb1, w.act, w.n_act, ring, stage, rbars, parity, tmem, abort);
+        }
+    };
+    if (MODE == kFewDown && cl == 1) {
+        __syncthreads();
+        if (*redo)
+            do_again();
+    }
     if (cl > 1) {
         __syncwarp();
         cluster_sync();
+        if (MODE == kFewDown && *static_cast<volatile uint32_t *>(any_redo)) {  // (the same in the whole cluster)
+            do_again();
+            cluster_sync();
+        }
         if (warp < kSumWarps && w.first < w.n_units && !*abort) {
             const Unit U = unit_of<MODE, NT>(a, w, w.first);
             // column n of the tile: CTA n % cl of the cluster, over all ranks in order

@@ -75,6 +75,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16])
 // Wait for the requested columns.
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// A column's value as it is behind the wait.
+__device__ __forceinline__ float tmem_value(uint32_t r)
+{
+    float v;
+    asm volatile("mov.b32 %0, %1;" : "=f"(v) : "r"(r));
+    return v;
+}
+
 // d += (lo, hi) * f, a pair of columns.  Volatile, so that it stays behind the wait for
 // lo and hi; with the registers as operands of the wait instead, the compiler moved
 // each of them once or twice (1.5 moves an FMA).

@@ -70,3 +70,46 @@ def test_moe_non_finite_output_column_keeps_to_itself(T, value):
     else:
         clean[:, 128:256] = out[:, 128:256]
     assert torch.equal(out, clean)
+
+
+# -------------------------------------------------------- what a token depends on
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,I,S", [(2, 384, 160, 128), (8, 384, 160, 128), (20, 384, 160, 128), (40, 384, 160, 128),
+                                     (64, 384, 160, 128), (90, 384, 160, 128), (64, 384, 64, 0), (20, 40000, 64, 0)])
+def test_moe_non_finite_weights_reach_their_tokens_alone(T, D, I, S, dtype):
+    """A NaN code, an infinite and a NaN scale of one expert's down matrix, a NaN code of its gate matrix: the tokens
+    that chose the expert have it, the others keep their bits."""
+    import torch
+    E, K = 6, 3
+    layer, ws, _ = make_layer(E, D, I, S, 220, K, mx.MX_SILU, dtype)
+    x = torch.randn(T, D, device="cuda", generator=gen(221)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    # token t: experts t, t + 1, t + 2 (modulo 6), so that each expert is some tokens' and not others'
+    idx = ((torch.arange(T, device="cuda")[:, None] + torch.arange(K, device="cuda")) % E).to(torch.int32)
+    wts = torch.rand(T, K, device="cuda", generator=gen(222)) + 0.1
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, T))
+    clean, out = torch.empty_like(x), torch.empty_like(x)
+    mx.fp8_moe_forward(x, idx, wts, layer, clean, work)
+    assert clean.isfinite().all()
+
+    def run(e, tensor, at, value, columns):
+        old = tensor[at].clone()
+        tensor[at] = value
+        mx.fp8_moe_forward(x, idx, wts, layer, out, work)
+        mx.workspace_check(work, torch.cuda.current_stream())
+        tensor[at] = old
+        chose = (idx == e).any(1)
+        assert torch.equal(out[~chose], clean[~chose])
+        assert not out[chose][:, columns].isfinite().any()
+        rest = torch.ones(D, dtype=torch.bool, device="cuda")
+        rest[columns] = False
+        if columns != slice(None):
+            assert torch.equal(out[chose][:, rest], clean[chose][:, rest])
+
+    down = ws[2][0].view(torch.uint8)
+    run(2, down, (2, 100, 7), 0x7F, slice(100, 101))
+    run(5, down, (5, D - 1, I - 1), 0xFF, slice(D - 1, D))
+    run(3, ws[2][1], (3, 1, 0), math.inf, slice(128, 256))
+    run(1, ws[2][1], (1, 2, nb(I) - 1), math.nan, slice(256, 384))
+    run(4, ws[0][0].view(torch.uint8), (4, 11, 300), 0x7F, slice(None))
+    run(0, ws[1][1], (0, 0, 2), math.nan, slice(None))
