@@ -58,6 +58,7 @@ struct GemmArgs {
     float lam;
     unsigned *err;
     int stages, cl;      // ring depth, cluster size (split of the inner dimension)
+    unsigned cl_inv;     // kFewDown, cl > 1: 2^32 / cl rounded up
     int pdl;             // lets the next launch start before this one has ended
 };
 

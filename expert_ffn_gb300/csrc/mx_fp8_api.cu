@@ -530,6 +530,7 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
     // A tile of 64 tokens wants an SM: 60 tokens in four 174 us, in six 155, in eight 184.
     const bool two = p.nt <= 32;
     d.cl = two ? split_of(DB, items, sms * 4 / 3, 8) : split_of(DB, items, sms, 6);
+    d.cl_inv = d.cl > 1 ? (unsigned)(((1ull << 32) + d.cl - 1) / d.cl) : 0;
     d.stages = fit_stages(kFewDown, p.nt, two ? kSmemHalf : kSmem, 16);
     const int grid = d.cl > 1 ? DB * d.cl : std::min(two ? 2 * sms : sms, DB);
     if ((e = launch_gemm(kFewDown, p.nt, d, grid, s)) != cudaSuccess)

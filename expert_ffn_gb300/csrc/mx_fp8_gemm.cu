@@ -21,7 +21,8 @@
 //        the summing warps read them as broadcast vectors
 // Few units: a cluster of `cl` CTAs splits the inner dimension of one unit; each CTA
 // sums every cl-th token column over the partial sums in all their shared memories,
-// in rank order, so the result does not depend on timing.
+// in rank order, so the result does not depend on timing; which block is whose goes by
+// the sizes alone (first_block), so it does not depend on the other tokens' experts either.
 //
 // What bounds it: an MMA of 128 weight rows takes 129 cycles whatever its N up to 256, so
 // an SM streams 32 bytes of weights a cycle, 1.5 times its share of HBM: few tokens are
@@ -103,8 +104,10 @@ struct Unit {
 // What the roles need to find units: tables in shared memory.
 struct Walk {
     int n_units, first, step;  // this cluster's units
-    int kb0, kb1;              // blocks of the inner dimension (items for kFewDown)
+    int kb0, kb1;              // blocks of the inner dimension; kFewDown: 0 and this rank's number
     int FT, n_act;
+    int n_routed, sh0, rank;   // kFewDown: of these the routed experts', the first of the shared expert
+    const uint32_t *list;      // and the routed ones, as far as they fit (see block_of)
     const int *tt, *lo, *len;  // by tokens: token-tile offsets [E + 1], group starts and lengths [E]
     const int *act;            // few tokens: active experts
     const int *idx;            // their routing: [T][topk] experts and weights
@@ -148,24 +151,63 @@ __device__ __forceinline__ Unit unit_of(const GemmArgs &a, const Walk &w, int u)
     return U;
 }
 
-// Weight tile of block kb of a unit: matrix (-1: shared), row tile, block column.
-template <int MODE>
-__device__ __forceinline__ void tile_of(const GemmArgs &a, const Walk &w, const Unit &U, int kb, int &e, int &c)
+// kFewDown: a cluster's ranks share the inner blocks of all active experts and the shared one.
+// Block c of expert e (the shared one counts as the one behind the last) is rank (e IB + c) mod
+// cl's, so that a token's sums are the same whichever experts the other tokens choose: their
+// blocks add zeros.  (An even cut of the active experts' blocks moved with those.  This one is
+// uneven where few are active: 2 tokens of top-8 of 128 experts 28.2 us, cut evenly 27.4.)
+__device__ __forceinline__ int div_cl(const GemmArgs &a, int x)  // (exact: x cl < 2^32)
 {
-    if (MODE == kFewDown) {
-        if (kb < w.n_act * a.IB) {
-            const int i = kb / a.IB;
-            e = w.act[i];
-            c = kb - i * a.IB;
-        } else {
-            e = -1;
-            c = kb - w.n_act * a.IB;
-        }
-    } else {
-        e = U.e;
-        c = kb;
-    }
+    return a.cl > 1 ? (int)__umulhi((unsigned)x, a.cl_inv) : x;
 }
+
+__device__ __forceinline__ int first_block(const GemmArgs &a, int e, int rank)
+{
+    const int x = e * a.IB, c = rank - (x - div_cl(a, x) * a.cl);
+    return c < 0 ? c + a.cl : c;
+}
+
+// Entries of Walk::list that there is room for, behind the active experts and their bits.
+constexpr int list_room(int nt) { return 2 * nt * kMaxTopK - kMaxExperts / 32; }
+
+// A list entry: expert, its place among the active ones, block.
+__device__ __forceinline__ uint32_t list_entry(int e, int at, int c) { return (uint32_t)e | at << 10 | (uint32_t)c << 19; }
+
+// The entry of this rank's routed block kb when there is no room for it in the list: the last
+// active expert whose first block comes at kb or before.
+__device__ __noinline__ uint32_t far_block(const GemmArgs &a, const int *act, int n_act, int rank, int kb)
+{
+    const int q = div_cl(a, a.IB);
+    int lo = 0, hi = n_act;
+    while (lo + 1 < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (q * mid + (act[mid] >> 16) <= kb)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int e = act[lo] & 0xFFFF;
+    return list_entry(e, lo, first_block(a, e, rank) + (kb - q * lo - (act[lo] >> 16)) * a.cl);
+}
+
+// Block kb of a unit: matrix (-1: shared), block column; kFewDown: hidden block among all experts'.
+struct Block {
+    int e, c, item;
+};
+template <int MODE, int NT>
+__device__ __forceinline__ Block block_of(const GemmArgs &a, const Walk &w, const Unit &U, int kb)
+{
+    if (MODE != kFewDown)
+        return Block{U.e, kb, kb};
+    if (kb >= w.n_routed) {
+        const int c = w.sh0 + (kb - w.n_routed) * a.cl;
+        return Block{-1, c, w.n_act * a.IB + c};
+    }
+    const uint32_t v = kb < list_room(NT) ? w.list[kb] : far_block(a, w.act, w.n_act, w.rank, kb);
+    const int c = (int)(v >> 19);
+    return Block{(int)(v & 1023), c, (int)(v >> 10 & 511) * a.IB + c};
+}
+static_assert(kMaxExperts <= 512, "list entries");
 
 // Results of token column n of a unit: 128 weight rows, four to a lane.
 template <int MODE, int NT>
@@ -247,16 +289,19 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Walk &w, const Uni
 // Leaves the sums [column][128 rows] in `stage`, of a cluster, or as results.  `bars`: three
 // barriers; parity: that of the next wait for them, which is returned.
 template <int NT>
-__device__ __noinline__ uint32_t redo_down(const GemmArgs &a, int f, int kb0, int kb1, const int *act, int n_act,
-                                           uint8_t *ring, float *stage, uint64_t *bars, uint32_t parity,
-                                           uint32_t tmem, volatile int *abort)
+__device__ __noinline__ uint32_t redo_down(const GemmArgs &a, int f, int n_blocks, int n_routed, const int *act,
+                                           const uint32_t *list, int n_act, int sh0, int rank, uint8_t *ring,
+                                           float *stage, uint64_t *bars, uint32_t parity, uint32_t tmem,
+                                           volatile int *abort)
 {
     constexpr int GC = pass_cols(kFewDown, NT);
     Walk w{};
-    w.kb0 = kb0;
-    w.kb1 = kb1;
+    w.n_routed = n_routed;
     w.act = act;
+    w.list = list;
     w.n_act = n_act;
+    w.sh0 = sh0;
+    w.rank = rank;
     w.FT = blocks(a.N);
     const Unit U = unit_of<kFewDown, NT>(a, w, f);
     const int warp = warp_index(), lane = threadIdx.x & 31, row = (warp & 3) * 32 + lane;
@@ -264,14 +309,14 @@ __device__ __noinline__ uint32_t redo_down(const GemmArgs &a, int f, int kb0, in
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         acc[n] = 0.0f;
-    for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        int e, c;
-        tile_of<kFewDown>(a, w, U, kb, e, c);
+    for (int kb = 0; kb < n_blocks; ++kb) {
+        const Block B = block_of<kFewDown, NT>(a, w, U, kb);
+        const int e = B.e, c = B.c;
         if (warp == kSumWarps) {
             if (elect_one()) {
                 mbar_arrive_expect_tx(bars, kTile + NT * 128);
                 tma_3d(ring, e < 0 ? &a.sa : &a.wa, c * kBlk, U.f * kBlk, e < 0 ? 0 : e, bars);
-                tma_2d(ring + kTile, &a.xm, 0, kb * NT, bars);
+                tma_2d(ring + kTile, &a.xm, 0, B.item * NT, bars);
             }
             __syncwarp();
         }
@@ -294,7 +339,7 @@ __device__ __noinline__ uint32_t redo_down(const GemmArgs &a, int f, int kb0, in
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const int n = ch * 16 + j;
-                    const float x = n < U.n ? a.hs[(int64_t)kb * NT + n] : __uint_as_float(kNotChosen);
+                    const float x = n < U.n ? a.hs[(int64_t)B.item * NT + n] : __uint_as_float(kNotChosen);
                     if (__float_as_uint(x) != kNotChosen)
                         acc[n] = fmaf(tmem_value(r[j]), x * sw + 0.0f, acc[n]);
                 }
@@ -354,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
     volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
     volatile uint64_t *redo = reinterpret_cast<volatile uint64_t *>(tslot + 2);  // kFewDown: units to do again
     uint32_t *any_redo = tslot + 4;                                              // some of the cluster's
+    volatile int *sh0 = reinterpret_cast<volatile int *>(tslot + 5);             // Walk::sh0
     uint64_t *rbars = reinterpret_cast<uint64_t *>(tslot + 6);                   // and the barriers of that
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const uint32_t rank = cl > 1 ? cluster_rank() : 0;
@@ -378,6 +424,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
                 mbar_init(rbars + i, 1);
         *redo = 0;
         *any_redo = 0;
+        if (MODE == kFewDown)
+            *sh0 = first_block(a, a.E, rank);
         *abort = 0;
         fence_mbar_init();
     }
@@ -413,13 +461,40 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
         int n = 0;
         for (int i = 0; i < kMaxExperts / 32; ++i)
             n += __popc(mask[i]);
-        for (int e = tid; e < a.E; e += kThreads)
-            if (mask[e >> 5] >> (e & 31) & 1) {
-                int at = __popc(mask[e >> 5] & ((1u << (e & 31)) - 1));
-                for (int i = 0; i < e >> 5; ++i)
-                    at += __popc(mask[i]);
-                act[at] = e;
+        auto place = [&](const uint32_t *bits, int e) {  // of expert e among those with a bit
+            int at = __popc(bits[e >> 5] & ((1u << (e & 31)) - 1));
+            for (int i = 0; i < e >> 5; ++i)
+                at += __popc(bits[i]);
+            return at;
+        };
+        if (MODE == kFewGateUp) {
+            for (int e = tid; e < a.E; e += kThreads)
+                if (mask[e >> 5] >> (e & 31) & 1)
+                    act[place(mask, e)] = e;
+        } else {
+            // of an expert's IB blocks this rank has q, or q + 1 where its first one is below IB - q cl
+            const int q = div_cl(a, a.IB), more = a.IB - q * cl;
+            uint32_t *extra = mask + kMaxExperts / 32, *list = extra + kMaxExperts / 32;
+            for (int i = warp; i < kMaxExperts / 32; i += kThreads / 32) {
+                const uint32_t v = __ballot_sync(0xFFFFFFFFu, first_block(a, i * 32 + lane, rank) < more);
+                if (lane == 0)
+                    extra[i] = v & mask[i];
             }
+            __syncthreads();
+            for (int e = tid; e < a.E; e += kThreads)
+                if (mask[e >> 5] >> (e & 31) & 1) {
+                    const int at = place(mask, e), before = place(extra, e);
+                    int c = first_block(a, e, rank), to = q * at + before;
+                    act[at] = e | before << 16;
+                    for (; c < a.IB && to < list_room(NT); c += cl)
+                        list[to++] = list_entry(e, at, c);
+                }
+            w.n_routed = q * n;
+            for (int i = 0; i < kMaxExperts / 32; ++i)
+                w.n_routed += __popc(extra[i]);
+            w.rank = rank;
+            w.list = list;
+        }
         w.n_act = n;
         w.act = act;
         w.idx = idx;
@@ -443,10 +518,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
         w.n_units = w.tt[a.E] * w.FT;
     w.first = blockIdx.x / cl;
     w.step = gridDim.x / cl;
-    {
-        const int n = MODE == kFewDown ? w.n_act * a.IB + a.SB : KB;
-        w.kb0 = (int)((int64_t)n * rank / cl);
-        w.kb1 = (int)((int64_t)n * (rank + 1) / cl);
+    if (MODE == kFewDown) {
+        // (by way of shared memory: known to be the same in all threads, it made 64 tokens of top-8 of 256
+        // experts take 485 us instead of 462)
+        w.sh0 = *sh0;
+        w.kb1 = w.n_routed + (w.sh0 < a.SB ? div_cl(a, a.SB - w.sh0 + cl - 1) : 0);
+    } else {
+        w.kb0 = KB * rank / cl;
+        w.kb1 = KB * (rank + 1) / cl;
     }
     const uint32_t tmem = *tslot;
 
@@ -457,19 +536,19 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
             // compiler issues each copy, or MMA, in a loop over lanes)
             auto weights = [&](const Unit &U, int kb, int s) {
                 uint8_t *st = ring + s * kStage;
-                int e, c;
-                tile_of<MODE>(a, w, U, kb, e, c);
-                const bool sh = FEW && e < 0;
-                tma_3d(st, sh ? &a.sa : &a.wa, c * kBlk, U.f * kBlk, sh ? 0 : e, full + s);
+                const Block B = block_of<MODE, NT>(a, w, U, kb);
+                const bool sh = FEW && B.e < 0;
+                tma_3d(st, sh ? &a.sa : &a.wa, B.c * kBlk, U.f * kBlk, sh ? 0 : B.e, full + s);
                 if (NMAT == 2)
-                    tma_3d(st + kTile, sh ? &a.sb : &a.wb, c * kBlk, U.f * kBlk, sh ? 0 : e, full + s);
+                    tma_3d(st + kTile, sh ? &a.sb : &a.wb, B.c * kBlk, U.f * kBlk, sh ? 0 : B.e, full + s);
             };
             auto tokens = [&](const Unit &U, int kb, int s) {
                 uint8_t *st = ring + s * kStage + NMAT * kTile;
+                const Block B = block_of<MODE, NT>(a, w, U, kb);
                 if (MODE == kFewDown)
-                    tma_2d(st, &a.xm, 0, kb * NT, full + s);
+                    tma_2d(st, &a.xm, 0, B.item * NT, full + s);
                 else
-                    tma_2d(st, &a.xm, kb * kBlk, U.tok0, full + s);
+                    tma_2d(st, &a.xm, B.c * kBlk, U.tok0, full + s);
             };
             constexpr uint32_t bytes = NMAT * kTile + NT * 128;
             int early = 0;  // stages whose weights were requested before the launch's inputs were complete
@@ -555,8 +634,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
                     for (int j = 0; j < NL; ++j)
                         x[i][j] = 0.0f;
                     if (kb < w.kb1) {
-                        int e, c;
-                        tile_of<MODE>(a, w, U, kb, e, c);
+                        const Block B = block_of<MODE, NT>(a, w, U, kb);
+                        const int e = B.e, c = B.c;
                         if (FEW && e < 0) {
                             const int64_t at = (int64_t)U.f * (MODE == kFewDown ? a.SB : KB) + c;
                             s0[i] = __ldg(a.ssa + at);
@@ -572,8 +651,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
                         for (int j = 0; j < NL; ++j) {
                             const int n = lane + 32 * j;
                             if (n < U.n)  // (written by the launch before: not through the read-only path)
-                                x[i][j] = MODE == kFewDown ? a.hs[(int64_t)kb * NT + n]
-                                                           : a.sx[(U.tok0 + n) * a.sx_r + kb * a.sx_b];
+                                x[i][j] = MODE == kFewDown ? a.hs[(int64_t)B.item * NT + n]
+                                                           : a.sx[(U.tok0 + n) * a.sx_r + c * a.sx_b];
                         }
                     }
                 }
@@ -735,7 +814,8 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
             uint32_t parity = 0;
             for (int u = w.first, k = 0; u < w.n_units && !*abort; u += w.step, ++k)
                 if (todo >> k & 1)
-                    parity = redo_down<NT>(a, u, w.kb0, w.kb1, w.act, w.n_act, ring, stage, rbars, parity, tmem, abort);
+                    parity = redo_down<NT>(a, u, w.kb1, w.n_routed, w.act, w.list, w.n_act, w.sh0, rank, ring, stage, rbars,
+                                           parity, tmem, abort);
         }
     };
     if (MODE == kFewDown && cl == 1) {

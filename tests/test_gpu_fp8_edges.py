@@ -113,3 +113,43 @@ def test_moe_non_finite_weights_reach_their_tokens_alone(T, D, I, S, dtype):
     run(1, ws[2][1], (1, 2, nb(I) - 1), math.nan, slice(256, 384))
     run(4, ws[0][0].view(torch.uint8), (4, 11, 300), 0x7F, slice(None))
     run(0, ws[1][1], (0, 0, 2), math.nan, slice(None))
+
+
+@pytest.mark.parametrize("T,E,K,D,I,S", [
+    (2, 16, 4, 2816, 384, 256), (5, 40, 2, 1040, 640, 0), (31, 32, 4, 2816, 704, 300), (20, 12, 3, 4096, 1024, 128),
+    (60, 24, 2, 2816, 256, 64), (64, 9, 3, 640, 130, 130), (90, 16, 4, 640, 384, 128)])
+def test_moe_bits_do_not_depend_on_the_other_tokens(T, E, K, D, I, S):
+    """A token has the same bits whatever the other tokens hold and whichever experts they choose."""
+    import torch
+    layer, _, _ = make_layer(E, D, I, S, 230, K, mx.MX_SILU, "f32")
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, T))
+    x, (idx, wts) = torch.randn(T, D, device="cuda", generator=gen(231)), routing(T, E, K, 232)
+    first, out = torch.empty_like(x), torch.empty_like(x)
+    mx.fp8_moe_forward(x, idx, wts, layer, first, work)
+    same = [0, T - 1] if T > 2 else [1]
+    for i in range(4):
+        y, (oidx, owts) = torch.randn(T, D, device="cuda", generator=gen(240 + i)), routing(T, E, K, 250 + i, skew=float(i))
+        if i == 3:
+            oidx.fill_(-1)  # (the others with no expert at all)
+        for t in same:
+            y[t], oidx[t], owts[t] = x[t], idx[t], wts[t]
+        mx.fp8_moe_forward(y, oidx, owts, layer, out, work)
+        mx.workspace_check(work, torch.cuda.current_stream())
+        assert torch.equal(out[same], first[same])
+
+
+def test_moe_thousands_of_hidden_blocks():
+    """More hidden blocks to a CTA of down than its list has room for."""
+    import torch
+    T, E, K, D, I, S = 9, 2, 1, 128, 530000, 128
+    layer, ws, sh = make_layer(E, D, I, S, 233, K, mx.MX_SILU, "f32")
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, T))
+    x, (idx, wts) = torch.randn(T, D, device="cuda", generator=gen(234)), routing(T, E, K, 235)
+    idx[0], idx[1] = 0, 1
+    first, out = torch.empty_like(x), torch.empty_like(x)
+    mx.fp8_moe_forward(x, idx, wts, layer, first, work)
+    mx.workspace_check(work, torch.cuda.current_stream())
+    check_layer(first, x, idx, wts, ws, sh, mx.MX_SILU, 0.5, None, K)
+    idx[2:] = 1 - idx[2:]
+    mx.fp8_moe_forward(x, idx, wts, layer, out, work)
+    assert torch.equal(out[:2], first[:2])
