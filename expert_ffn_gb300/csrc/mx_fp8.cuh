@@ -213,6 +213,30 @@ __device__ __forceinline__ float scale_of(float amax, int pow2)
     return pow2 ? __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0xFF800000u) : s;
 }
 
+// Quotients of a hidden block, x / s for its scale s: outside the plain range both are taken
+// times a power of two that brings them there, which leaves the quotient as it is (but for what
+// quantises to 0 either way; an infinite or NaN scale makes it NaN).
+struct Quotient {
+    float s, r, m;
+
+    __device__ __forceinline__ Quotient(float amax, float scale)
+    {
+        m = plain_range(amax) ? 1.0f : amax < 1.0f ? 1.2676506e30f : 9.094947e-13f;  // 2^100, 2^-40
+        s = scale * m;
+        r = __frcp_rn(s);
+    }
+    // Two values that have been taken times m, as two e4m3 bytes.
+    __device__ __forceinline__ uint32_t e4m3_of(float lo, float hi) const
+    {
+        const uint64_t p = pair_f32(lo, hi), r2 = pair_f32(r, r);
+        uint64_t q = mul_f32x2(p, r2), rem = p;
+        fma_f32x2(rem, q, pair_f32(-s, -s));
+        fma_f32x2(q, rem, r2);
+        unpair_f32(q, lo, hi);
+        return e4m3_x2(lo, hi);
+    }
+};
+
 // Quantise pairs of values of a block whose largest magnitude has the bits `amax`:
 // e[j] = two e4m3 bytes.  Returns the scale.
 template <int N>

@@ -238,10 +238,9 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Walk &w, const Uni
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 mx = max(mx, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-            const float s = scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, mx)), 0);
-            // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
-            const float inv = __frcp_rn(s);
-            e = e4m3_x2(h[0] * inv, h[1] * inv) | e4m3_x2(h[2] * inv, h[3] * inv) << 16;
+            const float top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, mx)), s = scale_of(top, 0);
+            const Quotient q(top, s);
+            e = q.e4m3_of(h[0] * q.m, h[1] * q.m) | q.e4m3_of(h[2] * q.m, h[3] * q.m) << 16;
             sc = s * wt + 0.0f;
         }
         const int64_t at = (int64_t)U.item * NT + n;

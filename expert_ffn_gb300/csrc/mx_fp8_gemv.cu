@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(kGuWarps * 32, 4) gemv_gate_up(const GemvArgs 
     for (int k = 0; k < kGuCluster; ++k)
         m = max(m, __float_as_uint(am[k]));
     const float s = scale_of(__uint_as_float(m), 0);
-    // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
-    a.h8[(int64_t)blk * kBlk + rank * 16 + r] = (uint8_t)e4m3_x2(h * __frcp_rn(s), 0.0f);
+    const Quotient q(__uint_as_float(m), s);
+    a.h8[(int64_t)blk * kBlk + rank * 16 + r] = (uint8_t)q.e4m3_of(h * q.m, 0.0f);
     if (rank == 0 && r == 0)  // (the routing weight joins the scale)
         a.hf[blk] = slot < 0 ? s : s * __ldg(a.wts + slot);
 }

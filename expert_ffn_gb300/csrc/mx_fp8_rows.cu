@@ -388,15 +388,18 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     break;
                 m = max(m, __float_as_uint(am[(wg ^ 1) * 128 + row]));
                 const float s = scale_of(__uint_as_float(m), 0);
-                // (by a reciprocal: h is a rounded sum, on no border between two e4m3 numbers)
-                const float inv = __frcp_rn(s);
+                const Quotient q(__uint_as_float(m), s);
+                if (q.m != 1.0f)
+#pragma unroll
+                    for (int i = 0; i < NC / 2; ++i)
+                        acc[i] *= q.m;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t e[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float *h = acc + 16 * c + 4 * i;
-                        e[i] = e4m3_x2(h[0] * inv, h[1] * inv) | e4m3_x2(h[2] * inv, h[3] * inv) << 16;
+                        e[i] = q.e4m3_of(h[0], h[1]) | q.e4m3_of(h[2], h[3]) << 16;
                     }
                     mine[piece(lane, c)] = make_uint4(e[0], e[1], e[2], e[3]);
                 }

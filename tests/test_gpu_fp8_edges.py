@@ -153,3 +153,57 @@ def test_moe_thousands_of_hidden_blocks():
     idx[2:] = 1 - idx[2:]
     mx.fp8_moe_forward(x, idx, wts, layer, out, work)
     assert torch.equal(out[:2], first[:2])
+
+
+# --------------------------------------------- hidden values on a border of e4m3
+
+TIES = {17: 16, 19: 20, 21: 20, 23: 24, 25: 24, 27: 28, 29: 28, 31: 32}  # between two e4m3 numbers: the even one
+
+
+@pytest.mark.parametrize("act", [mx.MX_SILU, mx.MX_GELU_TANH])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 5, 40, 90])
+@pytest.mark.parametrize("sigma", [262085 / 65536, 262080 / 65536])
+def test_moe_hidden_values_are_quantised_by_division(T, dtype, act, sigma):
+    """Hidden values that are exactly sigma times a number halfway between two e4m3 numbers, in a block whose scale is
+    exactly sigma: their quotients lie on the border and go to the even number.  (The product with the rounded 1 /
+    sigma lands beside it: above for the first sigma, below for the second, or the other way round.)"""
+    import torch
+    f8 = torch.float8_e4m3fn
+    D = I = 128
+    gate, up, down = (torch.zeros(1, 128, 128, device="cuda") for _ in range(3))
+    up[0, :, 2] = 1.0
+    gate[0, 0, 1] = 28.0  # 448: the block's largest
+    want = torch.zeros(128, device="cuda")
+    want[0] = 448.0
+    for j, (tie, even) in enumerate(TIES.items()):
+        gate[0, j + 1, 1], gate[0, j + 1, 2], want[j + 1] = 1.0, tie - 16.0, even
+    down[0].fill_diagonal_(1.0)
+    one = torch.ones(1, 1, 1, device="cuda")
+    layer = mx.Fp8Layer((gate.to(f8), one * sigma), (up.to(f8), one), (down.to(f8), one), top_k=1,
+                        act_dtype=mx.MX_BF16 if dtype == "bf16" else mx.MX_F32, activation=act)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = torch.zeros(T, D, device="cuda", dtype=dt)
+    x[:, 0], x[:, 1], x[:, 2] = 448.0, 16.0, 1.0  # (quantised by the scale 1: themselves)
+    out = torch.empty_like(x)
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, T))
+    mx.fp8_moe_forward(x, torch.zeros(T, 1, device="cuda", dtype=torch.int32), torch.ones(T, 1, device="cuda"), layer, out, work)
+    assert torch.equal(out, (want * sigma).to(dt).expand(T, D))
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 90])
+@pytest.mark.parametrize("power", [-92, 105])
+def test_moe_hidden_values_of_any_magnitude(T, power):
+    """Hidden values beyond the range in which their quotients come from a reciprocal as they are."""
+    import torch
+    D, I, E, K = 320, 200, 6, 3
+    layer, ws, _ = make_layer(E, D, I, 0, 265, K, mx.MX_GELU_TANH, "f32")
+    ws[1][1].mul_(2.0 ** power)
+    ws[2][1].mul_(2.0 ** -power)
+    x = torch.randn(T, D, device="cuda", generator=gen(266))
+    idx, wts = routing(T, E, K, 267)
+    out = torch.empty_like(x)
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, T))
+    mx.fp8_moe_forward(x, idx, wts, layer, out, work)
+    mx.workspace_check(work, torch.cuda.current_stream())
+    check_layer(out, x, idx, wts, ws, None, mx.MX_GELU_TANH, 0.5, None, K)
