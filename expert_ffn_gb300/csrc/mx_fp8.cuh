@@ -213,6 +213,19 @@ __device__ __forceinline__ float scale_of(float amax, int pow2)
     return pow2 ? __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0xFF800000u) : s;
 }
 
+// The same for a pair, in e4m3 (two bytes), from pairs of s and -r.  By way of -(x / s), whose
+// sign is flipped at the end: the sum that leaves the quotient of a negative zero would make it
+// a positive one, this one keeps it.
+__device__ __forceinline__ uint32_t e4m3_quotients(uint64_t x, uint64_t s, uint64_t nr)
+{
+    uint64_t q = mul_f32x2(x, nr);
+    fma_f32x2(x, q, s);
+    fma_f32x2(q, x, nr);
+    float lo, hi;
+    unpair_f32(q, lo, hi);
+    return e4m3_x2(lo, hi) ^ 0x8080u;
+}
+
 // Quotients of a hidden block, x / s for its scale s: outside the plain range both are taken
 // times a power of two that brings them there, which leaves the quotient as it is (but for what
 // quantises to 0 either way; an infinite or NaN scale makes it NaN).
@@ -225,15 +238,11 @@ struct Quotient {
         s = scale * m;
         r = __frcp_rn(s);
     }
+
     // Two values that have been taken times m, as two e4m3 bytes.
     __device__ __forceinline__ uint32_t e4m3_of(float lo, float hi) const
     {
-        const uint64_t p = pair_f32(lo, hi), r2 = pair_f32(r, r);
-        uint64_t q = mul_f32x2(p, r2), rem = p;
-        fma_f32x2(rem, q, pair_f32(-s, -s));
-        fma_f32x2(q, rem, r2);
-        unpair_f32(q, lo, hi);
-        return e4m3_x2(lo, hi);
+        return e4m3_quotients(pair_f32(lo, hi), pair_f32(s, s), pair_f32(-r, -r));
     }
 };
 
@@ -245,25 +254,18 @@ __device__ __forceinline__ float quantize_pairs(const uint64_t (&p)[N], uint32_t
     const float top = __uint_as_float(amax), s = scale_of(top, pow2);
     if (plain_range(top)) {
         const float r = __frcp_rn(s);
-        const uint64_t r2 = pair_f32(r, r), ns2 = pair_f32(-s, -s);
+        const uint64_t s2 = pair_f32(s, s), nr2 = pair_f32(-r, -r);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            uint64_t q = mul_f32x2(p[j], r2), rem = p[j];
-            fma_f32x2(rem, q, ns2);
-            fma_f32x2(q, rem, r2);
-            float lo, hi;
-            unpair_f32(q, lo, hi);
-            e[j] = e4m3_x2(lo, hi);
-        }
+        for (int j = 0; j < N; ++j)
+            e[j] = e4m3_quotients(p[j], s2, nr2);
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            e[j] = 0;  // (a block of zeros, as padding has them)
-            if (top != 0.0f) {
-                float lo, hi;
-                unpair_f32(p[j], lo, hi);
-                e[j] = e4m3_x2(divide_any(lo, s), divide_any(hi, s));
-            }
+            float lo, hi;
+            unpair_f32(p[j], lo, hi);
+            if (top != 0.0f)  // (not a block of zeros, as padding has them)
+                lo = divide_any(lo, s), hi = divide_any(hi, s);
+            e[j] = e4m3_x2(lo, hi);
         }
     }
     return s;

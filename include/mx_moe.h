@@ -401,7 +401,7 @@ typedef struct {
 /*
  * Quantise activations: for each block of 128 columns of a row, a = max |x|,
  *   s = max(fl32(a / 448), 2^-126);  with pow2 the smallest power of two >= s;
- *   q = e4m3(fl32(x / s)), round to nearest, ties to even.
+ *   q = e4m3(fl32(x / s)), round to nearest, ties to even; a zero keeps its sign.
  * A block with a NaN or an infinity gets that as its scale and dequantises to
  * NaN.
  *   x      device [rows][cols] of `dtype` (mx_dtype), row pitch ldx elements

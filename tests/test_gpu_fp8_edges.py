@@ -155,6 +155,35 @@ def test_moe_thousands_of_hidden_blocks():
     assert torch.equal(out[:2], first[:2])
 
 
+# ------------------------------------------------------------------ signs of zero
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pitch", [256, 259])
+def test_quantize_keeps_the_sign_of_zero(dtype, pow2, pitch):
+    """Byte for byte e4m3(x / s): a negative zero, and a negative value that rounds to zero, is 0x80 in a block of any
+    magnitude, of zeros as well."""
+    import torch
+    x = torch.randn(40, pitch, device="cuda", generator=gen(260))[:, :256]
+    x[:, ::3] = 0.0
+    x[:, 1::3] *= torch.where(torch.rand(40, 85, device="cuda", generator=gen(261)) < 0.5, 1e-7, 1.0)
+    x[:, 2::5] = -0.0
+    x[5, :128] = -0.0
+    x[6, :128], x[6, :64] = 0.0, -0.0
+    x[7] *= 2.0 ** -128
+    x[8] *= 2.0 ** -90
+    x[9] *= 2.0 ** 110
+    x = x.to(torch.bfloat16) if dtype == "bf16" else x
+    q = torch.empty(40, 256, device="cuda", dtype=torch.float8_e4m3fn)
+    s = torch.empty(40, 2, device="cuda")
+    mx.fp8_quantize(x, q, s, pow2=pow2)
+    rq, rs = ref_quantize(x.double(), pow2)
+    want = rq.float().to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(s.double(), rs)
+    assert (want == 0x80).any() and (want == 0).any()
+    assert torch.equal(q.view(torch.uint8), want)
+
+
 # --------------------------------------------- hidden values on a border of e4m3
 
 TIES = {17: 16, 19: 20, 21: 20, 23: 24, 25: 24, 27: 28, 29: 28, 31: 32}  # between two e4m3 numbers: the even one
