@@ -126,6 +126,8 @@ struct GemvArgs {
 };
 cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s);
 cudaError_t launch_gemv_moe(const GemvArgs &a, cudaStream_t s);
+constexpr int kGemvMoeCols = 32768;  // largest d_model of launch_gemv_moe
+int gemv_moe_blocks(int K);          // hidden blocks that its first launch works on at one time (0: none)
 
 struct QuantArgs {
     const void *x;       // [rows][cols]

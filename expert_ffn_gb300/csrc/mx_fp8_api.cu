@@ -400,13 +400,18 @@ void matrices(GemmArgs &g, const mx_fp8_matrix &a, const mx_fp8_matrix *b)
     g.swb = b ? b->scales : nullptr;
 }
 
-// One token by two launches (mx_fp8_gemv.cu), when all CTAs of the first run at once: 520
-// CTAs (d_model 2816) take 18.6 us and the few-token form 21.7, 576 (4096) 24.5 and 29; two
-// experts of 14336 hidden rows, 1792 CTAs, 67 and 61.
+// One token by two launches (mx_fp8_gemv.cu), when all hidden blocks are worked on at one time
+// (four CTAs to an SM up to d_model 7680, then three, two from 15 K on), and while each CTA's
+// own quantisation of the token is short: d_model 2816, 65 blocks, take 18.6 us and by the
+// few-token form 21.7, 4096 and 72 blocks 25.2 and 28.1, 5120 and 72 32.2 and 32.3, 76 39.0 and
+// 33.2; 7168, 40 blocks 30.8 and 31.8, 56 38.5 and 35.7; 16384, 32 blocks 47.6 and 55.7, 40
+// 60.9 and 59.2, 56 87 and 69; 32768, 32 blocks 88.9 and 99.9, 40 137 and 104.  256 experts of
+// 1024 with a shared one of 4096, d_model 4096, are 96 blocks, 32.5 and 32.8.
 bool one_token(const mx_fp8_layer *L, int T)
 {
-    const int64_t units = L->top_k * (int64_t)blocks(L->gate.rows) + (L->shared_gate.w ? blocks(L->shared_gate.rows) : 0);
-    return T == 1 && units * (kBlk / 16) <= 4 * num_sms() && L->gate.cols <= 32768;
+    const int64_t D = L->gate.cols;
+    const int64_t n = L->top_k * (int64_t)blocks(L->gate.rows) + (L->shared_gate.w ? blocks(L->shared_gate.rows) : 0);
+    return T == 1 && D <= kGemvMoeCols && n <= (D <= 5120 ? 76 : 40) && n <= gemv_moe_blocks((int)D);
 }
 
 mx_status run_gemv(const void *x, const int32_t *idx, const float *wts, const mx_fp8_layer *L,

@@ -25,6 +25,8 @@
 // here, 8 tokens 62 and 316, where the same expert's blocks made long chains).
 #include "mx_fp8.cuh"
 
+#include <mutex>
+
 namespace mx {
 namespace fp8 {
 
@@ -524,22 +526,53 @@ cudaError_t launch_gemv(const GemvArgs &a, cudaStream_t s)
     return cudaGetLastError();
 }
 
-cudaError_t launch_gemv_moe(const GemvArgs &a, cudaStream_t s)
+namespace {
+
+// Gate/up of one token: a cluster for each of n hidden blocks.
+cudaError_t gate_up_config(int K, int n, cudaLaunchConfig_t &c, cudaLaunchAttribute &at)
 {
-    const size_t smem = kGuRing + kGuWarps * ((blocks(a.K) + kGuWarps - 1) / kGuWarps) * (kBlk + 4);
-    cudaError_t e = smem_optin((const void *)gemv_gate_up, smem);
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchConfig_t c{};
-    cudaLaunchAttribute at;
-    c.gridDim = dim3((blocks(a.S) + a.topk * blocks(a.I)) * kGuCluster);
+    c = cudaLaunchConfig_t{};
+    c.gridDim = dim3(n * kGuCluster);
     c.blockDim = dim3(kGuWarps * 32);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
+    c.dynamicSmemBytes = kGuRing + kGuWarps * ((blocks(K) + kGuWarps - 1) / kGuWarps) * (kBlk + 4);
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim = {kGuCluster, 1, 1};
     c.attrs = &at;
     c.numAttrs = 1;
+    return smem_optin((const void *)gemv_gate_up, c.dynamicSmemBytes);
+}
+
+}  // namespace
+
+int gemv_moe_blocks(int K)
+{
+    constexpr int kDevices = 64, kSlices = kGemvMoeCols / kBlk / kGuWarps + 1;
+    static std::mutex mu;
+    static int16_t cache[kDevices][kSlices] = {{0}};  // plus one
+    const int slice = (blocks(K) + kGuWarps - 1) / kGuWarps;
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices || slice >= kSlices)
+        return 0;
+    std::lock_guard<std::mutex> g(mu);
+    if (!cache[dev][slice]) {
+        cudaLaunchConfig_t c;
+        cudaLaunchAttribute at;
+        if (gate_up_config(K, 1, c, at) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, gemv_gate_up, &c) != cudaSuccess)
+            return 0;
+        cache[dev][slice] = (int16_t)(n + 1);
+    }
+    return cache[dev][slice] - 1;
+}
+
+cudaError_t launch_gemv_moe(const GemvArgs &a, cudaStream_t s)
+{
+    cudaLaunchConfig_t c;
+    cudaLaunchAttribute at;
+    cudaError_t e = gate_up_config(a.K, blocks(a.S) + a.topk * blocks(a.I), c, at);
+    if (e != cudaSuccess)
+        return e;
+    c.stream = s;
     if ((e = cudaLaunchKernelEx(&c, gemv_gate_up, a)) != cudaSuccess)
         return e;
     c.gridDim = dim3((a.K + 15) / 16);

@@ -456,9 +456,10 @@ typedef struct {
  *   topk_idx  device int32 [T][top_k], topk_w device fp32 [T][top_k], as
  *            mx_moe_route writes them.  An index outside [0, n_experts)
  *            contributes nothing; one that a token repeats counts each time.
- * Up to 64 tokens the layer reads each selected expert's weights once: one token in
- * two launches, more in three.  Above, it runs as grouped products over the experts'
- * rows.
+ * Up to 64 tokens the layer reads each selected expert's weights once, in three
+ * launches; one token takes two while its hidden blocks are few enough to be worked on
+ * at one time (an expert that it repeats is read each time).  Above 64 tokens it runs
+ * as grouped products over the experts' rows.
  */
 MX_API mx_status mx_fp8_moe_forward(const void *x, int T, const int32_t *topk_idx, const float *topk_w,
                                     const mx_fp8_layer *layer, const void *residual, void *out, void *stream,

@@ -236,3 +236,22 @@ def test_moe_hidden_values_of_any_magnitude(T, power):
     mx.fp8_moe_forward(x, idx, wts, layer, out, work)
     mx.workspace_check(work, torch.cuda.current_stream())
     check_layer(out, x, idx, wts, ws, None, mx.MX_GELU_TANH, 0.5, None, K)
+
+
+@pytest.mark.parametrize("D,blocks,two", [(2816, 65, True), (4096, 72, True), (5120, 40, True), (5120, 80, False),
+                                          (8192, 24, True), (8192, 56, False), (16384, 16, True), (16384, 56, False),
+                                          (32768, 16, True), (32768, 40, False), (33024, 8, False)])
+def test_moe_one_token_takes_two_launches_while_its_blocks_run_at_once(D, blocks, two):
+    """The two launches leave the workspace's quantised token alone, the three write it.  Right either way."""
+    import torch
+    K = 4 if blocks % 4 == 0 else 5
+    layer, ws, _ = make_layer(5, D, 128 * blocks // K, 0, 290, K, mx.MX_SILU, "bf16")
+    x = torch.randn(1, D, device="cuda", generator=gen(291)).bfloat16()
+    idx, wts = routing(1, 5, K, 292)
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, 1))
+    work[256:256 + D] = 0x7F
+    out = torch.empty_like(x)
+    mx.fp8_moe_forward(x, idx, wts, layer, out, work)
+    mx.workspace_check(work, torch.cuda.current_stream())
+    assert (work[256:256 + D] == 0x7F).all().item() == two
+    check_layer(out, x, idx, wts, ws, None, mx.MX_SILU, 0.5, None, K)
