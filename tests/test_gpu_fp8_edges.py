@@ -238,6 +238,70 @@ def test_moe_hidden_values_of_any_magnitude(T, power):
     check_layer(out, x, idx, wts, ws, None, mx.MX_GELU_TANH, 0.5, None, K)
 
 
+# ----------------------------------------------------- precision of fp32 products
+
+@pytest.mark.parametrize("m,n,k", [(1, 2112, 2816), (8, 1000, 4096), (40, 1024, 2816), (64, 704, 4096), (500, 1024, 2816),
+                                   (600, 2600, 1037)])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_fp32_products_keep_fp32(m, n, k, grouped):
+    """In the 2-norm.  Were each of a block's 128 sums truncated (a step of 2^-23) in the direction of the running sum,
+    which grows like the square root of the terms, the block would be off by 2^-23 sum_i sqrt(i) / sqrt(128) = 2^-23 85
+    = 2^-16.6 of its deviation; blocks add as independent, and their B sums in fp32 are off by half a step of at most the
+    whole each, B 2^-24 <= 2^-18.9 for B <= 33.  Together below 2^-16 of the results' norm, a hundredth of what sums in
+    bf16 (2^-8, or 2^-9.6 in the norm) would leave."""
+    import torch
+    q, s = make_rows(m, k, 270)
+    w, ws = make_weight(1, n, k, 271)
+    out = torch.empty(m, n, device="cuda")
+    if grouped:
+        offsets = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+        mx.fp8_grouped_matmul(q, s, offsets, mx.Fp8Weight(w, ws), out, workspace(256))
+    else:
+        mx.fp8_matmul(q, s, mx.Fp8Weight(w[0], ws[0]), out, workspace(256))
+    exact = rows_value(q, s) @ weight_value(w[0], ws[0]).T
+    assert (out.double() - exact).norm() <= 2.0 ** -16 * exact.norm()
+
+
+# --------------------------------------------------------------------- one token
+
+def test_moe_one_token_in_place_and_captured():
+    """out may be x or the residual itself; a captured and replayed call follows its buffers' values."""
+    import torch
+    E, K, D, I, S = 16, 4, 1040, 256, 200
+    layer, ws, sh = make_layer(E, D, I, S, 280, K, mx.MX_GELU_TANH, "bf16")
+    x = torch.randn(1, D, device="cuda", generator=gen(281)).bfloat16()
+    residual = torch.randn(1, D, device="cuda", generator=gen(282)).bfloat16()
+    idx, wts = routing(1, E, K, 283)
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, 1))
+    out = torch.empty_like(x)
+    mx.fp8_moe_forward(x, idx, wts, layer, out, work, residual=residual)
+    check_layer(out, x, idx, wts, ws, sh, mx.MX_GELU_TANH, 0.5, residual, K)
+    for target in ("x", "residual"):
+        a = {"x": x.clone(), "residual": residual.clone()}
+        mx.fp8_moe_forward(a["x"], idx, wts, layer, a[target], work, residual=a["residual"])
+        assert torch.equal(a[target], out)
+    side, buf = torch.cuda.Stream(), torch.empty_like(x)
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            mx.fp8_moe_forward(x, idx, wts, layer, buf, work, residual=residual)
+            mx.fp8_moe_forward(buf, idx, wts, layer, buf, work, residual=buf)
+    torch.cuda.synchronize()
+    for seed in (284, 285):
+        x.copy_(torch.randn(1, D, device="cuda", generator=gen(seed)))
+        i2, w2 = routing(1, E, K, seed)
+        idx.copy_(i2)
+        wts.copy_(w2)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        one, two = torch.empty_like(x), torch.empty_like(x)
+        mx.fp8_moe_forward(x, idx, wts, layer, one, work, residual=residual)
+        mx.fp8_moe_forward(one, idx, wts, layer, two, work, residual=one)
+        assert torch.equal(buf, two)
+
+
 @pytest.mark.parametrize("D,blocks,two", [(2816, 65, True), (4096, 72, True), (5120, 40, True), (5120, 80, False),
                                           (8192, 24, True), (8192, 56, False), (16384, 16, True), (16384, 56, False),
                                           (32768, 16, True), (32768, 40, False), (33024, 8, False)])
