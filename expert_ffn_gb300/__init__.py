@@ -473,6 +473,7 @@ class Fp8Layer:
 
     def __init__(self, gate, up, down, shared=None, top_k=8, act_dtype=MX_BF16, activation=MX_GELU_TANH,
                  layer_scalar=1.0):
+        _need(not shared or len(shared) == 3, "shared must be the (w, scales) pairs of gate, up and down")
         self.tensors = [gate, up, down, *(shared or [])]
         c = Fp8LayerStruct()
         names = ("gate", "up", "down", "shared_gate", "shared_up", "shared_down")
