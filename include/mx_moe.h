@@ -365,8 +365,9 @@ MX_API mx_status mx_moe_profile_read(double *ms, int *launches, int reset);
  *                                      sum_{c in block b} qx[r][c] qw[o][c]
  * with every sum in fp32 and one rounding to the output type.  The last block
  * of columns (and of weight rows) may be shorter than 128; any size from 1 on
- * is accepted.  A result does not depend on the values of the call's other rows,
- * nor on timing; the order of its sums goes by the call's sizes.
+ * is accepted.  A result does not depend on the call's other rows (in the layer:
+ * tokens, nor on the experts that these choose), nor on timing; the order of its
+ * sums goes by the call's sizes and, in the layer, by the token's own experts.
  *
  * All calls are asynchronous on `stream` (NULL: the legacy default stream) and
  * run on the current device, which has to own every buffer.  They allocate
@@ -451,11 +452,14 @@ typedef struct {
  *   xq = quantise(x_t)
  *   expert(x) = Wd quantise( act(Wg xq) * (Wu xq) )
  *   out[t] = residual[t] + layer_scalar * ( shared(x_t) + sum_k topk_w[t,k] * expert_{topk_idx[t,k]}(x_t) )
- *   x, residual, out  device [T][D]; residual nullable; out may be x or
- *            residual itself but may not overlap them otherwise
+ *   x, residual, out  device [T][D], 16-byte aligned; residual nullable; out
+ *            may be x or residual itself but may not overlap them otherwise
  *   topk_idx  device int32 [T][top_k], topk_w device fp32 [T][top_k], as
  *            mx_moe_route writes them.  An index outside [0, n_experts)
  *            contributes nothing; one that a token repeats counts each time.
+ * Every sum is in fp32 and rounded once, at the end, with one exception: above 64
+ * tokens with bf16 activations each expert's row is held in FP16 with a power of
+ * two for each 64 columns (11 significant bits) before the weighted sum.
  * Up to 64 tokens the layer reads each selected expert's weights once, in three
  * launches; one token takes two while its hidden blocks are few enough to be worked on
  * at one time (an expert that it repeats is read each time).  Above 64 tokens it runs

@@ -7,7 +7,7 @@ import math
 import pytest
 
 import expert_ffn_gb300 as mx
-from tests.test_gpu_fp8 import (check_layer, gen, make_layer, make_rows, make_weight, nb, ref_quantize, ref_scale, routing,
+from tests.test_gpu_fp8 import (check_layer, gen, make_layer, make_rows, make_weight, nb, ref_expert, ref_quantize, routing,
                                 rows_value, weight_value, workspace)
 
 pytestmark = pytest.mark.gpu
@@ -319,3 +319,38 @@ def test_moe_one_token_takes_two_launches_while_its_blocks_run_at_once(D, blocks
     mx.workspace_check(work, torch.cuda.current_stream())
     assert (work[256:256 + D] == 0x7F).all().item() == two
     check_layer(out, x, idx, wts, ws, None, mx.MX_SILU, 0.5, None, K)
+
+
+# ------------------------------------------------------ rows held between launches
+
+@pytest.mark.parametrize("T,E,K,D,I,S", [(403, 78, 1, 6, 1, 0), (323, 22, 5, 21, 1, 0), (361, 3, 1, 6, 5, 5),
+                                         (490, 2, 2, 2, 129, 28), (200, 8, 4, 130, 40, 64)])
+def test_moe_rows_of_many_bf16_tokens_keep_eleven_bits(T, E, K, D, I, S):
+    """Above 64 tokens with bf16 activations an expert's row is rounded to 11 bits, half a step of 2^-11 of it, before
+    the weighted sum: where rows cancel one another or the residual, that is what is left of the result."""
+    import torch
+    layer, ws, sh = make_layer(E, D, I, S, 300, K, mx.MX_SILU, "bf16")
+    x = torch.randn(T, D, device="cuda", generator=gen(301)).bfloat16()
+    residual = torch.randn(T, D, device="cuda", generator=gen(302)).bfloat16()
+    idx, wts = routing(T, E, K, 303)
+    out = torch.empty_like(x)
+    work = workspace(mx.fp8_moe_workspace_bytes(layer, T))
+    mx.fp8_moe_forward(x, idx, wts, layer, out, work, residual=residual)
+    xv = rows_value(*ref_quantize(x.double()))
+    y, tol, mag = (torch.zeros_like(xv) for _ in range(3))
+    for e in range(E):
+        t, k = torch.nonzero(idx == e, as_tuple=True)
+        if len(t):
+            p, b = ref_expert(xv[t], *((w[0][e], w[1][e]) for w in ws), mx.MX_SILU)
+            wt = wts[t, k].double()[:, None]
+            y.index_add_(0, t, p * wt)
+            tol.index_add_(0, t, b * wt.abs())
+            mag.index_add_(0, t, (p * wt).abs())
+    if sh:
+        p, b = ref_expert(xv, *((w[0][0], w[1][0]) for w in sh), mx.MX_SILU)
+        y, tol, mag = y + p, tol + b, mag + p.abs()
+    exact = 0.5 * y + residual.double()
+    # as check_layer, with 2^-11 of each row (and of its own error)
+    tol = 0.5 * (tol * (1 + 2.0 ** -11) + (2.0 ** -11 + (K + 4) * 2.0 ** -23) * mag)
+    tol = tol + 2.0 ** -22 * exact.abs() + 2.0 ** -23 * residual.double().abs() + 2.0 ** -8 * exact.abs()
+    assert ((out.double() - exact).abs() <= tol).all()
