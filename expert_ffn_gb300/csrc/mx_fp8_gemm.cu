@@ -24,12 +24,12 @@
 // in rank order, so the result does not depend on timing; which block is whose goes by
 // the sizes alone (first_block), so it does not depend on the other tokens' experts either.
 //
-// What bounds it: an MMA of 128 weight rows takes 129 cycles whatever its N up to 256, so
-// an SM streams 32 bytes of weights a cycle, 1.5 times its share of HBM: few tokens are
-// bound by HBM where there are enough units, and by the chain (launch, tables, pipeline
-// fill, cluster) where there are not.  64 x 4096 x 4096 takes 8.5 us (HBM 2.6, as a chain
-// about 6); the layer of 31 tokens of top-8 of 128 experts 48 us, of which the first 5 pass
-// before the quantised tokens are there, 20 in gate/up and 13 in down and its cluster.
+// What bounds it: an MMA of 128 weight rows x 32 columns takes 47 cycles up to N = 32 and 53
+// at 64, so an SM could stream 77 bytes of weights a cycle, three times its share of HBM: few
+// tokens are bound by HBM where there are enough units, and by the chain (launch, tables,
+// pipeline fill, eight blocks, cluster) where there are not.  64 x 4096 x 4096 takes 8.5 us (HBM
+// 2.6); the layer of 31 tokens of top-8 of 128 experts 48 us, of which the first 5 pass before
+// the quantised tokens are there.
 //
 // Every wait is bounded: a wait that gives up sets the caller's error word and
 // ends the CTA's work.
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
         // ----------------------------------------------------------- factors
         if (FEW)
             pdl_wait();
-        constexpr int NL = (NT + 31) / 32, BATCH = NT > 64 ? 2 : 4;
+        constexpr int NL = (NT + 31) / 32, BATCH = 4;
         int q = 0;
         uint32_t ph = 1;
         bool ok = true;

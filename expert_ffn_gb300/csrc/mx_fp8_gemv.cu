@@ -1,5 +1,5 @@
 // mx_fp8_gemv.cu -- the FP8 products for one to eight rows, and the MoE layer of
-// as many tokens in two launches.
+// one token in two launches.
 //
 // These read every weight once and do next to nothing with it, so what counts is
 // that all SMs have loads in flight from the first moment to the last, and how

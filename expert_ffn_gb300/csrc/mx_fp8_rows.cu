@@ -5,10 +5,8 @@
 //
 // Same mathematics as mx_fp8_gemm.cu, the other way round.  There the scale of a
 // token belongs to a TMEM column, so the summing warps read a vector of factors
-// from shared memory for every block (2 wavefronts per 16 bytes, measured), and
-// under a busy tensor core, which itself reads 96 of the 128 bytes a cycle that
-// shared memory delivers, that took 9 cycles a column.  Here a token is a TMEM
-// lane and its factor for a block one register.
+// from shared memory for every block, beside a tensor core that reads its operands
+// there.  Here a token is a TMEM lane and its factor for a block one register.
 //
 // A tile is 128 tokens x BN weight rows (kGateUp: 128 gate and the same 128 up rows).
 // Warps:
@@ -17,25 +15,25 @@
 //   8     TMA producer: token and weight tiles (SWIZZLE_128B)
 //   9     MMA: four tcgen05.mma (K = 32) a block, two TMEM buffers of BN columns
 //   10    factors: sx * sw of a block for each token (and 128 weight rows) into shared
-//         memory, beside the TMEM buffer; loaded by the summing threads themselves they
-//         cost 560 cycles of waiting in every block
-// A barrier or a load of shared memory takes 100 to 300 cycles while an MMA reads its
-// operands there (15 to 30 without), so a buffer has one barrier for its products and
-// its factors, and one for its release.
+//         memory, beside the TMEM buffer, so that the summing threads wait for no load from
+//         global memory
+// A 16-byte load of shared memory takes a warp 110 to 220 cycles beside the MMAs' own reads and
+// 73 without, so a buffer has one barrier for its products and its factors, and one for its
+// release.
 // Results pass through 2 KB of shared memory a warp, 16 of its 32 rows at a time, so
 // that they leave as whole lines.
 //
 // A launch may hold two problems, the routed experts' and the shared expert's: the
 // first is bound by HBM, the second by the tensor cores, and their tiles alternate.
 //
-// What bounds it: a block of 128 x 256 x 128 takes the tensor core 516 cycles (four MMAs,
-// 129 each, where N = 256 comes at the price of N = 16) and the summing warps about 640,
-// two sums to an FMA instruction; a tile's end costs them some 4000.  4096 x 4096 x 4096
-// takes 58 us, 2.35 PFLOP/s (without the sums 46, without the results 53); 32768 rows of
-// 256 experts x 1024 x 4096 211 us, 6.0 TB/s; gate/up and down of 4096 tokens of top-8
-// of those, with a shared expert of 4096, 480 and 330 us.  Tried and slower: a CTA pair (141 us
-// at 4096^3: each block's hand-over crosses the pair), 128 columns a tile in four buffers
-// (104 us), sixteen summing warps (66 us).
+// What bounds it: a block of 128 x 256 x 128 takes the tensor core 512 cycles (four MMAs of
+// 128); the summing warps follow it, two sums to an FMA instruction, but a tile's end is
+// theirs, and the two buffers let the MMAs run only two blocks ahead of it.  4096 x 4096 x 4096
+// takes 58 us, 2.35 PFLOP/s: 512 tiles on 152 SMs are four rounds for 3.4 of work, 34 us of
+// MMAs; without the sums it takes 54.  32768 rows of 256 experts x 1024 x 4096 take 210 us, 6.1
+// TB/s; gate/up and down of 4096 tokens of top-8 of those, with a shared expert of 4096, 480
+// and 330 us.  Tried and slower: a CTA pair (141 us at 4096^3: each block's hand-over crosses
+// the pair), 128 columns a tile in four buffers (104 us), sixteen summing warps (66 us).
 #include "mx_fp8_tc.cuh"
 
 namespace mx {
@@ -424,7 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 const int es = P.out_kind == kOutF32 ? 4 : 2, per = 16 / es;
                 if (P.out_kind == kOutF16) {
                     // FP16 of y 2^-k, k such that the row's largest finite of 64 columns is below 2^15, and
-                    // 2^k beside it: 11 significant bits, enough under a bf16 result, at half the bytes.
+                    // 2^k beside it: 11 significant bits at half the bytes.  Under a bf16 result, whose 8 bits
+                    // are what is left of them: the layer of 4096 tokens takes 994 us, with fp32 rows 1110; of
+                    // 700 tokens it is off by 1.675e-3 of its norm, with fp32 rows by 1.662e-3.
                     // (2^-112 counts as the smallest: 2^k and 2^-k stay normal.)  The maximum is taken on the
                     // bits one exponent up, where infinities and NaN, which keep themselves, are negative.
 #pragma unroll
