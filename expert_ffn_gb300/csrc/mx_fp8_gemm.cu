@@ -278,13 +278,13 @@ __device__ __forceinline__ void emit(const GemmArgs &a, const Walk &w, const Uni
     }
 }
 
-// Down of few tokens once more, for a unit with a NaN or an infinity in its sums: block by
+// Down of few tokens once more, for a unit with NaN or infinities in its first two columns: block by
 // block, each column with the experts that its token chose alone.  (The weights of an expert
 // meet the other tokens' zeros too, and zero times a NaN, or a factor of zero times an infinite
 // scale, is NaN.)  Columns that were right come out the same, bit for bit.  Apart from the
 // kernel's loops, where every instruction counts: with a predicate for each column 64 tokens of
 // top-8 of 128 experts took 189 us instead of 153, with a test in the factors alone 31 tokens
-// 127 instead of 115; looking at the first column's sums at the unit's end costs 0.4 us at most.
+// 127 instead of 115; looking at two columns' sums at the unit's end costs 0.4 us at most.
 // Leaves the sums [column][128 rows] in `stage`, of a cluster, or as results.  `bars`: three
 // barriers; parity: that of the next wait for them, which is returned.
 template <int NT>
@@ -737,10 +737,10 @@ __global__ void __launch_bounds__(kThreads, per_sm(MODE, NT)) gemm_kernel(const 
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (MODE == kFewDown) {
                 // a NaN in a row's weights, or an infinite scale of theirs, is in the sums of every
-                // column, the first as well
+                // column; one of a token's own in that column alone
                 float first, second;
                 unpair_f32(acc[0][0], first, second);
-                const bool good = __all_sync(0xFFFFFFFFu, fabsf(first) < INFINITY);
+                const bool good = __all_sync(0xFFFFFFFFu, U.n < 2 || fabsf(first) < INFINITY || fabsf(second) < INFINITY);
                 if (cl > 1) {
                     if (!good) {
                         *redo = 1;
