@@ -532,10 +532,10 @@ mx_status run_few(const void *x, int T, const int32_t *idx, const float *wts, co
             return st;
     }
     const double items = active * IB + SB;
-    // Two CTAs to an SM take more blocks than SMs: 12, 31 tokens of top-8 of 128 experts
-    // (d_model 2816, 22 units) in four 91, 148 us for the layer, in eight 78, 123; 256
-    // experts with d_model 4096 in four 178, 339, in six 172, 317, in eight 194, 315.
-    // A tile of 64 tokens wants an SM: 60 tokens in four 174 us, in six 155, in eight 184.
+    // Two CTAs to an SM take more blocks than SMs: 8, 31 tokens of top-8 of 128 experts
+    // (d_model 2816, 22 units) in four 73, 143 us for the layer, in six 63, 123, in eight 61,
+    // 115; 256 experts with d_model 4096 (32 units, six at most) in four 126, 338, in six 122,
+    // 313.  A tile of 64 tokens wants an SM: 64 tokens in three 192 us, in four 170, in six 151.
     const bool two = p.nt <= 32;
     d.cl = two ? split_of(DB, items, sms * 4 / 3, 8) : split_of(DB, items, sms, 6);
     d.cl_inv = d.cl > 1 ? (unsigned)(((1ull << 32) + d.cl - 1) / d.cl) : 0;

@@ -21,8 +21,8 @@
 // experts, top-8, d_model 2816: 18.6 us for 65 MB, 3.5 TB/s.  Of them gate/up takes 11 (x
 // quantised after 5, the sums done at 9, the cluster's largest |h| at 10 to 11.5), down's
 // CTAs find room when gate/up's leave, and its 22 MB come in the 6.5 us after that.  Two
-// tokens and more are faster by mx_fp8_gemm.cu (128 experts, top-8: 2 tokens 27 us and 44
-// here, 8 tokens 62 and 316, where the same expert's blocks made long chains).
+// tokens and more are faster by mx_fp8_gemm.cu (128 experts, top-8: 2 tokens 28 us and 44
+// here, 8 tokens 61 and 316, where the same expert's blocks made long chains).
 #include "mx_fp8.cuh"
 
 #include <mutex>
