@@ -209,7 +209,8 @@ def prepare(case, seed):
     st["out"] = torch.zeros(rows, c["n"], device="cuda", dtype=_dt(c["out"]))
     if own:  # the weight handle, the buffers of quantised activations and the workspace that a program keeps
         import expert_ffn_gb300 as mx
-        st["weight"] = mx.Fp4Weight(st["w"], st["ws"], st["wt"], cols=c["k"])
+        w = torch.empty(*st["w"].shape[:2], _nb(c["k"], 32) * 16, device="cuda", dtype=torch.uint8)[..., :_nb(c["k"], 2)]
+        st["weight"] = mx.Fp4Weight(w.copy_(st["w"]), st["ws"], st["wt"], cols=c["k"])  # rows at multiples of 16 bytes
         st["q"], st["sx"] = mx.fp4_empty(rows, c["k"], c["block"], device="cuda")
         n = mx.fp4_matmul_workspace_bytes(st["weight"], rows)
         st["work"] = torch.empty(n, dtype=torch.uint8, device="cuda")
