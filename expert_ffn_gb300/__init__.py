@@ -20,12 +20,18 @@ __all__ = ["MxError", "lib", "QLinear", "Ffn", "Sub", "Layout", "Options", "LAYO
            "down_sb_bytes", "pack_down_sb",
            "MX_GELU_TANH", "MX_SILU", "Fp8Matrix", "Fp8Rows", "Fp8LayerStruct", "Fp8Weight", "Fp8Layer",
            "fp8_quantize", "fp8_matmul", "fp8_grouped_matmul", "fp8_moe_forward", "fp8_matmul_workspace_bytes",
-           "fp8_moe_workspace_bytes"]
+           "fp8_moe_workspace_bytes",
+           "RmsnormStruct", "fp8_rmsnorm",
+           "MX_FP4_E8M0", "MX_FP4_E4M3", "Fp4Tensor", "Fp4Weight", "fp4_empty", "fp4_quantize", "fp4_matmul",
+           "fp4_grouped_matmul", "fp4_matmul_workspace_bytes",
+           "MX_SOFTMAX", "MX_SIGMOID", "RouterStruct", "Router", "route_logits", "route_logits_workspace_bytes"]
 
 LAYOUT_MAGIC = 0x4D584D45
 LAYOUT_VERSION = 3
 MX_F32, MX_BF16 = 0, 1
 MX_GELU_TANH, MX_SILU = 0, 1
+MX_FP4_E8M0, MX_FP4_E4M3 = 0, 1
+MX_SOFTMAX, MX_SIGMOID = 0, 1
 
 # Every symbol include/mx_moe.h declares.
 EXPORTED = ("mx_moe_layer_forward", "mx_moe_layer_forward_ex", "mx_moe_workspace_bytes", "mx_moe_workspace_init",
@@ -33,7 +39,9 @@ EXPORTED = ("mx_moe_layer_forward", "mx_moe_layer_forward_ex", "mx_moe_workspace
             "mx_last_error_string", "mx_version", "mx_moe_profile_enable", "mx_moe_profile_read",
             "mx_moe_workspace_check", "mx_moe_layer_forward_static", "mx_moe_down_sb_bytes", "mx_moe_pack_down_sb",
             "mx_fp8_quantize", "mx_fp8_matmul", "mx_fp8_grouped_matmul", "mx_fp8_matmul_workspace_bytes",
-            "mx_fp8_moe_forward", "mx_fp8_moe_workspace_bytes")
+            "mx_fp8_moe_forward", "mx_fp8_moe_workspace_bytes", "mx_fp8_rmsnorm", "mx_fp4_quantize",
+            "mx_fp4_matmul", "mx_fp4_grouped_matmul", "mx_fp4_matmul_workspace_bytes", "mx_route_logits",
+            "mx_route_logits_workspace_bytes")
 
 
 class MxError(RuntimeError):
@@ -86,6 +94,26 @@ class Fp8LayerStruct(C.Structure):
         ("top_k", C.c_int32), ("act_dtype", C.c_int32), ("activation", C.c_int32), ("layer_scalar", C.c_float)]
 
 
+class RmsnormStruct(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("ldx", C.c_int64), ("residual", C.c_void_p), ("ldr", C.c_int64),
+                ("weight", C.c_void_p), ("sum", C.c_void_p), ("lds", C.c_int64), ("out", C.c_void_p),
+                ("ldo", C.c_int64), ("q", C.POINTER(Fp8Rows)), ("rows", C.c_int32), ("cols", C.c_int32),
+                ("dtype", C.c_int32), ("weight_dtype", C.c_int32), ("out_dtype", C.c_int32), ("pow2", C.c_int32),
+                ("eps", C.c_float), ("weight_offset", C.c_float)]
+
+
+class Fp4Tensor(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("scales", C.c_void_p), ("tensor_scale", C.c_void_p), ("rows", C.c_int32),
+                ("cols", C.c_int32), ("count", C.c_int32), ("format", C.c_int32), ("ld", C.c_int64),
+                ("scale_ld", C.c_int64)]
+
+
+class RouterStruct(C.Structure):
+    _fields_ = [("n_experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32), ("n_groups", C.c_int32),
+                ("topk_groups", C.c_int32), ("group_best", C.c_int32), ("renormalise", C.c_int32),
+                ("scale", C.c_float), ("bias", C.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -131,7 +159,18 @@ def lib():
             L.mx_fp8_moe_forward.argtypes = [P, I32, P, P, C.POINTER(Fp8LayerStruct), P, P, P, P, SZ]
             L.mx_fp8_moe_workspace_bytes.argtypes = [C.POINTER(Fp8LayerStruct), I32]
             L.mx_fp8_moe_workspace_bytes.restype = SZ
-            for name in ("mx_fp8_quantize", "mx_fp8_matmul", "mx_fp8_grouped_matmul", "mx_fp8_moe_forward",
+            L.mx_fp8_rmsnorm.argtypes = [P, P]  # (P: a RmsnormStruct, by reference or packed)
+            L.mx_fp4_quantize.argtypes = [P, I64, I32, P, P]  # (P: an Fp4Tensor, likewise)
+            L.mx_fp4_matmul.argtypes = [P, C.POINTER(Fp4Tensor), P, I64, I32, P, P, SZ]
+            L.mx_fp4_grouped_matmul.argtypes = [P, P, C.POINTER(Fp4Tensor), P, I64, I32, P, P, SZ]
+            L.mx_fp4_matmul_workspace_bytes.argtypes = [C.POINTER(Fp4Tensor), I32]
+            L.mx_fp4_matmul_workspace_bytes.restype = SZ
+            L.mx_route_logits.argtypes = [P, I64, I32, I32, C.POINTER(RouterStruct), P, P, P, P, P, P, P, SZ]
+            L.mx_route_logits_workspace_bytes.argtypes = [C.POINTER(RouterStruct), I32]
+            L.mx_route_logits_workspace_bytes.restype = SZ
+            for name in ("mx_fp8_rmsnorm", "mx_fp4_quantize", "mx_fp4_matmul", "mx_fp4_grouped_matmul",
+                         "mx_route_logits",
+                         "mx_fp8_quantize", "mx_fp8_matmul", "mx_fp8_grouped_matmul", "mx_fp8_moe_forward",
                          "mx_moe_layer_forward", "mx_moe_layer_forward_ex", "mx_moe_layer_forward_static",
                          "mx_moe_workspace_init", "mx_moe_pack_down_sb",
                          "mx_moe_route", "mx_moe_stack_forward", "mx_moe_profile_enable", "mx_moe_profile_read",
@@ -365,6 +404,8 @@ def profile_read(reset: bool = True) -> dict:
 # compared by index.
 
 _ROWS = _struct.Struct("@PPiiqqq")  # Fp8Rows
+_NORM = _struct.Struct("@PqPqPPqPqPiiiiiiff")  # RmsnormStruct
+_FP4 = _struct.Struct("@PPPiiiiqq")  # Fp4Tensor
 _t = None  # names of torch, filled on first use
 
 
@@ -381,6 +422,9 @@ class _Torch:
         L = lib()
         self.quantize, self.matmul, self.grouped = L.mx_fp8_quantize, L.mx_fp8_matmul, L.mx_fp8_grouped_matmul
         self.moe = L.mx_fp8_moe_forward
+        self.norm, self.route = L.mx_fp8_rmsnorm, L.mx_route_logits
+        self.quantize4, self.matmul4, self.grouped4 = L.mx_fp4_quantize, L.mx_fp4_matmul, L.mx_fp4_grouped_matmul
+        self.u8, self.e8m0 = torch.uint8, torch.float8_e8m0fnu
 
 
 def _torch():
@@ -561,3 +605,233 @@ def fp8_moe_forward(x, topk_idx, topk_w, layer: Fp8Layer, out, ws, residual=None
     _on(dev, t.moe, x.data_ptr(), T, topk_idx.data_ptr(), topk_w.data_ptr(), layer.ref,
         None if residual is None else residual.data_ptr(), out.data_ptr(), _stream_on(dev, stream), ws.data_ptr(),
         ws.nbytes)
+
+
+# ------------------------------------------------------------- RMS norm
+
+def _rows2d(t, shape, dev, name):
+    """Row pitch of a tensor of the given shape with contiguous rows."""
+    if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
+        raise MxError(-1, f"{name} must be {list(shape)} with contiguous rows")
+    if t.get_device() != dev:
+        raise MxError(-1, "all tensors must be on one device")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def fp8_rmsnorm(x, weight=None, eps=1e-6, weight_offset=0.0, residual=None, residual_out=None, out=None, q=None,
+                scales=None, pow2=False, stream=None):
+    """RMS norm of the rows of ``x`` (float32 or bfloat16 [rows, cols]) plus ``residual``, times ``weight_offset +
+    weight`` (mx_fp8_rmsnorm).  ``residual_out`` gets the sum (it may be ``residual`` or ``x`` itself), ``out`` the
+    normed rows, ``q`` and ``scales`` the same in e4m3 as fp8_quantize makes them; at least one of the three."""
+    t = _t or _torch()
+    dev = x.get_device()
+    if x.dim() != 2:
+        raise MxError(-1, "x must be [rows, cols]")
+    shape = x.shape
+    rows, cols = shape
+    dt = _dtype_code(x, "x")
+    ldx = _rows2d(x, shape, dev, "x")
+    rp = wp = sp = op = qp = None
+    ldr = lds = ldo = 0
+    wd = od = 0
+    if residual is not None:
+        if residual.dtype is not x.dtype:
+            raise MxError(-1, "residual must have x's dtype")
+        ldr, rp = _rows2d(residual, shape, dev, "residual"), residual.data_ptr()
+    if residual_out is not None:
+        if residual_out.dtype is not x.dtype:
+            raise MxError(-1, "residual_out must have x's dtype")
+        lds, sp = _rows2d(residual_out, shape, dev, "residual_out"), residual_out.data_ptr()
+    if weight is not None:
+        if weight.shape != (cols,) or not weight.is_contiguous() or weight.get_device() != dev:
+            raise MxError(-1, f"weight must be contiguous [{cols}] on x's device")
+        wd, wp = _dtype_code(weight, "weight"), weight.data_ptr()
+    if out is not None:
+        ldo, op, od = _rows2d(out, shape, dev, "out"), out.data_ptr(), _dtype_code(out, "out")
+    if (q is None) != (scales is None):
+        raise MxError(-1, "q and scales come together")
+    if q is not None:
+        qr, qc, r = _fp8_rows(t, q, scales, dev, False)
+        if (qr, qc) != (rows, cols):
+            raise MxError(-1, f"q must be [{rows}, {cols}]")
+        r = C.create_string_buffer(r, len(r))
+        qp = C.addressof(r)
+    if rows == 0:
+        ldx = ldx or cols
+    args = _NORM.pack(x.data_ptr(), ldx, rp or 0, ldr, wp or 0, sp or 0, lds, op or 0, ldo, qp or 0, rows, cols, dt, wd,
+                      od, 1 if pow2 else 0, eps, weight_offset)
+    _on(dev, t.norm, args, _stream_on(dev, stream))
+
+
+# ------------------------------------------- microscaled 4-bit operators
+
+def _fp4_format(t, scales, name):
+    if scales.dtype is t.f8:
+        return MX_FP4_E4M3, 16
+    if scales.dtype is t.e8m0:
+        return MX_FP4_E8M0, 32
+    raise MxError(-1, f"{name}: scales must be float8_e4m3fn (blocks of 16) or float8_e8m0fnu (of 32)")
+
+
+def _up(n, m):
+    return -(-n // m) * m
+
+
+def _fp4_rows(t, q, scales, cols, factor, dev):
+    """(rows, packed Fp4Tensor) of quantised activations."""
+    fmt, block = _fp4_format(t, scales, "q")
+    shape, strides = q.shape, q.stride()
+    if q.dtype is not t.u8 or len(shape) != 2 or shape[1] != (cols + 1) // 2 or (strides[1] != 1 and shape[1] > 1):
+        raise MxError(-1, f"q must be uint8 [rows, {(cols + 1) // 2}] with contiguous rows")
+    rows, nb = shape[0], -(-cols // block)
+    if scales.shape != (rows, nb) or (nb > 1 and scales.stride(1) != 1):
+        raise MxError(-1, f"scales must be [{rows}, {nb}] with contiguous rows")
+    if q.get_device() != dev or scales.get_device() != dev:
+        raise MxError(-1, "all tensors must be on one device")
+    # (the stride of a single row means nothing)
+    ld, lds = (strides[0], scales.stride(0)) if rows > 1 else (_up(shape[1], 16), _up(nb, 4))
+    return rows, _FP4.pack(q.data_ptr(), scales.data_ptr(), _factor(t, factor, 1, fmt, dev), rows, cols, 1, fmt, ld, lds)
+
+
+def _factor(t, factor, count, fmt, dev):
+    if factor is None:
+        return 0
+    if (fmt != MX_FP4_E4M3 or factor.dtype is not t.f32 or factor.numel() != count or not factor.is_contiguous()
+            or factor.get_device() != dev):
+        raise MxError(-1, f"tensor_scale must be {count} contiguous float32 on the tensors' device, with e4m3 scales")
+    return factor.data_ptr()
+
+
+class Fp4Weight:
+    """Microscaled e2m1 matrices on the device: ``w`` uint8 [count,] rows, ceil(cols / 2), two numbers to a byte, rows
+    at multiples of 16 bytes; ``scales`` float8_e4m3fn (a block of 16 columns each) or float8_e8m0fnu (32) [count,]
+    rows, blocks, rows at multiples of 4 bytes; ``tensor_scale`` float32 [count] or None (e4m3 only).  ``cols`` is
+    needed where it is odd.  The tensors are kept and read by every call, not copied."""
+
+    def __init__(self, w, scales, tensor_scale=None, cols=None):
+        t = _t or _torch()
+        _need(w.dtype is t.u8 and w.dim() in (2, 3), "w must be uint8 [count,] rows, bytes")
+        fmt, block = _fp4_format(t, scales, "w")
+        rows, nbytes = w.shape[-2:]
+        count = w.shape[0] if w.dim() == 3 else 1
+        cols = 2 * nbytes if cols is None else cols
+        _need((cols + 1) // 2 == nbytes, f"w has {nbytes} bytes a row, {cols} columns need {(cols + 1) // 2}")
+        nb = -(-cols // block)
+        _need(tuple(scales.shape) == (*w.shape[:-1], nb), f"scales must be [{count}, {rows}, {nb}]")
+        ld = w.stride(-2) if rows > 1 else w.stride(0) if count > 1 else _up(nbytes, 16)
+        lds = scales.stride(-2) if rows > 1 else scales.stride(0) if count > 1 else _up(nb, 4)
+        _need((w.stride(-1) == 1 or nbytes == 1) and (scales.stride(-1) == 1 or nb == 1), "rows must be contiguous")
+        _need(count == 1 or (w.stride(0) == rows * ld and scales.stride(0) == rows * lds),
+              "the matrices must follow one another")
+        dev = w.get_device()
+        _need(scales.get_device() == dev, f"scales must be on {w.device}")
+        self.w, self.scales, self.tensor_scale = w, scales, tensor_scale
+        self.c = Fp4Tensor(w.data_ptr(), scales.data_ptr(), _factor(t, tensor_scale, count, fmt, dev) or None, rows, cols,
+                           count, fmt, ld, lds)
+        self.ref, self.rows, self.cols, self.count, self.dev = C.byref(self.c), rows, cols, count, dev
+
+
+def fp4_empty(rows: int, cols: int, block: int, device="cuda"):
+    """Uninitialised (q, scales) for fp4_quantize, pitched as the products want them; block 16 (e4m3 scales) or 32
+    (e8m0)."""
+    import torch
+    _need(block in (16, 32) and rows >= 0 and cols >= 1, "block must be 16 or 32, rows >= 0, cols >= 1")
+    nbytes, nb = (cols + 1) // 2, -(-cols // block)
+    q = torch.empty(rows, _up(nbytes, 16), dtype=torch.uint8, device=device)[:, :nbytes]
+    s = torch.empty(rows, _up(nb, 4), dtype=torch.uint8, device=device)
+    return q, s.view(torch.float8_e4m3fn if block == 16 else torch.float8_e8m0fnu)[:, :nb]
+
+
+def fp4_quantize(x, q, scales, tensor_scale=None, stream=None):
+    """Quantise the rows of ``x`` (float32 or bfloat16 [rows, cols]) into ``q`` (uint8 [rows, ceil(cols / 2)]) and
+    ``scales`` (float8_e4m3fn for blocks of 16 columns, with the optional float32 ``tensor_scale`` on the device, or
+    float8_e8m0fnu for blocks of 32), see fp4_empty."""
+    t = _t or _torch()
+    dev = x.get_device()
+    if x.dim() != 2:
+        raise MxError(-1, "x must be [rows, cols]")
+    rows, cols = x.shape
+    n, r = _fp4_rows(t, q, scales, cols, tensor_scale, dev)
+    if n != rows or (cols > 1 and x.stride(1) != 1):
+        raise MxError(-1, f"x must be [{n}, cols] with contiguous rows")
+    _on(dev, t.quantize4, x.data_ptr(), x.stride(0) if rows > 1 else cols, _dtype_code(x, "x"), r,
+        _stream_on(dev, stream))
+
+
+def fp4_matmul_workspace_bytes(weight: Fp4Weight, rows: int) -> int:
+    return lib().mx_fp4_matmul_workspace_bytes(weight.ref, rows)
+
+
+def fp4_matmul(q, scales, weight: Fp4Weight, out, ws, tensor_scale=None, stream=None):
+    """out = (q, scales, tensor_scale) times the transposed ``weight``; out float32 or bfloat16 [rows, weight rows]; ws
+    a uint8 workspace of fp4_matmul_workspace_bytes, prepared by workspace_init."""
+    t = _t or _torch()
+    dev = weight.dev
+    rows, r = _fp4_rows(t, q, scales, weight.cols, tensor_scale, dev)
+    ldo = _out_pitch(rows, weight, out, ws)
+    _on(dev, t.matmul4, r, weight.ref, out.data_ptr(), ldo, _dtype_code(out, "out"), _stream_on(dev, stream),
+        ws.data_ptr(), ws.nbytes)
+
+
+def fp4_grouped_matmul(q, scales, offsets, weight: Fp4Weight, out, ws, tensor_scale=None, stream=None):
+    """The same with rows [offsets[e], offsets[e + 1]) against matrix e; offsets int32 [count + 1] on the device."""
+    t = _t or _torch()
+    dev = weight.dev
+    rows, r = _fp4_rows(t, q, scales, weight.cols, tensor_scale, dev)
+    ldo = _out_pitch(rows, weight, out, ws)
+    if (offsets.dtype is not t.i32 or offsets.shape != (weight.count + 1,) or not offsets.is_contiguous()
+            or offsets.get_device() != dev):
+        raise MxError(-1, f"offsets must be contiguous int32 [{weight.count + 1}] on the weight's device")
+    _on(dev, t.grouped4, r, offsets.data_ptr(), weight.ref, out.data_ptr(), ldo, _dtype_code(out, "out"),
+        _stream_on(dev, stream), ws.data_ptr(), ws.nbytes)
+
+
+# ------------------------------------------------------ routing from logits
+
+class Router:
+    """How tokens choose experts by their logits (mx_route_logits): scores MX_SOFTMAX or MX_SIGMOID; ``bias`` float32
+    [n_experts] on the device, added for the choice alone; the best ``topk_groups`` of ``n_groups`` runs of experts, by
+    their ``group_best`` (1 or 2) highest scores; the weights of the ``top_k`` chosen divided by their sum
+    (``renormalise``) and times ``scale``."""
+
+    def __init__(self, n_experts, top_k, score=MX_SOFTMAX, bias=None, n_groups=1, topk_groups=1, group_best=1,
+                 renormalise=True, scale=1.0):
+        t = _t or _torch()
+        _need(bias is None or (bias.dtype is t.f32 and bias.shape == (n_experts,) and bias.is_contiguous()),
+              f"bias must be contiguous float32 [{n_experts}]")
+        self.bias = bias
+        self.c = RouterStruct(n_experts, top_k, score, n_groups, topk_groups, group_best, 1 if renormalise else 0, scale,
+                              _ptr(bias))
+        self.ref, self.n_experts, self.top_k = C.byref(self.c), n_experts, top_k
+        self.dev = None if bias is None else bias.get_device()
+
+
+def route_logits_workspace_bytes(router: Router, T: int) -> int:
+    return lib().mx_route_logits_workspace_bytes(router.ref, T)
+
+
+def route_logits(logits, router: Router, topk_idx, topk_w, counts=None, offsets=None, perm=None, ws=None, stream=None):
+    """Choose the experts of each row of ``logits`` (float32 or bfloat16 [T, n_experts]): topk_idx int32 and topk_w
+    float32 [T, top_k].  With counts, offsets and perm (int32 [n_experts], [n_experts + 1], [T * top_k]) the slots are
+    grouped by expert as route() does; ws is then a uint8 workspace of route_logits_workspace_bytes, prepared by
+    workspace_init."""
+    t = _t or _torch()
+    dev = logits.get_device()
+    T, E, K = logits.shape[0], router.n_experts, router.top_k
+    ld = _rows2d(logits, (T, E), dev, "logits")
+    outs = [(topk_idx, t.i32, (T, K), "topk_idx"), (topk_w, t.f32, (T, K), "topk_w")]
+    if counts is not None or offsets is not None or perm is not None:
+        if counts is None or offsets is None or perm is None or ws is None:
+            raise MxError(-1, "counts, offsets, perm and ws come together")
+        outs += [(counts, t.i32, (E,), "counts"), (offsets, t.i32, (E + 1,), "offsets"), (perm, t.i32, (T * K,), "perm"),
+                 (ws, t.u8, ws.shape, "ws")]
+    for a, dtype, shape, name in outs:
+        if a.dtype is not dtype or a.shape != shape or not a.is_contiguous():
+            raise MxError(-1, f"{name} must be contiguous {dtype} {list(shape)}")
+        if a.get_device() != dev:
+            raise MxError(-1, "all tensors must be on one device")
+    if router.dev is not None and router.dev != dev:
+        raise MxError(-1, "all tensors must be on one device")
+    _on(dev, t.route, logits.data_ptr(), ld, _dtype_code(logits, "logits"), T, router.ref, topk_idx.data_ptr(),
+        topk_w.data_ptr(), _ptr(counts), _ptr(offsets), _ptr(perm), _stream_on(dev, stream), _ptr(ws),
+        0 if ws is None else ws.nbytes)

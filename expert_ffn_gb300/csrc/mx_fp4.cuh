@@ -1,0 +1,47 @@
+// mx_fp4.cuh -- what the translation units of the microscaled 4-bit operators share.
+//
+// Numbers: e2m1, two to a byte, the lower column in the low nibble; a scale for each block
+// of a row's columns: e8m0 for 32, or e4m3 for 16 and one fp32 factor of the tensor.
+#pragma once
+
+#include "mx_common.cuh"
+#include "mx_internal.h"
+#include "mx_moe.h"
+
+namespace mx {
+namespace fp4 {
+
+constexpr int kStageCols = 256;  // columns of one ring stage: 128 bytes of a row
+
+struct QuantArgs {
+    const void *x;  // [rows][cols]
+    int64_t ldx;
+    int rows, cols, bf16;
+    int vx, vq;     // pieces of x, of q may be moved as vectors
+    uint8_t *q, *scales;
+    int64_t ldq, lds;
+    const float *tensor_scale;  // e4m3; nullable
+};
+cudaError_t launch_quantize(int block, const QuantArgs &a, int sms, cudaStream_t s);
+
+struct GemmArgs {
+    CUtensorMap wm, xm;      // packed bytes of the weights [E][N][K / 2] and of the rows
+    int rows, K, N, E;
+    const int32_t *offsets;  // [E + 1] first row of each matrix's group, nullable: one group of all rows
+    const uint8_t *sx, *sw;  // scales, row pitches in bytes
+    int64_t sx_ld, sw_ld;
+    const float *tx, *tw;    // factors of the rows and of each matrix, nullable
+    void *out;
+    int64_t ldo;
+    int out_bf16, out_vec;
+    unsigned *err;
+    int stages, cl;          // ring depth, cluster size (split of the inner dimension)
+};
+
+// Token tiles of launch_gemm: 16, 32, 64, 128, 224.
+cudaError_t launch_gemm(int block, int nt, const GemmArgs &a, int grid, cudaStream_t s);
+size_t gemm_smem(int block, int nt, int stages);
+constexpr int box_rows(int nt) { return nt < 32 ? nt : 32; }  // token rows of one copy
+
+}  // namespace fp4
+}  // namespace mx

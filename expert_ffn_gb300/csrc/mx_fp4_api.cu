@@ -1,0 +1,218 @@
+// mx_fp4_api.cu -- the microscaled 4-bit entry points of include/mx_moe.h: argument
+// validation (all of it on the host, before any CUDA call) and the choice of tile, split
+// and grid for each launch.
+#include "mx_fp4.cuh"
+#include "mx_host.h"
+
+#include <algorithm>
+#include <cmath>
+
+using namespace mx;
+using namespace mx::fp4;
+
+namespace {
+
+constexpr int kMaxCols = 1 << 20, kMaxRows = 1 << 28;
+constexpr int kSmem = 227 * 1024;  // shared memory of a CTA alone on its SM
+
+int block_of(int format) { return format == MX_FP4_E4M3 ? 16 : 32; }
+
+mx_status check_tensor(const mx_fp4_tensor *t, const char *name, bool operand, bool matrix)
+{
+    if (!t)
+        return fail(MX_ERR_INVALID_ARG, "%s is NULL", name);
+    if (t->format != MX_FP4_E8M0 && t->format != MX_FP4_E4M3)
+        return fail(MX_ERR_INVALID_ARG, "%s: format %d is not MX_FP4_E8M0 or MX_FP4_E4M3", name, t->format);
+    if (t->tensor_scale && t->format != MX_FP4_E4M3)
+        return fail(MX_ERR_INVALID_ARG, "%s: a tensor_scale belongs to MX_FP4_E4M3", name);
+    if (t->cols < 1 || t->cols > kMaxCols)
+        return fail(MX_ERR_UNSUPPORTED, "%s: %d columns must be within [1, %d]", name, t->cols, kMaxCols);
+    if (matrix) {
+        if (t->rows < 1 || t->rows > kMaxCols)
+            return fail(MX_ERR_UNSUPPORTED, "%s: %d rows must be within [1, %d]", name, t->rows, kMaxCols);
+        if (t->count < 1 || t->count > kMaxExperts)
+            return fail(MX_ERR_UNSUPPORTED, "%s: %d matrices, at most %d are supported", name, t->count, kMaxExperts);
+    } else {
+        if (t->rows < 0 || t->rows > kMaxRows)
+            return fail(MX_ERR_INVALID_ARG, "%s: %d rows must be within [0, %d]", name, t->rows, kMaxRows);
+        if (t->count != 1)
+            return fail(MX_ERR_INVALID_ARG, "%s: count %d must be 1", name, t->count);
+    }
+    const int64_t bytes = ((int64_t)t->cols + 1) / 2, b = block_of(t->format), blocks = (t->cols + b - 1) / b;
+    if (t->ld < bytes || t->scale_ld < blocks)
+        return fail(MX_ERR_INVALID_ARG, "%s: row pitches %lld and %lld are below its %lld bytes and %lld scales", name,
+                    (long long)t->ld, (long long)t->scale_ld, (long long)bytes, (long long)blocks);
+    if (t->ld > 4 * (int64_t)kMaxCols || t->scale_ld > 4 * (int64_t)kMaxCols)
+        return fail(MX_ERR_UNSUPPORTED, "%s: a row pitch is above %d", name, 4 * kMaxCols);
+    if (t->rows == 0)
+        return MX_OK;
+    if (!t->q || !t->scales)
+        return fail(MX_ERR_INVALID_ARG, "%s has a NULL pointer", name);
+    if (operand && (!aligned(t->q, 16) || t->ld % 16))
+        return fail(MX_ERR_ALIGNMENT, "%s: address and row pitch must be multiples of 16 bytes", name);
+    if (operand && (!aligned(t->scales, 4) || t->scale_ld % 4))
+        return fail(MX_ERR_ALIGNMENT, "%s: scales and their row pitch must be multiples of 4 bytes", name);
+    if (!aligned(t->tensor_scale, 4))
+        return fail(MX_ERR_ALIGNMENT, "%s: tensor_scale must be 4-byte aligned", name);
+    return MX_OK;
+}
+
+// Token tile, cluster split and grid of a product.
+struct Choice {
+    int nt, cl, grid;
+};
+
+Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
+{
+    Choice c{16, 1, 1};
+    if (grouped) {
+        const double avg = (double)rows / E, most = avg + 3 * std::sqrt(avg);
+        for (int nt : {32, 64, 128, 224})
+            if (c.nt < most)
+                c.nt = nt;
+        const int64_t units = ((int64_t)rows / c.nt + E) * FT;
+        c.grid = (int)std::min<int64_t>(sms, units);
+        return c;
+    }
+    for (int nt : {32, 64})
+        if (c.nt < rows)
+            c.nt = nt;
+    int64_t units = (int64_t)((rows + c.nt - 1) / c.nt) * FT;
+    if (rows > 64 && 2 * units > sms) {
+        // the tile whose rounds take least: a tile of n tokens costs its MMAs and about 40 tokens' worth besides
+        double best = 1e30;
+        for (int nt : {64, 128, 224}) {
+            const int64_t u = (int64_t)((rows + nt - 1) / nt) * FT;
+            const double t = (double)((u + sms - 1) / sms) * (nt + 40);
+            if (t < best)
+                best = t, c.nt = nt;
+        }
+        units = (int64_t)((rows + c.nt - 1) / c.nt) * FT;
+    }
+    if (2 * units <= sms && KB >= 2)
+        c.cl = (int)std::min<int64_t>({8, sms / units, KB});
+    if (c.cl > 4 && c.cl < 8)
+        c.cl = 4;
+    if (c.cl == 3)
+        c.cl = 2;
+    c.grid = (int)std::min<int64_t>(sms / c.cl, units) * c.cl;
+    return c;
+}
+
+mx_status product(const mx_fp4_tensor *x, const int32_t *offsets, const mx_fp4_tensor *w, void *out, int64_t ldo,
+                  int out_dtype, void *stream, void *ws, size_t ws_bytes)
+{
+    mx_status st;
+    if ((st = check_tensor(x, "x", true, false)) != MX_OK || (st = check_tensor(w, "w", true, true)) != MX_OK ||
+        (st = check_dtype(out_dtype, "out_dtype")) != MX_OK)
+        return st;
+    if (x->cols != w->cols || x->format != w->format)
+        return fail(MX_ERR_INVALID_ARG, "x has %d columns in format %d, w has %d in format %d", x->cols, x->format, w->cols,
+                    w->format);
+    if (ldo < w->rows)
+        return fail(MX_ERR_INVALID_ARG, "output row pitch %lld is below its %d columns", (long long)ldo, w->rows);
+    if (ldo > ((int64_t)1 << 31))
+        return fail(MX_ERR_UNSUPPORTED, "output row pitch %lld is too large", (long long)ldo);
+    if (x->rows == 0)
+        return MX_OK;
+    if (!out)
+        return fail(MX_ERR_INVALID_ARG, "out is NULL");
+    if (!aligned(out, dtype_bytes(out_dtype)))
+        return fail(MX_ERR_ALIGNMENT, "out is misaligned");
+    if ((st = check_ws(ws, ws_bytes, kErrBytes)) != MX_OK)
+        return st;
+    const int block = block_of(w->format), FT = (w->rows + 127) / 128, KB = (w->cols + kStageCols - 1) / kStageCols;
+    const Choice c = choose(x->rows, offsets != nullptr, w->count, FT, KB, num_sms());
+    GemmArgs g{};
+    g.rows = x->rows;
+    g.K = w->cols;
+    g.N = w->rows;
+    g.E = w->count;
+    g.offsets = offsets;
+    g.sx = static_cast<const uint8_t *>(x->scales);
+    g.sw = static_cast<const uint8_t *>(w->scales);
+    g.sx_ld = x->scale_ld;
+    g.sw_ld = w->scale_ld;
+    g.tx = x->tensor_scale;
+    g.tw = w->tensor_scale;
+    g.out = out;
+    g.ldo = ldo;
+    g.out_bf16 = out_dtype == MX_BF16;
+    g.out_vec = vec16(out, ldo, g.out_bf16);
+    g.err = static_cast<unsigned *>(ws);
+    g.cl = c.cl;
+    g.stages = std::min(12, std::max(3, KB));
+    while (g.stages > 2 && gemm_smem(block, c.nt, g.stages) > (size_t)kSmem)
+        --g.stages;
+    const uint64_t bytes = ((uint64_t)w->cols + 1) / 2;
+    cudaError_t e = tma_map_bytes(&g.wm, w->q, TmaBytes{bytes, (uint64_t)w->rows, (uint64_t)w->count, (uint64_t)w->ld, 128});
+    if (e == cudaSuccess)
+        e = tma_map_bytes(&g.xm, x->q, TmaBytes{bytes, (uint64_t)x->rows, 0, (uint64_t)x->ld, (uint32_t)box_rows(c.nt)});
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tensor map of an FP4 operand");
+    e = launch_gemm(block, c.nt, g, c.grid, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP4 product");
+}
+
+}  // namespace
+
+extern "C" mx_status mx_fp4_quantize(const void *x, int64_t ldx, int dtype, const mx_fp4_tensor *out, void *stream)
+{
+    mx_status st;
+    if ((st = check_dtype(dtype, "dtype")) != MX_OK || (st = check_tensor(out, "out", false, false)) != MX_OK)
+        return st;
+    if (ldx < out->cols)
+        return fail(MX_ERR_INVALID_ARG, "x: row pitch %lld is below its %d columns", (long long)ldx, out->cols);
+    if (ldx > ((int64_t)1 << 31))
+        return fail(MX_ERR_UNSUPPORTED, "x: row pitch %lld is too large", (long long)ldx);
+    if (out->rows == 0)
+        return MX_OK;
+    if (!x)
+        return fail(MX_ERR_INVALID_ARG, "x is NULL");
+    if (!aligned(x, dtype_bytes(dtype)))
+        return fail(MX_ERR_ALIGNMENT, "x is misaligned");
+    QuantArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.rows = out->rows;
+    a.cols = out->cols;
+    a.bf16 = dtype == MX_BF16;
+    a.vx = vec16(x, ldx, a.bf16);
+    a.vq = aligned(out->q, 4) && out->ld % 4 == 0;
+    a.q = static_cast<uint8_t *>(out->q);
+    a.scales = static_cast<uint8_t *>(out->scales);
+    a.ldq = out->ld;
+    a.lds = out->scale_ld;
+    a.tensor_scale = out->tensor_scale;
+    const cudaError_t e = launch_quantize(block_of(out->format), a, num_sms(), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP4 quantisation");
+}
+
+extern "C" mx_status mx_fp4_matmul(const mx_fp4_tensor *x, const mx_fp4_tensor *w, void *out, int64_t ldo, int out_dtype,
+                                   void *stream, void *ws, size_t ws_bytes)
+{
+    if (w && w->count != 1)
+        return fail(MX_ERR_INVALID_ARG, "w holds %d matrices, one is needed", w->count);
+    return product(x, nullptr, w, out, ldo, out_dtype, stream, ws, ws_bytes);
+}
+
+extern "C" mx_status mx_fp4_grouped_matmul(const mx_fp4_tensor *x, const int32_t *offsets, const mx_fp4_tensor *w,
+                                           void *out, int64_t ldo, int out_dtype, void *stream, void *ws, size_t ws_bytes)
+{
+    if (!offsets)
+        return fail(MX_ERR_INVALID_ARG, "offsets is NULL");
+    if (!aligned(offsets, 4))
+        return fail(MX_ERR_ALIGNMENT, "offsets must be 4-byte aligned");
+    return product(x, offsets, w, out, ldo, out_dtype, stream, ws, ws_bytes);
+}
+
+extern "C" size_t mx_fp4_matmul_workspace_bytes(const mx_fp4_tensor *w, int rows)
+{
+    if (check_tensor(w, "w", true, true) != MX_OK)
+        return 0;
+    if (rows < 0) {
+        fail(MX_ERR_INVALID_ARG, "%d rows", rows);
+        return 0;
+    }
+    return kErrBytes;
+}

@@ -1,0 +1,514 @@
+// mx_fp4_gemm.cu -- products of microscaled e2m1 rows and matrices on the 5th-generation
+// tensor cores (tcgen05.mma kind::mxf4nvf4, block scales and accumulators in TMEM).
+//
+//   y[r, o] = tx tw sum_b sx[r, b] sw[o, b] sum_{c in b} qx[r, c] qw[o, c]
+//
+// The tensor core takes the block scales itself (scale_vec::4X for blocks of 16 e4m3,
+// 2X for blocks of 32 e8m0) and keeps a tile's whole sum in TMEM, so nothing is left to the
+// CUDA cores but the tensors' factors.  The weights take the M side (128 rows), the tokens
+// the N side (any multiple of 16 up to the tile's width), so one kernel serves one row and
+// thousands: a short group costs what its rows need.
+//
+// A stage of the ring is 256 columns: 128 bytes of each row (SWIZZLE_128B) and their
+// scales, 16 or 8 bytes a row.  The hardware wants the scales of 128 rows as 32 lines of 16 bytes,
+// line i with four scales of each of the rows i, 32 + i, 64 + i, 96 + i (512 bytes for four blocks of columns); they lie row by
+// row in memory, at rows that a group's offsets make arbitrary, so two warps gather them with 4-byte
+// asynchronous copies, whose completion is counted on the stage's own barrier.
+//
+// Warps:
+//   0-3  results: TMEM (lane quadrant = warp) to global memory
+//   4    TMA producer: weight and token tiles
+//   5    MMA: per stage the copies of its scales to TMEM (tcgen05.cp, in order with the
+//        MMAs) and four MMAs (K = 64)
+//   6-7  scales
+// Two TMEM accumulators: a tile's results leave while the next one is summed.  Few units: a
+// cluster of `cl` CTAs splits the inner dimension of one unit, and its partial sums are added
+// through distributed shared memory in rank order.
+//
+// Every wait is bounded: a wait that gives up sets the caller's error word and ends the
+// CTA's work.
+#include "mx_fp4.cuh"
+#include "mx_fp8_tc.cuh"
+
+namespace mx {
+namespace fp4 {
+
+namespace {
+
+using fp8::bwait;
+using fp8::cluster_rank;
+using fp8::cluster_sync;
+using fp8::elect_one;
+using fp8::fence_after;
+using fp8::fence_before;
+using fp8::group_table;
+using fp8::ld_cluster;
+using fp8::mapa;
+using fp8::sw128_desc;
+using fp8::tma_2d;
+using fp8::tma_3d;
+using fp8::tmem_ld16;
+using fp8::tmem_value;
+using fp8::tmem_wait;
+using fp8::warp_index;
+using fp8::wwait;
+
+constexpr uint32_t kTile = 128 * 128;  // bytes of one weight tile
+constexpr int kOutWarps = 4, kScaleWarps = 2, kThreads = (kOutWarps + 2 + kScaleWarps) * 32;
+constexpr int kAcc = 2;                // TMEM accumulators
+constexpr int kMaxStages = 12;
+
+constexpr int atoms_of(int block) { return 64 / block; }  // 512-byte scale atoms of 128 rows in a stage
+constexpr int halves(int nt) { return (nt + 127) / 128; }
+constexpr uint32_t scale_bytes(int block, int nt) { return atoms_of(block) * 512 * (1 + halves(nt)); }
+constexpr uint32_t stage_bytes(int block, int nt) { return kTile + nt * 128 + scale_bytes(block, nt); }
+constexpr int acc_cols(int nt) { return nt; }
+constexpr uint32_t tmem_cols(int block, int nt)
+{
+    const uint32_t need = kAcc * acc_cols(nt) + atoms_of(block) * 4 * (1 + halves(nt));
+    uint32_t c = 32;
+    while (c < need)
+        c *= 2;
+    return c;
+}
+
+// Dynamic shared memory after the ring.
+struct Tail {
+    int tab, bars, total;
+};
+__host__ __device__ constexpr Tail tail_of()
+{
+    Tail t{};
+    int o = 0;
+    t.tab = o;
+    o += (3 * kMaxExperts + 16) * 4;
+    t.bars = o;
+    o += 512;
+    t.total = o;
+    return t;
+}
+
+// e2m1 A and B (K-major), fp32 D, M = 128, N = n; scale type e8m0 (bit 23) or e4m3.
+__device__ __forceinline__ uint32_t idesc_e2m1(int n, int block)
+{
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (block == 32 ? 1u << 23 : 0u) | (8u << 24);
+}
+
+// 32 lines of 16 bytes without a swizzle (8 lines to a core matrix, 128 bytes apart).
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// `%2` scale atoms to TMEM, four columns each.  One elected lane of a converged warp.
+template <int N>
+__device__ __forceinline__ void scales_to_tmem(uint32_t to, uint64_t desc)
+{
+    static_assert(N == 2 || N == 4 || N == 8, "atoms");
+#define MX_CP "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [t], d;\n\tadd.u32 t, t, 4;\n\tadd.s64 d, d, 32;\n\t"
+#define MX_CP_HEAD "{\n\t.reg .pred q;\n\t.reg .b32 t;\n\t.reg .b64 d;\n\tmov.b32 t, %0;\n\tmov.b64 d, %1;\n\telect.sync _|q, 0xffffffff;\n\t"
+    if constexpr (N == 2)
+        asm volatile(MX_CP_HEAD MX_CP MX_CP "}" ::"r"(to), "l"(desc) : "memory");
+    else if constexpr (N == 4)
+        asm volatile(MX_CP_HEAD MX_CP MX_CP MX_CP MX_CP "}" ::"r"(to), "l"(desc) : "memory");
+    else
+        asm volatile(MX_CP_HEAD MX_CP MX_CP MX_CP MX_CP MX_CP MX_CP MX_CP MX_CP "}" ::"r"(to), "l"(desc) : "memory");
+#undef MX_CP
+#undef MX_CP_HEAD
+}
+
+// Four MMAs of K = 64, the first of which overwrites D unless `more`.  xs: TMEM columns of a
+// token atom.  (In one statement with the election inside: behind a branch on it the compiler
+// issues each in a loop over lanes.)
+template <int BLOCK>
+__device__ __forceinline__ void umma_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                           uint32_t xs, bool more)
+{
+    const uint32_t i2 = idesc | (BLOCK == 32 ? (2u << 29) | (2u << 4) : 0u);  // (second half of an atom)
+    // scale addresses of the four: an atom for each (blocks of 16) or for two (blocks of 32)
+    const uint32_t s1 = BLOCK == 32 ? 0 : 1, s2 = BLOCK == 32 ? 1 : 2, s3 = BLOCK == 32 ? 1 : 3;
+#define MX_MMA(vec)                                                                                                    \
+    asm volatile(                                                                                                      \
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"                                               \
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"                                           \
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"                                           \
+        "elect.sync _|q, 0xffffffff;\n\tsetp.ne.u32 p, %13, 0;\n\t"                                                    \
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::" vec " [%0], %1, %2, %3, [%5], [%9], p;\n\t"  \
+        "setp.ne.u32 p, %3, 0;\n\t"                                                                                    \
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::" vec " [%0], a1, b1, %4, [%6], [%10], p;\n\t" \
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::" vec " [%0], a2, b2, %3, [%7], [%11], p;\n\t" \
+        "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::" vec " [%0], a3, b3, %4, [%8], [%12], p;\n\t" \
+        "}" ::"r"(d),                                                                                                  \
+        "l"(a), "l"(b), "r"(idesc), "r"(i2), "r"(sfa), "r"(sfa + 4 * s1), "r"(sfa + 4 * s2), "r"(sfa + 4 * s3),        \
+        "r"(sfb), "r"(sfb + xs * s1), "r"(sfb + xs * s2), "r"(sfb + xs * s3), "r"((uint32_t)more)                      \
+        : "memory")
+    if constexpr (BLOCK == 32)
+        MX_MMA("2X");
+    else
+        MX_MMA("4X");
+#undef MX_MMA
+}
+
+__device__ __forceinline__ void umma_commit(uint64_t *x)
+{
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(x))
+                 : "memory");
+}
+
+// 4 bytes, the first n of them from src and zeros behind (n 0: src is not read).
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int n)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// Arrive on the barrier once this thread's copies so far have landed (an arrival that its count includes).
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+struct Unit {
+    int e, f;      // matrix, tile of 128 weight rows
+    int tok0, n;   // first token row, rows
+};
+
+struct Walk {
+    int n_units, first, step;
+    int kb0, kb1;  // this rank's stages of the inner dimension
+    int FT;
+    const int *tt, *lo, *len;
+};
+
+template <int NT>
+__device__ __forceinline__ Unit unit_of(const GemmArgs &a, const Walk &w, int u)
+{
+    Unit U;
+    const int tile = u / w.FT;
+    U.f = u - tile * w.FT;
+    int lo = 0, hi = a.E;
+    while (lo + 1 < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (w.tt[mid] <= tile)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    U.e = lo;
+    const int t = tile - w.tt[lo];
+    U.tok0 = w.lo[lo] + NT * t;
+    U.n = min(NT, w.len[lo] - NT * t);
+    return U;
+}
+
+template <int NT, int BLOCK>
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a)
+{
+    constexpr int NA = atoms_of(BLOCK), NH = halves(NT), NW = 4 * NA;  // atoms, token halves, scales of a row and stage
+    constexpr uint32_t kStage = stage_bytes(BLOCK, NT), kTmem = tmem_cols(BLOCK, NT);
+    constexpr int BOX = box_rows(NT);
+    constexpr Tail T = tail_of();
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    // (the same offset in every CTA of the cluster: remote addresses rely on it)
+    uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const int NS = a.stages, cl = a.cl;
+    uint8_t *tail = ring + NS * kStage;
+    int *tab = reinterpret_cast<int *>(tail + T.tab);
+    uint64_t *full = reinterpret_cast<uint64_t *>(tail + T.bars), *empty = full + kMaxStages;
+    uint64_t *tfull = empty + kMaxStages, *tempty = tfull + kAcc;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(tempty + kAcc);
+    volatile int *abort = reinterpret_cast<volatile int *>(tslot + 1);
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
+    const uint32_t rank = cl > 1 ? cluster_rank() : 0;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + i, 1 + 32 * kScaleWarps);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < kAcc; ++i) {
+            mbar_init(tfull + i, 1);
+            mbar_init(tempty + i, kOutWarps);
+        }
+        *abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kOutWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)),
+                     "r"(kTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();  // (nothing before this reads what an earlier launch may still write)
+    Walk w{};
+    {
+        int *tt = tab, *lo = tab + kMaxExperts + 1, *len = lo + kMaxExperts;
+        if (warp == 0)
+            group_table(a.offsets, a.E, a.rows, NT, lane, tt, lo, len);
+        w.tt = tt;
+        w.lo = lo;
+        w.len = len;
+    }
+    fence_before();
+    if (cl > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    fence_after();
+    const int KB = (a.K + kStageCols - 1) / kStageCols;
+    w.FT = (a.N + 127) / 128;
+    w.n_units = w.tt[a.E] * w.FT;
+    w.first = blockIdx.x / cl;
+    w.step = gridDim.x / cl;
+    w.kb0 = KB * rank / cl;
+    w.kb1 = KB * (rank + 1) / cl;
+    const uint32_t tmem = *tslot, tsw = tmem + kAcc * acc_cols(NT), tsx = tsw + 4 * NA;
+
+    if (warp == kOutWarps) {
+        // ------------------------------------------------------ TMA producer
+        int s = 0;
+        uint32_t ph = 1;
+        for (int u = w.first; u < w.n_units; u += w.step) {
+            const Unit U = unit_of<NT>(a, w, u);
+            const int boxes = (U.n + BOX - 1) / BOX;
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                if (!wwait(empty + s, ph, a.err, abort))
+                    goto produced;
+                uint8_t *st = ring + s * kStage;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(full + s, kTile + boxes * BOX * 128);
+                    tma_3d(st, &a.wm, kb * 128, U.f * 128, U.e, full + s);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_2d(st + kTile + b * BOX * 128, &a.xm, kb * 128, U.tok0 + b * BOX, full + s);
+                }
+                __syncwarp();
+                if (++s == NS)
+                    s = 0, ph ^= 1;
+            }
+        }
+    produced:;
+    } else if (warp == kOutWarps + 1) {
+        // --------------------------------------------------------------- MMA
+        int s = 0, b = 0;
+        uint32_t ph = 0, tph = 1;
+        for (int u = w.first; u < w.n_units; u += w.step) {
+            const Unit U = unit_of<NT>(a, w, u);
+            const uint32_t idesc = idesc_e2m1((U.n + 15) & ~15, BLOCK);
+            if (!wwait(tempty + b, tph, a.err, abort))
+                goto issued;
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                if (!wwait(full + s, ph, a.err, abort))
+                    goto issued;
+                // the scales were written by threads' copies; the tensor core reads them through the async proxy
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                fence_after();
+                const uint32_t st = smem_u32(ring + s * kStage), sc = st + kTile + NT * 128;
+                scales_to_tmem<NA>(tsw, scale_desc(sc));
+                scales_to_tmem<NA * NH>(tsx, scale_desc(sc + NA * 512));
+                umma_stage<BLOCK>(tmem + b * acc_cols(NT), sw128_desc(st), sw128_desc(st + kTile), idesc, tsw, tsx, 4 * NH,
+                                  kb != w.kb0);
+                umma_commit(empty + s);
+                if (++s == NS)
+                    s = 0, ph ^= 1;
+            }
+            umma_commit(tfull + b);
+            if (++b == kAcc)
+                b = 0, tph ^= 1;
+        }
+    issued:;
+    } else if (warp > kOutWarps + 1) {
+        // ------------------------------------------------------------ scales
+        // A lane has one word (four scales) of every (32 / NA)-th row.
+        constexpr int RPI = 32 / NA * kScaleWarps;  // rows that the warps cover at once
+        const int word = lane % NA, r0 = (warp - kOutWarps - 2) * (32 / NA) + lane / NA;
+        const int nblk = (a.K + BLOCK - 1) / BLOCK;
+        int s = 0;
+        uint32_t ph = 1;
+        for (int u = w.first; u < w.n_units; u += w.step) {
+            const Unit U = unit_of<NT>(a, w, u);
+            const uint8_t *pw = a.sw + ((int64_t)U.e * a.N + U.f * 128 + r0) * a.sw_ld;
+            const uint8_t *px = a.sx + (int64_t)(U.tok0 + r0) * a.sx_ld;
+            const int nw = a.N - U.f * 128;
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                if (!wwait(empty + s, ph, a.err, abort))
+                    goto scaled;
+                const int c = kb * NW + 4 * word, have = min(max(nblk - c, 0), 4);
+                const uint32_t to = smem_u32(ring + s * kStage) + kTile + NT * 128 + word * 512;
+#pragma unroll
+                for (int i = 0; i < 128 / RPI; ++i) {
+                    const int r = r0 + i * RPI;
+                    const int n = r < nw ? have : 0;
+                    cp_async4(to + (r & 31) * 16 + (r >> 5) * 4, n ? pw + (int64_t)i * RPI * a.sw_ld + c : a.sw, n);
+                }
+                const uint32_t tx = to + NA * 512 + word * 512 * (NH - 1);
+#pragma unroll
+                for (int i = 0; i < (NT + RPI - 1) / RPI; ++i) {
+                    const int r = r0 + i * RPI;
+                    if (i * RPI >= U.n)
+                        break;
+                    const int n = r < U.n ? have : 0;
+                    if (NT % RPI == 0 || r < NT)
+                        cp_async4(tx + (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4,
+                                  n ? px + (int64_t)i * RPI * a.sx_ld + c : a.sx, n);
+                }
+                cp_async_arrive(full + s);
+                if (++s == NS)
+                    s = 0, ph ^= 1;
+            }
+        }
+    scaled:;
+        // (no copy of this thread's is left in flight when its CTA's memory goes to another)
+        cp_async_wait_n(0);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        // ----------------------------------------------------------- results
+        const uint32_t ta = tmem + ((uint32_t)warp << 21);
+        const float tx = a.tx ? __ldg(a.tx) : 1.0f;
+        int b = 0;
+        uint32_t tph = 0;
+        for (int u = w.first; u < w.n_units; u += w.step) {
+            const Unit U = unit_of<NT>(a, w, u);
+            const float tw = a.tw ? __ldg(a.tw + U.e) : 1.0f;
+            if (!wwait(tfull + b, tph, a.err, abort))
+                break;
+            fence_after();
+            const uint32_t tb = ta + b * acc_cols(NT);
+            const int row = warp * 32 + lane, o = U.f * 128 + row;
+            float *part = reinterpret_cast<float *>(ring);
+#pragma unroll 1
+            for (int c0 = 0; c0 < U.n; c0 += 16) {
+                uint32_t r[16];
+                tmem_ld16(tb + c0, r);
+                tmem_wait();
+                if (cl > 1) {  // one unit; every operand has been read
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        part[(c0 + j) * 128 + row] = tmem_value(r[j]) * tx * tw;
+                } else if (o < a.N) {
+                    const int64_t at = (int64_t)(U.tok0 + c0) * a.ldo + o;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c0 + j < U.n) {
+                            const float y = tmem_value(r[j]) * tx * tw;
+                            if (a.out_bf16)
+                                static_cast<uint16_t *>(a.out)[at + j * a.ldo] = f2bf(y);
+                            else
+                                static_cast<float *>(a.out)[at + j * a.ldo] = y;
+                        }
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(tempty + b);
+            if (++b == kAcc)
+                b = 0, tph ^= 1;
+        }
+    }
+
+    if (cl > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp < kOutWarps && w.first < w.n_units && !*abort) {
+            const Unit U = unit_of<NT>(a, w, w.first);
+            const int o = U.f * 128 + 4 * lane;
+            // column n of the tile: CTA n % cl of the cluster, over all ranks in order
+            for (int n = rank + cl * warp; n < U.n; n += cl * kOutWarps) {
+                const uint32_t at = smem_u32(reinterpret_cast<float *>(ring) + n * 128 + 4 * lane);
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                for (int r = 0; r < cl; ++r) {
+                    const float4 p = ld_cluster(mapa(at, r));
+                    v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+                }
+                const int64_t to = (int64_t)(U.tok0 + n) * a.ldo + o;
+                const float y[4] = {v.x, v.y, v.z, v.w};
+                if (a.out_vec && o + 4 <= a.N) {
+                    if (a.out_bf16)
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to) =
+                            make_uint2(f2bf(y[0]) | (uint32_t)f2bf(y[1]) << 16, f2bf(y[2]) | (uint32_t)f2bf(y[3]) << 16);
+                    else
+                        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to) = v;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (o + i < a.N) {
+                            if (a.out_bf16)
+                                static_cast<uint16_t *>(a.out)[to + i] = f2bf(y[i]);
+                            else
+                                static_cast<float *>(a.out)[to + i] = y[i];
+                        }
+                }
+            }
+        }
+    }
+
+    fence_before();
+    if (*abort) {
+        // let this CTA's copies and MMAs in flight land before its memory goes to another
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < 200000ull)
+            __nanosleep(1000);
+    }
+    __syncthreads();
+    if (cl > 1)
+        cluster_sync();
+    fence_after();
+    __syncwarp();
+    if (warp == kOutWarps + 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+}
+
+template <int NT, int BLOCK>
+cudaError_t launch_t(const GemmArgs &a, int grid, cudaStream_t s)
+{
+    const size_t smem = gemm_smem(BLOCK, NT, a.stages);
+    cudaError_t e = smem_optin((const void *)gemm_kernel<NT, BLOCK>, smem);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute at[2];
+    unsigned n = 0;
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+    if (a.cl > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim = {(unsigned)a.cl, 1, 1};
+        ++n;
+    }
+    c.attrs = at;
+    c.numAttrs = n;
+    return cudaLaunchKernelEx(&c, gemm_kernel<NT, BLOCK>, a);
+}
+
+}  // namespace
+
+size_t gemm_smem(int block, int nt, int stages)
+{
+    return 1024 + (size_t)stages * stage_bytes(block, nt) + tail_of().total;
+}
+
+cudaError_t launch_gemm(int block, int nt, const GemmArgs &a, int grid, cudaStream_t s)
+{
+    static_assert(kMaxStages * 2 * 8 + 4 * 8 + 8 <= 512, "barriers");
+    if (a.stages > kMaxStages)
+        return cudaErrorInvalidValue;
+#define MX_CASE(N)                                                                              \
+    if (nt == N)                                                                                \
+        return block == 16 ? launch_t<N, 16>(a, grid, s) : launch_t<N, 32>(a, grid, s)
+    MX_CASE(16);
+    MX_CASE(32);
+    MX_CASE(64);
+    MX_CASE(128);
+    MX_CASE(224);
+#undef MX_CASE
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace fp4
+}  // namespace mx

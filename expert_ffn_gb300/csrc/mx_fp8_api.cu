@@ -1,8 +1,8 @@
 // mx_fp8_api.cu -- the FP8 block-scaled entry points of include/mx_moe.h:
 // argument validation (all of it on the host, before any CUDA call), the
 // workspace plan, and the choice of tile, split and grid for each launch.
-#include "mx_error.h"
 #include "mx_fp8.cuh"
+#include "mx_host.h"
 
 #include <algorithm>
 #include <cmath>
@@ -11,20 +11,7 @@
 using namespace mx;
 using namespace mx::fp8;
 
-namespace {
-
-constexpr int kMaxCols = 1 << 20, kMaxRows = 1 << 28;
-constexpr size_t kErrBytes = 256;      // the workspace's error word
-constexpr int kSmem = 227 * 1024;      // shared memory of a CTA alone on its SM
-constexpr int kSmemHalf = 113 * 1024;  // of one of two
-
-bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
-
-mx_status cuda_fail(cudaError_t e, const char *what)
-{
-    return fail(MX_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
+namespace mx {
 
 int num_sms()
 {
@@ -42,6 +29,14 @@ int num_sms()
     }
     return cache[dev];
 }
+
+}  // namespace mx
+
+namespace {
+
+constexpr int kMaxCols = 1 << 20, kMaxRows = 1 << 28;
+constexpr int kSmem = 227 * 1024;      // shared memory of a CTA alone on its SM
+constexpr int kSmemHalf = 113 * 1024;  // of one of two
 
 // ---------------------------------------------------------------- validation
 
@@ -88,22 +83,6 @@ mx_status check_rows(const mx_fp8_rows *r, const char *name, bool operand)
         return fail(MX_ERR_ALIGNMENT, "%s: address and row pitch must be multiples of 16 bytes", name);
     if (!aligned(r->scales, 4))
         return fail(MX_ERR_ALIGNMENT, "%s: scales must be 4-byte aligned", name);
-    return MX_OK;
-}
-
-mx_status check_dtype(int dtype, const char *name)
-{
-    if (dtype != MX_F32 && dtype != MX_BF16)
-        return fail(MX_ERR_INVALID_ARG, "%s %d is not MX_F32 or MX_BF16", name, dtype);
-    return MX_OK;
-}
-
-mx_status check_ws(const void *ws, size_t have, size_t need)
-{
-    if (!ws || have < need)
-        return fail(MX_ERR_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? have : (size_t)0, need);
-    if (!aligned(ws, 256))
-        return fail(MX_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
     return MX_OK;
 }
 
@@ -159,9 +138,6 @@ int tile_for(int n, int most)
         nt *= 2;
     return nt;
 }
-
-// Whether rows of `out` start at multiples of 16 bytes.
-bool vec16(const void *out, int64_t ldo, int bf16) { return aligned(out, 16) && ldo * (bf16 ? 2 : 4) % 16 == 0; }
 
 mx_status weight_map(CUtensorMap *m, const mx_fp8_matrix &w)
 {

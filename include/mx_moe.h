@@ -412,6 +412,46 @@ MX_API mx_status mx_fp8_quantize(const void *x, int64_t ldx, int dtype, int pow2
                                  void *stream);
 
 /*
+ * RMS norm with the residual's addition and an e4m3 output, before a product or
+ * a block.  Per row of D columns:
+ *   h = x + residual, added in fp32 and rounded to x's type (h = x without one)
+ *   r = 1 / sqrt(mean(h^2) + eps), rounded once to fp32
+ *   y = fl32(fl32(h r) * fl32(weight_offset + weight))   (h r without a weight)
+ *   sum = h;  out = y rounded to its type;  (q, scales) = mx_fp8_quantize of y
+ * The statistic carries about 48 bits, so that r, and with it every output, is
+ * the same on every machine but for rows whose r lies within 2^-40 of a border
+ * between two fp32 numbers.  A row with a NaN is NaN; an infinity makes it and
+ * its e4m3 block NaN and the rest 0.
+ *   x          device [rows][cols] of `dtype` (mx_dtype), row pitch ldx elements
+ *   residual   device, the same, pitch ldr; nullable
+ *   weight     device [cols] of weight_dtype, nullable
+ *   sum        device [rows][cols] of `dtype`, pitch lds, nullable; may be
+ *              residual or x itself (the same address and pitch)
+ *   out        device [rows][cols] of out_dtype, pitch ldo, nullable; may be x
+ *              or residual itself where type, address and pitch are the same
+ *   q          nullable; as for mx_fp8_quantize (its rows and cols: the call's)
+ * At least one of sum, out and q is given; outputs overlap nothing else.
+ */
+typedef struct {
+    const void *x;
+    int64_t ldx;
+    const void *residual;
+    int64_t ldr;
+    const void *weight;
+    void *sum;
+    int64_t lds;
+    void *out;
+    int64_t ldo;
+    const mx_fp8_rows *q;
+    int32_t rows, cols;      /* rows >= 0; 1 <= cols <= 32768 */
+    int32_t dtype, weight_dtype, out_dtype;
+    int32_t pow2;            /* of mx_fp8_quantize */
+    float eps;               /* >= 0 */
+    float weight_offset;
+} mx_rmsnorm;
+MX_API mx_status mx_fp8_rmsnorm(const mx_rmsnorm *args, void *stream);
+
+/*
  * out[r][o] = sum_c x[r][c] w[o][c], one matrix (w->count == 1).
  *   out    device [x->rows][w->rows] of out_dtype (mx_dtype), row pitch ldo elements
  */
@@ -471,6 +511,112 @@ MX_API mx_status mx_fp8_moe_forward(const void *x, int T, const int32_t *topk_id
 
 /* Workspace bytes of mx_fp8_moe_forward for up to T_max tokens (0 on an invalid layer). */
 MX_API size_t mx_fp8_moe_workspace_bytes(const mx_fp8_layer *layer, int T_max);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit operators: e2m1 numbers (0, 1/2, 1, 3/2, 2, 3, 4, 6 and
+ * their negatives), two to a byte, the lower column in the low nibble, with a
+ * scale for each block of a row's columns, in one of two formats:
+ *   MX_FP4_E8M0  blocks of 32, scales 2^(byte - 127) (byte 255: NaN)
+ *   MX_FP4_E4M3  blocks of 16, e4m3 scales (not negative), times one fp32
+ *                factor of the whole tensor (of each matrix)
+ *   value    x[r][c] = q[r][c] * s[r][c / block] * tensor_scale
+ *   product  y[r][o] = tx tw sum_b sx[r][b] sw[o][b] sum_{c in b} qx[r][c] qw[o][c]
+ * The tensor cores multiply numbers and scales and keep the sums in fp32; the
+ * tensors' factors follow, and one rounding to the output type.  The last block
+ * may be shorter; any size from 1 on is accepted.  What is said of the FP8
+ * operators' streams, workspaces, captures and errors holds here.  A result does
+ * not depend on the call's other rows nor on timing; the order of its sums goes
+ * by the call's sizes.
+ * ------------------------------------------------------------------------ */
+typedef enum { MX_FP4_E8M0 = 0, MX_FP4_E4M3 = 1 } mx_fp4_format;
+
+/* `count` matrices [rows][cols], or (count 1) quantised activations. */
+typedef struct {
+    void *q;              /* row pitch ld bytes, matrices rows * ld bytes apart; an odd last column's
+                             spare nibble is zero                                                   */
+    void *scales;         /* a byte for each block, row pitch scale_ld, matrices rows * scale_ld apart */
+    const float *tensor_scale; /* device [count], nullable (1); MX_FP4_E4M3 only; finite, positive and normal */
+    int32_t rows, cols, count;
+    int32_t format;       /* mx_fp4_format */
+    int64_t ld;           /* >= ceil(cols / 2); operands: q and ld multiples of 16 */
+    int64_t scale_ld;     /* >= blocks; operands: scales and scale_ld multiples of 4, and a row's bytes
+                             up to the next multiple of 4 behind its blocks are read, but not used   */
+} mx_fp4_tensor;
+
+/*
+ * Quantise rows.  For each block, a = max |x|:
+ *   MX_FP4_E8M0  s = the smallest power of two with 6 s >= a, within [2^-127, 2^127];
+ *                q = e2m1(x / s)
+ *   MX_FP4_E4M3  s = e4m3(fl32(a * fl32(1 / fl32(6 t)))), at most 448, t = *out->tensor_scale;
+ *                q = e2m1(fl32(x * fl32(1 / fl32(s t)))), zero where fl32(s t) < 2^-126
+ * rounded to nearest, ties to even, at most 6; a zero keeps its sign.  A block with
+ * a NaN or an infinity gets a NaN scale and zeros, and dequantises to NaN.
+ *   x    device [rows][cols] of `dtype`, row pitch ldx elements
+ *   out  count 1; only its rows' ceil(cols / 2) bytes and blocks are written
+ */
+MX_API mx_status mx_fp4_quantize(const void *x, int64_t ldx, int dtype, const mx_fp4_tensor *out, void *stream);
+
+/* out[r][o] = sum_c x[r][c] w[o][c], as mx_fp8_matmul; x and w of one format. */
+MX_API mx_status mx_fp4_matmul(const mx_fp4_tensor *x, const mx_fp4_tensor *w, void *out, int64_t ldo, int out_dtype,
+                               void *stream, void *ws, size_t ws_bytes);
+
+/* The same for rows grouped by matrix, as mx_fp8_grouped_matmul. */
+MX_API mx_status mx_fp4_grouped_matmul(const mx_fp4_tensor *x, const int32_t *offsets, const mx_fp4_tensor *w,
+                                       void *out, int64_t ldo, int out_dtype, void *stream, void *ws,
+                                       size_t ws_bytes);
+
+/* Workspace bytes of the two calls above for up to `rows` rows (0 on an invalid matrix). */
+MX_API size_t mx_fp4_matmul_workspace_bytes(const mx_fp4_tensor *w, int rows);
+
+/* ------------------------------------------------------------------------
+ * Routing from logits: for routers other than the 8-bit affine one of
+ * mx_moe_route.  Per token, with logits l over E experts:
+ *   s = softmax(l) or sigmoid(l);  c = s + bias (c = s without one)
+ *   groups: the experts are n_groups runs of E / n_groups neighbours; a run's
+ *     score is its largest c, or the sum of its two largest; the topk_groups
+ *     highest runs stay (ties to the lower run)
+ *   topk_idx = the top_k highest c of the runs that stay, in descending order,
+ *     ties to the lower expert
+ *   topk_w = scale * s[topk_idx] (the bias only chooses), divided by their sum
+ *     if renormalise
+ * Order is that of exact arithmetic as far as fp64 holds it: scores nearer to
+ * one another than fp32 tells apart are compared in fp64, and without a bias
+ * experts are compared by their logits.  A NaN logit, or a c that is NaN,
+ * ranks as -inf; a NaN logit has s = 0.  Logits of +inf share the softmax, one
+ * without a finite or +inf logit is uniform over its -inf.  Where the chosen
+ * sum to 0, topk_w is 0.
+ * ------------------------------------------------------------------------ */
+typedef enum { MX_SOFTMAX = 0, MX_SIGMOID = 1 } mx_score;
+
+typedef struct {
+    int32_t n_experts;    /* E, 1 <= E <= 512                                             */
+    int32_t top_k;        /* 1 <= top_k <= min(32, experts of topk_groups runs)           */
+    int32_t score;        /* mx_score                                                     */
+    int32_t n_groups;     /* 1 (no groups) to 32, a divisor of E                          */
+    int32_t topk_groups;  /* 1 <= topk_groups <= n_groups                                 */
+    int32_t group_best;   /* 1 or 2 experts make a run's score (2: runs of at least two)  */
+    int32_t renormalise;  /* 0 or 1                                                       */
+    float scale;          /* finite                                                       */
+    const float *bias;    /* device [E], nullable                                         */
+} mx_router;
+
+/*
+ *   logits    device [T][E] of `dtype` (mx_dtype), row pitch ld elements; T >= 0
+ *   topk_idx  device int32 [T][top_k];  topk_w device fp32 [T][top_k]
+ *   counts [E], offsets [E + 1], perm [T * top_k]  device int32, all or none:
+ *             the slots grouped by expert as mx_moe_route groups them
+ *   ws        with counts: mx_route_logits_workspace_bytes, 256-byte aligned,
+ *             prepared by mx_moe_workspace_init; else unused and may be NULL
+ * Outputs overlap no input and not one another.  Asynchronous on `stream` (NULL: the legacy default
+ * stream) on the current device; allocates nothing, may be captured.  Calls
+ * (and captured graphs) that share a workspace must be ordered on the GPU.
+ */
+MX_API mx_status mx_route_logits(const void *logits, int64_t ld, int dtype, int T, const mx_router *router,
+                                 int32_t *topk_idx, float *topk_w, int32_t *counts, int32_t *offsets, int32_t *perm,
+                                 void *stream, void *ws, size_t ws_bytes);
+
+/* Workspace bytes of the call above for up to T_max tokens (0 on an invalid router). */
+MX_API size_t mx_route_logits_workspace_bytes(const mx_router *router, int T_max);
 
 /* Human-readable status and the last error of the calling thread. */
 MX_API const char *mx_status_string(mx_status s);
