@@ -22,7 +22,7 @@ __all__ = ["MxError", "lib", "QLinear", "Ffn", "Sub", "Layout", "Options", "LAYO
            "fp8_quantize", "fp8_matmul", "fp8_grouped_matmul", "fp8_moe_forward", "fp8_matmul_workspace_bytes",
            "fp8_moe_workspace_bytes",
            "RmsnormStruct", "fp8_rmsnorm",
-           "MX_FP4_E8M0", "MX_FP4_E4M3", "Fp4Tensor", "Fp4Weight", "fp4_empty", "fp4_quantize", "fp4_matmul",
+           "MX_FP4_E8M0", "MX_FP4_E4M3", "Fp4Matrix", "Fp4Rows", "Fp4Weight", "fp4_empty", "fp4_quantize", "fp4_matmul",
            "fp4_grouped_matmul", "fp4_matmul_workspace_bytes",
            "MX_SOFTMAX", "MX_SIGMOID", "RouterStruct", "Router", "route_logits", "route_logits_workspace_bytes"]
 
@@ -40,7 +40,8 @@ EXPORTED = ("mx_moe_layer_forward", "mx_moe_layer_forward_ex", "mx_moe_workspace
             "mx_moe_workspace_check", "mx_moe_layer_forward_static", "mx_moe_down_sb_bytes", "mx_moe_pack_down_sb",
             "mx_fp8_quantize", "mx_fp8_matmul", "mx_fp8_grouped_matmul", "mx_fp8_matmul_workspace_bytes",
             "mx_fp8_moe_forward", "mx_fp8_moe_workspace_bytes", "mx_fp8_rmsnorm", "mx_fp4_quantize",
-            "mx_fp4_matmul", "mx_fp4_grouped_matmul", "mx_fp4_matmul_workspace_bytes", "mx_route_logits",
+            "mx_fp4_matmul", "mx_fp4_grouped_matmul", "mx_fp4_matmul_workspace_bytes", "mx_fp4_pack_bytes",
+            "mx_fp4_pack_scales", "mx_route_logits",
             "mx_route_logits_workspace_bytes")
 
 
@@ -102,10 +103,14 @@ class RmsnormStruct(C.Structure):
                 ("eps", C.c_float), ("weight_offset", C.c_float)]
 
 
-class Fp4Tensor(C.Structure):
+class Fp4Matrix(C.Structure):
     _fields_ = [("q", C.c_void_p), ("scales", C.c_void_p), ("tensor_scale", C.c_void_p), ("rows", C.c_int32),
-                ("cols", C.c_int32), ("count", C.c_int32), ("format", C.c_int32), ("ld", C.c_int64),
-                ("scale_ld", C.c_int64)]
+                ("cols", C.c_int32), ("count", C.c_int32), ("format", C.c_int32), ("ld", C.c_int64)]
+
+
+class Fp4Rows(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("scales", C.c_void_p), ("tensor_scale", C.c_void_p), ("rows", C.c_int32),
+                ("cols", C.c_int32), ("format", C.c_int32), ("ld", C.c_int64)]
 
 
 class RouterStruct(C.Structure):
@@ -160,16 +165,19 @@ def lib():
             L.mx_fp8_moe_workspace_bytes.argtypes = [C.POINTER(Fp8LayerStruct), I32]
             L.mx_fp8_moe_workspace_bytes.restype = SZ
             L.mx_fp8_rmsnorm.argtypes = [P, P]  # (P: a RmsnormStruct, by reference or packed)
-            L.mx_fp4_quantize.argtypes = [P, I64, I32, P, P]  # (P: an Fp4Tensor, likewise)
-            L.mx_fp4_matmul.argtypes = [P, C.POINTER(Fp4Tensor), P, I64, I32, P, P, SZ]
-            L.mx_fp4_grouped_matmul.argtypes = [P, P, C.POINTER(Fp4Tensor), P, I64, I32, P, P, SZ]
-            L.mx_fp4_matmul_workspace_bytes.argtypes = [C.POINTER(Fp4Tensor), I32]
+            L.mx_fp4_quantize.argtypes = [P, I64, I32, P, P]  # (P: an Fp4Rows, likewise)
+            L.mx_fp4_matmul.argtypes = [P, C.POINTER(Fp4Matrix), P, I64, I32, P, P, SZ]
+            L.mx_fp4_grouped_matmul.argtypes = [P, P, C.POINTER(Fp4Matrix), P, I64, I32, P, P, SZ]
+            L.mx_fp4_pack_bytes.argtypes = [I32, I32, I32, I32]
+            L.mx_fp4_pack_bytes.restype = SZ
+            L.mx_fp4_pack_scales.argtypes = [P, I64, I32, I32, I32, I32, P, P]
+            L.mx_fp4_matmul_workspace_bytes.argtypes = [C.POINTER(Fp4Matrix), I32]
             L.mx_fp4_matmul_workspace_bytes.restype = SZ
             L.mx_route_logits.argtypes = [P, I64, I32, I32, C.POINTER(RouterStruct), P, P, P, P, P, P, P, SZ]
             L.mx_route_logits_workspace_bytes.argtypes = [C.POINTER(RouterStruct), I32]
             L.mx_route_logits_workspace_bytes.restype = SZ
             for name in ("mx_fp8_rmsnorm", "mx_fp4_quantize", "mx_fp4_matmul", "mx_fp4_grouped_matmul",
-                         "mx_route_logits",
+                         "mx_fp4_pack_scales", "mx_route_logits",
                          "mx_fp8_quantize", "mx_fp8_matmul", "mx_fp8_grouped_matmul", "mx_fp8_moe_forward",
                          "mx_moe_layer_forward", "mx_moe_layer_forward_ex", "mx_moe_layer_forward_static",
                          "mx_moe_workspace_init", "mx_moe_pack_down_sb",
@@ -405,7 +413,7 @@ def profile_read(reset: bool = True) -> dict:
 
 _ROWS = _struct.Struct("@PPiiqqq")  # Fp8Rows
 _NORM = _struct.Struct("@PqPqPPqPqPiiiiiiff")  # RmsnormStruct
-_FP4 = _struct.Struct("@PPPiiiiqq")  # Fp4Tensor
+_FP4 = _struct.Struct("@PPPiiiq")  # Fp4Rows
 _t = None  # names of torch, filled on first use
 
 
@@ -678,19 +686,18 @@ def _up(n, m):
 
 
 def _fp4_rows(t, q, scales, cols, factor, dev):
-    """(rows, packed Fp4Tensor) of quantised activations."""
+    """(rows, packed Fp4Rows) of quantised activations."""
     fmt, block = _fp4_format(t, scales, "q")
     shape, strides = q.shape, q.stride()
     if q.dtype is not t.u8 or len(shape) != 2 or shape[1] != (cols + 1) // 2 or (strides[1] != 1 and shape[1] > 1):
         raise MxError(-1, f"q must be uint8 [rows, {(cols + 1) // 2}] with contiguous rows")
-    rows, nb = shape[0], -(-cols // block)
-    if scales.shape != (rows, nb) or (nb > 1 and scales.stride(1) != 1):
-        raise MxError(-1, f"scales must be [{rows}, {nb}] with contiguous rows")
+    rows = shape[0]
+    if scales.shape != ((cols + 255) // 256, rows, 256 // block) or not scales.is_contiguous():
+        raise MxError(-1, f"scales must be contiguous [{(cols + 255) // 256}, {rows}, {256 // block}]")
     if q.get_device() != dev or scales.get_device() != dev:
         raise MxError(-1, "all tensors must be on one device")
-    # (the stride of a single row means nothing)
-    ld, lds = (strides[0], scales.stride(0)) if rows > 1 else (_up(shape[1], 16), _up(nb, 4))
-    return rows, _FP4.pack(q.data_ptr(), scales.data_ptr(), _factor(t, factor, 1, fmt, dev), rows, cols, 1, fmt, ld, lds)
+    return rows, _FP4.pack(q.data_ptr(), scales.data_ptr(), _factor(t, factor, 1, fmt, dev), rows, cols, fmt,
+                           strides[0] if rows > 1 else _up(shape[1], 16))  # (the stride of a single row means nothing)
 
 
 def _factor(t, factor, count, fmt, dev):
@@ -705,10 +712,12 @@ def _factor(t, factor, count, fmt, dev):
 class Fp4Weight:
     """Microscaled e2m1 matrices on the device: ``w`` uint8 [count,] rows, ceil(cols / 2), two numbers to a byte, rows
     at multiples of 16 bytes; ``scales`` float8_e4m3fn (a block of 16 columns each) or float8_e8m0fnu (32) [count,]
-    rows, blocks, rows at multiples of 4 bytes; ``tensor_scale`` float32 [count] or None (e4m3 only).  ``cols`` is
-    needed where it is odd.  The tensors are kept and read by every call, not copied."""
+    rows, blocks; ``tensor_scale`` float32 [count] or None (e4m3 only).  ``cols`` is needed where it is odd.  ``w`` and
+    ``tensor_scale`` are kept and read by every call; of ``scales`` the products read a copy in their own order, made
+    here on ``stream`` (mx_fp4_pack_scales)."""
 
-    def __init__(self, w, scales, tensor_scale=None, cols=None):
+    def __init__(self, w, scales, tensor_scale=None, cols=None, stream=None):
+        import torch
         t = _t or _torch()
         _need(w.dtype is t.u8 and w.dim() in (2, 3), "w must be uint8 [count,] rows, bytes")
         fmt, block = _fp4_format(t, scales, "w")
@@ -719,33 +728,40 @@ class Fp4Weight:
         nb = -(-cols // block)
         _need(tuple(scales.shape) == (*w.shape[:-1], nb), f"scales must be [{count}, {rows}, {nb}]")
         ld = w.stride(-2) if rows > 1 else w.stride(0) if count > 1 else _up(nbytes, 16)
-        lds = scales.stride(-2) if rows > 1 else scales.stride(0) if count > 1 else _up(nb, 4)
+        lds = scales.stride(-2) if rows > 1 else scales.stride(0) if count > 1 else nb
         _need((w.stride(-1) == 1 or nbytes == 1) and (scales.stride(-1) == 1 or nb == 1), "rows must be contiguous")
         _need(count == 1 or (w.stride(0) == rows * ld and scales.stride(0) == rows * lds),
               "the matrices must follow one another")
         dev = w.get_device()
         _need(scales.get_device() == dev, f"scales must be on {w.device}")
-        self.w, self.scales, self.tensor_scale = w, scales, tensor_scale
-        self.c = Fp4Tensor(w.data_ptr(), scales.data_ptr(), _factor(t, tensor_scale, count, fmt, dev) or None, rows, cols,
-                           count, fmt, ld, lds)
+        factor = _factor(t, tensor_scale, count, fmt, dev)
+        n = lib().mx_fp4_pack_bytes(rows, cols, count, fmt)
+        if n == 0:
+            _check(-1)
+        self.w, self.tensor_scale = w, tensor_scale
+        self.packed = torch.empty(n, dtype=torch.uint8, device=w.device)
+        _on(dev, lib().mx_fp4_pack_scales, scales.data_ptr(), lds, rows, cols, count, fmt, self.packed.data_ptr(),
+            _stream_on(dev, stream))
+        self.c = Fp4Matrix(w.data_ptr(), self.packed.data_ptr(), factor or None, rows, cols, count, fmt, ld)
         self.ref, self.rows, self.cols, self.count, self.dev = C.byref(self.c), rows, cols, count, dev
 
 
 def fp4_empty(rows: int, cols: int, block: int, device="cuda"):
-    """Uninitialised (q, scales) for fp4_quantize, pitched as the products want them; block 16 (e4m3 scales) or 32
-    (e8m0)."""
+    """Uninitialised (q, scales) for fp4_quantize as the products want them: q uint8 [rows, ceil(cols / 2)], rows at
+    multiples of 16 bytes; scales [ceil(cols / 256), rows, 256 / block], float8_e4m3fn for block 16, float8_e8m0fnu for
+    32."""
     import torch
     _need(block in (16, 32) and rows >= 0 and cols >= 1, "block must be 16 or 32, rows >= 0, cols >= 1")
-    nbytes, nb = (cols + 1) // 2, -(-cols // block)
+    nbytes = (cols + 1) // 2
     q = torch.empty(rows, _up(nbytes, 16), dtype=torch.uint8, device=device)[:, :nbytes]
-    s = torch.empty(rows, _up(nb, 4), dtype=torch.uint8, device=device)
-    return q, s.view(torch.float8_e4m3fn if block == 16 else torch.float8_e8m0fnu)[:, :nb]
+    s = torch.empty(-(-cols // 256), rows, 256 // block, dtype=torch.uint8, device=device)
+    return q, s.view(torch.float8_e4m3fn if block == 16 else torch.float8_e8m0fnu)
 
 
 def fp4_quantize(x, q, scales, tensor_scale=None, stream=None):
-    """Quantise the rows of ``x`` (float32 or bfloat16 [rows, cols]) into ``q`` (uint8 [rows, ceil(cols / 2)]) and
-    ``scales`` (float8_e4m3fn for blocks of 16 columns, with the optional float32 ``tensor_scale`` on the device, or
-    float8_e8m0fnu for blocks of 32), see fp4_empty."""
+    """Quantise the rows of ``x`` (float32 or bfloat16 [rows, cols]) into ``q`` and ``scales`` of fp4_empty: e4m3 scales
+    for blocks of 16 columns, with the optional float32 ``tensor_scale`` on the device, or e8m0 scales for blocks of
+    32."""
     t = _t or _torch()
     dev = x.get_device()
     if x.dim() != 2:

@@ -18,8 +18,8 @@ struct QuantArgs {
     int64_t ldx;
     int rows, cols, bf16;
     int vx, vq;     // pieces of x, of q may be moved as vectors
-    uint8_t *q, *scales;
-    int64_t ldq, lds;
+    uint8_t *q, *scales;  // scales [ceil(cols / 256)][rows][256 / block]
+    int64_t ldq;
     const float *tensor_scale;  // e4m3; nullable
 };
 cudaError_t launch_quantize(int block, const QuantArgs &a, int sms, cudaStream_t s);
@@ -28,8 +28,7 @@ struct GemmArgs {
     CUtensorMap wm, xm;      // packed bytes of the weights [E][N][K / 2] and of the rows
     int rows, K, N, E;
     const int32_t *offsets;  // [E + 1] first row of each matrix's group, nullable: one group of all rows
-    const uint8_t *sx, *sw;  // scales, row pitches in bytes
-    int64_t sx_ld, sw_ld;
+    const uint8_t *sx, *sw;  // scales of the rows [stage][rows][256 / block], of the weights as packed
     const float *tx, *tw;    // factors of the rows and of each matrix, nullable
     void *out;
     int64_t ldo;
@@ -37,6 +36,17 @@ struct GemmArgs {
     unsigned *err;
     int stages, cl;          // ring depth, cluster size (split of the inner dimension)
 };
+
+struct PackArgs {
+    const uint8_t *scales;  // [count][rows][nb], row pitch ld
+    int64_t ld;
+    int rows, nb, count, block;
+    uint8_t *out;           // [count][tiles of 128 rows][stages][512-byte pieces]
+};
+cudaError_t launch_pack(const PackArgs &a, cudaStream_t s);
+
+__host__ __device__ constexpr int stages_of(int cols) { return (cols + kStageCols - 1) / kStageCols; }
+__host__ __device__ constexpr int atoms_of(int block) { return 64 / block; }  // pieces of 128 rows in a stage
 
 // Token tiles of launch_gemm: 16, 32, 64, 128, 224.
 cudaError_t launch_gemm(int block, int nt, const GemmArgs &a, int grid, cudaStream_t s);

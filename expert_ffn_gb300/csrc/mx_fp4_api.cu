@@ -17,43 +17,69 @@ constexpr int kSmem = 227 * 1024;  // shared memory of a CTA alone on its SM
 
 int block_of(int format) { return format == MX_FP4_E4M3 ? 16 : 32; }
 
-mx_status check_tensor(const mx_fp4_tensor *t, const char *name, bool operand, bool matrix)
+mx_status check_format(int format, const float *tensor_scale, const char *name)
 {
-    if (!t)
-        return fail(MX_ERR_INVALID_ARG, "%s is NULL", name);
-    if (t->format != MX_FP4_E8M0 && t->format != MX_FP4_E4M3)
-        return fail(MX_ERR_INVALID_ARG, "%s: format %d is not MX_FP4_E8M0 or MX_FP4_E4M3", name, t->format);
-    if (t->tensor_scale && t->format != MX_FP4_E4M3)
+    if (format != MX_FP4_E8M0 && format != MX_FP4_E4M3)
+        return fail(MX_ERR_INVALID_ARG, "%s: format %d is not MX_FP4_E8M0 or MX_FP4_E4M3", name, format);
+    if (tensor_scale && format != MX_FP4_E4M3)
         return fail(MX_ERR_INVALID_ARG, "%s: a tensor_scale belongs to MX_FP4_E4M3", name);
-    if (t->cols < 1 || t->cols > kMaxCols)
-        return fail(MX_ERR_UNSUPPORTED, "%s: %d columns must be within [1, %d]", name, t->cols, kMaxCols);
-    if (matrix) {
-        if (t->rows < 1 || t->rows > kMaxCols)
-            return fail(MX_ERR_UNSUPPORTED, "%s: %d rows must be within [1, %d]", name, t->rows, kMaxCols);
-        if (t->count < 1 || t->count > kMaxExperts)
-            return fail(MX_ERR_UNSUPPORTED, "%s: %d matrices, at most %d are supported", name, t->count, kMaxExperts);
-    } else {
-        if (t->rows < 0 || t->rows > kMaxRows)
-            return fail(MX_ERR_INVALID_ARG, "%s: %d rows must be within [0, %d]", name, t->rows, kMaxRows);
-        if (t->count != 1)
-            return fail(MX_ERR_INVALID_ARG, "%s: count %d must be 1", name, t->count);
-    }
-    const int64_t bytes = ((int64_t)t->cols + 1) / 2, b = block_of(t->format), blocks = (t->cols + b - 1) / b;
-    if (t->ld < bytes || t->scale_ld < blocks)
-        return fail(MX_ERR_INVALID_ARG, "%s: row pitches %lld and %lld are below its %lld bytes and %lld scales", name,
-                    (long long)t->ld, (long long)t->scale_ld, (long long)bytes, (long long)blocks);
-    if (t->ld > 4 * (int64_t)kMaxCols || t->scale_ld > 4 * (int64_t)kMaxCols)
-        return fail(MX_ERR_UNSUPPORTED, "%s: a row pitch is above %d", name, 4 * kMaxCols);
-    if (t->rows == 0)
-        return MX_OK;
-    if (!t->q || !t->scales)
-        return fail(MX_ERR_INVALID_ARG, "%s has a NULL pointer", name);
-    if (operand && (!aligned(t->q, 16) || t->ld % 16))
-        return fail(MX_ERR_ALIGNMENT, "%s: address and row pitch must be multiples of 16 bytes", name);
-    if (operand && (!aligned(t->scales, 4) || t->scale_ld % 4))
-        return fail(MX_ERR_ALIGNMENT, "%s: scales and their row pitch must be multiples of 4 bytes", name);
-    if (!aligned(t->tensor_scale, 4))
+    if (!aligned(tensor_scale, 4))
         return fail(MX_ERR_ALIGNMENT, "%s: tensor_scale must be 4-byte aligned", name);
+    return MX_OK;
+}
+
+mx_status check_sizes(int rows, int cols, int count, const char *name)
+{
+    if (rows < 1 || cols < 1 || rows > kMaxCols || cols > kMaxCols)
+        return fail(MX_ERR_UNSUPPORTED, "%s: shape [%d, %d] must be within [1, %d]", name, rows, cols, kMaxCols);
+    if (count < 1 || count > kMaxExperts)
+        return fail(MX_ERR_UNSUPPORTED, "%s: %d matrices, at most %d are supported", name, count, kMaxExperts);
+    return MX_OK;
+}
+
+mx_status check_pitch(int64_t ld, int cols, const char *name)
+{
+    if (ld < (cols + 1) / 2)
+        return fail(MX_ERR_INVALID_ARG, "%s: row pitch %lld is below %d bytes", name, (long long)ld, (cols + 1) / 2);
+    if (ld > 4 * (int64_t)kMaxCols)
+        return fail(MX_ERR_UNSUPPORTED, "%s: row pitch %lld is above %d", name, (long long)ld, 4 * kMaxCols);
+    return MX_OK;
+}
+
+mx_status check_matrix(const mx_fp4_matrix *m, const char *name)
+{
+    mx_status st;
+    if (!m)
+        return fail(MX_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!m->q || !m->scales)
+        return fail(MX_ERR_INVALID_ARG, "%s has a NULL pointer", name);
+    if ((st = check_format(m->format, m->tensor_scale, name)) != MX_OK ||
+        (st = check_sizes(m->rows, m->cols, m->count, name)) != MX_OK || (st = check_pitch(m->ld, m->cols, name)) != MX_OK)
+        return st;
+    if (!aligned(m->q, 16) || m->ld % 16 || !aligned(m->scales, 16))
+        return fail(MX_ERR_ALIGNMENT, "%s: addresses and the row pitch must be multiples of 16 bytes", name);
+    return MX_OK;
+}
+
+mx_status check_rows(const mx_fp4_rows *r, const char *name, bool operand)
+{
+    mx_status st;
+    if (!r)
+        return fail(MX_ERR_INVALID_ARG, "%s is NULL", name);
+    if (r->rows < 0 || r->rows > kMaxRows)
+        return fail(MX_ERR_INVALID_ARG, "%s: %d rows must be within [0, %d]", name, r->rows, kMaxRows);
+    if (r->cols < 1 || r->cols > kMaxCols)
+        return fail(MX_ERR_UNSUPPORTED, "%s: %d columns must be within [1, %d]", name, r->cols, kMaxCols);
+    if ((st = check_format(r->format, r->tensor_scale, name)) != MX_OK || (st = check_pitch(r->ld, r->cols, name)) != MX_OK)
+        return st;
+    if (r->rows == 0)
+        return MX_OK;
+    if (!r->q || !r->scales)
+        return fail(MX_ERR_INVALID_ARG, "%s has a NULL pointer", name);
+    if (operand && (!aligned(r->q, 16) || r->ld % 16))
+        return fail(MX_ERR_ALIGNMENT, "%s: address and row pitch must be multiples of 16 bytes", name);
+    if (!aligned(r->scales, 16))
+        return fail(MX_ERR_ALIGNMENT, "%s: scales must be 16-byte aligned", name);
     return MX_OK;
 }
 
@@ -99,11 +125,11 @@ Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
     return c;
 }
 
-mx_status product(const mx_fp4_tensor *x, const int32_t *offsets, const mx_fp4_tensor *w, void *out, int64_t ldo,
+mx_status product(const mx_fp4_rows *x, const int32_t *offsets, const mx_fp4_matrix *w, void *out, int64_t ldo,
                   int out_dtype, void *stream, void *ws, size_t ws_bytes)
 {
     mx_status st;
-    if ((st = check_tensor(x, "x", true, false)) != MX_OK || (st = check_tensor(w, "w", true, true)) != MX_OK ||
+    if ((st = check_rows(x, "x", true)) != MX_OK || (st = check_matrix(w, "w")) != MX_OK ||
         (st = check_dtype(out_dtype, "out_dtype")) != MX_OK)
         return st;
     if (x->cols != w->cols || x->format != w->format)
@@ -121,7 +147,7 @@ mx_status product(const mx_fp4_tensor *x, const int32_t *offsets, const mx_fp4_t
         return fail(MX_ERR_ALIGNMENT, "out is misaligned");
     if ((st = check_ws(ws, ws_bytes, kErrBytes)) != MX_OK)
         return st;
-    const int block = block_of(w->format), FT = (w->rows + 127) / 128, KB = (w->cols + kStageCols - 1) / kStageCols;
+    const int block = block_of(w->format), FT = (w->rows + 127) / 128, KB = stages_of(w->cols);
     const Choice c = choose(x->rows, offsets != nullptr, w->count, FT, KB, num_sms());
     GemmArgs g{};
     g.rows = x->rows;
@@ -131,8 +157,6 @@ mx_status product(const mx_fp4_tensor *x, const int32_t *offsets, const mx_fp4_t
     g.offsets = offsets;
     g.sx = static_cast<const uint8_t *>(x->scales);
     g.sw = static_cast<const uint8_t *>(w->scales);
-    g.sx_ld = x->scale_ld;
-    g.sw_ld = w->scale_ld;
     g.tx = x->tensor_scale;
     g.tw = w->tensor_scale;
     g.out = out;
@@ -156,10 +180,10 @@ mx_status product(const mx_fp4_tensor *x, const int32_t *offsets, const mx_fp4_t
 
 }  // namespace
 
-extern "C" mx_status mx_fp4_quantize(const void *x, int64_t ldx, int dtype, const mx_fp4_tensor *out, void *stream)
+extern "C" mx_status mx_fp4_quantize(const void *x, int64_t ldx, int dtype, const mx_fp4_rows *out, void *stream)
 {
     mx_status st;
-    if ((st = check_dtype(dtype, "dtype")) != MX_OK || (st = check_tensor(out, "out", false, false)) != MX_OK)
+    if ((st = check_dtype(dtype, "dtype")) != MX_OK || (st = check_rows(out, "out", false)) != MX_OK)
         return st;
     if (ldx < out->cols)
         return fail(MX_ERR_INVALID_ARG, "x: row pitch %lld is below its %d columns", (long long)ldx, out->cols);
@@ -182,13 +206,39 @@ extern "C" mx_status mx_fp4_quantize(const void *x, int64_t ldx, int dtype, cons
     a.q = static_cast<uint8_t *>(out->q);
     a.scales = static_cast<uint8_t *>(out->scales);
     a.ldq = out->ld;
-    a.lds = out->scale_ld;
     a.tensor_scale = out->tensor_scale;
     const cudaError_t e = launch_quantize(block_of(out->format), a, num_sms(), static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP4 quantisation");
 }
 
-extern "C" mx_status mx_fp4_matmul(const mx_fp4_tensor *x, const mx_fp4_tensor *w, void *out, int64_t ldo, int out_dtype,
+extern "C" size_t mx_fp4_pack_bytes(int rows, int cols, int count, int format)
+{
+    if (check_format(format, nullptr, "scales") != MX_OK || check_sizes(rows, cols, count, "scales") != MX_OK)
+        return 0;
+    return (size_t)count * ((rows + 127) / 128) * stages_of(cols) * atoms_of(block_of(format)) * 512;
+}
+
+extern "C" mx_status mx_fp4_pack_scales(const void *scales, int64_t ld, int rows, int cols, int count, int format, void *out,
+                                        void *stream)
+{
+    mx_status st;
+    if ((st = check_format(format, nullptr, "scales")) != MX_OK || (st = check_sizes(rows, cols, count, "scales")) != MX_OK)
+        return st;
+    const int block = block_of(format), nb = (cols + block - 1) / block;
+    if (ld < nb)
+        return fail(MX_ERR_INVALID_ARG, "scales: row pitch %lld is below %d blocks", (long long)ld, nb);
+    if (ld > 4 * (int64_t)kMaxCols)
+        return fail(MX_ERR_UNSUPPORTED, "scales: row pitch %lld is above %d", (long long)ld, 4 * kMaxCols);
+    if (!scales || !out)
+        return fail(MX_ERR_INVALID_ARG, "scales and out must not be NULL");
+    if (!aligned(out, 16))
+        return fail(MX_ERR_ALIGNMENT, "out must be 16-byte aligned");
+    PackArgs a{static_cast<const uint8_t *>(scales), ld, rows, nb, count, block, static_cast<uint8_t *>(out)};
+    const cudaError_t e = launch_pack(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP4 scales");
+}
+
+extern "C" mx_status mx_fp4_matmul(const mx_fp4_rows *x, const mx_fp4_matrix *w, void *out, int64_t ldo, int out_dtype,
                                    void *stream, void *ws, size_t ws_bytes)
 {
     if (w && w->count != 1)
@@ -196,8 +246,8 @@ extern "C" mx_status mx_fp4_matmul(const mx_fp4_tensor *x, const mx_fp4_tensor *
     return product(x, nullptr, w, out, ldo, out_dtype, stream, ws, ws_bytes);
 }
 
-extern "C" mx_status mx_fp4_grouped_matmul(const mx_fp4_tensor *x, const int32_t *offsets, const mx_fp4_tensor *w,
-                                           void *out, int64_t ldo, int out_dtype, void *stream, void *ws, size_t ws_bytes)
+extern "C" mx_status mx_fp4_grouped_matmul(const mx_fp4_rows *x, const int32_t *offsets, const mx_fp4_matrix *w, void *out,
+                                           int64_t ldo, int out_dtype, void *stream, void *ws, size_t ws_bytes)
 {
     if (!offsets)
         return fail(MX_ERR_INVALID_ARG, "offsets is NULL");
@@ -206,9 +256,9 @@ extern "C" mx_status mx_fp4_grouped_matmul(const mx_fp4_tensor *x, const int32_t
     return product(x, offsets, w, out, ldo, out_dtype, stream, ws, ws_bytes);
 }
 
-extern "C" size_t mx_fp4_matmul_workspace_bytes(const mx_fp4_tensor *w, int rows)
+extern "C" size_t mx_fp4_matmul_workspace_bytes(const mx_fp4_matrix *w, int rows)
 {
-    if (check_tensor(w, "w", true, true) != MX_OK)
+    if (check_matrix(w, "w") != MX_OK)
         return 0;
     if (rows < 0) {
         fail(MX_ERR_INVALID_ARG, "%d rows", rows);

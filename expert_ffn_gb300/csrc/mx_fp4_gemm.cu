@@ -10,17 +10,20 @@
 // thousands: a short group costs what its rows need.
 //
 // A stage of the ring is 256 columns: 128 bytes of each row (SWIZZLE_128B) and their
-// scales, 16 or 8 bytes a row.  The hardware wants the scales of 128 rows as 32 lines of 16 bytes,
-// line i with four scales of each of the rows i, 32 + i, 64 + i, 96 + i (512 bytes for four blocks of columns); they lie row by
-// row in memory, at rows that a group's offsets make arbitrary, so two warps gather them with 4-byte
-// asynchronous copies, whose completion is counted on the stage's own barrier.
+// scales, 16 or 8 bytes a row.  The tensor core wants the scales of 128 rows and four blocks as 32
+// lines of 16 bytes, line i with those of the rows i, 32 + i, 64 + i, 96 + i.  The weights' are laid out
+// so once (mx_fp4_pack_scales) and come by one bulk copy.  A token tile may begin at any row, so a
+// lane loads the 16 bytes of four rows 32 apart (neighbouring lanes neighbouring rows: the
+// quantiser keeps a stage's scales of all rows together) and stores four lines, a transposition
+// that costs no instruction.  (Both gathered from rows in memory by 4-byte asynchronous copies
+// bounded the kernel: 4096^3 82 us, without them 52.)
 //
 // Warps:
 //   0-3  results: TMEM (lane quadrant = warp) to global memory
 //   4    TMA producer: weight and token tiles
 //   5    MMA: per stage the copies of its scales to TMEM (tcgen05.cp, in order with the
 //        MMAs) and four MMAs (K = 64)
-//   6-7  scales
+//   6-7  the tokens' scales, every other stage each
 // Two TMEM accumulators: a tile's results leave while the next one is summed.  Few units: a
 // cluster of `cl` CTAs splits the inner dimension of one unit, and its partial sums are added
 // through distributed shared memory in rank order.
@@ -29,6 +32,8 @@
 // CTA's work.
 #include "mx_fp4.cuh"
 #include "mx_fp8_tc.cuh"
+
+#include <type_traits>
 
 namespace mx {
 namespace fp4 {
@@ -58,7 +63,6 @@ constexpr int kOutWarps = 4, kScaleWarps = 2, kThreads = (kOutWarps + 2 + kScale
 constexpr int kAcc = 2;                // TMEM accumulators
 constexpr int kMaxStages = 12;
 
-constexpr int atoms_of(int block) { return 64 / block; }  // 512-byte scale atoms of 128 rows in a stage
 constexpr int halves(int nt) { return (nt + 127) / 128; }
 constexpr uint32_t scale_bytes(int block, int nt) { return atoms_of(block) * 512 * (1 + halves(nt)); }
 constexpr uint32_t stage_bytes(int block, int nt) { return kTile + nt * 128 + scale_bytes(block, nt); }
@@ -100,11 +104,11 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr)
     return (uint64_t)((saddr & 0x3FFFF) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
 }
 
-// `%2` scale atoms to TMEM, four columns each.  One elected lane of a converged warp.
+// N scale pieces to TMEM, four columns each.  One elected lane of a converged warp.
 template <int N>
 __device__ __forceinline__ void scales_to_tmem(uint32_t to, uint64_t desc)
 {
-    static_assert(N == 2 || N == 4 || N == 8, "atoms");
+    static_assert(N == 2 || N == 4 || N == 8, "pieces");
 #define MX_CP "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [t], d;\n\tadd.u32 t, t, 4;\n\tadd.s64 d, d, 32;\n\t"
 #define MX_CP_HEAD "{\n\t.reg .pred q;\n\t.reg .b32 t;\n\t.reg .b64 d;\n\tmov.b32 t, %0;\n\tmov.b64 d, %1;\n\telect.sync _|q, 0xffffffff;\n\t"
     if constexpr (N == 2)
@@ -118,14 +122,14 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t to, uint64_t desc)
 }
 
 // Four MMAs of K = 64, the first of which overwrites D unless `more`.  xs: TMEM columns of a
-// token atom.  (In one statement with the election inside: behind a branch on it the compiler
+// token piece.  (In one statement with the election inside: behind a branch on it the compiler
 // issues each in a loop over lanes.)
 template <int BLOCK>
 __device__ __forceinline__ void umma_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                            uint32_t xs, bool more)
 {
-    const uint32_t i2 = idesc | (BLOCK == 32 ? (2u << 29) | (2u << 4) : 0u);  // (second half of an atom)
-    // scale addresses of the four: an atom for each (blocks of 16) or for two (blocks of 32)
+    const uint32_t i2 = idesc | (BLOCK == 32 ? (2u << 29) | (2u << 4) : 0u);  // (second half of a piece)
+    // scale addresses of the four: a piece for each (blocks of 16) or for two (blocks of 32)
     const uint32_t s1 = BLOCK == 32 ? 0 : 1, s2 = BLOCK == 32 ? 1 : 2, s3 = BLOCK == 32 ? 1 : 3;
 #define MX_MMA(vec)                                                                                                    \
     asm volatile(                                                                                                      \
@@ -154,18 +158,6 @@ __device__ __forceinline__ void umma_commit(uint64_t *x)
     asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
                  "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(x))
                  : "memory");
-}
-
-// 4 bytes, the first n of them from src and zeros behind (n 0: src is not read).
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int n)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-
-// Arrive on the barrier once this thread's copies so far have landed (an arrival that its count includes).
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 struct Unit {
@@ -204,7 +196,7 @@ __device__ __forceinline__ Unit unit_of(const GemmArgs &a, const Walk &w, int u)
 template <int NT, int BLOCK>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a)
 {
-    constexpr int NA = atoms_of(BLOCK), NH = halves(NT), NW = 4 * NA;  // atoms, token halves, scales of a row and stage
+    constexpr int NA = atoms_of(BLOCK), NH = halves(NT);  // scale pieces of 128 rows, of a stage; token halves
     constexpr uint32_t kStage = stage_bytes(BLOCK, NT), kTmem = tmem_cols(BLOCK, NT);
     constexpr int BOX = box_rows(NT);
     constexpr Tail T = tail_of();
@@ -223,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, 1 + 32 * kScaleWarps);
+            mbar_init(full + i, 2);  // copies, tokens' scales
             mbar_init(empty + i, 1);
         }
         for (int i = 0; i < kAcc; ++i) {
@@ -255,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     else
         __syncthreads();
     fence_after();
-    const int KB = (a.K + kStageCols - 1) / kStageCols;
+    const int KB = stages_of(a.K);
     w.FT = (a.N + 127) / 128;
     w.n_units = w.tt[a.E] * w.FT;
     w.first = blockIdx.x / cl;
@@ -276,8 +268,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     goto produced;
                 uint8_t *st = ring + s * kStage;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(full + s, kTile + boxes * BOX * 128);
+                    mbar_arrive_expect_tx(full + s, kTile + boxes * BOX * 128 + NA * 512);
                     tma_3d(st, &a.wm, kb * 128, U.f * 128, U.e, full + s);
+                    bulk_g2s(st + kTile + NT * 128, a.sw + (((int64_t)U.e * w.FT + U.f) * KB + kb) * (NA * 512), NA * 512,
+                             full + s);
                     for (int b = 0; b < boxes; ++b)
                         tma_2d(st + kTile + b * BOX * 128, &a.xm, kb * 128, U.tok0 + b * BOX, full + s);
                 }
@@ -299,8 +293,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
                 if (!wwait(full + s, ph, a.err, abort))
                     goto issued;
-                // the scales were written by threads' copies; the tensor core reads them through the async proxy
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 fence_after();
                 const uint32_t st = smem_u32(ring + s * kStage), sc = st + kTile + NT * 128;
                 scales_to_tmem<NA>(tsw, scale_desc(sc));
@@ -318,57 +310,83 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     issued:;
     } else if (warp > kOutWarps + 1) {
         // ------------------------------------------------------------ scales
-        // A lane has one word (four scales) of every (32 / NA)-th row.
-        constexpr int RPI = 32 / NA * kScaleWarps;  // rows that the warps cover at once
-        const int word = lane % NA, r0 = (warp - kOutWarps - 2) * (32 / NA) + lane / NA;
-        const int nblk = (a.K + BLOCK - 1) / BLOCK;
-        int s = 0;
+        constexpr int AHEAD = 2;  // stages of this warp under way in registers
+        using Row = typename std::conditional<BLOCK == 16, uint4, uint2>::type;  // a row's scales of a stage
+        const int me = warp - kOutWarps - 2;
+        Row v[AHEAD][4 * NH];
+        int fu = w.first, fkb = w.kb0 + me;  // what is fetched next
+        auto fetch = [&](Row (&d)[4 * NH]) {
+            while (fu < w.n_units && fkb >= w.kb1) {  // (a unit's stages run on into the next one's)
+                fkb -= w.kb1 - w.kb0;
+                fu += w.step;
+            }
+            if (fu >= w.n_units)
+                return;
+            const Unit U = unit_of<NT>(a, w, fu);
+            // (plain loads: the read-only path must not be used by a launch that began before its
+            // predecessor's end)
+            const Row *p = reinterpret_cast<const Row *>(a.sx) + (int64_t)fkb * a.rows;
+#pragma unroll
+            for (int i = 0; i < 4 * NH; ++i)
+                if (32 * i < NT && 32 * i < U.n)  // (a row behind the last: its own column alone, or none)
+                    d[i] = p[min(U.tok0 + 32 * i + lane, a.rows - 1)];
+            fkb += kScaleWarps;
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4 * NH; ++j)
+                v[i][j] = Row{};
+            fetch(v[i]);
+        }
+        const int units = w.first < w.n_units ? (w.n_units - w.first + w.step - 1) / w.step : 0;
+        const int64_t total = (int64_t)(w.kb1 - w.kb0) * units;
+        int s = me % NS;
         uint32_t ph = 1;
-        for (int u = w.first; u < w.n_units; u += w.step) {
-            const Unit U = unit_of<NT>(a, w, u);
-            const uint8_t *pw = a.sw + ((int64_t)U.e * a.N + U.f * 128 + r0) * a.sw_ld;
-            const uint8_t *px = a.sx + (int64_t)(U.tok0 + r0) * a.sx_ld;
-            const int nw = a.N - U.f * 128;
-            for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                if (!wwait(empty + s, ph, a.err, abort))
-                    goto scaled;
-                const int c = kb * NW + 4 * word, have = min(max(nblk - c, 0), 4);
-                const uint32_t to = smem_u32(ring + s * kStage) + kTile + NT * 128 + word * 512;
+        bool ok = true;
+        for (int64_t it = me; it < total && ok;) {
 #pragma unroll
-                for (int i = 0; i < 128 / RPI; ++i) {
-                    const int r = r0 + i * RPI;
-                    const int n = r < nw ? have : 0;
-                    cp_async4(to + (r & 31) * 16 + (r >> 5) * 4, n ? pw + (int64_t)i * RPI * a.sw_ld + c : a.sw, n);
-                }
-                const uint32_t tx = to + NA * 512 + word * 512 * (NH - 1);
+            for (int i = 0; i < AHEAD; ++i) {
+                if (it >= total)
+                    break;
+                ok = wwait(empty + s, ph, a.err, abort);
+                if (!ok)
+                    break;
+                uint4 *to = reinterpret_cast<uint4 *>(ring + s * kStage + kTile + NT * 128 + NA * 512) + lane;
 #pragma unroll
-                for (int i = 0; i < (NT + RPI - 1) / RPI; ++i) {
-                    const int r = r0 + i * RPI;
-                    if (i * RPI >= U.n)
-                        break;
-                    const int n = r < U.n ? have : 0;
-                    if (NT % RPI == 0 || r < NT)
-                        cp_async4(tx + (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4,
-                                  n ? px + (int64_t)i * RPI * a.sx_ld + c : a.sx, n);
+                for (int h = 0; h < NH; ++h) {
+                    uint32_t r[4][NA];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const Row x = v[i][4 * h + j];
+                        r[j][0] = x.x, r[j][1] = x.y;
+                        if constexpr (NA == 4)
+                            r[j][2] = x.z, r[j][3] = x.w;
+                    }
+#pragma unroll
+                    for (int k = 0; k < NA; ++k)
+                        to[(k * NH + h) * 32] = make_uint4(r[0][k], r[1][k], r[2][k], r[3][k]);
                 }
-                cp_async_arrive(full + s);
-                if (++s == NS)
-                    s = 0, ph ^= 1;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the tensor core's copies read them)
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(full + s);
+                fetch(v[i]);
+                it += kScaleWarps;
+                s += kScaleWarps;
+                if (s >= NS)
+                    s -= NS, ph ^= 1;
             }
         }
-    scaled:;
-        // (no copy of this thread's is left in flight when its CTA's memory goes to another)
-        cp_async_wait_n(0);
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ----------------------------------------------------------- results
         const uint32_t ta = tmem + ((uint32_t)warp << 21);
-        const float tx = a.tx ? __ldg(a.tx) : 1.0f;
+        const float tx = a.tx ? *a.tx : 1.0f;
         int b = 0;
         uint32_t tph = 0;
         for (int u = w.first; u < w.n_units; u += w.step) {
             const Unit U = unit_of<NT>(a, w, u);
-            const float tw = a.tw ? __ldg(a.tw + U.e) : 1.0f;
+            const float tw = a.tw ? a.tw[U.e] : 1.0f;
             if (!wwait(tfull + b, tph, a.err, abort))
                 break;
             fence_after();
@@ -459,6 +477,30 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
 }
 
+// One 16-byte line of a piece to a thread.
+__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a)
+{
+    const int NA = atoms_of(a.block), stages = (a.nb + 4 * NA - 1) / (4 * NA), FT = (a.rows + 127) / 128;
+    const int64_t lines = (int64_t)a.count * FT * stages * NA * 32;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < lines; i += (int64_t)gridDim.x * blockDim.x) {
+        const int line = (int)(i % 32);
+        int64_t x = i / 32;
+        const int b0 = (int)(x % ((int64_t)stages * NA)) * 4;  // first of four blocks
+        x /= (int64_t)stages * NA;
+        const int f = (int)(x % FT), e = (int)(x / FT);
+        uint32_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = f * 128 + 32 * j + line;
+            v[j] = 0;
+            for (int k = 0; k < 4; ++k)
+                if (row < a.rows && b0 + k < a.nb)
+                    v[j] |= (uint32_t)__ldg(a.scales + ((int64_t)e * a.rows + row) * a.ld + b0 + k) << (8 * k);
+        }
+        reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
 template <int NT, int BLOCK>
 cudaError_t launch_t(const GemmArgs &a, int grid, cudaStream_t s)
 {
@@ -487,6 +529,12 @@ cudaError_t launch_t(const GemmArgs &a, int grid, cudaStream_t s)
 }
 
 }  // namespace
+
+cudaError_t launch_pack(const PackArgs &a, cudaStream_t s)
+{
+    pack_kernel<<<1024, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
 
 size_t gemm_smem(int block, int nt, int stages)
 {

@@ -34,8 +34,8 @@ __device__ __forceinline__ Raw<BF16> load_raw(const QuantArgs &a, int64_t at, in
     if (a.vx && n >= 8) {
 #pragma unroll
         for (int i = 0; i < (BF16 ? 1 : 2); ++i)
-            v.r[i] = ldg_u4(BF16 ? static_cast<const void *>(static_cast<const uint16_t *>(a.x) + at)
-                                 : static_cast<const void *>(static_cast<const float *>(a.x) + at + 4 * i));
+            v.r[i] = *(BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at)
+                            : reinterpret_cast<const uint4 *>(static_cast<const float *>(a.x) + at + 4 * i));
         return v;
     }
     uint32_t w[8];
@@ -43,8 +43,7 @@ __device__ __forceinline__ Raw<BF16> load_raw(const QuantArgs &a, int64_t at, in
     for (int j = 0; j < 8; ++j) {
         w[j] = 0;
         if (j < n)
-            w[j] = BF16 ? __ldg(static_cast<const uint16_t *>(a.x) + at + j)
-                        : __ldg(static_cast<const uint32_t *>(a.x) + at + j);
+            w[j] = BF16 ? static_cast<const uint16_t *>(a.x)[at + j] : static_cast<const uint32_t *>(a.x)[at + j];
     }
     if (BF16) {
         v.r[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
@@ -107,9 +106,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
 {
     pdl_trigger();  // (a product may set itself up meanwhile; it waits for this launch's end before it reads)
     pdl_wait();
-    constexpr int LANES = BLOCK / 8;
-    // pieces of a row, so that a block has neighbouring lanes of one warp
-    const int ppr = (a.cols + BLOCK - 1) / BLOCK * LANES;
+    constexpr int LANES = BLOCK / 8, PER = kStageCols / BLOCK;  // lanes of a block; blocks of a stage
+    // pieces of a row, whole stages: a block has neighbouring lanes of one warp, and the scales behind the
+    // last block are written too, as zeros
+    const int ppr = stages_of(a.cols) * (kStageCols / 8);
     const int64_t stride = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int dr = (int)(stride / ppr), dp = (int)(stride - (int64_t)dr * ppr);
     int64_t row = first / ppr;
@@ -175,8 +175,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
                         if (2 * j < n)
                             to[j] = (uint8_t)(q >> (8 * j));
                 }
-                if (ps[i] % LANES == 0)
-                    a.scales[rows[i] * a.lds + ps[i] / LANES] = (uint8_t)code;
+                if (ps[i] % LANES == 0) {
+                    const int b = ps[i] / LANES;
+                    a.scales[((int64_t)(b / PER) * a.rows + rows[i]) * PER + b % PER] = n > 0 ? (uint8_t)code : 0;
+                }
             }
         }
     }
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
 template <bool BF16, int BLOCK>
 cudaError_t launch_t(const QuantArgs &a, int sms, cudaStream_t s)
 {
-    const int64_t pieces = (int64_t)a.rows * ((a.cols + BLOCK - 1) / BLOCK * (BLOCK / 8));
+    const int64_t pieces = (int64_t)a.rows * stages_of(a.cols) * (kStageCols / 8);
     const int64_t most = 6 * (int64_t)sms, one = (pieces + kThreads - 1) / kThreads;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)std::min(most, one));

@@ -190,8 +190,9 @@ __device__ __forceinline__ void group_table(const int32_t *offsets, int E, int r
         const int e = e0 + lane;
         int b = 0, c = 0;
         if (e < E) {
-            b = offsets ? min(max(__ldg(offsets + e), 0), rows) : 0;
-            const int d = offsets ? min(max(__ldg(offsets + e + 1), 0), rows) : rows;
+            // (plain loads: a launch that began before its predecessor's end must not use the read-only path)
+            b = offsets ? min(max(offsets[e], 0), rows) : 0;
+            const int d = offsets ? min(max(offsets[e + 1], 0), rows) : rows;
             c = max(d - b, 0);
         }
         const int t = (c + nt - 1) / nt;

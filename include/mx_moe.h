@@ -530,18 +530,41 @@ MX_API size_t mx_fp8_moe_workspace_bytes(const mx_fp8_layer *layer, int T_max);
  * ------------------------------------------------------------------------ */
 typedef enum { MX_FP4_E8M0 = 0, MX_FP4_E4M3 = 1 } mx_fp4_format;
 
-/* `count` matrices [rows][cols], or (count 1) quantised activations. */
+/* `count` matrices [rows][cols]. */
 typedef struct {
-    void *q;              /* row pitch ld bytes, matrices rows * ld bytes apart; an odd last column's
-                             spare nibble is zero                                                   */
-    void *scales;         /* a byte for each block, row pitch scale_ld, matrices rows * scale_ld apart */
+    const void *q;        /* row pitch ld bytes, matrices rows * ld bytes apart; 16-byte aligned; an odd
+                             last column's spare nibble is zero                                      */
+    const void *scales;   /* as mx_fp4_pack_scales leaves them; 16-byte aligned                      */
     const float *tensor_scale; /* device [count], nullable (1); MX_FP4_E4M3 only; finite, positive and normal */
     int32_t rows, cols, count;
     int32_t format;       /* mx_fp4_format */
-    int64_t ld;           /* >= ceil(cols / 2); operands: q and ld multiples of 16 */
-    int64_t scale_ld;     /* >= blocks; operands: scales and scale_ld multiples of 4, and a row's bytes
-                             up to the next multiple of 4 behind its blocks are read, but not used   */
-} mx_fp4_tensor;
+    int64_t ld;           /* >= ceil(cols / 2), a multiple of 16 */
+} mx_fp4_matrix;
+
+/* Quantised activations [rows][cols]. */
+typedef struct {
+    void *q;              /* row pitch ld bytes; 16-byte aligned for the products                    */
+    void *scales;         /* [ceil(cols / 256)][rows][256 / block]: the scales of 256 columns lie together,
+                             zeros behind the last block; 16-byte aligned                             */
+    const float *tensor_scale; /* device, nullable (1), as above */
+    int32_t rows, cols;
+    int32_t format;
+    int64_t ld;           /* >= ceil(cols / 2); for the products a multiple of 16 */
+} mx_fp4_rows;
+
+/*
+ * Lay out matrices' block scales once for the products: for each matrix, each 128
+ * rows and each 256 columns the pieces of the tensor core, 512 bytes for 128 rows
+ * and four blocks (line i of 32: four scales each of rows i, 32 + i, 64 + i, 96 + i),
+ * zeros behind the last row and block.
+ *   scales   device [count][rows][ceil(cols / block)] bytes, row pitch ld, matrices
+ *            rows * ld bytes apart
+ *   out      device, 16-byte aligned, mx_fp4_pack_bytes, not overlapping scales
+ * The copy is to be made again whenever the scales change.
+ */
+MX_API size_t mx_fp4_pack_bytes(int rows, int cols, int count, int format); /* 0 on bad sizes */
+MX_API mx_status mx_fp4_pack_scales(const void *scales, int64_t ld, int rows, int cols, int count, int format, void *out,
+                                    void *stream);
 
 /*
  * Quantise rows.  For each block, a = max |x|:
@@ -552,21 +575,21 @@ typedef struct {
  * rounded to nearest, ties to even, at most 6; a zero keeps its sign.  A block with
  * a NaN or an infinity gets a NaN scale and zeros, and dequantises to NaN.
  *   x    device [rows][cols] of `dtype`, row pitch ldx elements
- *   out  count 1; only its rows' ceil(cols / 2) bytes and blocks are written
+ *   out  only its rows' ceil(cols / 2) bytes and the scales are written
  */
-MX_API mx_status mx_fp4_quantize(const void *x, int64_t ldx, int dtype, const mx_fp4_tensor *out, void *stream);
+MX_API mx_status mx_fp4_quantize(const void *x, int64_t ldx, int dtype, const mx_fp4_rows *out, void *stream);
 
 /* out[r][o] = sum_c x[r][c] w[o][c], as mx_fp8_matmul; x and w of one format. */
-MX_API mx_status mx_fp4_matmul(const mx_fp4_tensor *x, const mx_fp4_tensor *w, void *out, int64_t ldo, int out_dtype,
+MX_API mx_status mx_fp4_matmul(const mx_fp4_rows *x, const mx_fp4_matrix *w, void *out, int64_t ldo, int out_dtype,
                                void *stream, void *ws, size_t ws_bytes);
 
 /* The same for rows grouped by matrix, as mx_fp8_grouped_matmul. */
-MX_API mx_status mx_fp4_grouped_matmul(const mx_fp4_tensor *x, const int32_t *offsets, const mx_fp4_tensor *w,
+MX_API mx_status mx_fp4_grouped_matmul(const mx_fp4_rows *x, const int32_t *offsets, const mx_fp4_matrix *w,
                                        void *out, int64_t ldo, int out_dtype, void *stream, void *ws,
                                        size_t ws_bytes);
 
 /* Workspace bytes of the two calls above for up to `rows` rows (0 on an invalid matrix). */
-MX_API size_t mx_fp4_matmul_workspace_bytes(const mx_fp4_tensor *w, int rows);
+MX_API size_t mx_fp4_matmul_workspace_bytes(const mx_fp4_matrix *w, int rows);
 
 /* ------------------------------------------------------------------------
  * Routing from logits: for routers other than the 8-bit affine one of
