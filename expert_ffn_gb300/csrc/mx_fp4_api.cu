@@ -202,7 +202,7 @@ extern "C" mx_status mx_fp4_quantize(const void *x, int64_t ldx, int dtype, cons
     a.cols = out->cols;
     a.bf16 = dtype == MX_BF16;
     a.vx = vec16(x, ldx, a.bf16);
-    a.vq = aligned(out->q, 4) && out->ld % 4 == 0;
+    a.vq = aligned(out->q, 8) && out->ld % 8 == 0;
     a.q = static_cast<uint8_t *>(out->q);
     a.scales = static_cast<uint8_t *>(out->scales);
     a.ldq = out->ld;

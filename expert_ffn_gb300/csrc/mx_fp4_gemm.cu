@@ -310,19 +310,23 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     issued:;
     } else if (warp > kOutWarps + 1) {
         // ------------------------------------------------------------ scales
-        constexpr int AHEAD = 2;  // stages of this warp under way in registers
+        constexpr int AHEAD = NH == 1 ? 4 : 2;  // stages of this warp under way in registers
         using Row = typename std::conditional<BLOCK == 16, uint4, uint2>::type;  // a row's scales of a stage
         const int me = warp - kOutWarps - 2;
         Row v[AHEAD][4 * NH];
         int fu = w.first, fkb = w.kb0 + me;  // what is fetched next
+        Unit U{};
+        if (fu < w.n_units)
+            U = unit_of<NT>(a, w, fu);
         auto fetch = [&](Row (&d)[4 * NH]) {
             while (fu < w.n_units && fkb >= w.kb1) {  // (a unit's stages run on into the next one's)
                 fkb -= w.kb1 - w.kb0;
                 fu += w.step;
+                if (fu < w.n_units)
+                    U = unit_of<NT>(a, w, fu);
             }
             if (fu >= w.n_units)
                 return;
-            const Unit U = unit_of<NT>(a, w, fu);
             // (plain loads: the read-only path must not be used by a launch that began before its
             // predecessor's end)
             const Row *p = reinterpret_cast<const Row *>(a.sx) + (int64_t)fkb * a.rows;

@@ -7,10 +7,10 @@
 // the stored codes are the same on every machine.  6 = 1.5 * 4: the power of two is the
 // maximum's exponent less 2, one more where its mantissa is above 1.5, and takes no division.
 //
-// A thread has eight neighbouring columns, a block two or four neighbouring lanes: loads
-// of 16 (fp32: 32) bytes and stores of 4 are whole lines for a warp.  The pieces of the
-// matrix are dealt out in order, so a ragged width leaves no warp idle; a thread's next
-// piece is a constant number of rows and columns on.  HBM bounds large matrices.
+// A thread has sixteen neighbouring columns, so a block of 16 is its own and a block of 32 takes
+// one exchange with its neighbour; the scale and its reciprocal are worked out once for sixteen values.
+// The pieces of the matrix are dealt out in order, so a ragged width leaves no warp idle; a
+// thread's next piece is a constant number of rows and columns on.  HBM bounds large matrices.
 #include "mx_fp4.cuh"
 
 #include <algorithm>
@@ -20,55 +20,87 @@ namespace fp4 {
 
 namespace {
 
-constexpr int kThreads = 256, kAhead = 4;
+constexpr int kThreads = 256, kPiece = 16;
 
+// Pieces of a thread under way: 64 bytes.
+template <bool BF16>
+constexpr int kAhead = BF16 ? 2 : 1;
+
+// Sixteen values as they were loaded.
 template <bool BF16>
 struct Raw {
-    uint4 r[BF16 ? 1 : 2];
+    uint4 r[BF16 ? 2 : 4];
 };
 
 template <bool BF16>
 __device__ __forceinline__ Raw<BF16> load_raw(const QuantArgs &a, int64_t at, int n)
 {
     Raw<BF16> v{};
-    if (a.vx && n >= 8) {
+    if (a.vx && n >= kPiece) {
+        const uint4 *p = BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at)
+                              : reinterpret_cast<const uint4 *>(static_cast<const float *>(a.x) + at);
 #pragma unroll
-        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
-            v.r[i] = *(BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at)
-                            : reinterpret_cast<const uint4 *>(static_cast<const float *>(a.x) + at + 4 * i));
+        for (int i = 0; i < (BF16 ? 2 : 4); ++i)
+            v.r[i] = p[i];
         return v;
     }
-    uint32_t w[8];
+    uint32_t w[kPiece];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kPiece; ++j) {
         w[j] = 0;
         if (j < n)
             w[j] = BF16 ? static_cast<const uint16_t *>(a.x)[at + j] : static_cast<const uint32_t *>(a.x)[at + j];
     }
-    if (BF16) {
-        v.r[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-    } else {
-        v.r[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        v.r[BF16 ? 0 : 1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 2 : 4); ++i) {
+        const uint32_t *b = w + (BF16 ? 8 : 4) * i;
+        v.r[i] = BF16 ? make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[BF16 ? 4 : 0] | b[BF16 ? 5 : 0] << 16,
+                                   b[BF16 ? 6 : 0] | b[BF16 ? 7 : 0] << 16)
+                      : make_uint4(b[0], b[1], b[2], b[3]);
     }
     return v;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void unpack(const Raw<BF16> &r, float (&v)[8])
+// Bits of the largest magnitude (two bf16 values to an operation).
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
 {
-    const uint32_t w[4] = {r.r[0].x, r.r[0].y, r.r[0].z, r.r[0].w};
-    if (BF16) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t largest(const Raw<true> &v)
+{
+    uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-        const uint4 b = r.r[BF16 ? 0 : 1];
-        v[0] = __uint_as_float(w[0]), v[1] = __uint_as_float(w[1]), v[2] = __uint_as_float(w[2]), v[3] = __uint_as_float(w[3]);
-        v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-    }
+    for (int i = 0; i < 2; ++i)
+        m = max_u16x2(m, max_u16x2(max_u16x2(v.r[i].x & 0x7FFF7FFFu, v.r[i].y & 0x7FFF7FFFu),
+                                   max_u16x2(v.r[i].z & 0x7FFF7FFFu, v.r[i].w & 0x7FFF7FFFu)));
+    return max(m & 0xFFFF0000u, m << 16);
+}
+
+__device__ __forceinline__ uint32_t largest(const Raw<false> &v)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = max(max(max(m, v.r[i].x & 0x7FFFFFFFu), max(v.r[i].y & 0x7FFFFFFFu, v.r[i].z & 0x7FFFFFFFu)),
+                v.r[i].w & 0x7FFFFFFFu);
+    return m;
+}
+
+// Values 2 j and 2 j + 1.
+__device__ __forceinline__ uint64_t pair_of(const Raw<true> &v, int j)
+{
+    const uint4 r = v.r[j >> 2];
+    const uint32_t w = (j & 3) == 0 ? r.x : (j & 3) == 1 ? r.y : (j & 3) == 2 ? r.z : r.w;
+    return pair_f32(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint64_t pair_of(const Raw<false> &v, int j)
+{
+    const uint4 r = v.r[j >> 1];
+    return (j & 1) ? pair_f32(__uint_as_float(r.z), __uint_as_float(r.w)) : pair_f32(__uint_as_float(r.x), __uint_as_float(r.y));
 }
 
 // Eight e2m1 codes, the first in the lowest nibble (round to nearest even, at most 6).
@@ -106,10 +138,10 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
 {
     pdl_trigger();  // (a product may set itself up meanwhile; it waits for this launch's end before it reads)
     pdl_wait();
-    constexpr int LANES = BLOCK / 8, PER = kStageCols / BLOCK;  // lanes of a block; blocks of a stage
-    // pieces of a row, whole stages: a block has neighbouring lanes of one warp, and the scales behind the
-    // last block are written too, as zeros
-    const int ppr = stages_of(a.cols) * (kStageCols / 8);
+    constexpr int PER = kStageCols / BLOCK, AHEAD = kAhead<BF16>;  // blocks of a stage
+    // pieces of a row, whole stages: a block of 32 has neighbouring lanes of one warp, and the scales behind
+    // the last block are written too, as zeros
+    const int ppr = stages_of(a.cols) * (kStageCols / kPiece);
     const int64_t stride = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int dr = (int)(stride / ppr), dp = (int)(stride - (int64_t)dr * ppr);
     int64_t row = first / ppr;
@@ -122,30 +154,24 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
     }
     // (a lane behind the last row still takes part in the warp's shuffles)
     while (__any_sync(0xFFFFFFFFu, row < a.rows)) {
-        Raw<BF16> raw[kAhead];
-        int64_t rows[kAhead];
-        int ps[kAhead];
+        Raw<BF16> raw[AHEAD];
+        int64_t rows[AHEAD];
+        int ps[AHEAD];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        for (int i = 0; i < AHEAD; ++i) {
             rows[i] = row;
             ps[i] = p;
-            raw[i] = row < a.rows ? load_raw<BF16>(a, row * a.ldx + 8 * p, a.cols - 8 * p) : Raw<BF16>{};
+            raw[i] = row < a.rows ? load_raw<BF16>(a, row * a.ldx + kPiece * p, a.cols - kPiece * p) : Raw<BF16>{};
             row += dr;
             p += dp;
             if (p >= ppr)
                 p -= ppr, ++row;
         }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            float v[8];
-            unpack(raw[i], v);
-            uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-#pragma unroll
-            for (int o = 1; o < LANES; o <<= 1)
-                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        for (int i = 0; i < AHEAD; ++i) {
+            uint32_t m = largest(raw[i]);
+            if (BLOCK == 32)
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             uint32_t code;
             float inv;
             if (BLOCK == 32) {
@@ -157,26 +183,33 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
                 const float s = from_e4m3(code) * t;
                 inv = s >= 1.17549435e-38f ? __frcp_rn(s) : 0.0f;
             }
-            const bool bad = m >= 0x7F800000u;  // a NaN or an infinity
-            if (bad)
-                code = BLOCK == 32 ? 255u : 127u;
+            uint32_t q[2];
+            const uint64_t inv2 = pair_f32(inv, inv);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = bad ? 0.0f : v[j] * inv;
-            const uint32_t q = e2m1_x8(v);
+            for (int h = 0; h < 2; ++h) {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    unpair_f32(mul_f32x2(pair_of(raw[i], 4 * h + j), inv2), v[2 * j], v[2 * j + 1]);
+                q[h] = e2m1_x8(v);
+            }
+            if (m >= 0x7F800000u) {  // a NaN or an infinity
+                code = BLOCK == 32 ? 255u : 127u;
+                q[0] = q[1] = 0;
+            }
             if (rows[i] < a.rows) {
-                const int n = a.cols - 8 * ps[i];
-                uint8_t *to = a.q + rows[i] * a.ldq + 4 * ps[i];
-                if (a.vq && n >= 7) {
-                    *reinterpret_cast<uint32_t *>(to) = q;
+                const int n = a.cols - kPiece * ps[i];
+                uint8_t *to = a.q + rows[i] * a.ldq + kPiece / 2 * ps[i];
+                if (a.vq && n >= kPiece - 1) {
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(q[0], q[1]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 8; ++j)
                         if (2 * j < n)
-                            to[j] = (uint8_t)(q >> (8 * j));
+                            to[j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
                 }
-                if (ps[i] % LANES == 0) {
-                    const int b = ps[i] / LANES;
+                if (BLOCK == 16 || !(ps[i] & 1)) {
+                    const int b = BLOCK == 16 ? ps[i] : ps[i] >> 1;
                     a.scales[((int64_t)(b / PER) * a.rows + rows[i]) * PER + b % PER] = n > 0 ? (uint8_t)code : 0;
                 }
             }
@@ -187,8 +220,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
 template <bool BF16, int BLOCK>
 cudaError_t launch_t(const QuantArgs &a, int sms, cudaStream_t s)
 {
-    const int64_t pieces = (int64_t)a.rows * stages_of(a.cols) * (kStageCols / 8);
-    const int64_t most = 6 * (int64_t)sms, one = (pieces + kThreads - 1) / kThreads;
+    const int64_t pieces = (int64_t)a.rows * stages_of(a.cols) * (kStageCols / kPiece);
+    const int64_t most = 8 * (int64_t)sms, one = (pieces + kThreads - 1) / kThreads;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)std::min(most, one));
     c.blockDim = dim3(kThreads);
