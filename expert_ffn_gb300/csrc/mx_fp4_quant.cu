@@ -33,24 +33,41 @@ struct Raw {
 };
 
 template <bool BF16>
-__device__ __forceinline__ Raw<BF16> load_raw(const QuantArgs &a, int64_t at, int n)
+__device__ __forceinline__ Raw<BF16> load_raw(const QuantArgs &a, int64_t at)
 {
-    Raw<BF16> v{};
-    if (a.vx && n >= kPiece) {
-        const uint4 *p = BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at)
-                              : reinterpret_cast<const uint4 *>(static_cast<const float *>(a.x) + at);
+    Raw<BF16> v;
+    const uint4 *p = BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at)
+                          : reinterpret_cast<const uint4 *>(static_cast<const float *>(a.x) + at);
 #pragma unroll
-        for (int i = 0; i < (BF16 ? 2 : 4); ++i)
-            v.r[i] = p[i];
-        return v;
-    }
+    for (int i = 0; i < (BF16 ? 2 : 4); ++i)
+        v.r[i] = p[i];
+    return v;
+}
+
+// Of a ragged or misaligned stage of 256 columns, by its sixteen lanes: value by value, neighbouring
+// lanes neighbouring columns, zeros behind the last of n, and exchanged through shared memory.
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_slow(const QuantArgs &a, int64_t at, int n, uint32_t *mine)
+{
+    const int l = threadIdx.x & 15;
+    const unsigned half = 0xFFFFu << (threadIdx.x & 16);
     uint32_t w[kPiece];
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) {
-        w[j] = 0;
-        if (j < n)
-            w[j] = BF16 ? static_cast<const uint16_t *>(a.x)[at + j] : static_cast<const uint32_t *>(a.x)[at + j];
+    for (int i = 0; i < kPiece; ++i) {
+        const int c = i * 16 + l;
+        w[i] = 0;
+        if (c < n)
+            w[i] = BF16 ? static_cast<const uint16_t *>(a.x)[at + c] : static_cast<const uint32_t *>(a.x)[at + c];
     }
+    __syncwarp(half);
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i)
+        mine[i * 17 + l] = w[i];
+    __syncwarp(half);
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i)
+        w[i] = mine[l * 17 + i];
+    Raw<BF16> v;
 #pragma unroll
     for (int i = 0; i < (BF16 ? 2 : 4); ++i) {
         const uint32_t *b = w + (BF16 ? 8 : 4) * i;
@@ -139,6 +156,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
     pdl_trigger();  // (a product may set itself up meanwhile; it waits for this launch's end before it reads)
     pdl_wait();
     constexpr int PER = kStageCols / BLOCK, AHEAD = kAhead<BF16>;  // blocks of a stage
+    __shared__ uint32_t swap[kThreads / 16][16 * 17];
     // pieces of a row, whole stages: a block of 32 has neighbouring lanes of one warp, and the scales behind
     // the last block are written too, as zeros
     const int ppr = stages_of(a.cols) * (kStageCols / kPiece);
@@ -161,7 +179,14 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a)
         for (int i = 0; i < AHEAD; ++i) {
             rows[i] = row;
             ps[i] = p;
-            raw[i] = row < a.rows ? load_raw<BF16>(a, row * a.ldx + kPiece * p, a.cols - kPiece * p) : Raw<BF16>{};
+            const int c0 = kPiece * (p & ~15);  // the stage's first column: the same row and stage for sixteen lanes
+            raw[i] = Raw<BF16>{};
+            if (row < a.rows) {
+                if (a.vx && c0 + kStageCols <= a.cols)
+                    raw[i] = load_raw<BF16>(a, row * a.ldx + kPiece * p);
+                else
+                    raw[i] = load_slow<BF16>(a, row * a.ldx + c0, a.cols - c0, swap[threadIdx.x >> 4]);
+            }
             row += dr;
             p += dp;
             if (p >= ppr)

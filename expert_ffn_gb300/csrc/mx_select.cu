@@ -4,19 +4,23 @@
 // One warp per token; lane i holds the P = E / 32 neighbouring experts from i P
 // on in registers, so that a lane's order is the experts' order and ties go to the
 // lower index by the first lane and the first register.  Scores are computed
-// in fp32.  The choice compares 32-bit keys (the score's bits, made to order as
+// in fp32, and only where the choice needs them: without a bias experts are compared by
+// their logits, and the chosen ones' weights are worked out at the end, a lane each.
+// The choice compares 32-bit keys (a number's bits, made to order as
 // unsigned integers; 0: no longer there), k times a maximum over registers and one
 // warp reduction.
 //
 // Exactness.  Where an fp32 score (with a bias, or the sum of a run's two best)
 // decides, everything within its error bound of the maximum is a candidate; a
 // second candidate, about one token in a thousand, sends the comparison to fp64, for
-// the candidates alone.  Without a bias experts compare by their logits, which no
-// rounding has touched.
+// the candidates alone.
 //
-// What bounds it: 4096 x 256 fp32 logits are 4 MB, 0.6 us of HBM; a token takes a warp
-// some 700 instructions, most of them the k rounds' maxima, and the launches (two where
-// slots are grouped and more than one block works on them) the rest.
+// Grouping.  A selecting block of eight warps leaves its tokens' counts by expert; the
+// placing kernel's blocks each add up all of them (bytes, so that 4096 tokens of 256 experts are
+// 128 KB) and put their own tokens' slots in order.  One selecting block does both.
+//
+// What bounds it: 4096 x 256 fp32 logits are 4 MB, 0.6 us of HBM; the k rounds are a chain of some 100
+// cycles each, and a launch or two the rest.
 #include "mx_common.cuh"
 #include "mx_host.h"
 #include "mx_internal.h"
@@ -31,7 +35,9 @@ namespace sel {
 namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kMaxBlocks = 256;  // blocks whose counts the grouping adds up
+constexpr int kRuns = 512;    // selecting blocks when slots are grouped, as long as kMaxRun allows
+constexpr int kMaxRun = 248;  // their tokens at most (their counts are bytes)
+constexpr int kPlaceWarps = 16;
 
 struct Args {
     const void *logits;
@@ -44,8 +50,9 @@ struct Args {
     int32_t *idx;
     float *w;
     int32_t *counts, *offsets, *perm;  // nullable together
-    int32_t *bc;           // [blocks][E] counts of each block's tokens
-    int per;               // tokens of a block
+    uint32_t *bc;          // [runs][ceil(E / 4)] counts of the selecting blocks' tokens, four bytes to a word
+    int per, runs, join;   // tokens of a selecting block, such blocks, how many of them a placing block joins
+    int lanes;             // lanes of a run of experts, a power of two; 0: it does not end with lanes
 };
 
 __device__ __forceinline__ uint32_t ordered(float f)
@@ -59,10 +66,21 @@ __device__ __forceinline__ float unordered(uint32_t o)
     return __uint_as_float(o ^ ((uint32_t)((int32_t)~o >> 31) | 0x80000000u));
 }
 
+// A logit; a NaN counts as -inf, and -0 as 0.
+__device__ __forceinline__ float tidy(float l) { return l == l ? l + 0.0f : -INFINITY; }
+
 __device__ __forceinline__ float load1(const Args &a, int64_t at)
 {
-    return a.bf16 ? bf2f(__ldg(reinterpret_cast<const uint16_t *>(a.logits) + at))
-                  : __ldg(reinterpret_cast<const float *>(a.logits) + at);
+    return tidy(a.bf16 ? bf2f(__ldg(reinterpret_cast<const uint16_t *>(a.logits) + at))
+                       : __ldg(reinterpret_cast<const float *>(a.logits) + at));
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
 }
 
 // ------------------------------------------------------- comparisons in fp64
@@ -86,30 +104,27 @@ __device__ __noinline__ Soft64 soft64(const Args &a, int t)
     const int lane = threadIdx.x & 31;
     float m = -INFINITY;
     for (int e = lane; e < a.E; e += 32)
-        m = fmaxf(m, load1(a, (int64_t)t * a.ld + e));  // (a NaN is left out)
+        m = fmaxf(m, load1(a, (int64_t)t * a.ld + e));
     for (int o = 16; o; o >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     double z = 0.0;
     for (int e = lane; e < a.E; e += 32) {
         const float l = load1(a, (int64_t)t * a.ld + e);
-        if (l == l)
-            z += l == m ? 1.0 : exp((double)l - (double)m);
+        z += l == m ? 1.0 : exp((double)l - (double)m);
     }
     for (int o = 16; o; o >>= 1)
         z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-    return Soft64{z > 0.0 ? 1.0 / z : 0.0, m};
+    return Soft64{1.0 / z, m};
 }
 
 // The score that expert e of token t is chosen by.
 __device__ double choice64(const Args &a, int t, int e, const Soft64 &S)
 {
     const float l = load1(a, (int64_t)t * a.ld + e);
-    double s = a.score == MX_SIGMOID ? 1.0 / (1.0 + exp(-(double)l))
-                                     : (l == S.m ? 1.0 : exp((double)l - (double)S.m)) * S.inv;
-    if (!(l == l))
-        s = 0.0;
-    double c = a.bias ? s + (double)__ldg(a.bias + e) : s;
-    return l == l && c == c ? c : -INFINITY;
+    const double s = a.score == MX_SIGMOID ? 1.0 / (1.0 + exp(-(double)l))
+                                           : (l == S.m ? 1.0 : exp((double)l - (double)S.m)) * S.inv;
+    const double c = a.bias ? s + (double)__ldg(a.bias + e) : s;
+    return c == c ? c : -INFINITY;
 }
 
 // Of the candidates (bit j of a lane's mask: expert lane P + j) the one with the highest score,
@@ -166,7 +181,7 @@ __device__ __noinline__ int best_group64(const Args &a, int t, uint32_t mask)
 
 // ------------------------------------------------------------------ selection
 
-// The key that the warp chooses next: the lane that holds it, or several candidates.
+// The lane's logits; behind the last expert -inf.
 template <int P>
 __device__ __forceinline__ void load_logits(const Args &a, int t, int lane, float (&l)[P])
 {
@@ -210,50 +225,59 @@ __device__ __forceinline__ void load_logits(const Args &a, int t, int lane, floa
     } else {
 #pragma unroll
         for (int j = 0; j < P; ++j)
-            l[j] = lane * P + j < a.E ? load1(a, at + j) : 0.0f;
+            l[j] = lane * P + j < a.E ? load1(a, at + j) : -INFINITY;
+        return;
     }
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+        l[j] = tidy(l[j]);
 }
 
-// One token by one warp.  row: E floats of shared memory (for groups).  Lane k < K returns
+// One token by one warp.  row: E floats of shared memory (for runs).  Lane k < K returns
 // the k-th choice and its weight.
 template <int P>
 __device__ __forceinline__ void select_token(const Args &a, int t, int lane, float *row, int &my_idx, float &my_w)
 {
     constexpr uint32_t FULL = 0xFFFFFFFFu;
-    float l[P], s[P];
+    float l[P];
     load_logits<P>(a, t, lane, l);
     const int here = min(max(a.E - lane * P, 0), P);  // experts of this lane
+    const bool groups = a.topk_groups < a.n_groups;
+    const bool by_score = groups && a.best == 2 && !a.bias;  // runs by sums of scores (else by the keys' own order)
+    const bool soft = a.score == MX_SOFTMAX;
 
-    // scores (a NaN logit: 0)
-    float smax = 0.0f;
-    if (a.score == MX_SIGMOID) {
+    // Scores, where the choice or a softmax's weights need them, and eps: more than any |score - exact one|.  A
+    // sigmoid by the fast exponential (2 + 1.16 |l| ulp) is off by s (1 - s) of that and two roundings, below
+    // 2^-20; a softmax by expf (2 ulp) by the arguments' shift, worth d e^-d ulp, and up to 25 roundings of its
+    // sum, below 2^-19 of the largest.
+    float s[P], m = 0.0f, z = 1.0f, off = 0.0f;
+    if (soft) {
+        m = l[0];
 #pragma unroll
-        for (int j = 0; j < P; ++j)
-            s[j] = j < here && l[j] == l[j] ? 1.0f / (1.0f + expf(-l[j])) : 0.0f;
-    } else {
-        float m = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-            m = fmaxf(m, j < here ? l[j] : -INFINITY);
+        for (int j = 1; j < P; ++j)
+            m = fmaxf(m, l[j]);
         m = unordered(__reduce_max_sync(FULL, ordered(m)));
-        float z = 0.0f;
+        if (a.bias || by_score || !a.renorm) {  // (the weights' own sum replaces it otherwise)
+            z = 0.0f;
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            s[j] = j < here && l[j] == l[j] ? (l[j] == m ? 1.0f : expf(l[j] - m)) : 0.0f;
-            z += s[j];
+            for (int j = 0; j < P; ++j) {
+                s[j] = j >= here ? 0.0f : l[j] == m ? 1.0f : expf(l[j] - m);
+                z += s[j];
+            }
+            z = warp_sum(z);
+            const float inv = 1.0f / z;
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                s[j] *= inv;
+            off = 1.9073486e-6f * inv;
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            z += __shfl_xor_sync(FULL, z, o);
-        const float inv = z > 0.0f ? 1.0f / z : 0.0f;
+    } else if (a.bias || by_score) {
 #pragma unroll
         for (int j = 0; j < P; ++j)
-            s[j] *= inv;
+            s[j] = __fdividef(1.0f, 1.0f + __expf(-l[j]));
+        off = 9.5367432e-7f;
     }
 
-    // keys of the choice.  eps: more than any |fp32 score - exact one|.  A sigmoid is right to
-    // 2^-22 of itself (expf 2 ulp, two roundings), a softmax to 2^-19 of the largest (its sum has up to 21
-    // roundings, its arguments' shift by d is worth d e^-d); a bias adds one rounding of c.
     uint32_t key[P];
     float eps = 0.0f;
     if (a.bias) {
@@ -263,179 +287,170 @@ __device__ __forceinline__ void select_token(const Args &a, int t, int lane, flo
             float c = -INFINITY;
             if (j < here) {
                 c = s[j] + __ldg(a.bias + lane * P + j);
-                c = l[j] == l[j] && c == c ? c : -INFINITY;
-                if (fabsf(c) < INFINITY)
-                    cmax = fmaxf(cmax, fabsf(c));
-                smax = fmaxf(smax, s[j]);
+                c = c == c ? c + 0.0f : -INFINITY;
+                cmax = fmaxf(cmax, fabsf(c) < INFINITY ? fabsf(c) : 0.0f);
             }
-            key[j] = j < here ? ordered(c + 0.0f) : 0u;
+            key[j] = j < here ? ordered(c) : 0u;
         }
-        eps = 1.9073486e-6f * __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(smax))) +
-              1.1920929e-7f * __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(cmax)));
+        eps = off + 1.1920929e-7f * __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(cmax)));
     } else {
 #pragma unroll
         for (int j = 0; j < P; ++j)
-            key[j] = j < here ? ordered((l[j] == l[j] ? l[j] : -INFINITY) + 0.0f) : 0u;
+            key[j] = j < here ? ordered(l[j]) : 0u;
     }
 
-    if (a.topk_groups < a.n_groups) {
-        // Runs: 32 / n_groups lanes (a power of two) each go over a part of one run's scores.
+    if (groups) {
+        // The two highest of each run: `per` lanes go over one run's scores.
         const int size = a.E / a.n_groups;
-        const bool by_score = a.best == 2 && !a.bias;  // (sums of scores; else the keys' own order)
-        float geps = a.best == 2 ? 2.0f * eps : eps;
-#pragma unroll
-        for (int j = 0; j < P; ++j)
-            if (j < here)
-                row[lane * P + j] = by_score ? (l[j] == l[j] ? s[j] : -INFINITY) : unordered(key[j]);
-        if (by_score) {
+        float c1 = -INFINITY, c2 = -INFINITY;
+        int per = a.lanes;
+        if (per) {
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                smax = fmaxf(smax, s[j]);
-            geps = 2.0f * 1.9073486e-6f * __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(smax)));
+                if (j < here) {
+                    const float c = by_score ? s[j] : unordered(key[j]);
+                    c2 = fmaxf(c2, fminf(c1, c));
+                    c1 = fmaxf(c1, c);
+                }
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                if (j < here)
+                    row[lane * P + j] = by_score ? s[j] : unordered(key[j]);
+            __syncwarp();
+            per = 1;
+            while (2 * per * a.n_groups <= 32)
+                per *= 2;
+            if (lane / per < a.n_groups)
+                for (int i = lane & (per - 1); i < size; i += per) {
+                    const float c = row[lane / per * size + i];
+                    c2 = fmaxf(c2, fminf(c1, c));
+                    c1 = fmaxf(c1, c);
+                }
+            __syncwarp();
         }
-        __syncwarp();
-        int per = 1;
-        while (2 * per * a.n_groups <= 32)
-            per *= 2;
-        const int g = lane / per, part = lane & (per - 1);
-        float c1 = -INFINITY, c2 = -INFINITY;
-        if (g < a.n_groups)
-            for (int i = part; i < size; i += per) {
-                // (each run starts at another place: runs are often 32 banks apart)
-                int at = i + g * per;
-                at = at < size ? at : at % size;
-                const float c = row[g * size + at];
-                c2 = fmaxf(c2, fminf(c1, c));
-                c1 = fmaxf(c1, c);
-            }
+        const int g = lane / per;
         for (int o = per >> 1; o; o >>= 1) {
             const float y1 = __shfl_xor_sync(FULL, c1, o), y2 = __shfl_xor_sync(FULL, c2, o);
             c2 = fmaxf(fminf(c1, y1), fmaxf(c2, y2));
             c1 = fmaxf(c1, y1);
         }
-        __syncwarp();
-        float gs = a.best == 2 ? c1 + c2 : c1;
-        if (a.best == 2 && geps > 0.0f && fabsf(gs) < INFINITY)
-            geps += 1.1920929e-7f * fabsf(gs);  // (the sum's own rounding; made the warp's largest below)
-        geps = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(geps)));
-        gs = gs == gs ? gs : -INFINITY;
-        uint32_t gkey = part == 0 && g < a.n_groups ? ordered(gs + 0.0f) : 0u;
+        float gs = a.best == 2 ? c1 + c2 : c1, geps = eps;
+        gs = gs == gs ? gs + 0.0f : -INFINITY;
+        if (a.best == 2) {  // (and the sum's own rounding)
+            geps = 2.0f * (by_score ? off : eps) + (fabsf(gs) < INFINITY ? 1.1920929e-7f * fabsf(gs) : 0.0f);
+            geps = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(geps)));
+        }
+        uint32_t gkey = (lane & (per - 1)) == 0 && g < a.n_groups ? ordered(gs) : 0u;
         uint32_t kept = 0;
         for (int k = 0; k < a.topk_groups; ++k) {
-            const uint32_t m = __reduce_max_sync(FULL, gkey);
-            uint32_t cand = __ballot_sync(FULL, gkey == m);
+            const uint32_t mk = __reduce_max_sync(FULL, gkey);
+            const uint32_t lo = geps > 0.0f ? ordered(unordered(mk) - 2.0f * geps) : mk;
+            const uint32_t cand = __ballot_sync(FULL, gkey >= lo && gkey != 0u);
             int win = (__ffs(cand) - 1) / per;
-            if (geps > 0.0f) {
-                const float mf = unordered(m), lo = mf - 2.0f * geps;
-                cand = __ballot_sync(FULL, gkey != 0u && unordered(gkey) >= lo);
-                if (cand & (cand - 1)) {
-                    uint32_t groups = 0;
-                    for (uint32_t left = cand; left; left &= left - 1)
-                        groups |= 1u << ((__ffs(left) - 1) / per);
-                    win = best_group64(a, t, groups);
-                }
+            if (geps > 0.0f && (cand & (cand - 1))) {
+                uint32_t all = 0;
+                for (uint32_t left = cand; left; left &= left - 1)
+                    all |= 1u << ((__ffs(left) - 1) / per);
+                win = best_group64(a, t, all);
             }
             kept |= 1u << win;
             if (g == win)
                 gkey = 0u;
         }
-        int r = lane * P % size, gg = lane * P / size;
+        if (a.lanes) {
+            const bool in = kept >> (g & 31) & 1u;  // (a lane behind the last expert has no keys)
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            if (j < here && !(kept >> gg & 1u))
-                key[j] = 0u;
-            if (++r == size)
-                r = 0, ++gg;
+            for (int j = 0; j < P; ++j)
+                key[j] = in ? key[j] : 0u;
+        } else {
+            int r = lane * P % size, gg = lane * P / size;
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                if (j < here && !(kept >> gg & 1u))
+                    key[j] = 0u;
+                if (++r == size)
+                    r = 0, ++gg;
+            }
         }
     }
 
     my_idx = 0;
-    my_w = 0.0f;
     for (int k = 0; k < a.K; ++k) {
         uint32_t top = key[0];
 #pragma unroll
         for (int j = 1; j < P; ++j)
             top = max(top, key[j]);
-        const uint32_t m = __reduce_max_sync(FULL, top);
-        int win = -1;
+        const uint32_t mk = __reduce_max_sync(FULL, top);
+        int src = __ffs(__ballot_sync(FULL, top == mk)) - 1, j0 = 0;
+#pragma unroll
+        for (int j = P - 1; j >= 0; --j)
+            j0 = key[j] == mk ? j : j0;
         if (eps > 0.0f) {
-            const uint32_t lo = ordered(unordered(m) - 2.0f * eps);
+            const uint32_t lo = ordered(unordered(mk) - 2.0f * eps);
             uint32_t mask = 0;
 #pragma unroll
             for (int j = 0; j < P; ++j)
                 mask |= key[j] >= lo && key[j] != 0u ? 1u << j : 0u;
             const uint32_t lanes = __ballot_sync(FULL, mask != 0u), more = __ballot_sync(FULL, (mask & (mask - 1)) != 0u);
-            if ((lanes & (lanes - 1)) || more)
-                win = best64(a, t, mask, P);
+            if ((lanes & (lanes - 1)) | more) {
+                const int e = best64(a, t, mask, P);
+                src = e / P;
+                j0 = e % P;
+            }
         }
-        if (win < 0) {
-            const int src = __ffs(__ballot_sync(FULL, top == m)) - 1;
-            int j0 = 0;
-#pragma unroll
-            for (int j = P - 1; j >= 0; --j)
-                if (key[j] == m)
-                    j0 = j;
-            win = __shfl_sync(FULL, lane * P + j0, src);
-        }
-        const int src = win / P;
-        float sv = 0.0f;
         if (lane == src) {
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                if (src * P + j == win) {
-                    sv = s[j];
-                    key[j] = 0u;
-                }
+                key[j] = j == j0 ? 0u : key[j];
         }
-        sv = __shfl_sync(FULL, sv, src);
-        if (lane == k) {
-            my_idx = win;
-            my_w = sv;
-        }
+        const int e = __shfl_sync(FULL, lane * P + j0, src);
+        if (lane == k)
+            my_idx = e;
     }
-    if (a.renorm) {
-        float sum = my_w;
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            sum += __shfl_xor_sync(FULL, sum, o);
-        my_w = sum > 0.0f ? my_w / sum : 0.0f;
-    }
-    my_w *= a.scale;
+
+    // The weights of the chosen, a lane each, from their logits.  (A renormalised softmax goes by the largest
+    // chosen one, which in runs need not be the largest of all.)
+    float w = 0.0f;
+    const float x = lane < a.K ? load1(a, (int64_t)t * a.ld + my_idx) : -INFINITY;
+    if (soft && a.renorm)
+        m = unordered(__reduce_max_sync(FULL, ordered(x)));
+    if (lane < a.K)
+        w = !soft ? 1.0f / (1.0f + expf(-x)) : x == m ? 1.0f : expf(x - m);
+    if (a.renorm)
+        z = warp_sum(w);
+    if (soft || a.renorm)
+        w = z > 0.0f ? w / z : 0.0f;
+    my_w = w * a.scale;
 }
 
 // ------------------------------------------------------------------- grouping
 
-// Slots [lo, hi) of a block to their places, in ascending order within an expert: h[w][e] starts
-// as the place of warp w's first slot of expert e.
-__device__ __forceinline__ void warp_counts(const int32_t *idx, int lo, int hi, int lane, int *mine)
+// Slots of tokens [t0, t1) to their places, in ascending order within an expert, by a block of WARPS
+// warps.  base[e]: place of the first of expert e; h: WARPS * E.
+template <int WARPS>
+__device__ __forceinline__ void place_slots(const Args &a, int64_t t0, int64_t t1, const int *base, int *h)
 {
-    for (int s0 = lo; s0 < hi; s0 += 32) {
-        const int s = s0 + lane, e = s < hi ? idx[s] : -1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t first = t0 * a.K, n = (t1 - t0) * a.K, part = ((n + WARPS - 1) / WARPS + 31) / 32 * 32;
+    const int32_t *idx = a.idx + first;
+    const int64_t lo = min(warp * part, n), hi = min(lo + part, n);
+    for (int i = threadIdx.x; i < WARPS * a.E; i += 32 * WARPS)
+        h[i] = 0;
+    __syncthreads();
+    int *mine = h + warp * a.E;
+    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
+        const int e = s0 + lane < hi ? idx[s0 + lane] : -1;
         const unsigned m = __match_any_sync(0xFFFFFFFFu, e);
         if (e >= 0 && lane == __ffs(m) - 1)
             mine[e] += __popc(m);
         __syncwarp();
     }
-}
-
-// Block b's slots into perm.  base[e]: place of its first slot of expert e; h: kWarps * E.
-__device__ void place_slots(const Args &a, int b, const int *base, int *h)
-{
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t first = (int64_t)b * a.per;
-    const int n = (int)min((int64_t)a.per, a.T - first) * a.K, part = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int32_t *idx = a.idx + first * a.K;
-    const int lo = min(warp * part, n), hi = min(lo + part, n);
-    for (int i = threadIdx.x; i < kWarps * a.E; i += kThreads)
-        h[i] = 0;
     __syncthreads();
-    int *mine = h + warp * a.E;
-    warp_counts(idx, lo, hi, lane, mine);
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    for (int e = threadIdx.x; e < a.E; e += 32 * WARPS) {
         int run = base[e];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const int c = h[w * a.E + e];
             h[w * a.E + e] = run;
             run += c;
@@ -443,11 +458,11 @@ __device__ void place_slots(const Args &a, int b, const int *base, int *h)
     }
     __syncthreads();
     const unsigned lt = (1u << lane) - 1u;
-    for (int s0 = lo; s0 < hi; s0 += 32) {
-        const int s = s0 + lane, e = s < hi ? idx[s] : -1;
+    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
+        const int e = s0 + lane < hi ? idx[s0 + lane] : -1;
         const unsigned m = __match_any_sync(0xFFFFFFFFu, e);
         if (e >= 0)
-            a.perm[mine[e] + __popc(m & lt)] = (int)(first * a.K) + s;
+            a.perm[mine[e] + __popc(m & lt)] = (int)(first + s0) + lane;
         __syncwarp();
         if (e >= 0 && lane == __ffs(m) - 1)
             mine[e] += __popc(m);
@@ -455,14 +470,22 @@ __device__ void place_slots(const Args &a, int b, const int *base, int *h)
     }
 }
 
-// Exclusive sum of v over the block's threads i < kMaxExperts, two values to a thread: in place
-// over cnt[E]; total into cnt[E].
-__device__ void scan_counts(int *cnt, int E)
+// Exclusive sum of cnt[E] over the experts, in place, by the block; the total into cnt[E].  An expert,
+// or two, to a thread.
+template <int WARPS>
+__device__ __forceinline__ void scan_counts(int *cnt, int E)
 {
-    __shared__ int wsum[kWarps];
+    constexpr int PER = kMaxExperts / (32 * WARPS);
+    static_assert(PER >= 1 && PER * 32 * WARPS == kMaxExperts, "experts of a thread");
+    __shared__ int wsum[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int v0 = 2 * tid < E ? cnt[2 * tid] : 0, v1 = 2 * tid + 1 < E ? cnt[2 * tid + 1] : 0;
-    int incl = v0 + v1;
+    int v[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        v[i] = PER * tid + i < E ? cnt[PER * tid + i] : 0;
+        sum += v[i];
+    }
+    int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
@@ -472,25 +495,25 @@ __device__ void scan_counts(int *cnt, int E)
     if (lane == 31)
         wsum[warp] = incl;
     __syncthreads();
-    int before = 0;
+    int run = incl - sum;
     for (int w = 0; w < warp; ++w)
-        before += wsum[w];
-    const int ex = before + incl - v0 - v1;
-    if (2 * tid < E)
-        cnt[2 * tid] = ex;
-    if (2 * tid + 1 < E)
-        cnt[2 * tid + 1] = ex + v0;
-    if (tid == kThreads - 1)
-        cnt[E] = ex + v0 + v1;
+        run += wsum[w];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (PER * tid + i < E)
+            cnt[PER * tid + i] = run;
+        run += v[i];
+    }
+    if (tid == 32 * WARPS - 1)
+        cnt[E] = run;
     __syncthreads();
 }
-static_assert(2 * kThreads >= kMaxExperts, "two experts to a thread");
 
-// Dynamic shared memory: rows for groups [kWarps][E] floats, later the warps' counts; then counts [E + 1].
-size_t smem_bytes(int E) { return (size_t)(kWarps * E + E + 1) * 4; }
+// Dynamic shared memory: rows for runs, or the warps' counts [warps][E]; then counts [E + 1].
+size_t smem_bytes(int warps, int E) { return (size_t)(warps * E + E + 1) * 4; }
 
 template <int P>
-__global__ void __launch_bounds__(kThreads) select_kernel(const Args a)
+__global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) select_kernel(const Args a)
 {
     extern __shared__ __align__(16) float sm[];
     int *cnt = reinterpret_cast<int *>(sm + kWarps * a.E);
@@ -518,72 +541,88 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Args a)
     if (!a.counts)
         return;
     __syncthreads();
-    if (gridDim.x > 1) {
-        for (int e = threadIdx.x; e < a.E; e += kThreads)
-            a.bc[(int64_t)blockIdx.x * a.E + e] = cnt[e];
+    if (a.runs > 1) {
+        const int words = (a.E + 3) / 4;
+        for (int i = threadIdx.x; i < words; i += kThreads) {
+            uint32_t v = 0;
+            for (int k = 0; k < 4; ++k)
+                if (4 * i + k < a.E)
+                    v |= (uint32_t)cnt[4 * i + k] << (8 * k);
+            a.bc[(int64_t)blockIdx.x * words + i] = v;
+        }
         return;
     }
     for (int e = threadIdx.x; e < a.E; e += kThreads)
         a.counts[e] = cnt[e];
     __syncthreads();
-    scan_counts(cnt, a.E);
+    scan_counts<kWarps>(cnt, a.E);
     for (int e = threadIdx.x; e <= a.E; e += kThreads)
         a.offsets[e] = cnt[e];
-    place_slots(a, 0, cnt, reinterpret_cast<int *>(sm));
+    place_slots<kWarps>(a, 0, a.T, cnt, reinterpret_cast<int *>(sm));
 }
 
-// More than one block: each adds up all blocks' counts itself (an eighth of them to a warp)
-// and places its own slots.
-__global__ void __launch_bounds__(kThreads) place_kernel(const Args a)
+__global__ void __launch_bounds__(32 * kPlaceWarps) place_kernel(const Args a)
 {
+    constexpr int THREADS = 32 * kPlaceWarps;
     extern __shared__ __align__(16) int smi[];
-    int *h = smi, *cnt = smi + kWarps * a.E;
-    const int nb = gridDim.x, me = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int *h = smi, *cnt = smi + kPlaceWarps * a.E;
     __shared__ int below[kMaxExperts];
-    for (int e = tid; e < a.E; e += kThreads)
+    const int me = blockIdx.x, tid = threadIdx.x, words = (a.E + 3) / 4;
+    for (int e = tid; e < a.E; e += THREADS)
         cnt[e] = below[e] = 0;
     __syncthreads();
     pdl_wait();
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-        const int e = e0 + lane;
-        if (e < a.E) {
-            int all = 0, low = 0;
+    {
+        // all runs' counts, and those of the runs before this block's
+        const int word = tid % words, part = tid / words, parts = THREADS / words, mine = me * a.join;
+        uint32_t all[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
+        if (part < parts) {
 #pragma unroll 8
-            for (int b = warp; b < nb; b += kWarps) {
-                const int c = a.bc[(int64_t)b * a.E + e];
-                all += c;
-                low += b < me ? c : 0;
+            for (int r = part; r < a.runs; r += parts) {
+                const uint32_t v = a.bc[(int64_t)r * words + word];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t c = v >> (8 * k) & 255u;
+                    all[k] += c;
+                    low[k] += r < mine ? c : 0u;
+                }
             }
-            atomicAdd(cnt + e, all);
-            atomicAdd(below + e, low);
+            for (int k = 0; k < 4 && 4 * word + k < a.E; ++k) {
+                atomicAdd(cnt + 4 * word + k, (int)all[k]);
+                atomicAdd(below + 4 * word + k, (int)low[k]);
+            }
         }
     }
     __syncthreads();
     if (me == 0)
-        for (int e = tid; e < a.E; e += kThreads)
+        for (int e = tid; e < a.E; e += THREADS)
             a.counts[e] = cnt[e];
     __syncthreads();
-    scan_counts(cnt, a.E);
+    scan_counts<kPlaceWarps>(cnt, a.E);
     if (me == 0)
-        for (int e = tid; e <= a.E; e += kThreads)
+        for (int e = tid; e <= a.E; e += THREADS)
             a.offsets[e] = cnt[e];
-    for (int e = tid; e < a.E; e += kThreads)
+    for (int e = tid; e < a.E; e += THREADS)
         below[e] += cnt[e];
-    place_slots(a, me, below, h);
+    const int64_t t0 = (int64_t)me * a.join * a.per;
+    place_slots<kPlaceWarps>(a, t0, min((int64_t)a.T, t0 + (int64_t)a.join * a.per), below, h);
 }
 
-// Blocks that share T tokens whose slots are grouped: eight tokens to a block (a warp each), more
-// where that would be above kMaxBlocks.
-int tokens_of_block(int T) { return std::max(kWarps, ((T + kMaxBlocks - 1) / kMaxBlocks + kWarps - 1) / kWarps * kWarps); }
+// Tokens of a selecting block when slots are grouped: a warp each, more above kRuns blocks.
+int run_tokens(int T)
+{
+    const int64_t per = ((int64_t)T + kRuns - 1) / kRuns;
+    return (int)std::min<int64_t>(kMaxRun, std::max<int64_t>(kWarps, (per + kWarps - 1) / kWarps * kWarps));
+}
+int runs_of(int T) { return (int)(((int64_t)T + run_tokens(T) - 1) / run_tokens(T)); }
 
 template <int P>
 cudaError_t launch(const Args &a, int grid, cudaStream_t s)
 {
-    const size_t smem = smem_bytes(a.E);
-    select_kernel<P><<<grid, kThreads, smem, s>>>(a);
+    select_kernel<P><<<grid, kThreads, smem_bytes(kWarps, a.E), s>>>(a);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && a.counts && grid > 1)
-        e = launch_dependent(place_kernel, grid, kThreads, smem, s, a);
+    if (e == cudaSuccess && a.counts && a.runs > 1)
+        e = launch_dependent(place_kernel, (a.runs + a.join - 1) / a.join, 32 * kPlaceWarps, smem_bytes(kPlaceWarps, a.E), s, a);
     return e;
 }
 
@@ -617,8 +656,8 @@ mx_status check_router(const mx_router *r)
 
 size_t ws_bytes_of(int E, int T)
 {
-    const int per = tokens_of_block(T), nb = (T + per - 1) / per;
-    return kErrBytes + up256(nb > 1 ? (size_t)nb * E * 4 : 0);
+    const int runs = runs_of(T);
+    return kErrBytes + up256(runs > 1 ? (size_t)runs * ((E + 3) / 4) * 4 : 0);
 }
 
 }  // namespace
@@ -635,11 +674,10 @@ extern "C" size_t mx_route_logits_workspace_bytes(const mx_router *router, int T
         fail(MX_ERR_INVALID_ARG, "T_max %d is negative", T_max);
         return 0;
     }
-    // (fewer tokens never need more: blocks and tokens of a block both grow with T, up to the rounding
-    // of the tokens of a block, which kMaxBlocks blocks bound)
+    // (any number of tokens up to T_max: up to kWarps * kRuns tokens there are the more runs the more there
+    // are, then at most kRuns until a run has kMaxRun tokens)
     return std::max(sel::ws_bytes_of(router->n_experts, T_max),
-                    T_max > sel::kWarps * sel::kMaxBlocks ? kErrBytes + up256((size_t)sel::kMaxBlocks * router->n_experts * 4)
-                                                          : (size_t)0);
+                    sel::ws_bytes_of(router->n_experts, std::min(T_max, sel::kWarps * sel::kRuns)));
 }
 
 extern "C" mx_status mx_route_logits(const void *logits, int64_t ld, int dtype, int T, const mx_router *router,
@@ -688,13 +726,18 @@ extern "C" mx_status mx_route_logits(const void *logits, int64_t ld, int dtype, 
         a.counts = counts;
         a.offsets = offsets;
         a.perm = perm;
-        a.bc = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + kErrBytes);
+        a.bc = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + kErrBytes);
+        a.runs = sel::runs_of(T);
+        // (four runs, 32 tokens, to a placing block, and no more such blocks than 128)
+        a.join = std::max(4, (a.runs + 127) / 128);
     }
-    a.per = group ? sel::tokens_of_block(T) : sel::kWarps;
+    a.per = group ? sel::run_tokens(T) : sel::kWarps;
     const int grid = std::max<int64_t>(1, ((int64_t)T + a.per - 1) / a.per);
     int P = 1;
     while (32 * P < E)
         P *= 2;
+    const int size = E / a.n_groups, lanes = size / P;
+    a.lanes = size % P == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const size_t piece = std::min<size_t>(16, P * dtype_bytes(dtype));
     a.vec = E == 32 * P && aligned(logits, piece) && ld * dtype_bytes(dtype) % piece == 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -604,10 +604,10 @@ MX_API size_t mx_fp4_matmul_workspace_bytes(const mx_fp4_matrix *w, int rows);
  *     if renormalise
  * Order is that of exact arithmetic as far as fp64 holds it: scores nearer to
  * one another than fp32 tells apart are compared in fp64, and without a bias
- * experts are compared by their logits.  A NaN logit, or a c that is NaN,
- * ranks as -inf; a NaN logit has s = 0.  Logits of +inf share the softmax, one
- * without a finite or +inf logit is uniform over its -inf.  Where the chosen
- * sum to 0, topk_w is 0.
+ * experts are compared by their logits.  A NaN logit counts as -inf; a c or a
+ * run's score that is NaN (by the bias) ranks as -inf.  Logits that equal the largest
+ * share the softmax where that is infinite.  Where the chosen scores are all 0,
+ * renormalised weights are 0.
  * ------------------------------------------------------------------------ */
 typedef enum { MX_SOFTMAX = 0, MX_SIGMOID = 1 } mx_score;
 
