@@ -43,15 +43,16 @@ struct Args {
     const void *logits;
     int64_t ld;
     int bf16, T, E, K;
-    int vec;               // a lane's logits are one aligned piece
+    int vec, vec_bias;     // a lane's logits, its biases are aligned pieces
     int score, n_groups, topk_groups, best, renorm;
     float scale;
     const float *bias;
     int32_t *idx;
     float *w;
     int32_t *counts, *offsets, *perm;  // nullable together
-    uint32_t *bc;          // [runs][ceil(E / 4)] counts of the selecting blocks' tokens, four bytes to a word
+    uint32_t *bc;          // [ceil(E / 4)][runs] counts of the selecting blocks' tokens, four bytes to a word
     int per, runs, join;   // tokens of a selecting block, such blocks, how many of them a placing block joins
+    int pitch;             // runs rounded up to a multiple of 4
     int lanes;             // lanes of a run of experts, a power of two; 0: it does not end with lanes
 };
 
@@ -281,12 +282,23 @@ __device__ __forceinline__ void select_token(const Args &a, int t, int lane, flo
     uint32_t key[P];
     float eps = 0.0f;
     if (a.bias) {
-        float cmax = 0.0f;
+        float cmax = 0.0f, b[P];
+        if (P >= 4 && a.vec_bias) {
+#pragma unroll
+            for (int i = 0; i < P / 4; ++i) {
+                const float4 v = __ldg(reinterpret_cast<const float4 *>(a.bias + lane * P) + i);
+                b[4 * i] = v.x, b[P >= 4 ? 4 * i + 1 : 0] = v.y, b[P >= 4 ? 4 * i + 2 : 0] = v.z, b[P >= 4 ? 4 * i + 3 : 0] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                b[j] = j < here ? __ldg(a.bias + lane * P + j) : 0.0f;
+        }
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             float c = -INFINITY;
             if (j < here) {
-                c = s[j] + __ldg(a.bias + lane * P + j);
+                c = s[j] + b[j];
                 c = c == c ? c + 0.0f : -INFINITY;
                 cmax = fmaxf(cmax, fabsf(c) < INFINITY ? fabsf(c) : 0.0f);
             }
@@ -375,30 +387,48 @@ __device__ __forceinline__ void select_token(const Args &a, int t, int lane, flo
         }
     }
 
+    // K rounds.  Whether a second key was within the error bound of a round's highest shows in the next one (one more
+    // at the end): then the winner is put back and the round decided in fp64.
     my_idx = 0;
-    for (int k = 0; k < a.K; ++k) {
+    uint32_t lo = 0, before = 0;  // the last round's bound (0: none) and its winner's key,
+    int src = 0, j0 = 0;          // lane and register
+    auto highest = [&]() {
         uint32_t top = key[0];
 #pragma unroll
         for (int j = 1; j < P; ++j)
             top = max(top, key[j]);
-        const uint32_t mk = __reduce_max_sync(FULL, top);
-        int src = __ffs(__ballot_sync(FULL, top == mk)) - 1, j0 = 0;
+        return top;
+    };
+    for (int k = 0;; ++k) {
+        if (k == a.K && lo == 0u)
+            break;
+        uint32_t top = highest(), mk = __reduce_max_sync(FULL, top);
+        if (lo != 0u && mk >= lo) {
+            if (lane == src) {
 #pragma unroll
-        for (int j = P - 1; j >= 0; --j)
-            j0 = key[j] == mk ? j : j0;
-        if (eps > 0.0f) {
-            const uint32_t lo = ordered(unordered(mk) - 2.0f * eps);
+                for (int j = 0; j < P; ++j)
+                    key[j] = j == j0 ? before : key[j];
+            }
             uint32_t mask = 0;
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                mask |= key[j] >= lo && key[j] != 0u ? 1u << j : 0u;
-            const uint32_t lanes = __ballot_sync(FULL, mask != 0u), more = __ballot_sync(FULL, (mask & (mask - 1)) != 0u);
-            if ((lanes & (lanes - 1)) | more) {
-                const int e = best64(a, t, mask, P);
-                src = e / P;
-                j0 = e % P;
-            }
+                mask |= key[j] >= lo ? 1u << j : 0u;
+            const int e = best64(a, t, mask, P);
+            if (lane == k - 1)
+                my_idx = e;
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                key[j] = lane * P + j == e ? 0u : key[j];
+            top = highest();
+            mk = __reduce_max_sync(FULL, top);
         }
+        if (k == a.K)
+            break;
+        src = __ffs(__ballot_sync(FULL, top == mk)) - 1;
+        j0 = 0;
+#pragma unroll
+        for (int j = P - 1; j >= 0; --j)
+            j0 = key[j] == mk ? j : j0;
         if (lane == src) {
 #pragma unroll
             for (int j = 0; j < P; ++j)
@@ -407,6 +437,10 @@ __device__ __forceinline__ void select_token(const Args &a, int t, int lane, flo
         const int e = __shfl_sync(FULL, lane * P + j0, src);
         if (lane == k)
             my_idx = e;
+        if (eps > 0.0f) {
+            before = mk;
+            lo = ordered(unordered(mk) - 2.0f * eps);
+        }
     }
 
     // The weights of the chosen, a lane each, from their logits.  (A renormalised softmax goes by the largest
@@ -548,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) select_kernel(const 
             for (int k = 0; k < 4; ++k)
                 if (4 * i + k < a.E)
                     v |= (uint32_t)cnt[4 * i + k] << (8 * k);
-            a.bc[(int64_t)blockIdx.x * words + i] = v;
+            a.bc[(int64_t)i * a.pitch + blockIdx.x] = v;
         }
         return;
     }
@@ -568,28 +602,34 @@ __global__ void __launch_bounds__(32 * kPlaceWarps) place_kernel(const Args a)
     int *h = smi, *cnt = smi + kPlaceWarps * a.E;
     __shared__ int below[kMaxExperts];
     const int me = blockIdx.x, tid = threadIdx.x, words = (a.E + 3) / 4;
-    for (int e = tid; e < a.E; e += THREADS)
-        cnt[e] = below[e] = 0;
-    __syncthreads();
     pdl_wait();
     {
-        // all runs' counts, and those of the runs before this block's
-        const int word = tid % words, part = tid / words, parts = THREADS / words, mine = me * a.join;
-        uint32_t all[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
-        if (part < parts) {
-#pragma unroll 8
-            for (int r = part; r < a.runs; r += parts) {
-                const uint32_t v = a.bc[(int64_t)r * words + word];
+        // all runs' counts, and those of the runs before this block's: a warp has every 16th word of four experts, a
+        // lane four neighbouring runs at a time
+        const int mine = me * a.join, lane = tid & 31;
+#pragma unroll 4
+        for (int w = tid >> 5; w < words; w += kPlaceWarps) {
+            int all[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
+#pragma unroll 4
+            for (int r = 4 * lane; r < a.runs; r += 128) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(a.bc + (int64_t)w * a.pitch + r);
+                const uint32_t x[4] = {v.x, r + 1 < a.runs ? v.y : 0u, r + 2 < a.runs ? v.z : 0u, r + 3 < a.runs ? v.w : 0u};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t c = v >> (8 * k) & 255u;
-                    all[k] += c;
-                    low[k] += r < mine ? c : 0u;
-                }
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = (int)(x[i] >> (8 * k) & 255u);
+                        all[k] += c;
+                        low[k] += r + i < mine ? c : 0;
+                    }
             }
-            for (int k = 0; k < 4 && 4 * word + k < a.E; ++k) {
-                atomicAdd(cnt + 4 * word + k, (int)all[k]);
-                atomicAdd(below + 4 * word + k, (int)low[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int s = __reduce_add_sync(0xFFFFFFFFu, all[k]), b = __reduce_add_sync(0xFFFFFFFFu, low[k]);
+                if (lane == 0 && 4 * w + k < a.E) {
+                    cnt[4 * w + k] = s;
+                    below[4 * w + k] = b;
+                }
             }
         }
     }
@@ -657,7 +697,7 @@ mx_status check_router(const mx_router *r)
 size_t ws_bytes_of(int E, int T)
 {
     const int runs = runs_of(T);
-    return kErrBytes + up256(runs > 1 ? (size_t)runs * ((E + 3) / 4) * 4 : 0);
+    return kErrBytes + up256(runs > 1 ? (size_t)((runs + 3) / 4 * 4) * ((E + 3) / 4) * 4 : 0);
 }
 
 }  // namespace
@@ -728,6 +768,7 @@ extern "C" mx_status mx_route_logits(const void *logits, int64_t ld, int dtype, 
         a.perm = perm;
         a.bc = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + kErrBytes);
         a.runs = sel::runs_of(T);
+        a.pitch = (a.runs + 3) / 4 * 4;
         // (four runs, 32 tokens, to a placing block, and no more such blocks than 128)
         a.join = std::max(4, (a.runs + 127) / 128);
     }
@@ -740,6 +781,7 @@ extern "C" mx_status mx_route_logits(const void *logits, int64_t ld, int dtype, 
     a.lanes = size % P == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const size_t piece = std::min<size_t>(16, P * dtype_bytes(dtype));
     a.vec = E == 32 * P && aligned(logits, piece) && ld * dtype_bytes(dtype) % piece == 0;
+    a.vec_bias = E == 32 * P && aligned(a.bias, 16);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = P == 1   ? sel::launch<1>(a, grid, s)
                           : P == 2 ? sel::launch<2>(a, grid, s)
