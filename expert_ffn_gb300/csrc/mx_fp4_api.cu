@@ -116,7 +116,7 @@ Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
         units = (int64_t)((rows + c.nt - 1) / c.nt) * FT;
     }
     if (2 * units <= sms && KB >= 2)
-        c.cl = (int)std::min<int64_t>({8, sms / units, KB});
+        c.cl = (int)std::min<int64_t>({units <= 8 ? 8 : 4, sms / units, KB});
     if (c.cl > 4 && c.cl < 8)
         c.cl = 4;
     if (c.cl == 3)

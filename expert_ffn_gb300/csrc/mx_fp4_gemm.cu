@@ -19,11 +19,12 @@
 // bounded the kernel: 4096^3 82 us, without them 52.)
 //
 // Warps:
-//   0-3  results: TMEM (lane quadrant = warp) to global memory
-//   4    TMA producer: weight and token tiles
-//   5    MMA: per stage the copies of its scales to TMEM (tcgen05.cp, in order with the
+//   0-7  results: TMEM (lane quadrant = warp % 4, every other 16 tokens) to global memory, bf16 ones by
+//        way of shared memory in pieces of 16 bytes
+//   8    TMA producer: weight and token tiles
+//   9    MMA: per stage the copies of its scales to TMEM (tcgen05.cp, in order with the
 //        MMAs) and four MMAs (K = 64)
-//   6-7  the tokens' scales, every other stage each
+//   10-11  the tokens' scales, every other stage each
 // Two TMEM accumulators: a tile's results leave while the next one is summed.  Few units: a
 // cluster of `cl` CTAs splits the inner dimension of one unit, and its partial sums are added
 // through distributed shared memory in rank order.
@@ -59,7 +60,7 @@ using fp8::warp_index;
 using fp8::wwait;
 
 constexpr uint32_t kTile = 128 * 128;  // bytes of one weight tile
-constexpr int kOutWarps = 4, kScaleWarps = 2, kThreads = (kOutWarps + 2 + kScaleWarps) * 32;
+constexpr int kOutWarps = 8, kScaleWarps = 2, kThreads = (kOutWarps + 2 + kScaleWarps) * 32;
 constexpr int kAcc = 2;                // TMEM accumulators
 constexpr int kMaxStages = 12;
 
@@ -78,12 +79,14 @@ constexpr uint32_t tmem_cols(int block, int nt)
 
 // Dynamic shared memory after the ring.
 struct Tail {
-    int tab, bars, total;
+    int out, tab, bars, total;
 };
 __host__ __device__ constexpr Tail tail_of()
 {
     Tail t{};
     int o = 0;
+    t.out = o;  // a warp's results on their way out: 16 tokens x 32 bf16
+    o += kOutWarps * 1024;
     t.tab = o;
     o += (3 * kMaxExperts + 16) * 4;
     t.bars = o;
@@ -384,8 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
     } else {
         // ----------------------------------------------------------- results
-        const uint32_t ta = tmem + ((uint32_t)warp << 21);
+        const int quad = warp & 3;
+        const uint32_t ta = tmem + ((uint32_t)quad << 21);
         const float tx = a.tx ? *a.tx : 1.0f;
+        uint8_t *mine = tail + T.out + warp * 1024;
+        const int es = a.out_bf16 ? 2 : 4;
+        const int64_t pitch = a.ldo * es;
         int b = 0;
         uint32_t tph = 0;
         for (int u = w.first; u < w.n_units; u += w.step) {
@@ -395,27 +402,47 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 break;
             fence_after();
             const uint32_t tb = ta + b * acc_cols(NT);
-            const int row = warp * 32 + lane, o = U.f * 128 + row;
+            const int row = quad * 32 + lane, o0 = U.f * 128 + quad * 32, o = o0 + lane;
             float *part = reinterpret_cast<float *>(ring);
+            const bool whole = a.out_bf16 && a.out_vec && o0 + 32 <= a.N;
 #pragma unroll 1
-            for (int c0 = 0; c0 < U.n; c0 += 16) {
+            for (int c0 = (warp >> 2) * 16; c0 < U.n; c0 += 32) {
                 uint32_t r[16];
                 tmem_ld16(tb + c0, r);
                 tmem_wait();
+                float y[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    y[j] = tmem_value(r[j]) * tx * tw;
+                const int n = U.n - c0;  // tokens of these columns
+                char *to = static_cast<char *>(a.out) + (int64_t)(U.tok0 + c0) * pitch + (int64_t)o0 * es;
                 if (cl > 1) {  // one unit; every operand has been read
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        part[(c0 + j) * 128 + row] = tmem_value(r[j]) * tx * tw;
-                } else if (o < a.N) {
-                    const int64_t at = (int64_t)(U.tok0 + c0) * a.ldo + o;
+                        part[(c0 + j) * 128 + row] = y[j];
+                } else if (whole) {
+                    uint16_t *m = reinterpret_cast<uint16_t *>(mine) + lane;
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        if (c0 + j < U.n) {
-                            const float y = tmem_value(r[j]) * tx * tw;
+                        m[j * 32] = f2bf(y[j]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int j = i * 8 + (lane >> 2);
+                        const uint4 v = reinterpret_cast<const uint4 *>(mine)[i * 32 + lane];
+                        if (j < n)
+                            *reinterpret_cast<uint4 *>(to + j * pitch + (lane & 3) * 16) = v;
+                    }
+                    __syncwarp();
+                } else if (o < a.N) {
+                    to += lane * es;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j, to += pitch)
+                        if (j < n) {
                             if (a.out_bf16)
-                                static_cast<uint16_t *>(a.out)[at + j * a.ldo] = f2bf(y);
+                                *reinterpret_cast<uint16_t *>(to) = f2bf(y[j]);
                             else
-                                static_cast<float *>(a.out)[at + j * a.ldo] = y;
+                                *reinterpret_cast<float *>(to) = y[j];
                         }
                 }
             }
