@@ -10,11 +10,13 @@
 // few values of a large matrix to their neighbours.  The sum of squares is
 // therefore kept as two floats (Knuth's two-sum; a bf16 square is exact in fp32, an fp32
 // square's error comes from an fma), and the root is rounded once: Newton's correction of
-// rsqrtf, with the residual of r0^2 A = D computed exactly.  That is about ten
-// instructions a value, which a kernel bound by memory has to spare.
+// rsqrtf, with the residual of r0^2 A = D computed exactly.
 //
-// What bounds it: HBM.  4096 x 4096 bf16 with residual, sum, out and q move 151 MB, 22.4 us at
-// the copy rate.
+// What bounds it: HBM, where instructions allow it.  4096 x 4096 bf16 with residual, sum, out and
+// q move 151 MB, 22.4 us at the copy rate; a warp's 256 columns took 568 instructions in a
+// first form and 40 us.  So values go two to an instruction (f32x2), a warp's sums are added
+// as integers (redux, at the scale of the largest: 50 bits) instead of by five exchanges of two floats,
+// and one warp joins them and takes the root.
 #include "mx_fp8.cuh"
 #include "mx_host.h"
 
@@ -55,14 +57,6 @@ __device__ __forceinline__ float two_sum(float a, float b, float &err)
     return s;
 }
 
-__device__ __forceinline__ void add_square(Two &t, float h, bool exact)
-{
-    const float p = __fmul_rn(h, h);
-    float e;
-    t.hi = two_sum(t.hi, p, e);
-    t.lo += exact ? e : e + fmaf(h, h, -p);
-}
-
 __device__ __forceinline__ Two add_two(Two a, Two b)
 {
     float e;
@@ -70,77 +64,130 @@ __device__ __forceinline__ Two add_two(Two a, Two b)
     return Two{s, a.lo + b.lo + e};
 }
 
+__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The squares of a pair of values onto a pair of sums.
+template <bool EXACT>  // squares that fp32 holds
+__device__ __forceinline__ void add_squares(uint64_t &hi, uint64_t &lo, uint64_t h)
+{
+    const uint64_t p = mul_f32x2(h, h);
+    const uint64_t s = add_f32x2(hi, p), bb = sub_f32x2(s, hi);
+    uint64_t e = add_f32x2(sub_f32x2(hi, sub_f32x2(s, bb)), sub_f32x2(p, bb));
+    if (!EXACT) {
+        uint64_t r = mul_f32x2(p, pair_f32(-1.0f, -1.0f));
+        fma_f32x2(r, h, h);  // h^2 - p
+        e = add_f32x2(e, r);
+    }
+    hi = s;
+    lo = add_f32x2(lo, e);
+}
+
+__device__ __forceinline__ uint32_t bf16_x2(uint64_t v)
+{
+    float lo, hi;
+    unpair_f32(v, lo, hi);
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t of_bf16_x2(uint32_t w)
+{
+    return pair_f32(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Eight neighbouring values, zeros behind the last of n, as pairs.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *p, int64_t at, int n, bool vec, float (&v)[8])
+__device__ __forceinline__ void load8(const void *p, int64_t at, int n, bool vec, uint64_t (&v)[4])
 {
     if (vec && n >= 8) {
         if (BF16) {
             const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
-            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
+            v[0] = of_bf16_x2(r.x), v[1] = of_bf16_x2(r.y), v[2] = of_bf16_x2(r.z), v[3] = of_bf16_x2(r.w);
         } else {
             const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
             const float4 a = f[0], b = f[1];
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            v[0] = pair_f32(a.x, a.y), v[1] = pair_f32(a.z, a.w), v[2] = pair_f32(b.x, b.y), v[3] = pair_f32(b.z, b.w);
         }
     } else {
+        float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            v[j] = 0.0f;
+            f[j] = 0.0f;
             if (j < n)
-                v[j] = BF16 ? bf2f(static_cast<const uint16_t *>(p)[at + j]) : static_cast<const float *>(p)[at + j];
+                f[j] = BF16 ? bf2f(static_cast<const uint16_t *>(p)[at + j]) : static_cast<const float *>(p)[at + j];
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = pair_f32(f[2 * j], f[2 * j + 1]);
     }
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store8(void *p, int64_t at, int n, bool vec, const float (&v)[8])
+__device__ __forceinline__ void store8(void *p, int64_t at, int n, bool vec, const uint64_t (&v)[4])
 {
     if (vec && n >= 8) {
         if (BF16) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = f2bf(v[2 * i]) | (uint32_t)f2bf(v[2 * i + 1]) << 16;
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) =
+                make_uint4(bf16_x2(v[0]), bf16_x2(v[1]), bf16_x2(v[2]), bf16_x2(v[3]));
         } else {
-            float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
-            f[0] = make_float4(v[0], v[1], v[2], v[3]);
-            f[1] = make_float4(v[4], v[5], v[6], v[7]);
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                unpair_f32(v[j], f[2 * j], f[2 * j + 1]);
+            float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
+            to[0] = make_float4(f[0], f[1], f[2], f[3]);
+            to[1] = make_float4(f[4], f[5], f[6], f[7]);
         }
     } else {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            unpair_f32(v[j], f[2 * j], f[2 * j + 1]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (j < n) {
                 if (BF16)
-                    static_cast<uint16_t *>(p)[at + j] = f2bf(v[j]);
+                    static_cast<uint16_t *>(p)[at + j] = f2bf(f[j]);
                 else
-                    static_cast<float *>(p)[at + j] = v[j];
+                    static_cast<float *>(p)[at + j] = f[j];
             }
     }
 }
 
-// Sum over the CTA's threads: every thread gets the same two floats.
-__device__ __forceinline__ Two block_sum(Two t, Two *part, int warps)
+// A warp's sum of hi + lo (hi >= 0, lo within half an ulp of it) as integers: hi below 2^25 at the scale
+// of the warp's largest, the rest in units 2^-25 of that.  Every lane gets it.
+struct Part {
+    int hi, lo;
+    uint32_t top;  // bits of the largest hi
+};
+__device__ __forceinline__ int part_scale(uint32_t top) { return 151 - max((int)(top >> 23), 27); }
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(127 + k) << 23); }
+
+__device__ __forceinline__ Part warp_part(float hi, float lo)
 {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        t = add_two(t, Two{__shfl_xor_sync(0xFFFFFFFFu, t.hi, o), __shfl_xor_sync(0xFFFFFFFFu, t.lo, o)});
-    if (lane == 0)
-        part[threadIdx.x >> 5] = t;
-    __syncthreads();
-    t = lane < warps ? part[lane] : Two{0.0f, 0.0f};
-    for (int o = 16; o; o >>= 1)
-        if (o < warps)
-            t = add_two(t, Two{__shfl_xor_sync(0xFFFFFFFFu, t.hi, o), __shfl_xor_sync(0xFFFFFFFFu, t.lo, o)});
-    t.hi = __shfl_sync(0xFFFFFFFFu, t.hi, 0);
-    t.lo = __shfl_sync(0xFFFFFFFFu, t.lo, 0);
-    return t;
+    Part p;
+    p.top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(hi));  // (a NaN's bits are above infinity's)
+    const float f = pow2(part_scale(p.top)), h = hi * f;
+    const int hi_i = __float2int_rn(h);
+    const int lo_i = __float2int_rn(((h - (float)hi_i) + __fmul_rn(lo, f)) * 33554432.0f);
+    p.hi = __reduce_add_sync(0xFFFFFFFFu, hi_i);
+    p.lo = __reduce_add_sync(0xFFFFFFFFu, lo_i);
+    return p;
+}
+
+__device__ __forceinline__ Two of_part(Part p)
+{
+    if (p.top >= 0x7F800000u)
+        return Two{__uint_as_float(p.top), 0.0f};
+    const float g = pow2(-part_scale(p.top));
+    const float hi = (float)(p.hi & ~127), lo = (float)(p.hi & 127) + (float)p.lo * 2.9802322e-8f;
+    return Two{hi * g, lo * g};
 }
 
 // sqrt(D / (S + D eps)), rounded once.
@@ -162,11 +209,12 @@ __device__ __forceinline__ float root(Two S, float D, float eps)
 template <bool BF16, int V>
 __global__ void norm_kernel(const Args a)
 {
-    __shared__ Two part[2][32];
-    const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5;
+    __shared__ Part part[32];
+    __shared__ float shared_r, shared_f;
+    const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x;
     const float D = (float)a.cols;
-    float h[V][8];
+    uint64_t h[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = (i * threads + tid) * 8, n = a.cols - c;
@@ -176,13 +224,13 @@ __global__ void norm_kernel(const Args a)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = (i * threads + tid) * 8, n = a.cols - c;
-            float r[8];
+            uint64_t r[4];
             load8<BF16>(a.residual, row * a.ldr + c, n, a.vr, r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                h[i][j] += r[j];
+            for (int j = 0; j < 4; ++j) {
+                h[i][j] = add_f32x2(h[i][j], r[j]);
                 if (BF16)
-                    h[i][j] = bf2f(f2bf(h[i][j]));
+                    h[i][j] = of_bf16_x2(bf16_x2(h[i][j]));
             }
         }
     }
@@ -195,45 +243,73 @@ __global__ void norm_kernel(const Args a)
     }
     if (!a.out && !a.q)
         return;
-    Two S{0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            add_square(S, h[i][j], BF16);
-    S = block_sum(S, part[0], warps);
-    float r;
-    if (S.hi < 1.2676506e30f && S.hi + D * a.eps > 8.6736174e-19f) {
-        r = root(S, D, a.eps);
-    } else {
-        // squares beyond fp32's range (2^100, 2^-60): once more with h times a power of two
-        const float f = S.hi < 1.0f ? 1.1529215e18f : 8.4703295e-22f;  // 2^60, 2^-70
-        S = Two{0.0f, 0.0f};
+
+    float r, f = 1.0f;
+    // (a second time, with h times a power of two, where squares leave fp32's range)
+    for (int pass = 0;; ++pass) {
+        uint64_t hi2 = 0, lo2 = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                add_square(S, h[i][j] * f, false);
-        S = block_sum(S, part[1], warps);
-        r = root(S, D, a.eps * f * f) * f;
+            for (int j = 0; j < 4; ++j) {
+                if (pass == 0)
+                    add_squares<BF16>(hi2, lo2, h[i][j]);
+                else
+                    add_squares<false>(hi2, lo2, mul_f32x2(h[i][j], pair_f32(f, f)));
+            }
+        float h0, h1, l0, l1, e;
+        unpair_f32(hi2, h0, h1);
+        unpair_f32(lo2, l0, l1);
+        const float s = two_sum(h0, h1, e), l = l0 + l1 + e, hi = s + l, lo = l - (hi - s);
+        const Part p = warp_part(s < INFINITY ? hi : s, lo);
+        if (lane == 0)
+            part[tid >> 5] = p;
+        __syncthreads();
+        if (tid < 32) {
+            Two S = lane < warps ? of_part(part[lane]) : Two{0.0f, 0.0f};
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+                S = add_two(S, Two{__shfl_xor_sync(0xFFFFFFFFu, S.hi, o), __shfl_xor_sync(0xFFFFFFFFu, S.lo, o)});
+            float g = 0.0f;  // (done)
+            if (pass == 0 && !(S.hi < 1.2676506e30f && S.hi + D * a.eps > 8.6736174e-19f))  // 2^100, 2^-60
+                g = S.hi < 1.0f ? 1.1529215e18f : 8.4703295e-22f;                          // 2^60, 2^-70
+            if (lane == 0) {
+                shared_r = root(S, D, a.eps * f * f) * f;
+                shared_f = g;
+            }
+        }
+        __syncthreads();
+        r = shared_r;
+        if (shared_f == 0.0f)
+            break;
+        f = shared_f;
     }
+
+    const uint64_t r2 = pair_f32(r, r), off2 = pair_f32(a.offset, a.offset);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = (i * threads + tid) * 8, n = a.cols - c;
-        float y[8];
+        uint64_t y[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = j < n ? h[i][j] * r : 0.0f;
+        for (int j = 0; j < 4; ++j)
+            y[j] = mul_f32x2(h[i][j], r2);
         if (a.weight) {
-            float w[8];
+            uint64_t w[4];
             if (a.w_bf16)
                 load8<true>(a.weight, c, n, a.vw, w);
             else
                 load8<false>(a.weight, c, n, a.vw, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n)
-                    y[j] *= a.offset + w[j];
+            for (int j = 0; j < 4; ++j)
+                y[j] = mul_f32x2(y[j], add_f32x2(off2, w[j]));
+        }
+        if (n < 8) {  // (behind the last column: zeros, whatever r is)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float lo, hi;
+                unpair_f32(y[j], lo, hi);
+                y[j] = pair_f32(2 * j < n ? lo : 0.0f, 2 * j + 1 < n ? hi : 0.0f);
+            }
         }
         if (a.out) {
             if (a.out_bf16)
@@ -244,17 +320,16 @@ __global__ void norm_kernel(const Args a)
         if (a.q) {
             uint32_t m = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                m = max(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+            for (int j = 0; j < 4; ++j) {
+                float lo, hi;
+                unpair_f32(y[j], lo, hi);
+                m = max(m, max(__float_as_uint(lo) & 0x7FFFFFFFu, __float_as_uint(hi) & 0x7FFFFFFFu));
+            }
 #pragma unroll
             for (int o = 8; o; o >>= 1)
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            uint64_t p[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                p[j] = pair_f32(y[2 * j], y[2 * j + 1]);
             uint32_t e[4];
-            const float s = fp8::quantize_pairs(p, m, a.pow2, e);
+            const float s = fp8::quantize_pairs(y, m, a.pow2, e);
             if (n > 0) {
                 uint8_t *q = a.q + row * a.ldq + c;
                 const uint2 w = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
