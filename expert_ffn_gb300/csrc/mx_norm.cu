@@ -101,37 +101,61 @@ __device__ __forceinline__ uint64_t of_bf16_x2(uint32_t w)
     return pair_f32(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// Eight neighbouring values, zeros behind the last of n, as pairs.
+// Eight neighbouring values as they were loaded, zeros behind the last of n.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *p, int64_t at, int n, bool vec, uint64_t (&v)[4])
+struct Raw {
+    uint4 r[BF16 ? 1 : 2];
+};
+
+template <bool BF16, bool FAST>
+__device__ __forceinline__ Raw<BF16> load8(const void *p, int64_t at, int n, bool vec)
 {
-    if (vec && n >= 8) {
-        if (BF16) {
-            const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
-            v[0] = of_bf16_x2(r.x), v[1] = of_bf16_x2(r.y), v[2] = of_bf16_x2(r.z), v[3] = of_bf16_x2(r.w);
-        } else {
-            const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-            const float4 a = f[0], b = f[1];
-            v[0] = pair_f32(a.x, a.y), v[1] = pair_f32(a.z, a.w), v[2] = pair_f32(b.x, b.y), v[3] = pair_f32(b.z, b.w);
-        }
+    Raw<BF16> v{};
+    if (FAST && n <= 0)
+        return v;
+    if (FAST || (vec && n >= 8)) {
+        const uint4 *q = BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at)
+                              : reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + at);
+        v.r[0] = q[0];
+        if (!BF16)
+            v.r[BF16 ? 0 : 1] = q[1];
     } else {
-        float f[8];
+        uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            f[j] = 0.0f;
+            w[j] = 0;
             if (j < n)
-                f[j] = BF16 ? bf2f(static_cast<const uint16_t *>(p)[at + j]) : static_cast<const float *>(p)[at + j];
+                w[j] = BF16 ? static_cast<const uint16_t *>(p)[at + j] : static_cast<const uint32_t *>(p)[at + j];
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[j] = pair_f32(f[2 * j], f[2 * j + 1]);
+        if (BF16) {
+            v.r[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        } else {
+            v.r[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            v.r[BF16 ? 0 : 1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+    return v;
+}
+
+// The same as pairs.
+template <bool BF16>
+__device__ __forceinline__ void pairs(const Raw<BF16> &x, uint64_t (&v)[4])
+{
+    const uint4 a = x.r[0], b = x.r[BF16 ? 0 : 1];
+    if (BF16) {
+        v[0] = of_bf16_x2(a.x), v[1] = of_bf16_x2(a.y), v[2] = of_bf16_x2(a.z), v[3] = of_bf16_x2(a.w);
+    } else {
+        v[0] = pair_f32(__uint_as_float(a.x), __uint_as_float(a.y)), v[1] = pair_f32(__uint_as_float(a.z), __uint_as_float(a.w));
+        v[2] = pair_f32(__uint_as_float(b.x), __uint_as_float(b.y)), v[3] = pair_f32(__uint_as_float(b.z), __uint_as_float(b.w));
     }
 }
 
-template <bool BF16>
+template <bool BF16, bool FAST>
 __device__ __forceinline__ void store8(void *p, int64_t at, int n, bool vec, const uint64_t (&v)[4])
 {
-    if (vec && n >= 8) {
+    if (FAST && n <= 0)
+        return;
+    if (FAST || (vec && n >= 8)) {
         if (BF16) {
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) =
                 make_uint4(bf16_x2(v[0]), bf16_x2(v[1]), bf16_x2(v[2]), bf16_x2(v[3]));
@@ -206,143 +230,167 @@ __device__ __forceinline__ float root(Two S, float D, float eps)
     return fmaf(r0, d * fmaf(0.375f, d, 0.5f), r0);
 }
 
-template <bool BF16, int V>
-__global__ void norm_kernel(const Args a)
+// The largest of m, |a| and |b|; a NaN stays one.
+__device__ __forceinline__ float max_abs(float m, float a, float b)
 {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
+
+// A CTA takes every gridDim.x-th row; the next one's loads are under way while one is worked on (`AHEAD`).
+// FAST: every tensor may be moved in whole pieces, and the columns end with one.
+template <bool BF16, int V, bool FAST>
+__global__ void __launch_bounds__(512, V == 1 ? (BF16 ? 3 : 2) : 1) norm_kernel(const Args a)
+{
+    constexpr bool AHEAD = V <= 2;
     __shared__ Part part[32];
     __shared__ float shared_r, shared_f;
     const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5, lane = tid & 31;
-    const int64_t row = blockIdx.x;
     const float D = (float)a.cols;
-    uint64_t h[V][4];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = (i * threads + tid) * 8, n = a.cols - c;
-        load8<BF16>(a.x, row * a.ldx + c, n, a.vx, h[i]);
-    }
-    if (a.residual) {
+    // first column of piece i, and how many of the eight there are
+    auto column = [&](int i) { return (i * threads + tid) * 8; };
+    auto count = [&](int i) { return FAST ? (column(i) < a.cols ? 8 : 0) : a.cols - column(i); };
+    Raw<BF16> x[V], res[V];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = (i * threads + tid) * 8, n = a.cols - c;
-            uint64_t r[4];
-            load8<BF16>(a.residual, row * a.ldr + c, n, a.vr, r);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                h[i][j] = add_f32x2(h[i][j], r[j]);
-                if (BF16)
-                    h[i][j] = of_bf16_x2(bf16_x2(h[i][j]));
-            }
+            x[i] = load8<BF16, FAST>(a.x, row * a.ldx + column(i), count(i), a.vx);
+            if (a.residual)
+                res[i] = load8<BF16, FAST>(a.residual, row * a.ldr + column(i), count(i), a.vr);
         }
-    }
-    if (a.sum) {
+    };
+    if (AHEAD)
+        fetch(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        if (!AHEAD)
+            fetch(row);
+        uint64_t h[V][4];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = (i * threads + tid) * 8, n = a.cols - c;
-            store8<BF16>(a.sum, row * a.lds + c, n, a.vs, h[i]);
-        }
-    }
-    if (!a.out && !a.q)
-        return;
-
-    float r, f = 1.0f;
-    // (a second time, with h times a power of two, where squares leave fp32's range)
-    for (int pass = 0;; ++pass) {
-        uint64_t hi2 = 0, lo2 = 0;
+            pairs<BF16>(x[i], h[i]);
+            if (a.residual) {
+                uint64_t r[4];
+                pairs<BF16>(res[i], r);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (pass == 0)
-                    add_squares<BF16>(hi2, lo2, h[i][j]);
-                else
-                    add_squares<false>(hi2, lo2, mul_f32x2(h[i][j], pair_f32(f, f)));
-            }
-        float h0, h1, l0, l1, e;
-        unpair_f32(hi2, h0, h1);
-        unpair_f32(lo2, l0, l1);
-        const float s = two_sum(h0, h1, e), l = l0 + l1 + e, hi = s + l, lo = l - (hi - s);
-        const Part p = warp_part(s < INFINITY ? hi : s, lo);
-        if (lane == 0)
-            part[tid >> 5] = p;
-        __syncthreads();
-        if (tid < 32) {
-            Two S = lane < warps ? of_part(part[lane]) : Two{0.0f, 0.0f};
-#pragma unroll
-            for (int o = 16; o; o >>= 1)
-                S = add_two(S, Two{__shfl_xor_sync(0xFFFFFFFFu, S.hi, o), __shfl_xor_sync(0xFFFFFFFFu, S.lo, o)});
-            float g = 0.0f;  // (done)
-            if (pass == 0 && !(S.hi < 1.2676506e30f && S.hi + D * a.eps > 8.6736174e-19f))  // 2^100, 2^-60
-                g = S.hi < 1.0f ? 1.1529215e18f : 8.4703295e-22f;                          // 2^60, 2^-70
-            if (lane == 0) {
-                shared_r = root(S, D, a.eps * f * f) * f;
-                shared_f = g;
+                for (int j = 0; j < 4; ++j) {
+                    h[i][j] = add_f32x2(h[i][j], r[j]);
+                    if (BF16)
+                        h[i][j] = of_bf16_x2(bf16_x2(h[i][j]));
+                }
             }
         }
-        __syncthreads();
-        r = shared_r;
-        if (shared_f == 0.0f)
-            break;
-        f = shared_f;
-    }
+        if (AHEAD && row + gridDim.x < a.rows)
+            fetch(row + gridDim.x);
+        if (a.sum) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                store8<BF16, FAST>(a.sum, row * a.lds + column(i), count(i), a.vs, h[i]);
+        }
+        if (!a.out && !a.q)
+            continue;
 
-    const uint64_t r2 = pair_f32(r, r), off2 = pair_f32(a.offset, a.offset);
+        float r, f = 1.0f;
+        // (a second time, with h times a power of two, where squares leave fp32's range)
+        for (int pass = 0;; ++pass) {
+            uint64_t hi2 = 0, lo2 = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = (i * threads + tid) * 8, n = a.cols - c;
-        uint64_t y[4];
+            for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            y[j] = mul_f32x2(h[i][j], r2);
-        if (a.weight) {
-            uint64_t w[4];
-            if (a.w_bf16)
-                load8<true>(a.weight, c, n, a.vw, w);
-            else
-                load8<false>(a.weight, c, n, a.vw, w);
+                for (int j = 0; j < 4; ++j) {
+                    if (pass == 0)
+                        add_squares<BF16>(hi2, lo2, h[i][j]);
+                    else
+                        add_squares<false>(hi2, lo2, mul_f32x2(h[i][j], pair_f32(f, f)));
+                }
+            float h0, h1, l0, l1, e;
+            unpair_f32(hi2, h0, h1);
+            unpair_f32(lo2, l0, l1);
+            const float s = two_sum(h0, h1, e), l = l0 + l1 + e, hi = s + l, lo = l - (hi - s);
+            const Part p = warp_part(s < INFINITY ? hi : s, lo);
+            if (lane == 0)
+                part[tid >> 5] = p;
+            __syncthreads();
+            if (tid < 32) {
+                Two S = lane < warps ? of_part(part[lane]) : Two{0.0f, 0.0f};
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    S = add_two(S, Two{__shfl_xor_sync(0xFFFFFFFFu, S.hi, o), __shfl_xor_sync(0xFFFFFFFFu, S.lo, o)});
+                float g = 0.0f;  // (done)
+                if (pass == 0 && !(S.hi < 1.2676506e30f && S.hi + D * a.eps > 8.6736174e-19f))  // 2^100, 2^-60
+                    g = S.hi < 1.0f ? 1.1529215e18f : 8.4703295e-22f;                          // 2^60, 2^-70
+                if (lane == 0) {
+                    shared_r = root(S, D, a.eps * f * f) * f;
+                    shared_f = g;
+                }
+            }
+            __syncthreads();
+            r = shared_r;
+            if (shared_f == 0.0f)
+                break;
+            f = shared_f;
+        }
+
+        const uint64_t r2 = pair_f32(r, r), off2 = pair_f32(a.offset, a.offset);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = column(i), n = count(i);
+            uint64_t y[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                y[j] = mul_f32x2(y[j], add_f32x2(off2, w[j]));
-        }
-        if (n < 8) {  // (behind the last column: zeros, whatever r is)
+                y[j] = mul_f32x2(h[i][j], r2);
+            if (a.weight) {
+                uint64_t w[4];
+                if (a.w_bf16)
+                    pairs<true>(load8<true, FAST>(a.weight, c, n, a.vw), w);
+                else
+                    pairs<false>(load8<false, FAST>(a.weight, c, n, a.vw), w);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float lo, hi;
-                unpair_f32(y[j], lo, hi);
-                y[j] = pair_f32(2 * j < n ? lo : 0.0f, 2 * j + 1 < n ? hi : 0.0f);
+                for (int j = 0; j < 4; ++j)
+                    y[j] = mul_f32x2(y[j], add_f32x2(off2, w[j]));
             }
-        }
-        if (a.out) {
-            if (a.out_bf16)
-                store8<true>(a.out, row * a.ldo + c, n, a.vo, y);
-            else
-                store8<false>(a.out, row * a.ldo + c, n, a.vo, y);
-        }
-        if (a.q) {
-            uint32_t m = 0;
+            if (n < 8) {  // (behind the last column: zeros, whatever r is)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float lo, hi;
-                unpair_f32(y[j], lo, hi);
-                m = max(m, max(__float_as_uint(lo) & 0x7FFFFFFFu, __float_as_uint(hi) & 0x7FFFFFFFu));
-            }
-#pragma unroll
-            for (int o = 8; o; o >>= 1)
-                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            uint32_t e[4];
-            const float s = fp8::quantize_pairs(y, m, a.pow2, e);
-            if (n > 0) {
-                uint8_t *q = a.q + row * a.ldq + c;
-                const uint2 w = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
-                if (a.vq && n >= 8) {
-                    *reinterpret_cast<uint2 *>(q) = w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < n)
-                            q[j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+                for (int j = 0; j < 4; ++j) {
+                    float lo, hi;
+                    unpair_f32(y[j], lo, hi);
+                    y[j] = FAST ? 0 : pair_f32(2 * j < n ? lo : 0.0f, 2 * j + 1 < n ? hi : 0.0f);
                 }
-                if ((tid & 15) == 0)
-                    a.scales[row * a.s_r + (int64_t)(c / kBlk) * a.s_b] = s;
+            }
+            if (a.out) {
+                if (a.out_bf16)
+                    store8<true, FAST>(a.out, row * a.ldo + c, n, a.vo, y);
+                else
+                    store8<false, FAST>(a.out, row * a.ldo + c, n, a.vo, y);
+            }
+            if (a.q) {
+                float top = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float lo, hi;
+                    unpair_f32(y[j], lo, hi);
+                    top = max_abs(top, lo, hi);
+                }
+                uint32_t m = __float_as_uint(top);
+#pragma unroll
+                for (int o = 8; o; o >>= 1)
+                    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                uint32_t e[4];
+                const float s = fp8::quantize_pairs(y, m, a.pow2, e);
+                if (n > 0) {
+                    uint8_t *q = a.q + row * a.ldq + c;
+                    const uint2 w = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+                    if (FAST || (a.vq && n >= 8)) {
+                        *reinterpret_cast<uint2 *>(q) = w;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < n)
+                                q[j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+                    }
+                    if ((tid & 15) == 0)
+                        a.scales[row * a.s_r + (int64_t)(c / kBlk) * a.s_b] = s;
+                }
             }
         }
     }
@@ -351,7 +399,14 @@ __global__ void norm_kernel(const Args a)
 template <bool BF16, int V>
 cudaError_t launch_v(const Args &a, int threads, cudaStream_t s)
 {
-    norm_kernel<BF16, V><<<a.rows, threads, 0, s>>>(a);
+    const bool fast = a.vx && a.cols % 8 == 0 && (!a.residual || a.vr) && (!a.sum || a.vs) && (!a.out || a.vo) &&
+                      (!a.q || a.vq) && (!a.weight || a.vw);
+    const int per_sm = V == 1 ? (BF16 ? 1536 : 1024) / threads : 1;
+    const int grid = std::min(a.rows, num_sms() * std::max(1, per_sm));
+    if (fast)
+        norm_kernel<BF16, V, true><<<grid, threads, 0, s>>>(a);
+    else
+        norm_kernel<BF16, V, false><<<grid, threads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
