@@ -7,20 +7,23 @@
 // in fp32, and only where the choice needs them: without a bias experts are compared by
 // their logits, and the chosen ones' weights are worked out at the end, a lane each.
 // The choice compares 32-bit keys (a number's bits, made to order as
-// unsigned integers; 0: no longer there), k times a maximum over registers and one
-// warp reduction.
+// unsigned integers; 0: no longer there): each lane sorts its own, then k times the
+// highest of the 32 heads is taken off by one warp reduction; which expert a key was, lane k finds
+// at the end among the winning lane's keys in shared memory.
 //
 // Exactness.  Where an fp32 score (with a bias, or the sum of a run's two best)
-// decides, everything within its error bound of the maximum is a candidate; a
-// second candidate, about one token in a thousand, sends the comparison to fp64, for
-// the candidates alone.
+// decides, the chosen ones and the next are looked at once more: any two neighbours
+// within their error bounds, about one token in a thousand, send the token to a loop that
+// compares the candidates in fp64.  Without a bias experts compare by their logits, which no
+// rounding has touched.
 //
 // Grouping.  A selecting block of eight warps leaves its tokens' counts by expert; the
-// placing kernel's blocks each add up all of them (bytes, so that 4096 tokens of 256 experts are
-// 128 KB) and put their own tokens' slots in order.  One selecting block does both.
+// placing kernel's blocks each add up all of them (bytes, an expert's neighbouring, so that 4096
+// tokens of 256 experts are 128 KB and four runs one dp4a) and put their own tokens' slots in order.  One
+// selecting block does both.
 //
-// What bounds it: 4096 x 256 fp32 logits are 4 MB, 0.6 us of HBM; the k rounds are a chain of some 100
-// cycles each, and a launch or two the rest.
+// What bounds it: 4096 x 256 fp32 logits are 4 MB, 0.6 us of HBM; instructions (some 600 a token) and
+// a launch or two are the rest.
 #include "mx_common.cuh"
 #include "mx_host.h"
 #include "mx_internal.h"
@@ -37,7 +40,7 @@ namespace {
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kRuns = 512;    // selecting blocks when slots are grouped, as long as kMaxRun allows
 constexpr int kMaxRun = 248;  // their tokens at most (their counts are bytes)
-constexpr int kPlaceWarps = 16;
+constexpr int kPlaceWarps = 8;
 
 struct Args {
     const void *logits;
@@ -50,9 +53,9 @@ struct Args {
     int32_t *idx;
     float *w;
     int32_t *counts, *offsets, *perm;  // nullable together
-    uint32_t *bc;          // [ceil(E / 4)][runs] counts of the selecting blocks' tokens, four bytes to a word
+    uint8_t *bc;           // [E][pitch] counts of the selecting blocks' tokens
     int per, runs, join;   // tokens of a selecting block, such blocks, how many of them a placing block joins
-    int pitch;             // runs rounded up to a multiple of 4
+    int pitch;             // runs rounded up to a multiple of 16
     int lanes;             // lanes of a run of experts, a power of two; 0: it does not end with lanes
 };
 
@@ -67,8 +70,8 @@ __device__ __forceinline__ float unordered(uint32_t o)
     return __uint_as_float(o ^ ((uint32_t)((int32_t)~o >> 31) | 0x80000000u));
 }
 
-// A logit; a NaN counts as -inf, and -0 as 0.
-__device__ __forceinline__ float tidy(float l) { return l == l ? l + 0.0f : -INFINITY; }
+// A logit; a NaN counts as -inf (fmaxf leaves it out), and -0 as 0.
+__device__ __forceinline__ float tidy(float l) { return fmaxf(l + 0.0f, -INFINITY); }
 
 __device__ __forceinline__ float load1(const Args &a, int64_t at)
 {
@@ -180,7 +183,80 @@ __device__ __noinline__ int best_group64(const Args &a, int t, uint32_t mask)
     return at;
 }
 
+// A bound of a score's rounding: relative to it, on top of the score's own error `off`.
+constexpr float kRel = 2.3841858e-7f;  // 2^-22
+
+// The chosen runs (a bit each) where fp32 leaves them open.  gs, ge: this lane's run's score and its error bound;
+// leader: a lane that speaks for run g.
+__device__ __noinline__ uint32_t exact_groups(const Args &a, int t, float gs, float ge, bool leader, int g)
+{
+    uint32_t kept = 0;
+    for (int k = 0; k < a.topk_groups; ++k) {
+        const bool in = leader && !(kept >> g & 1u);
+        const uint32_t low = __reduce_max_sync(0xFFFFFFFFu, in ? ordered(gs - ge) : 0u);
+        const uint32_t all = __reduce_or_sync(0xFFFFFFFFu, in && ordered(gs + ge) >= low ? 1u << g : 0u);
+        kept |= 1u << (all & (all - 1) ? best_group64(a, t, all) : __ffs(all) - 1);
+    }
+    return kept;
+}
+
+// The chosen experts, lane k the k-th, where fp32 leaves their order open.  keys: of all experts, in shared memory.
+template <int P>
+__device__ __noinline__ int exact_experts(const Args &a, int t, const uint32_t *keys, float off)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t key[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+        key[j] = lane * P + j < a.E ? keys[lane * P + j] : 0u;
+    int mine = 0;
+    for (int k = 0; k < a.K; ++k) {
+        uint32_t top = key[0];
+#pragma unroll
+        for (int j = 1; j < P; ++j)
+            top = max(top, key[j]);
+        const uint32_t mk = __reduce_max_sync(0xFFFFFFFFu, top);
+        const float f = unordered(mk);
+        const uint32_t lo = fabsf(f) < INFINITY ? ordered(f - 2.0f * (off + kRel * fabsf(f))) : mk;
+        uint32_t mask = 0;
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            mask |= key[j] >= lo ? 1u << j : 0u;
+        const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, mask != 0u);
+        int e;
+        if ((lanes & (lanes - 1)) | __ballot_sync(0xFFFFFFFFu, (mask & (mask - 1)) != 0u))
+            e = best64(a, t, mask, P);
+        else
+            e = __shfl_sync(0xFFFFFFFFu, lane * P + __ffs(mask) - 1, __ffs(lanes) - 1);
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            key[j] = lane * P + j == e ? 0u : key[j];
+        if (lane == k)
+            mine = e;
+    }
+    return mine;
+}
+
 // ------------------------------------------------------------------ selection
+
+// Sorts descending (Batcher's odd-even merge sort).
+template <int P>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[P])
+{
+#pragma unroll
+    for (int p = 1; p < P; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < P; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (j + i + q < P && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
+                        const uint32_t x = k[j + i], y = k[j + i + q];
+                        k[j + i] = max(x, y);
+                        k[j + i + q] = min(x, y);
+                    }
+}
 
 // The lane's logits; behind the last expert -inf.
 template <int P>
@@ -234,24 +310,23 @@ __device__ __forceinline__ void load_logits(const Args &a, int t, int lane, floa
         l[j] = tidy(l[j]);
 }
 
-// One token by one warp.  row: E floats of shared memory (for runs).  Lane k < K returns
-// the k-th choice and its weight.
+// One token by one warp.  row: E words of shared memory.  Lane k < K returns the k-th choice and its
+// weight.
 template <int P>
-__device__ __forceinline__ void select_token(const Args &a, int t, int lane, float *row, int &my_idx, float &my_w)
+__device__ __forceinline__ void select_token(const Args &a, int t, int lane, uint32_t *row, int &my_idx, float &my_w)
 {
     constexpr uint32_t FULL = 0xFFFFFFFFu;
     float l[P];
     load_logits<P>(a, t, lane, l);
     const int here = min(max(a.E - lane * P, 0), P);  // experts of this lane
     const bool groups = a.topk_groups < a.n_groups;
-    const bool by_score = groups && a.best == 2 && !a.bias;  // runs by sums of scores (else by the keys' own order)
+    const bool by_score = groups && a.best == 2 && !a.bias;  // runs by sums of scores (else by what experts go by)
     const bool soft = a.score == MX_SOFTMAX;
 
-    // Scores, where the choice or a softmax's weights need them, and eps: more than any |score - exact one|.  A
-    // sigmoid by the fast exponential (2 + 1.16 |l| ulp) is off by s (1 - s) of that and two roundings, below
-    // 2^-20; a softmax by expf (2 ulp) by the arguments' shift, worth d e^-d ulp, and up to 25 roundings of its
-    // sum, below 2^-19 of the largest.
-    float s[P], m = 0.0f, z = 1.0f, off = 0.0f;
+    // c: what experts are chosen by.  off: more than the error of any score in it.  A sigmoid by the fast exponential
+    // (2 + 1.16 |l| ulp) is off by s (1 - s) of that, 0.62 2^-23 at most, and two roundings; a softmax by expf (2 ulp)
+    // by the arguments' shift, worth d e^-d ulp, and up to 25 roundings of its sum, below 2^-19 of the largest.
+    float c[P], s[P], m = 0.0f, z = 1.0f, off = 0.0f;
     if (soft) {
         m = l[0];
 #pragma unroll
@@ -276,172 +351,164 @@ __device__ __forceinline__ void select_token(const Args &a, int t, int lane, flo
 #pragma unroll
         for (int j = 0; j < P; ++j)
             s[j] = __fdividef(1.0f, 1.0f + __expf(-l[j]));
-        off = 9.5367432e-7f;
+        off = 2.9802322e-7f;
     }
-
-    uint32_t key[P];
-    float eps = 0.0f;
     if (a.bias) {
-        float cmax = 0.0f, b[P];
         if (P >= 4 && a.vec_bias) {
 #pragma unroll
             for (int i = 0; i < P / 4; ++i) {
                 const float4 v = __ldg(reinterpret_cast<const float4 *>(a.bias + lane * P) + i);
-                b[4 * i] = v.x, b[P >= 4 ? 4 * i + 1 : 0] = v.y, b[P >= 4 ? 4 * i + 2 : 0] = v.z, b[P >= 4 ? 4 * i + 3 : 0] = v.w;
+                c[4 * i] = v.x, c[P >= 4 ? 4 * i + 1 : 0] = v.y, c[P >= 4 ? 4 * i + 2 : 0] = v.z, c[P >= 4 ? 4 * i + 3 : 0] = v.w;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                b[j] = j < here ? __ldg(a.bias + lane * P + j) : 0.0f;
+                c[j] = j < here ? __ldg(a.bias + lane * P + j) : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            float c = -INFINITY;
-            if (j < here) {
-                c = s[j] + b[j];
-                c = c == c ? c + 0.0f : -INFINITY;
-                cmax = fmaxf(cmax, fabsf(c) < INFINITY ? fabsf(c) : 0.0f);
-            }
-            key[j] = j < here ? ordered(c) : 0u;
-        }
-        eps = off + 1.1920929e-7f * __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(cmax)));
+        for (int j = 0; j < P; ++j)
+            c[j] = fmaxf(s[j] + c[j], -INFINITY);  // (a NaN, by the bias, ranks as -inf; a sum of -0 and a score is not -0)
     } else {
 #pragma unroll
         for (int j = 0; j < P; ++j)
-            key[j] = j < here ? ordered(l[j]) : 0u;
+            c[j] = l[j];
     }
 
+    uint32_t kept = FULL;
+    int per = a.lanes;
     if (groups) {
         // The two highest of each run: `per` lanes go over one run's scores.
         const int size = a.E / a.n_groups;
         float c1 = -INFINITY, c2 = -INFINITY;
-        int per = a.lanes;
         if (per) {
 #pragma unroll
-            for (int j = 0; j < P; ++j)
-                if (j < here) {
-                    const float c = by_score ? s[j] : unordered(key[j]);
-                    c2 = fmaxf(c2, fminf(c1, c));
-                    c1 = fmaxf(c1, c);
-                }
+            for (int j = 0; j < P; ++j) {
+                const float x = j >= here ? -INFINITY : by_score ? s[j] : c[j];
+                c2 = fmaxf(c2, fminf(c1, x));
+                c1 = fmaxf(c1, x);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < P; ++j)
                 if (j < here)
-                    row[lane * P + j] = by_score ? s[j] : unordered(key[j]);
+                    row[lane * P + j] = __float_as_uint(by_score ? s[j] : c[j]);
             __syncwarp();
             per = 1;
             while (2 * per * a.n_groups <= 32)
                 per *= 2;
             if (lane / per < a.n_groups)
                 for (int i = lane & (per - 1); i < size; i += per) {
-                    const float c = row[lane / per * size + i];
-                    c2 = fmaxf(c2, fminf(c1, c));
-                    c1 = fmaxf(c1, c);
+                    const float x = __uint_as_float(row[lane / per * size + i]);
+                    c2 = fmaxf(c2, fminf(c1, x));
+                    c1 = fmaxf(c1, x);
                 }
             __syncwarp();
         }
-        const int g = lane / per;
+        const int shift = __ffs(per) - 1, g = lane >> shift;
         for (int o = per >> 1; o; o >>= 1) {
             const float y1 = __shfl_xor_sync(FULL, c1, o), y2 = __shfl_xor_sync(FULL, c2, o);
             c2 = fmaxf(fminf(c1, y1), fmaxf(c2, y2));
             c1 = fmaxf(c1, y1);
         }
-        float gs = a.best == 2 ? c1 + c2 : c1, geps = eps;
-        gs = gs == gs ? gs + 0.0f : -INFINITY;
-        if (a.best == 2) {  // (and the sum's own rounding)
-            geps = 2.0f * (by_score ? off : eps) + (fabsf(gs) < INFINITY ? 1.1920929e-7f * fabsf(gs) : 0.0f);
-            geps = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(geps)));
-        }
-        uint32_t gkey = (lane & (per - 1)) == 0 && g < a.n_groups ? ordered(gs) : 0u;
-        uint32_t kept = 0;
+        const bool leader = (lane & (per - 1)) == 0 && g < a.n_groups;
+        float gs = a.best == 2 ? fmaxf(c1 + c2, -INFINITY) : c1;  // (a NaN ranks as -inf)
+        uint32_t gkey = leader ? ordered(gs + 0.0f) : 0u;
+        kept = 0;
         for (int k = 0; k < a.topk_groups; ++k) {
             const uint32_t mk = __reduce_max_sync(FULL, gkey);
-            const uint32_t lo = geps > 0.0f ? ordered(unordered(mk) - 2.0f * geps) : mk;
-            const uint32_t cand = __ballot_sync(FULL, gkey >= lo && gkey != 0u);
-            int win = (__ffs(cand) - 1) / per;
-            if (geps > 0.0f && (cand & (cand - 1))) {
-                uint32_t all = 0;
-                for (uint32_t left = cand; left; left &= left - 1)
-                    all |= 1u << ((__ffs(left) - 1) / per);
-                win = best_group64(a, t, all);
-            }
-            kept |= 1u << win;
-            if (g == win)
+            const int src = __ffs(__ballot_sync(FULL, gkey == mk)) - 1;
+            kept |= 1u << (src >> shift);
+            if (lane == src)
                 gkey = 0u;
         }
-        if (a.lanes) {
-            const bool in = kept >> (g & 31) & 1u;  // (a lane behind the last expert has no keys)
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-                key[j] = in ? key[j] : 0u;
-        } else {
-            int r = lane * P % size, gg = lane * P / size;
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                if (j < here && !(kept >> gg & 1u))
-                    key[j] = 0u;
-                if (++r == size)
-                    r = 0, ++gg;
-            }
+        if (off > 0.0f && (a.best == 2 || a.bias)) {
+            // open, unless the chosen runs are above the others by more than their errors
+            const bool finite = fabsf(gs) < INFINITY;
+            const float ge = !finite ? 0.0f : a.best == 2 ? 2.0f * off + kRel * (fabsf(c1) + fabsf(c2)) : off + kRel * fabsf(gs);
+            const bool in = kept >> g & 1u;
+            const uint32_t low = __reduce_min_sync(FULL, leader && in ? ordered(gs - ge) : FULL);
+            const uint32_t high = __reduce_max_sync(FULL, leader && !in ? ordered(gs + ge) : 0u);
+            if (high >= low)
+                kept = exact_groups(a, t, gs, ge, leader, g);
         }
+        if (a.lanes && !(kept >> (g & 31) & 1u))  // (a lane behind the last run has no experts)
+            per = -1;
     }
 
-    // K rounds.  Whether a second key was within the error bound of a round's highest shows in the next one (one more
-    // at the end): then the winner is put back and the round decided in fp64.
-    my_idx = 0;
-    uint32_t lo = 0, before = 0;  // the last round's bound (0: none) and its winner's key,
-    int src = 0, j0 = 0;          // lane and register
-    auto highest = [&]() {
-        uint32_t top = key[0];
+    // Keys, and a copy of them in shared memory.
+    uint32_t key[P];
+    if (groups && !a.lanes) {
+        const int size = a.E / a.n_groups;
+        int r = lane * P % size, g = lane * P / size;
 #pragma unroll
-        for (int j = 1; j < P; ++j)
-            top = max(top, key[j]);
-        return top;
-    };
-    for (int k = 0;; ++k) {
-        if (k == a.K && lo == 0u)
-            break;
-        uint32_t top = highest(), mk = __reduce_max_sync(FULL, top);
-        if (lo != 0u && mk >= lo) {
-            if (lane == src) {
-#pragma unroll
-                for (int j = 0; j < P; ++j)
-                    key[j] = j == j0 ? before : key[j];
-            }
-            uint32_t mask = 0;
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-                mask |= key[j] >= lo ? 1u << j : 0u;
-            const int e = best64(a, t, mask, P);
-            if (lane == k - 1)
-                my_idx = e;
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-                key[j] = lane * P + j == e ? 0u : key[j];
-            top = highest();
-            mk = __reduce_max_sync(FULL, top);
+        for (int j = 0; j < P; ++j) {
+            key[j] = j < here && (kept >> g & 1u) ? ordered(c[j]) : 0u;
+            if (++r == size)
+                r = 0, ++g;
         }
-        if (k == a.K)
-            break;
-        src = __ffs(__ballot_sync(FULL, top == mk)) - 1;
-        j0 = 0;
+    } else {
 #pragma unroll
-        for (int j = P - 1; j >= 0; --j)
-            j0 = key[j] == mk ? j : j0;
+        for (int j = 0; j < P; ++j)
+            key[j] = j < here && per >= 0 ? ordered(c[j]) : 0u;
+    }
+    if (P >= 4 && a.E == 32 * P) {
+#pragma unroll
+        for (int i = 0; i < P / 4; ++i)
+            reinterpret_cast<uint4 *>(row + lane * P)[i] =
+                make_uint4(key[4 * i], key[P >= 4 ? 4 * i + 1 : 0], key[P >= 4 ? 4 * i + 2 : 0], key[P >= 4 ? 4 * i + 3 : 0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            if (j < here)
+                row[lane * P + j] = key[j];
+    }
+    __syncwarp();
+    sort_keys(key);
+
+    // The highest heads, one after another; with scores that carry an error one more than the call wants.
+    const bool open = a.bias != nullptr;
+    uint32_t my_key = 0, mk = 0;
+    int my_src = 0;
+    for (int k = 0; k < a.K + (open ? 1 : 0); ++k) {
+        mk = __reduce_max_sync(FULL, key[0]);
+        const int src = __ffs(__ballot_sync(FULL, key[0] == mk)) - 1;
+        if (lane == k) {
+            my_key = mk;
+            my_src = src;
+        }
         if (lane == src) {
 #pragma unroll
-            for (int j = 0; j < P; ++j)
-                key[j] = j == j0 ? 0u : key[j];
-        }
-        const int e = __shfl_sync(FULL, lane * P + j0, src);
-        if (lane == k)
-            my_idx = e;
-        if (eps > 0.0f) {
-            before = mk;
-            lo = ordered(unordered(mk) - 2.0f * eps);
+            for (int j = 0; j + 1 < P; ++j)
+                key[j] = key[j + 1];
+            key[P - 1] = 0u;
         }
     }
+    bool close = false;
+    if (open) {
+        uint32_t next = __shfl_down_sync(FULL, my_key, 1);
+        if (lane == a.K - 1)
+            next = mk;
+        const float f = unordered(my_key);
+        close = lane < a.K && fabsf(f) < INFINITY && next >= ordered(f - 2.0f * (off + kRel * fabsf(f)));
+        close = __any_sync(FULL, close);
+    }
+    if (close) {
+        my_idx = exact_experts<P>(a, t, row, off);
+    } else {
+        // the key's place among the winning lane's (equal keys of a lane were taken in their order)
+        const unsigned long long who = lane < a.K ? (unsigned long long)my_src << 32 | my_key : ~(unsigned long long)lane;
+        int skip = __popc(__match_any_sync(FULL, who) & ((1u << lane) - 1u));
+        my_idx = 0;
+        if (lane < a.K) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const int e = my_src * P + j;
+                if (e < a.E && row[e] == my_key && skip-- == 0)
+                    my_idx = e;
+            }
+        }
+    }
+    __syncwarp();
 
     // The weights of the chosen, a lane each, from their logits.  (A renormalised softmax goes by the largest
     // chosen one, which in runs need not be the largest of all.)
@@ -543,13 +610,13 @@ __device__ __forceinline__ void scan_counts(int *cnt, int E)
     __syncthreads();
 }
 
-// Dynamic shared memory: rows for runs, or the warps' counts [warps][E]; then counts [E + 1].
+// Dynamic shared memory: the warps' keys, or counts [warps][E]; then counts [E + 1].
 size_t smem_bytes(int warps, int E) { return (size_t)(warps * E + E + 1) * 4; }
 
 template <int P>
 __global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) select_kernel(const Args a)
 {
-    extern __shared__ __align__(16) float sm[];
+    extern __shared__ __align__(16) uint32_t sm[];
     int *cnt = reinterpret_cast<int *>(sm + kWarps * a.E);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (a.counts) {
@@ -576,14 +643,8 @@ __global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) select_kernel(const 
         return;
     __syncthreads();
     if (a.runs > 1) {
-        const int words = (a.E + 3) / 4;
-        for (int i = threadIdx.x; i < words; i += kThreads) {
-            uint32_t v = 0;
-            for (int k = 0; k < 4; ++k)
-                if (4 * i + k < a.E)
-                    v |= (uint32_t)cnt[4 * i + k] << (8 * k);
-            a.bc[(int64_t)i * a.pitch + blockIdx.x] = v;
-        }
+        for (int e = threadIdx.x; e < a.E; e += kThreads)
+            a.bc[(int64_t)e * a.pitch + blockIdx.x] = (uint8_t)cnt[e];
         return;
     }
     for (int e = threadIdx.x; e < a.E; e += kThreads)
@@ -601,35 +662,43 @@ __global__ void __launch_bounds__(32 * kPlaceWarps) place_kernel(const Args a)
     extern __shared__ __align__(16) int smi[];
     int *h = smi, *cnt = smi + kPlaceWarps * a.E;
     __shared__ int below[kMaxExperts];
-    const int me = blockIdx.x, tid = threadIdx.x, words = (a.E + 3) / 4;
+    const int me = blockIdx.x, tid = threadIdx.x;
     pdl_wait();
-    {
-        // all runs' counts, and those of the runs before this block's: a warp has every 16th word of four experts, a
-        // lane four neighbouring runs at a time
-        const int mine = me * a.join, lane = tid & 31;
-#pragma unroll 4
-        for (int w = tid >> 5; w < words; w += kPlaceWarps) {
-            int all[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
-#pragma unroll 4
-            for (int r = 4 * lane; r < a.runs; r += 128) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(a.bc + (int64_t)w * a.pitch + r);
-                const uint32_t x[4] = {v.x, r + 1 < a.runs ? v.y : 0u, r + 2 < a.runs ? v.z : 0u, r + 3 < a.runs ? v.w : 0u};
+    // all runs' counts, and those of the runs before this block's (a multiple of four): a warp has every
+    // eighth expert, a lane sixteen neighbouring runs at a time
+    const int mine = me * a.join, lane = tid & 31;
+    // (each block from another expert on: in one order all of them met at the same lines, and the kernel took
+    // 20 us instead of ROT)
+    constexpr int BATCH = 8;
+    const int turn = (int)((int64_t)me * a.E / gridDim.x);
+    auto expert = [&](int i) { return i + turn < a.E ? i + turn : i + turn - a.E; };
+    for (int e0 = tid >> 5; e0 < a.E; e0 += BATCH * kPlaceWarps) {
+        unsigned all[BATCH] = {}, low[BATCH] = {};
+        for (int r = 16 * lane; r < a.runs; r += 512) {
+            uint4 v[BATCH];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int b = 0; b < BATCH; ++b)
+                v[b] = *reinterpret_cast<const uint4 *>(a.bc + (int64_t)expert(min(e0 + b * kPlaceWarps, a.E - 1)) * a.pitch + r);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = (int)(x[i] >> (8 * k) & 255u);
-                        all[k] += c;
-                        low[k] += r + i < mine ? c : 0;
-                    }
-            }
+            for (int i = 0; i < 4; ++i) {
+                const int n = a.runs - r - 4 * i;  // runs of this word
+                const uint32_t ones = n >= 4 ? 0x01010101u : n > 0 ? 0x01010101u >> (8 * (4 - n)) : 0u;
+                const bool before = r + 4 * i < mine;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int s = __reduce_add_sync(0xFFFFFFFFu, all[k]), b = __reduce_add_sync(0xFFFFFFFFu, low[k]);
-                if (lane == 0 && 4 * w + k < a.E) {
-                    cnt[4 * w + k] = s;
-                    below[4 * w + k] = b;
+                for (int b = 0; b < BATCH; ++b) {
+                    const uint32_t x = i == 0 ? v[b].x : i == 1 ? v[b].y : i == 2 ? v[b].z : v[b].w;
+                    all[b] = __dp4a(x, ones, all[b]);
+                    low[b] = __dp4a(x, before ? ones : 0u, low[b]);
                 }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const unsigned sum = __reduce_add_sync(0xFFFFFFFFu, all[b]), under = __reduce_add_sync(0xFFFFFFFFu, low[b]);
+            if (lane == 0 && e0 + b * kPlaceWarps < a.E) {
+                const int e = expert(e0 + b * kPlaceWarps);
+                cnt[e] = (int)sum;
+                below[e] = (int)under;
             }
         }
     }
@@ -694,10 +763,12 @@ mx_status check_router(const mx_router *r)
     return MX_OK;
 }
 
+int pitch_of(int runs) { return (runs + 15) / 16 * 16; }
+
 size_t ws_bytes_of(int E, int T)
 {
     const int runs = runs_of(T);
-    return kErrBytes + up256(runs > 1 ? (size_t)((runs + 3) / 4 * 4) * ((E + 3) / 4) * 4 : 0);
+    return kErrBytes + up256(runs > 1 ? (size_t)pitch_of(runs) * E : 0);
 }
 
 }  // namespace
@@ -766,11 +837,11 @@ extern "C" mx_status mx_route_logits(const void *logits, int64_t ld, int dtype, 
         a.counts = counts;
         a.offsets = offsets;
         a.perm = perm;
-        a.bc = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + kErrBytes);
+        a.bc = static_cast<uint8_t *>(ws) + kErrBytes;
         a.runs = sel::runs_of(T);
-        a.pitch = (a.runs + 3) / 4 * 4;
-        // (four runs, 32 tokens, to a placing block, and no more such blocks than 128)
-        a.join = std::max(4, (a.runs + 127) / 128);
+        a.pitch = sel::pitch_of(a.runs);
+        // (four runs, 32 tokens, to a placing block, more from 128 such blocks on)
+        a.join = std::max(1, (a.runs + 511) / 512) * 4;
     }
     a.per = group ? sel::run_tokens(T) : sel::kWarps;
     const int grid = std::max<int64_t>(1, ((int64_t)T + a.per - 1) / a.per);
