@@ -17,10 +17,10 @@
 // compares the candidates in fp64.  Without a bias experts compare by their logits, which no
 // rounding has touched.
 //
-// Grouping.  A selecting block of eight warps leaves its tokens' counts by expert; the
-// placing kernel's blocks each add up all of them (bytes, an expert's neighbouring, so that 4096
-// tokens of 256 experts are 128 KB and four runs one dp4a) and put their own tokens' slots in order.  One
-// selecting block does both.
+// Grouping.  One selecting block (up to eight tokens) puts its slots in order itself.  Of more each leaves its
+// tokens' counts by expert, and the placing kernel's blocks each add up all of them (bytes, an expert's
+// neighbouring, so that 4096 tokens of 256 experts are 32 KB and four blocks' one dp4a) and put
+// their own tokens' slots in order.
 //
 // What bounds it: 4096 x 256 fp32 logits are 4 MB, 0.6 us of HBM; instructions (some 600 a token) and
 // a launch or two are the rest.
@@ -37,10 +37,16 @@ namespace sel {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kRuns = 512;    // selecting blocks when slots are grouped, as long as kMaxRun allows
-constexpr int kMaxRun = 248;  // their tokens at most (their counts are bytes)
-constexpr int kPlaceWarps = 8;
+// Warps of a selecting block: eight.  When many tokens' slots are grouped 32 (16 for more than 256 experts,
+// whose keys take more registers), so that the placing blocks have fewer counts to add up: 4096 x 256 in runs
+// 15.8 us (by eight 18.9), 2048 13; but 32 warps on one SM take each other's time: 333 x 60 by eight 6.8 us, by
+// 32 8.1.
+constexpr int kWarps = 8;
+constexpr int many_warps(int P) { return P <= 8 ? 32 : 16; }
+constexpr int kManyTokens = 2048;
+constexpr int kRuns = 512;    // selecting blocks when many tokens' slots are grouped, as long as kMaxRun allows
+constexpr int kMaxRun = 224;  // tokens of a block at most (its counts are bytes)
+constexpr int kPlaceWarps = 8, kPlaceBlocks = 128;
 
 struct Args {
     const void *logits;
@@ -55,7 +61,7 @@ struct Args {
     int32_t *counts, *offsets, *perm;  // nullable together
     uint8_t *bc;           // [E][pitch] counts of the selecting blocks' tokens
     int per, runs, join;   // tokens of a selecting block, such blocks, how many of them a placing block joins
-    int pitch;             // runs rounded up to a multiple of 16
+    int pitch, run_lanes;  // runs rounded up to a multiple of 16; lanes that share an expert's, a power of two
     int lanes;             // lanes of a run of experts, a power of two; 0: it does not end with lanes
 };
 
@@ -526,58 +532,16 @@ __device__ __forceinline__ void select_token(const Args &a, int t, int lane, uin
 }
 
 // ------------------------------------------------------------------- grouping
+//
+// A token chooses an expert once at most, so the slots of 32 tokens are a word of bits for each expert: a slot's
+// rank among its expert's is the number of bits below its token's.
 
-// Slots of tokens [t0, t1) to their places, in ascending order within an expert, by a block of WARPS
-// warps.  base[e]: place of the first of expert e; h: WARPS * E.
-template <int WARPS>
-__device__ __forceinline__ void place_slots(const Args &a, int64_t t0, int64_t t1, const int *base, int *h)
-{
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t first = t0 * a.K, n = (t1 - t0) * a.K, part = ((n + WARPS - 1) / WARPS + 31) / 32 * 32;
-    const int32_t *idx = a.idx + first;
-    const int64_t lo = min(warp * part, n), hi = min(lo + part, n);
-    for (int i = threadIdx.x; i < WARPS * a.E; i += 32 * WARPS)
-        h[i] = 0;
-    __syncthreads();
-    int *mine = h + warp * a.E;
-    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
-        const int e = s0 + lane < hi ? idx[s0 + lane] : -1;
-        const unsigned m = __match_any_sync(0xFFFFFFFFu, e);
-        if (e >= 0 && lane == __ffs(m) - 1)
-            mine[e] += __popc(m);
-        __syncwarp();
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += 32 * WARPS) {
-        int run = base[e];
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-            const int c = h[w * a.E + e];
-            h[w * a.E + e] = run;
-            run += c;
-        }
-    }
-    __syncthreads();
-    const unsigned lt = (1u << lane) - 1u;
-    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
-        const int e = s0 + lane < hi ? idx[s0 + lane] : -1;
-        const unsigned m = __match_any_sync(0xFFFFFFFFu, e);
-        if (e >= 0)
-            a.perm[mine[e] + __popc(m & lt)] = (int)(first + s0) + lane;
-        __syncwarp();
-        if (e >= 0 && lane == __ffs(m) - 1)
-            mine[e] += __popc(m);
-        __syncwarp();
-    }
-}
-
-// Exclusive sum of cnt[E] over the experts, in place, by the block; the total into cnt[E].  An expert,
-// or two, to a thread.
+// Exclusive sum of cnt[E] over the experts, in place, by the block; the total into cnt[E].
 template <int WARPS>
 __device__ __forceinline__ void scan_counts(int *cnt, int E)
 {
-    constexpr int PER = kMaxExperts / (32 * WARPS);
-    static_assert(PER >= 1 && PER * 32 * WARPS == kMaxExperts, "experts of a thread");
+    constexpr int PER = 32 * WARPS >= kMaxExperts ? 1 : kMaxExperts / (32 * WARPS);
+    static_assert(PER * 32 * WARPS >= kMaxExperts, "experts of a thread");
     __shared__ int wsum[WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int v[PER], sum = 0;
@@ -596,9 +560,7 @@ __device__ __forceinline__ void scan_counts(int *cnt, int E)
     if (lane == 31)
         wsum[warp] = incl;
     __syncthreads();
-    int run = incl - sum;
-    for (int w = 0; w < warp; ++w)
-        run += wsum[w];
+    int run = incl - sum + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wsum[lane] : 0);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         if (PER * tid + i < E)
@@ -610,95 +572,118 @@ __device__ __forceinline__ void scan_counts(int *cnt, int E)
     __syncthreads();
 }
 
-// Dynamic shared memory: the warps' keys, or counts [warps][E]; then counts [E + 1].
-size_t smem_bytes(int warps, int E) { return (size_t)(warps * E + E + 1) * 4; }
+// Dynamic shared memory of a selecting block: the warps' keys [warps][E], then bits [E] and counts [E + 1].
+size_t smem_bytes(int warps, int E) { return (size_t)(warps * E + 2 * E + 1) * 4; }
 
-template <int P>
-__global__ void __launch_bounds__(kThreads, P <= 8 ? 4 : 2) select_kernel(const Args a)
+template <int P, int WARPS, bool GROUP>
+__global__ void __launch_bounds__(32 * WARPS, many_warps(P) / WARPS) select_kernel(const Args a)
 {
+    constexpr int THREADS = 32 * WARPS;
     extern __shared__ __align__(16) uint32_t sm[];
-    int *cnt = reinterpret_cast<int *>(sm + kWarps * a.E);
+    uint32_t *bits = sm + WARPS * a.E;
+    int *cnt = reinterpret_cast<int *>(bits + a.E);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (a.counts) {
+    if (GROUP) {
         pdl_trigger();  // (the placing kernel waits for this one's end)
-        for (int e = threadIdx.x; e < a.E; e += kThreads)
-            cnt[e] = 0;
+        for (int e = threadIdx.x; e < a.E; e += THREADS)
+            bits[e] = cnt[e] = 0;
         __syncthreads();
     }
     const int64_t first = (int64_t)blockIdx.x * a.per;
     const int last = (int)min((int64_t)a.T, first + a.per);
-    for (int t = (int)first + warp; t < last; t += kWarps) {
-        int i;
+    int i = 0;
+    for (int t = (int)first + warp; t < last; t += WARPS) {
         float w;
         select_token<P>(a, t, lane, sm + warp * a.E, i, w);
         if (lane < a.K) {
             a.idx[(int64_t)t * a.K + lane] = i;
             a.w[(int64_t)t * a.K + lane] = w;
-            if (a.counts)
+            if (GROUP)
                 atomicAdd(cnt + i, 1);
+            if (GROUP && a.runs <= 1)
+                atomicOr(bits + i, 1u << warp);
         }
         __syncwarp();
     }
-    if (!a.counts)
+    if (!GROUP)
         return;
     __syncthreads();
     if (a.runs > 1) {
-        for (int e = threadIdx.x; e < a.E; e += kThreads)
+        for (int e = threadIdx.x; e < a.E; e += THREADS)
             a.bc[(int64_t)e * a.pitch + blockIdx.x] = (uint8_t)cnt[e];
         return;
     }
-    for (int e = threadIdx.x; e < a.E; e += kThreads)
+    // a warp a token, and no more than these
+    for (int e = threadIdx.x; e < a.E; e += THREADS)
         a.counts[e] = cnt[e];
-    __syncthreads();
-    scan_counts<kWarps>(cnt, a.E);
-    for (int e = threadIdx.x; e <= a.E; e += kThreads)
+    scan_counts<WARPS>(cnt, a.E);
+    for (int e = threadIdx.x; e <= a.E; e += THREADS)
         a.offsets[e] = cnt[e];
-    place_slots<kWarps>(a, 0, a.T, cnt, reinterpret_cast<int *>(sm));
+    if (warp < a.T && lane < a.K)
+        a.perm[cnt[i] + __popc(bits[i] & ((1u << warp) - 1u))] = warp * a.K + lane;
 }
 
 __global__ void __launch_bounds__(32 * kPlaceWarps) place_kernel(const Args a)
 {
-    constexpr int THREADS = 32 * kPlaceWarps;
-    extern __shared__ __align__(16) int smi[];
-    int *h = smi, *cnt = smi + kPlaceWarps * a.E;
-    __shared__ int below[kMaxExperts];
-    const int me = blockIdx.x, tid = threadIdx.x;
+    constexpr int THREADS = 32 * kPlaceWarps, SLOTS = 32 * kMaxTopK / THREADS;  // slots of a thread, of 32 tokens
+    __shared__ uint32_t bits[kMaxExperts];
+    __shared__ int cnt[kMaxExperts + 1], place[kMaxExperts];
+    const int me = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int e = tid; e < a.E; e += THREADS)
+        bits[e] = 0;
+    const int64_t t0 = (int64_t)me * a.join * a.per, t1 = min((int64_t)a.T, t0 + (int64_t)a.join * a.per);
     pdl_wait();
-    // all runs' counts, and those of the runs before this block's (a multiple of four): a warp has every
-    // eighth expert, a lane sixteen neighbouring runs at a time
-    const int mine = me * a.join, lane = tid & 31;
-    // (each block from another expert on: in one order all of them met at the same lines, and the kernel took
-    // 20 us instead of ROT)
+    // slot tid + i * THREADS of the 32 tokens from t on
+    int expert_of[SLOTS];
+    auto load_slots = [&](int64_t t) {
+        const int n = (int)min((int64_t)32, t1 - t) * a.K;
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+            expert_of[i] = tid + i * THREADS < n ? __ldcg(a.idx + t * a.K + tid + i * THREADS) : -1;
+    };
+    load_slots(t0);
+    // All blocks' counts, and those of the blocks before this one's: `lanes` neighbouring lanes have an expert, a lane sixteen
+    // neighbouring blocks at a time.  Each begins with another expert: in one order all met at the same lines
+    // (4096 x 256: 20 us instead of 11).
     constexpr int BATCH = 8;
+    const int mine = me * a.join, lanes = a.run_lanes, each = 32 / lanes, part = lane & (lanes - 1);
     const int turn = (int)((int64_t)me * a.E / gridDim.x);
     auto expert = [&](int i) { return i + turn < a.E ? i + turn : i + turn - a.E; };
-    for (int e0 = tid >> 5; e0 < a.E; e0 += BATCH * kPlaceWarps) {
+    for (int i0 = warp * each + lane / lanes; i0 - lane / lanes < a.E; i0 += BATCH * kPlaceWarps * each) {
         unsigned all[BATCH] = {}, low[BATCH] = {};
-        for (int r = 16 * lane; r < a.runs; r += 512) {
+        for (int r = 16 * part; r < a.runs; r += 16 * lanes) {
             uint4 v[BATCH];
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b)
-                v[b] = *reinterpret_cast<const uint4 *>(a.bc + (int64_t)expert(min(e0 + b * kPlaceWarps, a.E - 1)) * a.pitch + r);
+            for (int b = 0; b < BATCH; ++b) {
+                const int i = i0 + b * kPlaceWarps * each;
+                v[b] = make_uint4(0, 0, 0, 0);
+                if (i < a.E)
+                    v[b] = *reinterpret_cast<const uint4 *>(a.bc + (int64_t)expert(i) * a.pitch + r);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int n = a.runs - r - 4 * i;  // runs of this word
-                const uint32_t ones = n >= 4 ? 0x01010101u : n > 0 ? 0x01010101u >> (8 * (4 - n)) : 0u;
-                const bool before = r + 4 * i < mine;
+                auto ones = [&](int n) {  // a one for each of a word's first n bytes
+                    return n >= 4 ? 0x01010101u : n > 0 ? 0x01010101u >> (8 * (4 - n)) : 0u;
+                };
+                const uint32_t in = ones(a.runs - r - 4 * i), under = ones(mine - r - 4 * i);
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b) {
                     const uint32_t x = i == 0 ? v[b].x : i == 1 ? v[b].y : i == 2 ? v[b].z : v[b].w;
-                    all[b] = __dp4a(x, ones, all[b]);
-                    low[b] = __dp4a(x, before ? ones : 0u, low[b]);
+                    all[b] = __dp4a(x, in, all[b]);
+                    low[b] = __dp4a(x, under, low[b]);
                 }
             }
         }
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
-            const unsigned sum = __reduce_add_sync(0xFFFFFFFFu, all[b]), under = __reduce_add_sync(0xFFFFFFFFu, low[b]);
-            if (lane == 0 && e0 + b * kPlaceWarps < a.E) {
-                const int e = expert(e0 + b * kPlaceWarps);
-                cnt[e] = (int)sum;
-                below[e] = (int)under;
+            for (int o = lanes >> 1; o; o >>= 1) {
+                all[b] += __shfl_xor_sync(0xFFFFFFFFu, all[b], o);
+                low[b] += __shfl_xor_sync(0xFFFFFFFFu, low[b], o);
+            }
+            const int i = i0 + b * kPlaceWarps * each;
+            if (part == 0 && i < a.E) {
+                cnt[expert(i)] = (int)all[b];
+                place[expert(i)] = (int)low[b];
             }
         }
     }
@@ -706,33 +691,85 @@ __global__ void __launch_bounds__(32 * kPlaceWarps) place_kernel(const Args a)
     if (me == 0)
         for (int e = tid; e < a.E; e += THREADS)
             a.counts[e] = cnt[e];
-    __syncthreads();
+    if (me == 0)
+        __syncthreads();
     scan_counts<kPlaceWarps>(cnt, a.E);
     if (me == 0)
         for (int e = tid; e <= a.E; e += THREADS)
             a.offsets[e] = cnt[e];
-    for (int e = tid; e < a.E; e += THREADS)
-        below[e] += cnt[e];
-    const int64_t t0 = (int64_t)me * a.join * a.per;
-    place_slots<kPlaceWarps>(a, t0, min((int64_t)a.T, t0 + (int64_t)a.join * a.per), below, h);
+    for (int64_t t = t0; t < t1; t += 32) {
+        int token[SLOTS];
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            token[i] = (tid + i * THREADS) / a.K;
+            if (expert_of[i] >= 0)
+                atomicOr(bits + expert_of[i], 1u << token[i]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            const int e = expert_of[i];
+            if (e >= 0)
+                a.perm[cnt[e] + place[e] + __popc(bits[e] & ((1u << token[i]) - 1u))] = (int)(t * a.K) + tid + i * THREADS;
+        }
+        if (t + 32 >= t1)
+            break;
+        load_slots(t + 32);
+        __syncthreads();
+        for (int e = tid; e < a.E; e += THREADS) {
+            place[e] += __popc(bits[e]);
+            bits[e] = 0;
+        }
+        __syncthreads();
+    }
 }
 
-// Tokens of a selecting block when slots are grouped: a warp each, more above kRuns blocks.
-int run_tokens(int T)
+// Registers of a lane for E experts.
+int width_of(int E)
 {
-    const int64_t per = ((int64_t)T + kRuns - 1) / kRuns;
-    return (int)std::min<int64_t>(kMaxRun, std::max<int64_t>(kWarps, (per + kWarps - 1) / kWarps * kWarps));
+    int P = 1;
+    while (32 * P < E)
+        P *= 2;
+    return P;
 }
-int runs_of(int T) { return (int)(((int64_t)T + run_tokens(T) - 1) / run_tokens(T)); }
+
+// Warps and tokens of a selecting block when slots are grouped.
+int group_warps(int T, int E)
+{
+    return T > kManyTokens ? many_warps(width_of(E)) : kWarps;
+}
+int run_tokens(int T, int E)
+{
+    const int warps = group_warps(T, E);
+    if (warps == kWarps)
+        return warps;
+    const int64_t per = ((int64_t)T + kRuns - 1) / kRuns;
+    return (int)std::min<int64_t>(kMaxRun, std::max<int64_t>(warps, (per + warps - 1) / warps * warps));
+}
+int runs_of(int T, int E) { return (int)(((int64_t)T + run_tokens(T, E) - 1) / run_tokens(T, E)); }
+
+template <int P, int WARPS>
+cudaError_t launch_grouped(const Args &a, cudaStream_t s)
+{
+    const size_t smem = smem_bytes(WARPS, a.E);
+    cudaError_t e = smem_optin((const void *)select_kernel<P, WARPS, true>, smem);
+    if (e != cudaSuccess)
+        return e;
+    select_kernel<P, WARPS, true><<<std::max(1, a.runs), 32 * WARPS, smem, s>>>(a);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && a.runs > 1)
+        e = launch_dependent(place_kernel, (a.runs + a.join - 1) / a.join, 32 * kPlaceWarps, 0, s, a);
+    return e;
+}
 
 template <int P>
-cudaError_t launch(const Args &a, int grid, cudaStream_t s)
+cudaError_t launch(const Args &a, cudaStream_t s)
 {
-    select_kernel<P><<<grid, kThreads, smem_bytes(kWarps, a.E), s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && a.counts && a.runs > 1)
-        e = launch_dependent(place_kernel, (a.runs + a.join - 1) / a.join, 32 * kPlaceWarps, smem_bytes(kPlaceWarps, a.E), s, a);
-    return e;
+    if (a.counts)
+        return group_warps(a.T, a.E) == kWarps ? launch_grouped<P, kWarps>(a, s) : launch_grouped<P, many_warps(P)>(a, s);
+    const int grid = (int)(((int64_t)a.T + kWarps - 1) / kWarps);
+    select_kernel<P, kWarps, false><<<grid, 32 * kWarps, smem_bytes(kWarps, a.E), s>>>(a);
+    return cudaGetLastError();
 }
 
 mx_status check_router(const mx_router *r)
@@ -767,7 +804,7 @@ int pitch_of(int runs) { return (runs + 15) / 16 * 16; }
 
 size_t ws_bytes_of(int E, int T)
 {
-    const int runs = runs_of(T);
+    const int runs = runs_of(T, E);
     return kErrBytes + up256(runs > 1 ? (size_t)pitch_of(runs) * E : 0);
 }
 
@@ -785,10 +822,11 @@ extern "C" size_t mx_route_logits_workspace_bytes(const mx_router *router, int T
         fail(MX_ERR_INVALID_ARG, "T_max %d is negative", T_max);
         return 0;
     }
-    // (any number of tokens up to T_max: up to kWarps * kRuns tokens there are the more runs the more there
-    // are, then at most kRuns until a run has kMaxRun tokens)
-    return std::max(sel::ws_bytes_of(router->n_experts, T_max),
-                    sel::ws_bytes_of(router->n_experts, std::min(T_max, sel::kWarps * sel::kRuns)));
+    // (any number of tokens up to T_max: there are the more blocks the more tokens there are, up to kManyTokens and
+    // from there to kRuns whole blocks and again when those are full)
+    const int E = router->n_experts;
+    return std::max({sel::ws_bytes_of(E, T_max), sel::ws_bytes_of(E, std::min(T_max, sel::kManyTokens)),
+                     sel::ws_bytes_of(E, std::min(T_max, sel::kRuns * sel::many_warps(sel::width_of(E))))});
 }
 
 extern "C" mx_status mx_route_logits(const void *logits, int64_t ld, int dtype, int T, const mx_router *router,
@@ -838,26 +876,26 @@ extern "C" mx_status mx_route_logits(const void *logits, int64_t ld, int dtype, 
         a.offsets = offsets;
         a.perm = perm;
         a.bc = static_cast<uint8_t *>(ws) + kErrBytes;
-        a.runs = sel::runs_of(T);
+        a.runs = sel::runs_of(T, E);
         a.pitch = sel::pitch_of(a.runs);
-        // (four runs, 32 tokens, to a placing block, more from 128 such blocks on)
-        a.join = std::max(1, (a.runs + 511) / 512) * 4;
+        // (32 tokens to a placing block, more from kPlaceBlocks on)
+        a.join = std::max(32 / sel::run_tokens(T, E), (a.runs + sel::kPlaceBlocks - 1) / sel::kPlaceBlocks);
+        a.run_lanes = 1;
+        while (a.run_lanes < 32 && 16 * a.run_lanes < a.runs)
+            a.run_lanes *= 2;
     }
-    a.per = group ? sel::run_tokens(T) : sel::kWarps;
-    const int grid = std::max<int64_t>(1, ((int64_t)T + a.per - 1) / a.per);
-    int P = 1;
-    while (32 * P < E)
-        P *= 2;
+    a.per = group ? sel::run_tokens(T, E) : sel::kWarps;
+    const int P = sel::width_of(E);
     const int size = E / a.n_groups, lanes = size / P;
     a.lanes = size % P == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const size_t piece = std::min<size_t>(16, P * dtype_bytes(dtype));
     a.vec = E == 32 * P && aligned(logits, piece) && ld * dtype_bytes(dtype) % piece == 0;
     a.vec_bias = E == 32 * P && aligned(a.bias, 16);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = P == 1   ? sel::launch<1>(a, grid, s)
-                          : P == 2 ? sel::launch<2>(a, grid, s)
-                          : P == 4 ? sel::launch<4>(a, grid, s)
-                          : P == 8 ? sel::launch<8>(a, grid, s)
-                                   : sel::launch<16>(a, grid, s);
+    const cudaError_t e = P == 1   ? sel::launch<1>(a, s)
+                          : P == 2 ? sel::launch<2>(a, s)
+                          : P == 4 ? sel::launch<4>(a, s)
+                          : P == 8 ? sel::launch<8>(a, s)
+                                   : sel::launch<16>(a, s);
     return e == cudaSuccess ? MX_OK : cuda_fail(e, "routing");
 }
