@@ -98,7 +98,7 @@ class Fp8LayerStruct(C.Structure):
 class RmsnormStruct(C.Structure):
     _fields_ = [("x", C.c_void_p), ("ldx", C.c_int64), ("residual", C.c_void_p), ("ldr", C.c_int64),
                 ("weight", C.c_void_p), ("sum", C.c_void_p), ("lds", C.c_int64), ("out", C.c_void_p),
-                ("ldo", C.c_int64), ("q", C.POINTER(Fp8Rows)), ("rows", C.c_int32), ("cols", C.c_int32),
+                ("ldo", C.c_int64), ("q", Fp8Rows), ("rows", C.c_int32), ("cols", C.c_int32),
                 ("dtype", C.c_int32), ("weight_dtype", C.c_int32), ("out_dtype", C.c_int32), ("pow2", C.c_int32),
                 ("eps", C.c_float), ("weight_offset", C.c_float)]
 
@@ -412,7 +412,7 @@ def profile_read(reset: bool = True) -> dict:
 # compared by index.
 
 _ROWS = _struct.Struct("@PPiiqqq")  # Fp8Rows
-_NORM = _struct.Struct("@PqPqPPqPqPiiiiiiff")  # RmsnormStruct
+_NORM = _struct.Struct("@PqPqPPqPqPPiiqqqiiiiiiff")  # RmsnormStruct
 _FP4 = _struct.Struct("@PPPiiiq")  # Fp4Rows
 _t = None  # names of torch, filled on first use
 
@@ -632,43 +632,38 @@ def fp8_rmsnorm(x, weight=None, eps=1e-6, weight_offset=0.0, residual=None, resi
     weight`` (mx_fp8_rmsnorm).  ``residual_out`` gets the sum (it may be ``residual`` or ``x`` itself), ``out`` the
     normed rows, ``q`` and ``scales`` the same in e4m3 as fp8_quantize makes them; at least one of the three."""
     t = _t or _torch()
-    dev = x.get_device()
-    if x.dim() != 2:
+    dev, dtype, shape = x.get_device(), x.dtype, x.shape
+    if len(shape) != 2:
         raise MxError(-1, "x must be [rows, cols]")
-    shape = x.shape
     rows, cols = shape
     dt = _dtype_code(x, "x")
     ldx = _rows2d(x, shape, dev, "x")
-    rp = wp = sp = op = qp = None
-    ldr = lds = ldo = 0
-    wd = od = 0
+    rp = wp = sp = op = qp = cp = ldr = lds = ldo = ldq = wd = od = sr = sb = 0
     if residual is not None:
-        if residual.dtype is not x.dtype:
-            raise MxError(-1, "residual must have x's dtype")
         ldr, rp = _rows2d(residual, shape, dev, "residual"), residual.data_ptr()
+        if residual.dtype is not dtype:
+            raise MxError(-1, "residual must have x's dtype")
     if residual_out is not None:
-        if residual_out.dtype is not x.dtype:
-            raise MxError(-1, "residual_out must have x's dtype")
         lds, sp = _rows2d(residual_out, shape, dev, "residual_out"), residual_out.data_ptr()
+        if residual_out.dtype is not dtype:
+            raise MxError(-1, "residual_out must have x's dtype")
     if weight is not None:
         if weight.shape != (cols,) or not weight.is_contiguous() or weight.get_device() != dev:
             raise MxError(-1, f"weight must be contiguous [{cols}] on x's device")
         wd, wp = _dtype_code(weight, "weight"), weight.data_ptr()
     if out is not None:
         ldo, op, od = _rows2d(out, shape, dev, "out"), out.data_ptr(), _dtype_code(out, "out")
-    if (q is None) != (scales is None):
+    if q is not None and scales is not None:
+        if q.dtype is not t.f8 or scales.dtype is not t.f32 or scales.shape != (rows, (cols + 127) // 128):
+            raise MxError(-1, f"q must be float8_e4m3fn, scales float32 [{rows}, {(cols + 127) // 128}]")
+        if scales.get_device() != dev:
+            raise MxError(-1, "all tensors must be on one device")
+        ldq, qp, cp = _rows2d(q, shape, dev, "q"), q.data_ptr(), scales.data_ptr()
+        sr, sb = scales.stride()
+    elif q is not None or scales is not None:
         raise MxError(-1, "q and scales come together")
-    if q is not None:
-        qr, qc, r = _fp8_rows(t, q, scales, dev, False)
-        if (qr, qc) != (rows, cols):
-            raise MxError(-1, f"q must be [{rows}, {cols}]")
-        r = C.create_string_buffer(r, len(r))
-        qp = C.addressof(r)
-    if rows == 0:
-        ldx = ldx or cols
-    args = _NORM.pack(x.data_ptr(), ldx, rp or 0, ldr, wp or 0, sp or 0, lds, op or 0, ldo, qp or 0, rows, cols, dt, wd,
-                      od, 1 if pow2 else 0, eps, weight_offset)
-    _on(dev, t.norm, args, _stream_on(dev, stream))
+    _on(dev, t.norm, _NORM.pack(x.data_ptr(), ldx, rp, ldr, wp, sp, lds, op, ldo, qp, cp, rows, cols, ldq, sr, sb, rows,
+                                cols, dt, wd, od, 1 if pow2 else 0, eps, weight_offset), _stream_on(dev, stream))
 
 
 # ------------------------------------------- microscaled 4-bit operators

@@ -37,6 +37,18 @@ struct GemmArgs {
     int stages, cl;          // ring depth, cluster size (split of the inner dimension)
 };
 
+// One row (mx_fp4_gemv.cu), of up to about 30000 columns (it lies in shared memory).
+struct GemvArgs {
+    int K, N;
+    const uint8_t *q, *sx;   // the row, its scales
+    const uint8_t *w, *sw;   // the matrix, its scales as packed
+    int64_t ldw;
+    const float *tx, *tw;    // nullable
+    void *out;
+    int out_bf16;
+};
+cudaError_t launch_gemv(int block, const GemvArgs &a, cudaStream_t s);
+
 struct PackArgs {
     const uint8_t *scales;  // [count][rows][nb], row pitch ld
     int64_t ld;

@@ -125,6 +125,15 @@ Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
     return c;
 }
 
+// One row by mx_fp4_gemv.cu, while its CTAs' rounds over the SMs have few steps of 1024 columns: 2112 x 2816 (one round
+// of three) 3.3 us, by the tensor cores 5.1; 2112 x 4096 3.8, 5.3; 3328 x 2816 (two of three) 4.4, 5.2; 4096 x 4096 (two of
+// four) 5.5, 5.6; 704 x 8192 (one of eight) 5.4, 5.4; 14336 x 4096 14.5, 6.8.
+bool one_row(int rows, const int32_t *offsets, const mx_fp4_matrix &w)
+{
+    const int64_t ctas = (w.rows + 127) / 128 * 8, rounds = (ctas + num_sms() - 1) / num_sms();
+    return rows == 1 && !offsets && rounds * ((w.cols + 1023) / 1024) <= 6;
+}
+
 mx_status product(const mx_fp4_rows *x, const int32_t *offsets, const mx_fp4_matrix *w, void *out, int64_t ldo,
                   int out_dtype, void *stream, void *ws, size_t ws_bytes)
 {
@@ -148,6 +157,22 @@ mx_status product(const mx_fp4_rows *x, const int32_t *offsets, const mx_fp4_mat
     if ((st = check_ws(ws, ws_bytes, kErrBytes)) != MX_OK)
         return st;
     const int block = block_of(w->format), FT = (w->rows + 127) / 128, KB = stages_of(w->cols);
+    if (one_row(x->rows, offsets, *w)) {
+        GemvArgs v{};
+        v.K = w->cols;
+        v.N = w->rows;
+        v.q = static_cast<const uint8_t *>(x->q);
+        v.sx = static_cast<const uint8_t *>(x->scales);
+        v.w = static_cast<const uint8_t *>(w->q);
+        v.sw = static_cast<const uint8_t *>(w->scales);
+        v.ldw = w->ld;
+        v.tx = x->tensor_scale;
+        v.tw = w->tensor_scale;
+        v.out = out;
+        v.out_bf16 = out_dtype == MX_BF16;
+        const cudaError_t e = launch_gemv(block, v, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? MX_OK : cuda_fail(e, "FP4 product");
+    }
     const Choice c = choose(x->rows, offsets != nullptr, w->count, FT, KB, num_sms());
     GemmArgs g{};
     g.rows = x->rows;

@@ -458,10 +458,11 @@ extern "C" mx_status mx_fp8_rmsnorm(const mx_rmsnorm *n, void *stream)
         return fail(MX_ERR_INVALID_ARG, "pow2 %d is not 0 or 1", n->pow2);
     if (!(n->eps >= 0.0f) || !std::isfinite(n->eps) || !std::isfinite(n->weight_offset))
         return fail(MX_ERR_INVALID_ARG, "eps must be finite and at least 0, weight_offset finite");
-    if (!n->sum && !n->out && !n->q)
+    const mx_fp8_rows &q = n->q;
+    if (!n->sum && !n->out && !q.q)
         return fail(MX_ERR_INVALID_ARG, "one of sum, out and q must be given");
-    if (n->q && (n->q->rows != n->rows || n->q->cols != n->cols))
-        return fail(MX_ERR_INVALID_ARG, "q is [%d, %d], x is [%d, %d]", n->q->rows, n->q->cols, n->rows, n->cols);
+    if (q.q && (q.rows != n->rows || q.cols != n->cols))
+        return fail(MX_ERR_INVALID_ARG, "q is [%d, %d], x is [%d, %d]", q.rows, q.cols, n->rows, n->cols);
     if (n->rows == 0)
         return MX_OK;
     if (!n->x)
@@ -475,9 +476,8 @@ extern "C" mx_status mx_fp8_rmsnorm(const mx_rmsnorm *n, void *stream)
         return fail(MX_ERR_ALIGNMENT, "weight is misaligned");
     const int es = (int)dtype_bytes(n->dtype), bf16 = n->dtype == MX_BF16;
     norm::Args a{};
-    if (n->q) {
-        const mx_fp8_rows &q = *n->q;
-        if (!q.q || !q.scales)
+    if (q.q) {
+        if (!q.scales)
             return fail(MX_ERR_INVALID_ARG, "q has a NULL pointer");
         if (q.ld < q.cols || q.scale_row < 0 || q.scale_block < 0)
             return fail(MX_ERR_INVALID_ARG, "q: row pitch %lld is below its %d columns, or a scale stride is negative",

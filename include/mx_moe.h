@@ -429,7 +429,7 @@ MX_API mx_status mx_fp8_quantize(const void *x, int64_t ldx, int dtype, int pow2
  *              residual or x itself (the same address and pitch)
  *   out        device [rows][cols] of out_dtype, pitch ldo, nullable; may be x
  *              or residual itself where type, address and pitch are the same
- *   q          nullable; as for mx_fp8_quantize (its rows and cols: the call's)
+ *   q          as for mx_fp8_quantize, its rows and cols the call's; q.q NULL: none
  * At least one of sum, out and q is given; outputs overlap nothing else.
  */
 typedef struct {
@@ -442,7 +442,7 @@ typedef struct {
     int64_t lds;
     void *out;
     int64_t ldo;
-    const mx_fp8_rows *q;
+    mx_fp8_rows q;
     int32_t rows, cols;      /* rows >= 0; 1 <= cols <= 32768 */
     int32_t dtype, weight_dtype, out_dtype;
     int32_t pow2;            /* of mx_fp8_quantize */
@@ -538,7 +538,8 @@ typedef struct {
     const float *tensor_scale; /* device [count], nullable (1); MX_FP4_E4M3 only; finite, positive and normal */
     int32_t rows, cols, count;
     int32_t format;       /* mx_fp4_format */
-    int64_t ld;           /* >= ceil(cols / 2), a multiple of 16 */
+    int64_t ld;           /* >= ceil(cols / 2), a multiple of 16; a row's bytes up to the next multiple of
+                             16 behind its last are read, but not used                                */
 } mx_fp4_matrix;
 
 /* Quantised activations [rows][cols]. */
@@ -549,7 +550,8 @@ typedef struct {
     const float *tensor_scale; /* device, nullable (1), as above */
     int32_t rows, cols;
     int32_t format;
-    int64_t ld;           /* >= ceil(cols / 2); for the products a multiple of 16 */
+    int64_t ld;           /* >= ceil(cols / 2); for the products a multiple of 16, and bytes behind a row's
+                             last as in mx_fp4_matrix                                                 */
 } mx_fp4_rows;
 
 /*
