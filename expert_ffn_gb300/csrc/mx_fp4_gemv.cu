@@ -13,6 +13,7 @@
 //
 // What bounds it: the launch and two trips to memory.
 #include "mx_fp4.cuh"
+#include "mx_host.h"
 
 namespace mx {
 namespace fp4 {
@@ -53,6 +54,17 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
     return f;
 }
 
+// Read once: kept out of L1.  (Not by the read-only path: the launch may have begun before its predecessor's end.)
+__device__ __forceinline__ uint4 load_once(const void *p)
+{
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
 template <int BLOCK>
 __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a)
 {
@@ -76,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a)
         q = make_uint4(0, 0, 0, 0);
         scales = 0;
         if (live && col < a.K) {
-            q = ld_stream_u4(w + col / 2);
+            q = load_once(w + col / 2);
             const int b = col / BLOCK;
             const uint8_t *p = sw + (int64_t)(b / 4) * 512 + b % 4;
             scales = NB == 2 ? *reinterpret_cast<const uint16_t *>(p) : *p;
@@ -141,17 +153,7 @@ template <int BLOCK>
 cudaError_t launch_t(const GemvArgs &a, cudaStream_t s)
 {
     const int padded = (a.K + kChunk - 1) / kChunk * kChunk;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((a.N + 127) / 128 * 8);
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = padded + padded / BLOCK * 4;
-    c.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, gemv_kernel<BLOCK>, a);
+    return launch_dependent(gemv_kernel<BLOCK>, (a.N + 127) / 128 * 8, kThreads, padded + padded / BLOCK * 4, s, a);
 }
 
 }  // namespace

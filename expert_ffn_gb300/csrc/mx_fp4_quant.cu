@@ -12,6 +12,7 @@
 // The pieces of the matrix are dealt out in order, so a ragged width leaves no warp idle; a
 // thread's next piece is a constant number of rows and columns on.  HBM bounds large matrices.
 #include "mx_fp4.cuh"
+#include "mx_host.h"
 
 #include <algorithm>
 
@@ -247,16 +248,7 @@ cudaError_t launch_t(const QuantArgs &a, int sms, cudaStream_t s)
 {
     const int64_t pieces = (int64_t)a.rows * stages_of(a.cols) * (kStageCols / kPiece);
     const int64_t most = 8 * (int64_t)sms, one = (pieces + kThreads - 1) / kThreads;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)std::min(most, one));
-    c.blockDim = dim3(kThreads);
-    c.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, quantize_kernel<BF16, BLOCK>, a);
+    return launch_dependent(quantize_kernel<BF16, BLOCK>, (int)std::min(most, one), kThreads, 0, s, a);
 }
 
 }  // namespace

@@ -260,6 +260,9 @@ __global__ void __launch_bounds__(512, V == 1 ? (BF16 ? 3 : 2) : 1) norm_kernel(
                 res[i] = load8<BF16, FAST>(a.residual, row * a.ldr + column(i), count(i), a.vr);
         }
     };
+    // (the launch behind may set itself up; it waits for this one's end)
+    pdl_trigger();
+    pdl_wait();
     if (AHEAD)
         fetch(blockIdx.x);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -403,11 +406,8 @@ cudaError_t launch_v(const Args &a, int threads, cudaStream_t s)
                       (!a.q || a.vq) && (!a.weight || a.vw);
     const int per_sm = V == 1 ? (BF16 ? 1536 : 1024) / threads : 1;
     const int grid = std::min(a.rows, num_sms() * std::max(1, per_sm));
-    if (fast)
-        norm_kernel<BF16, V, true><<<grid, threads, 0, s>>>(a);
-    else
-        norm_kernel<BF16, V, false><<<grid, threads, 0, s>>>(a);
-    return cudaGetLastError();
+    return fast ? launch_dependent(norm_kernel<BF16, V, true>, grid, threads, 0, s, a)
+                : launch_dependent(norm_kernel<BF16, V, false>, grid, threads, 0, s, a);
 }
 
 template <bool BF16>

@@ -81,8 +81,8 @@ __device__ __forceinline__ float tidy(float l) { return fmaxf(l + 0.0f, -INFINIT
 
 __device__ __forceinline__ float load1(const Args &a, int64_t at)
 {
-    return tidy(a.bf16 ? bf2f(__ldg(reinterpret_cast<const uint16_t *>(a.logits) + at))
-                       : __ldg(reinterpret_cast<const float *>(a.logits) + at));
+    return tidy(a.bf16 ? bf2f(reinterpret_cast<const uint16_t *>(a.logits)[at])
+                       : reinterpret_cast<const float *>(a.logits)[at]);
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -133,7 +133,7 @@ __device__ double choice64(const Args &a, int t, int e, const Soft64 &S)
     const float l = load1(a, (int64_t)t * a.ld + e);
     const double s = a.score == MX_SIGMOID ? 1.0 / (1.0 + exp(-(double)l))
                                            : (l == S.m ? 1.0 : exp((double)l - (double)S.m)) * S.inv;
-    const double c = a.bias ? s + (double)__ldg(a.bias + e) : s;
+    const double c = a.bias ? s + (double)a.bias[e] : s;
     return c == c ? c : -INFINITY;
 }
 
@@ -274,16 +274,16 @@ __device__ __forceinline__ void load_logits(const Args &a, int t, int lane, floa
             uint32_t r[P < 2 ? 1 : P / 2];
             const uint16_t *p = reinterpret_cast<const uint16_t *>(a.logits) + at;
             if constexpr (P == 1)
-                r[0] = __ldg(p);
+                r[0] = *p;
             else if constexpr (P == 2)
-                r[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+                r[0] = *reinterpret_cast<const uint32_t *>(p);
             else if constexpr (P == 4) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+                const uint2 v = *reinterpret_cast<const uint2 *>(p);
                 r[0] = v.x, r[1] = v.y;
             } else {
 #pragma unroll
                 for (int i = 0; i < P / 8; ++i) {
-                    const uint4 v = ldg_u4(p + 8 * i);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(p + 8 * i);
                     r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
                 }
             }
@@ -293,14 +293,14 @@ __device__ __forceinline__ void load_logits(const Args &a, int t, int lane, floa
         } else {
             const float *p = reinterpret_cast<const float *>(a.logits) + at;
             if constexpr (P == 1)
-                l[0] = __ldg(p);
+                l[0] = *p;
             else if constexpr (P == 2) {
-                const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
+                const float2 v = *reinterpret_cast<const float2 *>(p);
                 l[0] = v.x, l[1] = v.y;
             } else {
 #pragma unroll
                 for (int i = 0; i < P / 4; ++i) {
-                    const float4 v = __ldg(reinterpret_cast<const float4 *>(p) + i);
+                    const float4 v = reinterpret_cast<const float4 *>(p)[i];
                     l[4 * i] = v.x, l[4 * i + 1] = v.y, l[4 * i + 2] = v.z, l[4 * i + 3] = v.w;
                 }
             }
@@ -363,13 +363,13 @@ __device__ __forceinline__ void select_token(const Args &a, int t, int lane, uin
         if (P >= 4 && a.vec_bias) {
 #pragma unroll
             for (int i = 0; i < P / 4; ++i) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(a.bias + lane * P) + i);
+                const float4 v = reinterpret_cast<const float4 *>(a.bias + lane * P)[i];
                 c[4 * i] = v.x, c[P >= 4 ? 4 * i + 1 : 0] = v.y, c[P >= 4 ? 4 * i + 2 : 0] = v.z, c[P >= 4 ? 4 * i + 3 : 0] = v.w;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                c[j] = j < here ? __ldg(a.bias + lane * P + j) : 0.0f;
+                c[j] = j < here ? a.bias[lane * P + j] : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < P; ++j)
@@ -583,14 +583,17 @@ __global__ void __launch_bounds__(32 * WARPS, many_warps(P) / WARPS) select_kern
     uint32_t *bits = sm + WARPS * a.E;
     int *cnt = reinterpret_cast<int *>(bits + a.E);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (the launch behind may set itself up; it waits for this one's end.  Plain loads: the read-only path is
+    // not for a launch that began before its predecessor's end)
+    pdl_trigger();
     if (GROUP) {
-        pdl_trigger();  // (the placing kernel waits for this one's end)
         for (int e = threadIdx.x; e < a.E; e += THREADS)
             bits[e] = cnt[e] = 0;
         __syncthreads();
     }
     const int64_t first = (int64_t)blockIdx.x * a.per;
     const int last = (int)min((int64_t)a.T, first + a.per);
+    pdl_wait();
     int i = 0;
     for (int t = (int)first + warp; t < last; t += WARPS) {
         float w;
@@ -755,8 +758,7 @@ cudaError_t launch_grouped(const Args &a, cudaStream_t s)
     cudaError_t e = smem_optin((const void *)select_kernel<P, WARPS, true>, smem);
     if (e != cudaSuccess)
         return e;
-    select_kernel<P, WARPS, true><<<std::max(1, a.runs), 32 * WARPS, smem, s>>>(a);
-    e = cudaGetLastError();
+    e = launch_dependent(select_kernel<P, WARPS, true>, std::max(1, a.runs), 32 * WARPS, smem, s, a);
     if (e == cudaSuccess && a.runs > 1)
         e = launch_dependent(place_kernel, (a.runs + a.join - 1) / a.join, 32 * kPlaceWarps, 0, s, a);
     return e;
@@ -768,8 +770,7 @@ cudaError_t launch(const Args &a, cudaStream_t s)
     if (a.counts)
         return group_warps(a.T, a.E) == kWarps ? launch_grouped<P, kWarps>(a, s) : launch_grouped<P, many_warps(P)>(a, s);
     const int grid = (int)(((int64_t)a.T + kWarps - 1) / kWarps);
-    select_kernel<P, kWarps, false><<<grid, 32 * kWarps, smem_bytes(kWarps, a.E), s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(select_kernel<P, kWarps, false>, grid, 32 * kWarps, smem_bytes(kWarps, a.E), s, a);
 }
 
 mx_status check_router(const mx_router *r)
