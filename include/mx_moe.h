@@ -608,8 +608,8 @@ MX_API size_t mx_fp4_matmul_workspace_bytes(const mx_fp4_matrix *w, int rows);
  * one another than fp32 tells apart are compared in fp64, and without a bias
  * experts are compared by their logits.  A NaN logit counts as -inf; a c or a
  * run's score that is NaN (by the bias) ranks as -inf.  Logits that equal the largest
- * share the softmax where that is infinite.  Where the chosen scores are all 0,
- * renormalised weights are 0.
+ * share the softmax where that is infinite.  Where the chosen sigmoids are all
+ * below e^-700, they count as 0, and so do their renormalised weights.
  * ------------------------------------------------------------------------ */
 typedef enum { MX_SOFTMAX = 0, MX_SIGMOID = 1 } mx_score;
 
