@@ -682,20 +682,30 @@ def _up(n, m):
 
 def _fp4_rows(t, q, scales, cols, factor, dev):
     """(rows, packed Fp4Rows) of quantised activations."""
-    fmt, block = _fp4_format(t, scales, "q")
-    shape, strides = q.shape, q.stride()
-    if q.dtype is not t.u8 or len(shape) != 2 or shape[1] != (cols + 1) // 2 or (strides[1] != 1 and shape[1] > 1):
-        raise MxError(-1, f"q must be uint8 [rows, {(cols + 1) // 2}] with contiguous rows")
+    kind = scales.dtype
+    if kind is t.f8:
+        fmt, per = MX_FP4_E4M3, 16
+    elif kind is t.e8m0:
+        fmt, per = MX_FP4_E8M0, 8
+    else:
+        fmt, per = _fp4_format(t, scales, "q")
+    shape, (ld, one) = q.shape, q.stride() if q.dim() == 2 else (0, 0)
+    nbytes = (cols + 1) // 2
+    if q.dtype is not t.u8 or len(shape) != 2 or shape[1] != nbytes or (one != 1 and nbytes > 1):
+        raise MxError(-1, f"q must be uint8 [rows, {nbytes}] with contiguous rows")
     rows = shape[0]
-    if scales.shape != ((cols + 255) // 256, rows, 256 // block) or not scales.is_contiguous():
-        raise MxError(-1, f"scales must be contiguous [{(cols + 255) // 256}, {rows}, {256 // block}]")
+    if scales.shape != ((cols + 255) // 256, rows, per) or not scales.is_contiguous():
+        raise MxError(-1, f"scales must be contiguous [{(cols + 255) // 256}, {rows}, {per}]")
     if q.get_device() != dev or scales.get_device() != dev:
         raise MxError(-1, "all tensors must be on one device")
-    return rows, _FP4.pack(q.data_ptr(), scales.data_ptr(), _factor(t, factor, 1, fmt, dev), rows, cols, fmt,
-                           strides[0] if rows > 1 else _up(shape[1], 16))  # (the stride of a single row means nothing)
+    if rows <= 1:  # (the stride of a single row means nothing)
+        ld = _up(nbytes, 16)
+    return rows, _FP4.pack(q.data_ptr(), scales.data_ptr(), 0 if factor is None else _factor(t, factor, 1, fmt, dev), rows,
+                           cols, fmt, ld)
 
 
 def _factor(t, factor, count, fmt, dev):
+    """Address of the tensors' fp32 factors, 0 without."""
     if factor is None:
         return 0
     if (fmt != MX_FP4_E4M3 or factor.dtype is not t.f32 or factor.numel() != count or not factor.is_contiguous()
@@ -758,15 +768,15 @@ def fp4_quantize(x, q, scales, tensor_scale=None, stream=None):
     for blocks of 16 columns, with the optional float32 ``tensor_scale`` on the device, or e8m0 scales for blocks of
     32."""
     t = _t or _torch()
-    dev = x.get_device()
-    if x.dim() != 2:
+    dev, shape = x.get_device(), x.shape
+    if len(shape) != 2:
         raise MxError(-1, "x must be [rows, cols]")
-    rows, cols = x.shape
+    cols = shape[1]
     n, r = _fp4_rows(t, q, scales, cols, tensor_scale, dev)
-    if n != rows or (cols > 1 and x.stride(1) != 1):
+    ldx, one = x.stride()
+    if shape[0] != n or (one != 1 and cols > 1):
         raise MxError(-1, f"x must be [{n}, cols] with contiguous rows")
-    _on(dev, t.quantize4, x.data_ptr(), x.stride(0) if rows > 1 else cols, _dtype_code(x, "x"), r,
-        _stream_on(dev, stream))
+    _on(dev, t.quantize4, x.data_ptr(), ldx if n > 1 else cols, _dtype_code(x, "x"), r, _stream_on(dev, stream))
 
 
 def fp4_matmul_workspace_bytes(weight: Fp4Weight, rows: int) -> int:

@@ -88,14 +88,29 @@ struct Choice {
     int nt, cl, grid;
 };
 
+// Rounds of `units` tiles over the SMs, each as long as the MMAs of `rows` tokens and about 40 tokens' worth besides.
+double rounds(double units, double rows, int sms) { return std::ceil(units / sms) * (rows + 40); }
+
 Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
 {
     Choice c{16, 1, 1};
     if (grouped) {
+        // The smallest tile that holds a group with as many rows as an even routing gives; of many rows that whose
+        // rounds take least (a group of other sizes ends with half a tile on average).  An empty part of a tile
+        // costs shared memory alone: 4096 rows of 128 matrices 704 x 2816 by 64, 128 and 224 29.1, 28.8 and 31.7 us;
+        // 32768 of 256 matrices 1024 x 4096 140, 121 and 119; 4096 of 8 such 18.5, 15.0 and 18.4.
         const double avg = (double)rows / E, most = avg + 3 * std::sqrt(avg);
-        for (int nt : {32, 64, 128, 224})
+        for (int nt : {32, 64})
             if (c.nt < most)
                 c.nt = nt;
+        double best = 1e30;
+        if (most > 64)
+            for (int nt : {64, 128, 224}) {
+                const double tiles = most <= nt ? 1.0 : avg / nt + 0.5;
+                const double t = rounds(E * tiles * FT, avg / tiles, sms);
+                if (t < best)
+                    best = t, c.nt = nt;
+            }
         const int64_t units = ((int64_t)rows / c.nt + E) * FT;
         c.grid = (int)std::min<int64_t>(sms, units);
         return c;
@@ -103,24 +118,20 @@ Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
     for (int nt : {32, 64})
         if (c.nt < rows)
             c.nt = nt;
-    int64_t units = (int64_t)((rows + c.nt - 1) / c.nt) * FT;
-    if (rows > 64 && 2 * units > sms) {
-        // the tile whose rounds take least: a tile of n tokens costs its MMAs and about 40 tokens' worth besides
+    auto units_of = [&](int nt) { return (int64_t)((rows + nt - 1) / nt) * FT; };
+    if (rows > 64 && 2 * units_of(64) > sms) {
         double best = 1e30;
         for (int nt : {64, 128, 224}) {
-            const int64_t u = (int64_t)((rows + nt - 1) / nt) * FT;
-            const double t = (double)((u + sms - 1) / sms) * (nt + 40);
+            const double t = rounds((double)units_of(nt), nt, sms);
             if (t < best)
                 best = t, c.nt = nt;
         }
-        units = (int64_t)((rows + c.nt - 1) / c.nt) * FT;
     }
-    if (2 * units <= sms && KB >= 2)
-        c.cl = (int)std::min<int64_t>({units <= 8 ? 8 : 4, sms / units, KB});
-    if (c.cl > 4 && c.cl < 8)
-        c.cl = 4;
-    if (c.cl == 3)
-        c.cl = 2;
+    // Few units: clusters split the inner dimension.  More than four CTAs wait for room (a GPC holds one or two clusters of
+    // eight): 1 x 2112 x 2816, 17 units, by eight 9.2 us, by four 5.2.
+    const int64_t units = units_of(c.nt), cl = std::min<int64_t>({units <= 8 ? 8 : 4, sms / units, KB});
+    if (2 * units <= sms)
+        c.cl = cl >= 8 ? 8 : cl >= 4 ? 4 : cl >= 2 ? 2 : 1;
     c.grid = (int)std::min<int64_t>(sms / c.cl, units) * c.cl;
     return c;
 }
