@@ -245,10 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         w.len = len;
     }
     fence_before();
-    if (cl > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+    __syncthreads();  // (the CTAs of a cluster meet when each has its partial sums)
     fence_after();
     const int KB = stages_of(a.K);
     w.FT = (a.N + 127) / 128;

@@ -108,14 +108,13 @@ struct Raw {
 };
 
 template <bool BF16, bool FAST>
-__device__ __forceinline__ Raw<BF16> load8(const void *p, int64_t at, int n, bool vec)
+__device__ __forceinline__ Raw<BF16> load8(const char *p, uint32_t at, int n, bool vec)
 {
     Raw<BF16> v{};
     if (FAST && n <= 0)
         return v;
     if (FAST || (vec && n >= 8)) {
-        const uint4 *q = BF16 ? reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at)
-                              : reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + at);
+        const uint4 *q = reinterpret_cast<const uint4 *>(p + at * (BF16 ? 2 : 4));
         v.r[0] = q[0];
         if (!BF16)
             v.r[BF16 ? 0 : 1] = q[1];
@@ -125,7 +124,7 @@ __device__ __forceinline__ Raw<BF16> load8(const void *p, int64_t at, int n, boo
         for (int j = 0; j < 8; ++j) {
             w[j] = 0;
             if (j < n)
-                w[j] = BF16 ? static_cast<const uint16_t *>(p)[at + j] : static_cast<const uint32_t *>(p)[at + j];
+                w[j] = BF16 ? reinterpret_cast<const uint16_t *>(p)[at + j] : reinterpret_cast<const uint32_t *>(p)[at + j];
         }
         if (BF16) {
             v.r[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
@@ -151,35 +150,30 @@ __device__ __forceinline__ void pairs(const Raw<BF16> &x, uint64_t (&v)[4])
 }
 
 template <bool BF16, bool FAST>
-__device__ __forceinline__ void store8(void *p, int64_t at, int n, bool vec, const uint64_t (&v)[4])
+__device__ __forceinline__ void store8(char *p, uint32_t at, int n, bool vec, const uint64_t (&v)[4])
 {
     if (FAST && n <= 0)
         return;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        unpair_f32(v[j], f[2 * j], f[2 * j + 1]);
     if (FAST || (vec && n >= 8)) {
         if (BF16) {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) =
-                make_uint4(bf16_x2(v[0]), bf16_x2(v[1]), bf16_x2(v[2]), bf16_x2(v[3]));
+            *reinterpret_cast<uint4 *>(p + at * 2) = make_uint4(bf16_x2(v[0]), bf16_x2(v[1]), bf16_x2(v[2]), bf16_x2(v[3]));
         } else {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                unpair_f32(v[j], f[2 * j], f[2 * j + 1]);
-            float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
+            float4 *to = reinterpret_cast<float4 *>(p + at * 4);
             to[0] = make_float4(f[0], f[1], f[2], f[3]);
             to[1] = make_float4(f[4], f[5], f[6], f[7]);
         }
     } else {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            unpair_f32(v[j], f[2 * j], f[2 * j + 1]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (j < n) {
                 if (BF16)
-                    static_cast<uint16_t *>(p)[at + j] = f2bf(f[j]);
+                    reinterpret_cast<uint16_t *>(p)[at + j] = f2bf(f[j]);
                 else
-                    static_cast<float *>(p)[at + j] = f[j];
+                    reinterpret_cast<float *>(p)[at + j] = f[j];
             }
     }
 }
@@ -251,13 +245,17 @@ __global__ void __launch_bounds__(512, V == 1 ? (BF16 ? 3 : 2) : 1) norm_kernel(
     // first column of piece i, and how many of the eight there are
     auto column = [&](int i) { return (i * threads + tid) * 8; };
     auto count = [&](int i) { return FAST ? (column(i) < a.cols ? 8 : 0) : a.cols - column(i); };
+    constexpr int ES = BF16 ? 2 : 4;
+    // (rows by addresses that the whole CTA shares, a thread's columns by 32-bit offsets)
+    auto row_of = [](const void *p, int64_t at) { return const_cast<char *>(static_cast<const char *>(p)) + at; };
     Raw<BF16> x[V], res[V];
     auto fetch = [&](int64_t row) {
+        const char *px = row_of(a.x, row * a.ldx * ES), *pr = row_of(a.residual, row * a.ldr * ES);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i] = load8<BF16, FAST>(a.x, row * a.ldx + column(i), count(i), a.vx);
+            x[i] = load8<BF16, FAST>(px, column(i), count(i), a.vx);
             if (a.residual)
-                res[i] = load8<BF16, FAST>(a.residual, row * a.ldr + column(i), count(i), a.vr);
+                res[i] = load8<BF16, FAST>(pr, column(i), count(i), a.vr);
         }
     };
     // (the launch behind may set itself up; it waits for this one's end)
@@ -269,6 +267,7 @@ __global__ void __launch_bounds__(512, V == 1 ? (BF16 ? 3 : 2) : 1) norm_kernel(
         if (!AHEAD)
             fetch(row);
         uint64_t h[V][4];
+        char *psum = row_of(a.sum, row * a.lds * ES);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             pairs<BF16>(x[i], h[i]);
@@ -276,20 +275,21 @@ __global__ void __launch_bounds__(512, V == 1 ? (BF16 ? 3 : 2) : 1) norm_kernel(
                 uint64_t r[4];
                 pairs<BF16>(res[i], r);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 4; ++j)
                     h[i][j] = add_f32x2(h[i][j], r[j]);
-                    if (BF16)
-                        h[i][j] = of_bf16_x2(bf16_x2(h[i][j]));
+                if (BF16) {
+                    Raw<true> w;
+                    w.r[0] = make_uint4(bf16_x2(h[i][0]), bf16_x2(h[i][1]), bf16_x2(h[i][2]), bf16_x2(h[i][3]));
+                    pairs<true>(w, h[i]);
+                    if (FAST && a.sum && count(i) > 0)
+                        *reinterpret_cast<uint4 *>(psum + column(i) * 2) = w.r[0];
                 }
             }
+            if (a.sum && !(BF16 && FAST && a.residual))
+                store8<BF16, FAST>(psum, column(i), count(i), a.vs, h[i]);
         }
         if (AHEAD && row + gridDim.x < a.rows)
             fetch(row + gridDim.x);
-        if (a.sum) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                store8<BF16, FAST>(a.sum, row * a.lds + column(i), count(i), a.vs, h[i]);
-        }
         if (!a.out && !a.q)
             continue;
 
@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(512, V == 1 ? (BF16 ? 3 : 2) : 1) norm_kernel(
             if (a.weight) {
                 uint64_t w[4];
                 if (a.w_bf16)
-                    pairs<true>(load8<true, FAST>(a.weight, c, n, a.vw), w);
+                    pairs<true>(load8<true, FAST>(static_cast<const char *>(a.weight), c, n, a.vw), w);
                 else
-                    pairs<false>(load8<false, FAST>(a.weight, c, n, a.vw), w);
+                    pairs<false>(load8<false, FAST>(static_cast<const char *>(a.weight), c, n, a.vw), w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     y[j] = mul_f32x2(y[j], add_f32x2(off2, w[j]));
@@ -361,10 +361,11 @@ __global__ void __launch_bounds__(512, V == 1 ? (BF16 ? 3 : 2) : 1) norm_kernel(
                 }
             }
             if (a.out) {
+                char *po = row_of(a.out, row * a.ldo * (a.out_bf16 ? 2 : 4));
                 if (a.out_bf16)
-                    store8<true, FAST>(a.out, row * a.ldo + c, n, a.vo, y);
+                    store8<true, FAST>(po, c, n, a.vo, y);
                 else
-                    store8<false, FAST>(a.out, row * a.ldo + c, n, a.vo, y);
+                    store8<false, FAST>(po, c, n, a.vo, y);
             }
             if (a.q) {
                 float top = 0.0f;
@@ -381,18 +382,18 @@ __global__ void __launch_bounds__(512, V == 1 ? (BF16 ? 3 : 2) : 1) norm_kernel(
                 uint32_t e[4];
                 const float s = fp8::quantize_pairs(y, m, a.pow2, e);
                 if (n > 0) {
-                    uint8_t *q = a.q + row * a.ldq + c;
+                    char *q = row_of(a.q, row * a.ldq);
                     const uint2 w = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
                     if (FAST || (a.vq && n >= 8)) {
-                        *reinterpret_cast<uint2 *>(q) = w;
+                        *reinterpret_cast<uint2 *>(q + (uint32_t)c) = w;
                     } else {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             if (j < n)
-                                q[j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
+                                reinterpret_cast<uint8_t *>(q)[c + j] = (uint8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
                     }
                     if ((tid & 15) == 0)
-                        a.scales[row * a.s_r + (int64_t)(c / kBlk) * a.s_b] = s;
+                        (a.scales + row * a.s_r)[(int64_t)(c / kBlk) * a.s_b] = s;
                 }
             }
         }
