@@ -234,6 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (warp == kOutWarps && lane < 2)  // (the descriptors are the launch's own)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &a.xm : &a.wm) : "memory");
     pdl_wait();  // (nothing before this reads what an earlier launch may still write)
     Walk w{};
     {
