@@ -460,12 +460,12 @@ extern "C" mx_status mx_fp8_rmsnorm(const mx_rmsnorm *n, void *stream)
     if (!(n->eps >= 0.0f) || !std::isfinite(n->eps) || !std::isfinite(n->weight_offset))
         return fail(MX_ERR_INVALID_ARG, "eps must be finite and at least 0, weight_offset finite");
     const mx_fp8_rows &q = n->q;
-    if (!n->sum && !n->out && !q.q)
-        return fail(MX_ERR_INVALID_ARG, "one of sum, out and q must be given");
     if (q.q && (q.rows != n->rows || q.cols != n->cols))
         return fail(MX_ERR_INVALID_ARG, "q is [%d, %d], x is [%d, %d]", q.rows, q.cols, n->rows, n->cols);
     if (n->rows == 0)
         return MX_OK;
+    if (!n->sum && !n->out && !q.q)
+        return fail(MX_ERR_INVALID_ARG, "one of sum, out and q must be given");
     if (!n->x)
         return fail(MX_ERR_INVALID_ARG, "x is NULL");
     if ((st = norm::check_operand(n->x, n->ldx, n->cols, n->dtype, "x")) != MX_OK ||

@@ -47,6 +47,7 @@ constexpr int kManyTokens = 2048;
 constexpr int kRuns = 512;    // selecting blocks when many tokens' slots are grouped, as long as kMaxRun allows
 constexpr int kMaxRun = 224;  // tokens of a block at most (its counts are bytes)
 constexpr int kPlaceWarps = 8, kPlaceBlocks = 128;
+constexpr int kMaxTokens = 1 << 30;
 
 struct Args {
     const void *logits;
@@ -825,8 +826,8 @@ extern "C" size_t mx_route_logits_workspace_bytes(const mx_router *router, int T
 {
     if (sel::check_router(router) != MX_OK)
         return 0;
-    if (T_max < 0) {
-        fail(MX_ERR_INVALID_ARG, "T_max %d is negative", T_max);
+    if (T_max < 0 || T_max > sel::kMaxTokens) {
+        fail(MX_ERR_INVALID_ARG, "T_max %d must be in [0, 2^30]", T_max);
         return 0;
     }
     // (any number of tokens up to T_max: there are the more blocks the more tokens there are, up to kManyTokens and
@@ -844,8 +845,8 @@ extern "C" mx_status mx_route_logits(const void *logits, int64_t ld, int dtype, 
     if ((st = sel::check_router(router)) != MX_OK || (st = check_dtype(dtype, "dtype")) != MX_OK)
         return st;
     const int E = router->n_experts, K = router->top_k;
-    if (T < 0 || (int64_t)T * K > 0x7FFFFFFF)
-        return fail(MX_ERR_INVALID_ARG, "T %d must be at least 0, T * top_k below 2^31", T);
+    if (T < 0 || T > sel::kMaxTokens || (int64_t)T * K > 0x7FFFFFFF)
+        return fail(MX_ERR_INVALID_ARG, "T %d must be in [0, 2^30], T * top_k below 2^31", T);
     if (ld < E)
         return fail(MX_ERR_INVALID_ARG, "row pitch %lld is below the %d experts", (long long)ld, E);
     if (ld > ((int64_t)1 << 31))

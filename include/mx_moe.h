@@ -626,7 +626,7 @@ typedef struct {
 } mx_router;
 
 /*
- *   logits    device [T][E] of `dtype` (mx_dtype), row pitch ld elements; T >= 0
+ *   logits    device [T][E] of `dtype` (mx_dtype), row pitch ld elements; 0 <= T <= 2^30, T * top_k < 2^31
  *   topk_idx  device int32 [T][top_k];  topk_w device fp32 [T][top_k]
  *   counts [E], offsets [E + 1], perm [T * top_k]  device int32, all or none:
  *             the slots grouped by expert as mx_moe_route groups them

@@ -73,7 +73,7 @@ def test_router_refusals(L, field, status):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(T=-1), INVALID), (dict(T=1 << 30), INVALID), (dict(ld=63), INVALID), (dict(ld=1 << 40), UNSUP),
+    (dict(T=-1), INVALID), (dict(T=1 << 30), INVALID), (dict(T=(1 << 30) + 1), INVALID), (dict(ld=63), INVALID), (dict(ld=1 << 40), UNSUP),
     (dict(dtype=2), INVALID), (dict(logits=0), INVALID), (dict(idx=0), INVALID), (dict(w=0), INVALID),
     (dict(counts=0), INVALID), (dict(offsets=0), INVALID), (dict(perm=0), INVALID), (dict(counts=0, offsets=0), INVALID),
     (dict(logits=FAKE + 2), ALIGN), (dict(logits=FAKE + 1, dtype=mx.MX_BF16), ALIGN), (dict(idx=FAKE + 2), ALIGN),
@@ -135,6 +135,7 @@ def test_norm_refusals(L, kw, status):
 
 def test_norm_of_no_rows_is_done(L):
     assert norm(L, rows=0, q__rows=0) == OK
+    assert norm(L, rows=0, x=0, sum=0, out=0, q__q=0) == OK  # (tensors without rows have no address)
     assert L.mx_fp8_rmsnorm(None, None) == INVALID
 
 
