@@ -86,6 +86,7 @@ mx_status check_rows(const mx_fp4_rows *r, const char *name, bool operand)
 // Token tile, cluster split and grid of a product.
 struct Choice {
     int nt, cl, grid;
+    bool several;  // tiles to a CTA
 };
 
 // Rounds of `units` tiles over the SMs, each as long as the MMAs of `rows` tokens and about 40 tokens' worth besides.
@@ -93,7 +94,7 @@ double rounds(double units, double rows, int sms) { return std::ceil(units / sms
 
 Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
 {
-    Choice c{16, 1, 1};
+    Choice c{16, 1, 1, true};
     if (grouped) {
         // The smallest tile that holds a group with as many rows as an even routing gives; of many rows that whose
         // rounds take least (a group of other sizes ends with half a tile on average).  An empty part of a tile
@@ -133,6 +134,7 @@ Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
     if (2 * units <= sms)
         c.cl = cl >= 8 ? 8 : cl >= 4 ? 4 : cl >= 2 ? 2 : 1;
     c.grid = (int)std::min<int64_t>(sms / c.cl, units) * c.cl;
+    c.several = units > c.grid / c.cl;
     return c;
 }
 
@@ -201,7 +203,9 @@ mx_status product(const mx_fp4_rows *x, const int32_t *offsets, const mx_fp4_mat
     g.out_vec = vec16(out, ldo, g.out_bf16);
     g.err = static_cast<unsigned *>(ws);
     g.cl = c.cl;
-    g.stages = std::min(12, std::max(3, KB));
+    // (a CTA of several tiles loads on into the next ones: 4096 rows of 128 matrices 2816 x 704, three stages a tile, 36 us
+    // with a ring of three, 30 with all that fit)
+    g.stages = c.several ? 12 : std::min(12, std::max(2, KB));
     while (g.stages > 2 && gemm_smem(block, c.nt, g.stages) > (size_t)kSmem)
         --g.stages;
     const uint64_t bytes = ((uint64_t)w->cols + 1) / 2;
