@@ -619,11 +619,14 @@ def fp8_moe_forward(x, topk_idx, topk_w, layer: Fp8Layer, out, ws, residual=None
 
 def _rows2d(t, shape, dev, name):
     """Row pitch of a tensor of the given shape with contiguous rows."""
-    if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
-        raise MxError(-1, f"{name} must be {list(shape)} with contiguous rows")
+    if t.shape != shape:
+        raise MxError(-1, f"{name} must be {list(shape)}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise MxError(-1, f"{name} must have contiguous rows")
     if t.get_device() != dev:
         raise MxError(-1, "all tensors must be on one device")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    return ld if shape[0] > 1 else shape[1]  # (the stride of a single row means nothing)
 
 
 def fp8_rmsnorm(x, weight=None, eps=1e-6, weight_offset=0.0, residual=None, residual_out=None, out=None, q=None,
@@ -689,17 +692,20 @@ def _fp4_rows(t, q, scales, cols, factor, dev):
         fmt, per = MX_FP4_E8M0, 8
     else:
         fmt, per = _fp4_format(t, scales, "q")
-    shape, (ld, one) = q.shape, q.stride() if q.dim() == 2 else (0, 0)
     nbytes = (cols + 1) // 2
-    if q.dtype is not t.u8 or len(shape) != 2 or shape[1] != nbytes or (one != 1 and nbytes > 1):
-        raise MxError(-1, f"q must be uint8 [rows, {nbytes}] with contiguous rows")
+    shape = q.shape
+    if len(shape) != 2 or shape[1] != nbytes or q.dtype is not t.u8:
+        raise MxError(-1, f"q must be uint8 [rows, {nbytes}]")
     rows = shape[0]
+    ld, one = q.stride()
+    if one != 1 and nbytes > 1:
+        raise MxError(-1, "q must have contiguous rows")
     if scales.shape != ((cols + 255) // 256, rows, per) or not scales.is_contiguous():
         raise MxError(-1, f"scales must be contiguous [{(cols + 255) // 256}, {rows}, {per}]")
     if q.get_device() != dev or scales.get_device() != dev:
         raise MxError(-1, "all tensors must be on one device")
     if rows <= 1:  # (the stride of a single row means nothing)
-        ld = _up(nbytes, 16)
+        ld = (nbytes + 15) // 16 * 16
     return rows, _FP4.pack(q.data_ptr(), scales.data_ptr(), 0 if factor is None else _factor(t, factor, 1, fmt, dev), rows,
                            cols, fmt, ld)
 
@@ -708,8 +714,8 @@ def _factor(t, factor, count, fmt, dev):
     """Address of the tensors' fp32 factors, 0 without."""
     if factor is None:
         return 0
-    if (fmt != MX_FP4_E4M3 or factor.dtype is not t.f32 or factor.numel() != count or not factor.is_contiguous()
-            or factor.get_device() != dev):
+    if (fmt != MX_FP4_E4M3 or factor.dtype is not t.f32 or factor.numel() != count or factor.get_device() != dev
+            or (count > 1 and not factor.is_contiguous())):
         raise MxError(-1, f"tensor_scale must be {count} contiguous float32 on the tensors' device, with e4m3 scales")
     return factor.data_ptr()
 
@@ -837,22 +843,31 @@ def route_logits(logits, router: Router, topk_idx, topk_w, counts=None, offsets=
     grouped by expert as route() does; ws is then a uint8 workspace of route_logits_workspace_bytes, prepared by
     workspace_init."""
     t = _t or _torch()
-    dev = logits.get_device()
-    T, E, K = logits.shape[0], router.n_experts, router.top_k
-    ld = _rows2d(logits, (T, E), dev, "logits")
-    outs = [(topk_idx, t.i32, (T, K), "topk_idx"), (topk_w, t.f32, (T, K), "topk_w")]
+    dev, shape = logits.get_device(), logits.shape
+    E, K = router.n_experts, router.top_k
+    if len(shape) != 2 or shape[1] != E:
+        raise MxError(-1, f"logits must be [T, {E}]")
+    T = shape[0]
+    ld, one = logits.stride()
+    if one != 1 and E > 1:
+        raise MxError(-1, "logits must have contiguous rows")
+    chosen = (T, K)
+    if (topk_idx.dtype is not t.i32 or topk_w.dtype is not t.f32 or topk_idx.shape != chosen or topk_w.shape != chosen
+            or not topk_idx.is_contiguous() or not topk_w.is_contiguous()):
+        raise MxError(-1, f"topk_idx and topk_w must be contiguous int32 and float32 [{T}, {K}]")
+    if topk_idx.get_device() != dev or topk_w.get_device() != dev or (router.dev is not None and router.dev != dev):
+        raise MxError(-1, "all tensors must be on one device")
+    cp = op = pp = wp = None
+    n = 0
     if counts is not None or offsets is not None or perm is not None:
         if counts is None or offsets is None or perm is None or ws is None:
             raise MxError(-1, "counts, offsets, perm and ws come together")
-        outs += [(counts, t.i32, (E,), "counts"), (offsets, t.i32, (E + 1,), "offsets"), (perm, t.i32, (T * K,), "perm"),
-                 (ws, t.u8, ws.shape, "ws")]
-    for a, dtype, shape, name in outs:
-        if a.dtype is not dtype or a.shape != shape or not a.is_contiguous():
-            raise MxError(-1, f"{name} must be contiguous {dtype} {list(shape)}")
-        if a.get_device() != dev:
+        for a, size in ((counts, E), (offsets, E + 1), (perm, T * K)):
+            if a.dtype is not t.i32 or a.numel() != size or not a.is_contiguous() or a.get_device() != dev:
+                raise MxError(-1, f"counts, offsets and perm must be contiguous int32 [{E}], [{E + 1}] and [{T * K}] on "
+                                  "the logits' device")
+        if ws.get_device() != dev:
             raise MxError(-1, "all tensors must be on one device")
-    if router.dev is not None and router.dev != dev:
-        raise MxError(-1, "all tensors must be on one device")
-    _on(dev, t.route, logits.data_ptr(), ld, _dtype_code(logits, "logits"), T, router.ref, topk_idx.data_ptr(),
-        topk_w.data_ptr(), _ptr(counts), _ptr(offsets), _ptr(perm), _stream_on(dev, stream), _ptr(ws),
-        0 if ws is None else ws.nbytes)
+        cp, op, pp, wp, n = counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(), ws.data_ptr(), ws.nbytes
+    _on(dev, t.route, logits.data_ptr(), ld if T > 1 else E, _dtype_code(logits, "logits"), T, router.ref,
+        topk_idx.data_ptr(), topk_w.data_ptr(), cp, op, pp, _stream_on(dev, stream), wp, n)
