@@ -16,7 +16,7 @@
 // q move 151 MB, 22.4 us at the copy rate; a warp's 256 columns took 568 instructions in a
 // first form and 40 us.  So values go two to an instruction (f32x2), a warp's sums are added
 // as integers (redux, at the scale of the largest: 50 bits) instead of by five exchanges of two floats,
-// and one warp joins them and takes the root.
+// and one warp joins them and takes the root: 385 instructions and 30.5 us, 62 % of the issue slots.
 #include "mx_fp8.cuh"
 #include "mx_host.h"
 
