@@ -39,14 +39,14 @@ namespace {
 
 // Warps of a selecting block: eight.  When many tokens' slots are grouped 32 (16 for more than 256 experts,
 // whose keys take more registers), so that the placing blocks have fewer counts to add up: 4096 x 256 in runs
-// 15.8 us (by eight 18.9), 2048 13; but 32 warps on one SM take each other's time: 333 x 60 by eight 6.8 us, by
+// 15.1 us (by eight 18.9), 2048 13; but 32 warps on one SM take each other's time: 333 x 60 by eight 6.8 us, by
 // 32 8.1.
 constexpr int kWarps = 8;
 constexpr int many_warps(int P) { return P <= 8 ? 32 : 16; }
 constexpr int kManyTokens = 2048;
 constexpr int kRuns = 512;    // selecting blocks when many tokens' slots are grouped, as long as kMaxRun allows
 constexpr int kMaxRun = 224;  // tokens of a block at most (its counts are bytes)
-constexpr int kPlaceWarps = 8, kPlaceBlocks = 128;
+constexpr int kPlaceWarps = 16, kPlaceBlocks = 128;
 constexpr int kMaxTokens = 1 << 30;
 // Slots up to which the last selecting block places them all: one launch less, of about 2.5 us on the host, for 9 tokens 5.4
 // us instead of 5.6, 333 x 60 top-4 7.0 instead of 6.5, 256 x 256 top-8 9.4 instead of 8.5 (512 x 256 top-8 15.0, 8.9).
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(32 * kPlaceWarps) place_kernel(const Args a)
     // All blocks' counts, and those of the blocks before this one's: `lanes` neighbouring lanes have an expert, a lane sixteen
     // neighbouring blocks at a time.  Each begins with another expert: in one order all met at the same lines
     // (4096 x 256: 20 us instead of 11).
-    constexpr int BATCH = 8;
+    constexpr int BATCH = 4;
     const int mine = me * a.join, lanes = a.run_lanes, each = 32 / lanes, part = lane & (lanes - 1);
     const int turn = (int)((int64_t)me * a.E / gridDim.x);
     auto expert = [&](int i) { return i + turn < a.E ? i + turn : i + turn - a.E; };
