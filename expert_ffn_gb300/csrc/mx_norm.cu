@@ -457,8 +457,8 @@ extern "C" mx_status mx_fp8_rmsnorm(const mx_rmsnorm *n, void *stream)
         return fail(MX_ERR_UNSUPPORTED, "%d columns must be within [1, %d]", n->cols, norm::kMaxCols);
     if (n->pow2 != 0 && n->pow2 != 1)
         return fail(MX_ERR_INVALID_ARG, "pow2 %d is not 0 or 1", n->pow2);
-    if (!(n->eps >= 0.0f) || !std::isfinite(n->eps) || !std::isfinite(n->weight_offset))
-        return fail(MX_ERR_INVALID_ARG, "eps must be finite and at least 0, weight_offset finite");
+    if (!(n->eps >= 0.0f && n->eps <= 1e30f) || !std::isfinite(n->weight_offset))
+        return fail(MX_ERR_INVALID_ARG, "eps must be in [0, 1e30], weight_offset finite");
     const mx_fp8_rows &q = n->q;
     if (q.q && (q.rows != n->rows || q.cols != n->cols))
         return fail(MX_ERR_INVALID_ARG, "q is [%d, %d], x is [%d, %d]", q.rows, q.cols, n->rows, n->cols);
@@ -475,6 +475,14 @@ extern "C" mx_status mx_fp8_rmsnorm(const mx_rmsnorm *n, void *stream)
         return st;
     if (n->weight && !aligned(n->weight, dtype_bytes(n->weight_dtype)))
         return fail(MX_ERR_ALIGNMENT, "weight is misaligned");
+    // in place: a thread reads its columns of a row before it writes them, so the rows have to be the same
+    if (n->sum && ((n->sum == n->x && n->lds != n->ldx) || (n->sum == n->residual && n->lds != n->ldr)))
+        return fail(MX_ERR_INVALID_ARG, "sum in place of x or residual needs the same row pitch");
+    if (n->out && ((n->out == n->x && (n->ldo != n->ldx || n->out_dtype != n->dtype)) ||
+                   (n->out == n->residual && (n->ldo != n->ldr || n->out_dtype != n->dtype))))
+        return fail(MX_ERR_INVALID_ARG, "out in place of x or residual needs the same type and row pitch");
+    if ((n->sum && n->sum == n->out) || (q.q && (q.q == n->sum || q.q == n->out || q.q == n->x || q.q == n->residual)))
+        return fail(MX_ERR_INVALID_ARG, "sum, out and q must be different buffers, q none of the inputs");
     const int es = (int)dtype_bytes(n->dtype), bf16 = n->dtype == MX_BF16;
     norm::Args a{};
     if (q.q) {

@@ -446,7 +446,7 @@ typedef struct {
     int32_t rows, cols;      /* rows >= 0; 1 <= cols <= 32768 */
     int32_t dtype, weight_dtype, out_dtype;
     int32_t pow2;            /* of mx_fp8_quantize */
-    float eps;               /* >= 0 */
+    float eps;               /* within [0, 1e30] */
     float weight_offset;
 } mx_rmsnorm;
 MX_API mx_status mx_fp8_rmsnorm(const mx_rmsnorm *args, void *stream);

@@ -120,7 +120,7 @@ def norm(L, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=2), INVALID), (dict(weight_dtype=-1), INVALID), (dict(out_dtype=3), INVALID), (dict(rows=-1), INVALID),
     (dict(cols=0), UNSUP), (dict(cols=32769), UNSUP), (dict(pow2=2), INVALID), (dict(eps=-1e-6), INVALID),
-    (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID), (dict(weight_offset=NAN), INVALID), (dict(x=0), INVALID),
+    (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID), (dict(eps=1.1e30), INVALID), (dict(weight_offset=NAN), INVALID), (dict(x=0), INVALID),
     (dict(sum=0, out=0, q__q=0), INVALID), (dict(q__rows=3), INVALID), (dict(q__cols=255), INVALID),
     (dict(q__scales=0), INVALID), (dict(q__ld=255), INVALID), (dict(q__scale_row=-1), INVALID),
     (dict(q__scale_block=-1), INVALID), (dict(q__ld=1 << 40), UNSUP), (dict(q__scales=FAKE + 2), ALIGN),
@@ -128,6 +128,11 @@ def norm(L, **kw):
     (dict(ldx=1 << 40), UNSUP), (dict(x=FAKE + 1), ALIGN), (dict(residual=FAKE + 1), ALIGN), (dict(weight=FAKE + 1), ALIGN),
     (dict(weight=FAKE + 2, weight_dtype=mx.MX_F32), ALIGN), (dict(sum=FAKE + 1), ALIGN),
     (dict(out=FAKE + 2, out_dtype=mx.MX_F32), ALIGN),
+    # in place with other rows or types, and outputs in one another's place
+    (dict(sum=FAKE, lds=264), INVALID), (dict(sum=FAKE + (1 << 20), lds=264), INVALID), (dict(out=FAKE, ldo=264), INVALID),
+    (dict(out=FAKE, out_dtype=mx.MX_F32), INVALID), (dict(out=FAKE + (1 << 20), out_dtype=mx.MX_F32), INVALID),
+    (dict(out=FAKE + (3 << 20)), INVALID), (dict(q__q=FAKE), INVALID), (dict(q__q=FAKE + (3 << 20)), INVALID),
+    (dict(q__q=FAKE + (4 << 20)), INVALID),
 ])
 def test_norm_refusals(L, kw, status):
     assert norm(L, **kw) == status
