@@ -128,11 +128,15 @@ Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
                 best = t, c.nt = nt;
         }
     }
-    // Few units: clusters split the inner dimension.  More than four CTAs wait for room (a GPC holds one or two clusters of
-    // eight): 1 x 2112 x 2816, 17 units, by eight 9.2 us, by four 5.2.
-    const int64_t units = units_of(c.nt), cl = std::min<int64_t>({units <= 8 ? 8 : 4, sms / units, KB});
-    if (2 * units <= sms)
-        c.cl = cl >= 8 ? 8 : cl >= 4 ? 4 : cl >= 2 ? 2 : 1;
+    // Few units of many stages: clusters of four split the inner dimension, of eight where a few such clusters do.  A
+    // cluster costs 1 to 1.5 us: 20 x 4096 x 4096 (16 stages) whole 6.2 us, in four 6.0, 64 rows 6.6, 6.8; 2112 x 5120 6.8, 5.9 and
+    // 7.3, 6.8; 4096 x 2048 4.8, 5.3.  In two it gains nothing while more do not fit (20 x 7680 x 8192 9.9 and 10.0 us), and 17
+    // units in eight wait for room (a GPC holds one or two clusters of eight; 20 x 2112 x 8192 10.9 us, in four 6.4).
+    const int64_t units = units_of(c.nt);
+    if (units <= 8 && KB >= 16)
+        c.cl = 8;
+    else if (4 * units <= sms && KB >= (rows <= 32 ? 16 : 18))
+        c.cl = 4;
     c.grid = (int)std::min<int64_t>(sms / c.cl, units) * c.cl;
     c.several = units > c.grid / c.cl;
     return c;

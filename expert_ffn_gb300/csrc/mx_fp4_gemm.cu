@@ -25,14 +25,14 @@
 //   9    MMA: per stage the copies of its scales to TMEM (tcgen05.cp, in order with the
 //        MMAs) and four MMAs (K = 64)
 //   10-11  the tokens' scales, every other stage each
-// Two TMEM accumulators: a tile's results leave while the next one is summed.  Few units: a
+// Two TMEM accumulators: a tile's results leave while the next one is summed.  Few units of many stages: a
 // cluster of `cl` CTAs splits the inner dimension of one unit, and its partial sums are added
 // through distributed shared memory in rank order.
 //
 // What bounds it: 4096 x 4096 x 4096 takes 30 us, of which the MMAs are 18 (7.6 PFLOP/s, what another
 // 4096 columns of K add); the rest is launch, the first fill, the last tile's results, and results that
 // reach memory.  32768 rows of 256 matrices 1024 x 4096 are bound by HBM, 119 us (0.84 of the copy rate); 64 x 4096 x
-// 4096 by its chain, 6.5 us: launch, fill, four stages, the cluster's sums.
+// 4096 by its chain, 6.2 us: launch, fill, the MMAs of sixteen stages.
 //
 // Every wait is bounded: a wait that gives up sets the caller's error word and ends the
 // CTA's work.
@@ -192,6 +192,13 @@ __device__ __forceinline__ uint32_t scaled_bf16(uint32_t lo, uint32_t hi, float 
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(tmem_value(hi) * f * g), "f"(tmem_value(lo) * f * g));
     return r;
+}
+
+__device__ __forceinline__ float ld_cluster1(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 struct Unit {
@@ -508,33 +515,53 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         cluster_sync();
         if (warp < kOutWarps && w.first < w.n_units && !*abort) {
             const Unit U = unit_of<NT>(a, w, w.first);
-            const int o = U.f * 128 + 4 * lane;
             // column n of the tile: CTA n % cl of the cluster, over all ranks in order
             for (int n = rank + cl * warp; n < U.n; n += cl * kOutWarps) {
-                const uint32_t at = smem_u32(reinterpret_cast<float *>(ring) + n * 128 + 4 * lane);
-                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const uint32_t col = smem_u32(reinterpret_cast<float *>(ring) + n * 128);
+                const int64_t to = (int64_t)(U.tok0 + n) * a.ldo + U.f * 128;
+                if (a.out_vec) {  // four neighbouring rows to a lane
+                    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-                for (int r = 0; r < cl; ++r) {
-                    const float4 p = ld_cluster(mapa(at, r));
-                    v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
-                }
-                const int64_t to = (int64_t)(U.tok0 + n) * a.ldo + o;
-                const float y[4] = {v.x, v.y, v.z, v.w};
-                if (a.out_vec && o + 4 <= a.N) {
-                    if (a.out_bf16)
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to) =
+                    for (int r = 0; r < cl; ++r) {
+                        const float4 p = ld_cluster(mapa(col + 16 * lane, r));
+                        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+                    }
+                    const float y[4] = {v.x, v.y, v.z, v.w};
+                    const int64_t at = to + 4 * lane;
+                    const int left = a.N - U.f * 128 - 4 * lane;
+                    if (left >= 4 && a.out_bf16)
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
                             make_uint2(f2bf(y[0]) | (uint32_t)f2bf(y[1]) << 16, f2bf(y[2]) | (uint32_t)f2bf(y[3]) << 16);
+                    else if (left >= 4)
+                        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = v;
                     else
-                        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to) = v;
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (o + i < a.N) {
+                        for (int i = 0; i < 3; ++i)
+                            if (i < left) {
+                                if (a.out_bf16)
+                                    static_cast<uint16_t *>(a.out)[at + i] = f2bf(y[i]);
+                                else
+                                    static_cast<float *>(a.out)[at + i] = y[i];
+                            }
+                } else {  // neighbouring rows to neighbouring lanes
+                    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+                    for (int r = 0; r < cl; ++r) {
+                        const uint32_t at = mapa(col + 4 * lane, r);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            y[i] += ld_cluster1(at + 128 * i);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = 32 * i + lane;
+                        if (U.f * 128 + row < a.N) {
                             if (a.out_bf16)
-                                static_cast<uint16_t *>(a.out)[to + i] = f2bf(y[i]);
+                                static_cast<uint16_t *>(a.out)[to + row] = f2bf(y[i]);
                             else
-                                static_cast<float *>(a.out)[to + i] = y[i];
+                                static_cast<float *>(a.out)[to + row] = y[i];
                         }
+                    }
                 }
             }
         }

@@ -256,11 +256,12 @@ def test_quantise_without_a_factor_is_one():
 
 # ------------------------------------------------------------------- products
 
-# one row by integers and by the tensor cores; every token tile; splits in one, two, four, eight
+# one row by integers and by the tensor cores; every token tile; whole, and in four and eight
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 100, 31), (1, 704, 2816), (1, 2112, 2817), (1, 300, 6144), (1, 4096, 7000),
                                    (1, 129, 9000), (2, 5, 3), (3, 129, 64), (5, 128, 257), (8, 2112, 1000), (16, 64, 2048), (17, 700, 333),
                                    (32, 2816, 512), (33, 1000, 4096), (64, 300, 2000), (65, 1024, 1024), (100, 4096, 300), (128, 512, 777),
-                                   (200, 5001, 1037), (224, 130, 256), (225, 2000, 255), (449, 1500, 640), (1000, 4096, 700)])
+                                   (200, 5001, 1037), (224, 130, 256), (225, 2000, 255), (449, 1500, 640), (1000, 4096, 700),
+                                   (20, 131, 8000), (40, 2047, 5000), (64, 700, 4500), (30, 3000, 4096)])
 @pytest.mark.parametrize("block", [16, 32])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_product(M, N, K, block, out):
@@ -315,7 +316,7 @@ def test_nan_scales_stay_in_their_row_and_column(M, N, K, block):
     assert got[:, 77].isnan().all() and torch.equal(got[:, cols], clean[:, cols])
 
 
-@pytest.mark.parametrize("M,N,K", [(40, 300, 2000), (200, 300, 500), (600, 2048, 800)])
+@pytest.mark.parametrize("M,N,K", [(40, 300, 2000), (40, 300, 4096), (40, 2001, 5000), (200, 300, 500), (600, 2048, 800)])
 def test_a_row_does_not_depend_on_the_others(M, N, K):
     import torch
     q, s, tx, weight, X, W = operands(M, N, K, 16)
