@@ -474,6 +474,19 @@ def _stream_on(dev, stream):
     return _stream_handle(stream)
 
 
+def _bytes_on(dev, stream, n, device):
+    """n bytes for the work of `stream`, from that stream's own pool: a block of the current stream's may still be in
+    use there, and goes back to it when the tensor goes, whatever `stream` still does with it."""
+    import torch
+    if dev < 0 or stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def _fp8_matrix(w, scales, name):
     t = _torch()
     _need(w.dtype is t.f8 and w.dim() in (2, 3), f"{name} must be float8_e4m3fn [count,] rows, cols")
@@ -725,10 +738,10 @@ class Fp4Weight:
     at multiples of 16 bytes; ``scales`` float8_e4m3fn (a block of 16 columns each) or float8_e8m0fnu (32) [count,]
     rows, blocks; ``tensor_scale`` float32 [count] or None (e4m3 only).  ``cols`` is needed where it is odd.  ``w`` and
     ``tensor_scale`` are kept and read by every call; of ``scales`` the products read a copy in their own order, made
-    here on ``stream`` (mx_fp4_pack_scales)."""
+    here on ``stream`` (mx_fp4_pack_scales) in memory of that stream: products on others come after it, and the handle
+    is kept until they have ended."""
 
     def __init__(self, w, scales, tensor_scale=None, cols=None, stream=None):
-        import torch
         t = _t or _torch()
         _need(w.dtype is t.u8 and w.dim() in (2, 3), "w must be uint8 [count,] rows, bytes")
         fmt, block = _fp4_format(t, scales, "w")
@@ -750,7 +763,7 @@ class Fp4Weight:
         if n == 0:
             _check(-1)
         self.w, self.tensor_scale = w, tensor_scale
-        self.packed = torch.empty(n, dtype=torch.uint8, device=w.device)
+        self.packed = _bytes_on(dev, stream, n, w.device)
         _on(dev, lib().mx_fp4_pack_scales, scales.data_ptr(), lds, rows, cols, count, fmt, self.packed.data_ptr(),
             _stream_on(dev, stream))
         self.c = Fp4Matrix(w.data_ptr(), self.packed.data_ptr(), factor or None, rows, cols, count, fmt, ld)
