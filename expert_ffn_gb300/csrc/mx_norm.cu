@@ -208,8 +208,8 @@ __device__ __forceinline__ Two of_part(Part p)
     return Two{hi * g, lo * g};
 }
 
-// sqrt(D / (S + D eps)), rounded once.
-__device__ __forceinline__ float root(Two S, float D, float eps)
+// f sqrt(D / (S + D eps)), rounded once; f: a power of two, and S and eps those of f h.
+__device__ __forceinline__ float root(Two S, float D, float eps, float f)
 {
     const float pe = __fmul_rn(D, eps), ee = fmaf(D, eps, -pe);
     float t;
@@ -217,11 +217,14 @@ __device__ __forceinline__ float root(Two S, float D, float eps)
     const float a = b + bl, al = bl - (a - b);
     if (!(a > 0.0f && a < INFINITY))
         return a == 0.0f ? INFINITY : S.hi != S.hi ? NAN : 0.0f;
-    const float r0 = rsqrtf(__fdividef(a, D));
+    float r0 = rsqrtf(__fdividef(a, D));
+    if (f < 1.0f)  // (of 20 bits, so that f r0 is exact where it is subnormal)
+        r0 = __uint_as_float(__float_as_uint(r0) & ~15u);
     const float th = __fmul_rn(r0, r0), tl = fmaf(r0, r0, -th), u = __fmul_rn(th, a), ul = fmaf(th, a, -u);
     const float rho = ((D - u) - ul) - fmaf(tl, a, th * al);
     const float d = __fdividef(rho, D);  // r0^2 A / D = 1 - d
-    return fmaf(r0, d * fmaf(0.375f, d, 0.5f), r0);
+    const float c = d * fmaf(0.375f, d, 0.5f);
+    return f < 1.0f ? fmaf(r0 * f, c, r0 * f) : fmaf(r0, c, r0) * f;
 }
 
 // The largest of m, |a| and |b|; a NaN stays one.
@@ -319,11 +322,13 @@ __global__ void __launch_bounds__(512, V == 1 ? (BF16 ? 3 : 2) : 1) norm_kernel(
 #pragma unroll
                 for (int o = 16; o; o >>= 1)
                     S = add_two(S, Two{__shfl_xor_sync(0xFFFFFFFFu, S.hi, o), __shfl_xor_sync(0xFFFFFFFFu, S.lo, o)});
+                // h times 2^-80: its largest square, from 2^85 on, comes to 2^-75 to 2^96.  Times 2^60 where S + D eps is at
+                // most 2^-60; times 2^110, which takes the least h to 2^-39, where that is below 2^-100.
                 float g = 0.0f;  // (done)
-                if (pass == 0 && !(S.hi < 1.2676506e30f && S.hi + D * a.eps > 8.6736174e-19f))  // 2^100, 2^-60
-                    g = S.hi < 1.0f ? 1.1529215e18f : 8.4703295e-22f;                          // 2^60, 2^-70
+                if (pass == 0 && !(S.hi < 0x1p100f && S.hi + D * a.eps > 0x1p-60f))
+                    g = !(S.hi < 1.0f) ? 0x1p-80f : S.hi + D * a.eps > 0x1p-100f ? 0x1p60f : 0x1p110f;
                 if (lane == 0) {
-                    shared_r = root(S, D, a.eps * f * f) * f;
+                    shared_r = root(S, D, a.eps * f * f, f);
                     shared_f = g;
                 }
             }
