@@ -57,6 +57,18 @@ struct PackArgs {
 };
 cudaError_t launch_pack(const PackArgs &a, cudaStream_t s);
 
+// What a sum is multiplied by, one after the other, for the factors tx and tw: their product where that is a normal
+// number, so that a large factor meets the small one and not the sum; else both are above 1, or both below, and one after the
+// other leaves fp32's range only where the result does.
+struct Factors {
+    float a, b;
+};
+__device__ __forceinline__ Factors factors_of(float tx, float tw)
+{
+    const float both = tx * tw;
+    return both >= 0x1p-126f && both < INFINITY ? Factors{both, 1.0f} : Factors{tx, tw};
+}
+
 __host__ __device__ constexpr int stages_of(int cols) { return (cols + kStageCols - 1) / kStageCols; }
 __host__ __device__ constexpr int atoms_of(int block) { return 64 / block; }  // pieces of 128 rows in a stage
 

@@ -443,10 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const int row = quad * 32 + lane, o0 = U.f * 128 + quad * 32, o = o0 + lane;
             float *part = reinterpret_cast<float *>(ring);
             const bool whole = cl == 1 && a.out_bf16 && a.out_vec && o0 + 32 <= a.N;
-            // both factors at once where their product keeps its bits
-            const float both = tx * tw;
-            const bool one = both >= 7.888609e-31f && both <= 1.2676506e30f;  // 2^-100, 2^100
-            const float f1 = one ? both : tx, f2 = one ? 1.0f : tw;
+            const Factors f = factors_of(tx, tw);
+            const float f1 = f.a, f2 = f.b;
 #pragma unroll 1
             for (int c0 = (warp >> 2) * 16; c0 < U.n; c0 += 32) {
                 const int n = U.n - c0;  // tokens of these columns

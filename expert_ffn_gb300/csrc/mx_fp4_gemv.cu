@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a)
     for (int o = 16; o; o >>= 1)
         acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
     if (lane == 0 && live) {
-        const float y = 0.25f * acc * (a.tx ? *a.tx : 1.0f) * (a.tw ? *a.tw : 1.0f);
+        const Factors t = factors_of(a.tx ? *a.tx : 1.0f, a.tw ? *a.tw : 1.0f);
+        const float y = 0.25f * acc * t.a * t.b;
         if (a.out_bf16)
             static_cast<uint16_t *>(a.out)[row] = f2bf(y);
         else

@@ -1,4 +1,4 @@
-"""The 4-bit operators at their edges: a handle built on another stream than the current one.
+"""The 4-bit operators at their edges: a handle built on another stream than the current one, factors of any size.
 
 Tolerances are those of the products' own tests."""
 from __future__ import annotations
@@ -6,7 +6,7 @@ from __future__ import annotations
 import pytest
 
 import expert_ffn_gb300 as mx
-from tests.test_gpu_fp4 import check_product, operands, random_scales, workspace
+from tests.test_gpu_fp4 import check_product, matmul, operands, pack, random_scales, scale_rows, values, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,27 @@ def test_weights_of_a_side_stream_while_the_current_one_is_busy(as_handle):
     torch.cuda.synchronize()
     assert torch.equal(other.packed, clean)
     check_product(out, X, W[0], K)
+
+
+# one row by integers and by the tensor cores, more rows, clusters
+@pytest.mark.parametrize("M,N,K", [(1, 300, 30), (1, 300, 500), (1, 4096, 7000), (20, 300, 30), (20, 300, 500), (20, 300, 6000), (300, 520, 300)])
+@pytest.mark.parametrize("tx,tw", [(-120, 120), (120, -120), (-126, 126), (126, -126), (-100, 60), (118, -12), (-12, 118), (60, -126),
+                                   (20, -126), (-126, 20)])
+@pytest.mark.parametrize("top", [2.0 ** -9, 16.0, 448.0])
+def test_factors_that_make_up_for_one_another(M, N, K, tx, tw, top):
+    """Neither factor alone takes the sums out of fp32's range where the result is in it."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + N + K)
+    xc = torch.randint(0, 16, (M, K), device="cuda", generator=g, dtype=torch.uint8)
+    wc = torch.randint(0, 16, (1, N, K), device="cuda", generator=g, dtype=torch.uint8)
+    scales = [torch.full(shape, top, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+              for shape in ((M, -(-K // 16)), (1, N, -(-K // 16)))]
+    t = [torch.full((1,), 2.0 ** e, device="cuda") * 1.37 for e in (tx, tw)]
+    weight = mx.Fp4Weight(pack(wc), scales[1].view(torch.float8_e4m3fn), t[1], cols=K)
+    X = values(xc, scales[0], 16, t[0].double())
+    W = values(wc, scales[1], 16, t[1].double().view(1, 1, 1))
+    mag = float((X.abs() @ W[0].abs().T).max())
+    if not 2.0 ** -112 < mag < 2.0 ** 127:
+        pytest.skip("the result itself leaves fp32's range")
+    check_product(matmul(pack(xc), scale_rows(scales[0], K, 16), t[0], weight, torch.float32), X, W[0], K)
