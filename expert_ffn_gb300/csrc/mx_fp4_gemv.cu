@@ -54,6 +54,18 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
     return f;
 }
 
+// acc + n f g for a block's sum n of products.  Two e8m0 scales may leave fp32's range together where the block's term does
+// not (n = 0, or the one far below 1), so the smaller meets n first, exactly; two e4m3 scales do not.
+template <int BLOCK>
+__device__ __forceinline__ float add_block(float acc, int n, float f, float g)
+{
+    if (BLOCK == 16)
+        return fmaf((float)n, f * g, acc);
+    float lo;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(f), "f"(g));
+    return fmaf((float)n * lo, fmaxf(f, g), acc);
+}
+
 // Read once: kept out of L1.  (Not by the read-only path: the launch may have begun before its predecessor's end.)
 __device__ __forceinline__ uint4 load_once(const void *p)
 {
@@ -69,7 +81,7 @@ template <int BLOCK>
 __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a)
 {
     constexpr int NA = atoms_of(BLOCK), NB = 32 / BLOCK, PER = kStageCols / BLOCK;  // blocks of a lane's piece, of a stage
-    extern __shared__ __align__(16) uint8_t xs[];  // 2q of the row [padded], then its scales
+    extern __shared__ __align__(16) uint8_t xs[];  // 2q of the row [padded], then a quarter of its scales
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int chunks = (a.K + kChunk - 1) / kChunk, padded = chunks * kChunk;
     float *fs = reinterpret_cast<float *>(xs + padded);
@@ -108,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a)
         reinterpret_cast<uint2 *>(xs)[i] = make_uint2(signed_bytes(q), signed_bytes(q >> 16));
     }
     for (int b = tid; b < padded / BLOCK; b += kThreads)
-        fs[b] = b * BLOCK < a.K ? scale_value<BLOCK>(a.sx[(int64_t)(b / PER) * PER + b % PER]) : 0.0f;
+        fs[b] = b * BLOCK < a.K ? 0.25f * scale_value<BLOCK>(a.sx[(int64_t)(b / PER) * PER + b % PER]) : 0.0f;
     __syncthreads();
 
     float acc = 0.0f;
@@ -135,14 +147,14 @@ __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
                 if (col + b * BLOCK < a.K)  // (a scale behind the last block is not read)
-                    acc = fmaf((float)(p[b] - 2 * n[b]), scale_value<BLOCK>(sc >> (8 * b) & 255u) * fs[col / BLOCK + b], acc);
+                    acc = add_block<BLOCK>(acc, p[b] - 2 * n[b], scale_value<BLOCK>(sc >> (8 * b) & 255u), fs[col / BLOCK + b]);
         }
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
     if (lane == 0 && live) {
         const Factors t = factors_of(a.tx ? *a.tx : 1.0f, a.tw ? *a.tw : 1.0f);
-        const float y = 0.25f * acc * t.a * t.b;
+        const float y = acc * t.a * t.b;
         if (a.out_bf16)
             static_cast<uint16_t *>(a.out)[row] = f2bf(y);
         else

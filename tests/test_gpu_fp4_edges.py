@@ -1,4 +1,5 @@
-"""The 4-bit operators at their edges: a handle built on another stream than the current one, factors of any size.
+"""The 4-bit operators at their edges: a handle built on another stream than the current one, factors and scales of any
+size.
 
 Tolerances are those of the products' own tests."""
 from __future__ import annotations
@@ -61,3 +62,22 @@ def test_factors_that_make_up_for_one_another(M, N, K, tx, tw, top):
     if not 2.0 ** -112 < mag < 2.0 ** 127:
         pytest.skip("the result itself leaves fp32's range")
     check_product(matmul(pack(xc), scale_rows(scales[0], K, 16), t[0], weight, torch.float32), X, W[0], K)
+
+
+# (2^a and 2^b: scales of a block of the rows and of the matrix; x and w: one code of each there, the others are 0)
+@pytest.mark.parametrize("M", [1, 2, 40])
+@pytest.mark.parametrize("a,b,x,w", [(100, 100, 0, 2), (127, 127, 0, 7), (64, 64, 0, 0), (64, 64, 1, 1), (65, 64, 1, 1), (127, 1, 1, 1),
+                                     (1, 127, 9, 1), (127, -120, 7, 7), (-120, 127, 7, 15), (-100, -100, 7, 7), (-127, 127, 1, 1),
+                                     (-127, 120, 7, 7), (-70, -75, 2, 2)])
+def test_e8m0_scales_whose_product_leaves_the_range(M, a, b, x, w):
+    """A block's term counts as the definition has it, whatever its two scales are by themselves."""
+    import torch
+    K, N = 96, 130
+    xc, wc = (torch.full(shape, 2, dtype=torch.uint8, device="cuda") for shape in ((M, K), (1, N, K)))
+    xs, ws = (torch.full(shape, 127, dtype=torch.uint8, device="cuda") for shape in ((M, 3), (1, N, 3)))
+    xc[:, 32:64], wc[..., 32:64] = 0, 0
+    xc[:, 37], wc[..., 37] = x, w
+    xs[:, 1], ws[..., 1] = 127 + a, 127 + b
+    weight = mx.Fp4Weight(pack(wc), ws.view(torch.float8_e8m0fnu), cols=K)
+    got = matmul(pack(xc), scale_rows(xs, K, 32), None, weight, torch.float32)
+    check_product(got, values(xc, xs, 32), values(wc, ws, 32)[0], K)
