@@ -523,19 +523,22 @@ __device__ __forceinline__ void select_token(const Args &a, int t, int lane, uin
     __syncwarp();
 
     // The weights of the chosen, a lane each, from their logits.  (A renormalised softmax goes by the largest
-    // chosen one, which in runs need not be the largest of all; so do sigmoids that fp32 would lose, which are e^l but for a
-    // part of e^l.)
+    // chosen one, which in runs need not be the largest of all.  So do renormalised sigmoids below 1/2, as e^(l - m) / (1 + e^l):
+    // by themselves fp32 would lose them from -88 on, whatever they are to the largest.)
     float w = 0.0f;
     const float x = lane < a.K ? load1(a, (int64_t)t * a.ld + my_idx) : -INFINITY;
     bool by_exp = soft;
     if (a.renorm) {
         const float top = unordered(__reduce_max_sync(FULL, ordered(x)));
-        by_exp = soft || (top < -60.0f && top > -700.0f);
+        by_exp = soft || (top < 0.0f && top > -700.0f);
         if (by_exp)
             m = top;
     }
-    if (lane < a.K)
+    if (lane < a.K) {
         w = !by_exp ? 1.0f / (1.0f + expf(-x)) : x == m ? 1.0f : expf(x - m);
+        if (by_exp && !soft)
+            w /= 1.0f + expf(x);
+    }
     if (a.renorm)
         z = warp_sum(w);
     if (soft || a.renorm)
