@@ -106,16 +106,11 @@ __device__ __forceinline__ void affine_acc(float (&acc)[4], const float (&R)[4],
     acc[3] = fmaf(c8, X[3], fmaf(s8, R[3], acc[3]));
 }
 
-template <bool SMEM>
+// (From global memory too by plain loads: the launch before, whose end this one did not wait for to begin, writes it.)
 __device__ __forceinline__ void load_b(const uint16_t *p, uint4 &v0, uint4 &v1)
 {
-    if constexpr (SMEM) {
-        v0 = *reinterpret_cast<const uint4 *>(p);
-        v1 = *reinterpret_cast<const uint4 *>(p + 8);
-    } else {
-        v0 = ldg_u4(p);
-        v1 = ldg_u4(p + 8);
-    }
+    v0 = *reinterpret_cast<const uint4 *>(p);
+    v1 = *reinterpret_cast<const uint4 *>(p + 8);
 }
 
 // Routing metadata staged in shared memory.
@@ -322,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int sp = 0; sp < NS; ++sp) {
                         uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
                         if (rowoff[nt] >= 0)
-                            load_b<BS>(bsrc + sp * TD + rowoff[nt] + kGroup * g + 16 * c, v0, v1);
+                            load_b(bsrc + sp * TD + rowoff[nt] + kGroup * g + 16 * c, v0, v1);
                         mma_r(A, v0, v1, R);
                     }
                     const float x0 = xg[ct0[nt] * G + g], x1 = xg[ct1[nt] * G + g];
@@ -534,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float R[4] = {0.f, 0.f, 0.f, 0.f}, X[4] = {0.f, 0.f, 0.f, 0.f};
                     uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
                     if (rowoff[nt] >= 0)
-                        load_b<false>(bp[nt] + rowoff[nt] + kGroup * g + 16 * c, v0, v1);
+                        load_b(bp[nt] + rowoff[nt] + kGroup * g + 16 * c, v0, v1);
                     mma_r(A, v0, v1, R);
                     mma_x(v0, v1, X);
                     affine_acc(acc[nt], R, X, s0, s8, b0, b8);

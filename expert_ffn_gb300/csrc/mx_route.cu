@@ -34,12 +34,14 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kXPad = 68;  // floats per staged group row (64 + 4): conflict-free 16-byte reads
 
+// Activations by plain loads: the launch may have begun before the end of the one that writes them (a norm, the
+// layer before), and the read-only path is for memory that nothing writes while a launch lives.
 __device__ __forceinline__ float load_x(const RouteArgs &a, int t, int col)
 {
     const size_t i = (size_t)t * a.D + col;
     if (a.x_dtype == 1)
-        return bf2f(__ldg(reinterpret_cast<const uint16_t *>(a.x) + i));
-    return __ldg(reinterpret_cast<const float *>(a.x) + i);
+        return bf2f(reinterpret_cast<const uint16_t *>(a.x)[i]);
+    return reinterpret_cast<const float *>(a.x)[i];
 }
 
 // The 64 activations of group g of token t, with 16-byte loads.
@@ -50,7 +52,7 @@ __device__ __forceinline__ void load_group(const RouteArgs &a, int t, int g, flo
         const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(a.x) + i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint4 w = __ldg(p + j);
+            const uint4 w = p[j];
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -62,7 +64,7 @@ __device__ __forceinline__ void load_group(const RouteArgs &a, int t, int g, flo
         const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.x) + i);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const float4 w = __ldg(p + j);
+            const float4 w = p[j];
             v[4 * j] = w.x;
             v[4 * j + 1] = w.y;
             v[4 * j + 2] = w.z;
