@@ -1,8 +1,10 @@
-"""The RMS norm at both ends of its types' range, bit for bit against its definition in fp64 (as in its own tests)."""
+"""The RMS norm at both ends of its types' range and of more rows than there are CTAs, bit for bit against its definition
+in fp64 (as in its own tests)."""
 from __future__ import annotations
 
 import pytest
 
+import expert_ffn_gb300 as mx
 from tests.test_gpu_rmsnorm import check, dt, make, reference, run
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +45,22 @@ def test_rows_of_subnormal_values():
     got = run(x, None, None, eps=0.0, out_dtype=dt("f32"), sum_=False, q=False)
     check(got, reference(x, None, None, 0.0, 0.0, dt("f32"), False))
     assert (got["out"][:2] > 0.99).all() and (got["out"][4:] == float("inf")).all()
+
+
+# more rows than CTAs, for one to eight pieces of eight columns a thread, whole and ragged
+@pytest.mark.parametrize("rows,cols", [(16000, 256), (16000, 251), (1000, 4096), (1000, 4090), (400, 4104), (400, 5001), (330, 8192),
+                                       (330, 8200), (330, 16383), (320, 16400), (320, 20003)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["apart", "sum is residual", "sum is x, out is residual", "out is x"])
+def test_several_rows_to_a_block(rows, cols, dtype, where):
+    """A row's loads are under way while the one before is worked on, and may be written where that one's were."""
+    import torch
+    x, r, w = make(rows, cols, 1, dtype), make(rows, cols, 2, dtype), make(1, cols, 3, "bf16")[0]
+    want = reference(x, w, r, 1e-6, 0.0, dt(dtype), False)
+    if where == "apart":
+        check(run(x, w, r, out_dtype=dt(dtype)), want)
+        return
+    kw = {"sum is residual": dict(residual_out=r), "sum is x, out is residual": dict(residual_out=x, out=r), "out is x": dict(out=x)}[where]
+    mx.fp8_rmsnorm(x, w, residual=r, **kw)
+    torch.cuda.synchronize()
+    check({"sum" if k == "residual_out" else k: t for k, t in kw.items()}, want)
