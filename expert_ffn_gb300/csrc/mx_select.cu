@@ -591,33 +591,27 @@ __device__ __forceinline__ void scan_counts(int *cnt, int E)
 // last block's placing bits and places [E][words].
 size_t smem_bytes(int warps, int E, int words = 0) { return (size_t)(warps * E + 2 * E + 1 + 2 * words * E) * 4; }
 
-// All tokens' slots by one block of THREADS threads, the other blocks' choices among them.  cnt [E + 1], bits and
-// places [E][a.words]: shared memory.
+// All tokens' slots, at most kLastSlots, by one block of THREADS threads, the other blocks' choices among them.  cnt
+// [E + 1], bits and places [E][a.words]: shared memory.
 template <int THREADS>
 __device__ __forceinline__ void place_all(const Args &a, int *cnt, uint32_t *bits, int *places)
 {
-    constexpr int EACH = 8;  // slots of a thread under way
+    constexpr int EACH = kLastSlots / THREADS;  // slots of a thread
+    static_assert(EACH * THREADS == kLastSlots, "slots");
     const int tid = threadIdx.x, n = a.T * a.K, W = a.words;
+    int e[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        e[i] = tid + i * THREADS < n ? __ldcg(a.idx + tid + i * THREADS) : -1;
     for (int i = tid; i < a.E * W; i += THREADS)
         bits[i] = 0;
-    int e[EACH];
-    auto load = [&](int s0) {
-#pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            e[i] = s0 + tid + i * THREADS < n ? __ldcg(a.idx + s0 + tid + i * THREADS) : -1;
-    };
-    load(0);
     __syncthreads();
-    for (int s0 = 0; s0 < n; s0 += EACH * THREADS) {
-        if (s0)
-            load(s0);
 #pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            if (e[i] >= 0) {
-                const int t = (s0 + tid + i * THREADS) / a.K;
-                atomicOr(bits + e[i] * W + (t >> 5), 1u << (t & 31));
-            }
-    }
+    for (int i = 0; i < EACH; ++i)
+        if (e[i] >= 0) {
+            const int t = (tid + i * THREADS) / a.K;
+            atomicOr(bits + e[i] * W + (t >> 5), 1u << (t & 31));
+        }
     __syncthreads();
     for (int x = tid; x < a.E; x += THREADS) {
         int run = 0;
@@ -632,16 +626,12 @@ __device__ __forceinline__ void place_all(const Args &a, int *cnt, uint32_t *bit
     scan_counts<THREADS / 32>(cnt, a.E);
     for (int x = tid; x <= a.E; x += THREADS)
         a.offsets[x] = cnt[x];
-    for (int s0 = 0; s0 < n; s0 += EACH * THREADS) {
-        if (n > EACH * THREADS)
-            load(s0);
 #pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            if (e[i] >= 0) {
-                const int s = s0 + tid + i * THREADS, t = s / a.K, at = e[i] * W + (t >> 5);
-                a.perm[cnt[e[i]] + places[at] + __popc(bits[at] & ((1u << (t & 31)) - 1u))] = s;
-            }
-    }
+    for (int i = 0; i < EACH; ++i)
+        if (e[i] >= 0) {
+            const int s = tid + i * THREADS, t = s / a.K, at = e[i] * W + (t >> 5);
+            a.perm[cnt[e[i]] + places[at] + __popc(bits[at] & ((1u << (t & 31)) - 1u))] = s;
+        }
 }
 
 template <int P, int WARPS, bool GROUP>
@@ -679,24 +669,25 @@ __global__ void __launch_bounds__(32 * WARPS, many_warps(P) / WARPS) select_kern
     }
     if (!GROUP)
         return;
-    if (a.words) {
-        // the last block to come here puts all slots in order
-        __shared__ bool last_block;
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            last_block = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
-            if (last_block)
-                *a.ticket = 0;  // (as the next call finds it)
-        }
-        __syncthreads();
-        if (!last_block)
+    if constexpr (WARPS == kWarps)  // (more warps are for more tokens than those)
+        if (a.words) {
+            // the last block to come here puts all slots in order
+            __shared__ bool last_block;
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                last_block = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+                if (last_block)
+                    *a.ticket = 0;  // (as the next call finds it)
+            }
+            __syncthreads();
+            if (!last_block)
+                return;
+            __threadfence();
+            uint32_t *all = reinterpret_cast<uint32_t *>(cnt + a.E + 1);
+            place_all<THREADS>(a, cnt, all, reinterpret_cast<int *>(all + a.words * a.E));
             return;
-        __threadfence();
-        uint32_t *all = reinterpret_cast<uint32_t *>(cnt + a.E + 1);
-        place_all<THREADS>(a, cnt, all, reinterpret_cast<int *>(all + a.words * a.E));
-        return;
-    }
+        }
     __syncthreads();
     if (a.runs > 1) {
         for (int e = threadIdx.x; e < a.E; e += THREADS)
