@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a)
     for (int i = 0; i < kAhead; ++i)
         fetch(i, v[i], s[i]);
 
+    const Factors t = factors_of(a.tx ? *a.tx : 1.0f, a.tw ? *a.tw : 1.0f);
+
     for (int i = tid; i < padded / 8; i += kThreads) {
         uint32_t q = 0;
         if (8 * i < a.K) {
@@ -153,7 +155,6 @@ __global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvArgs a)
     for (int o = 16; o; o >>= 1)
         acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
     if (lane == 0 && live) {
-        const Factors t = factors_of(a.tx ? *a.tx : 1.0f, a.tw ? *a.tw : 1.0f);
         const float y = acc * t.a * t.b;
         if (a.out_bf16)
             static_cast<uint16_t *>(a.out)[row] = f2bf(y);
