@@ -37,7 +37,7 @@ struct GemmArgs {
     int stages, cl;          // ring depth, cluster size (split of the inner dimension)
 };
 
-// One row (mx_fp4_gemv.cu), of up to about 30000 columns (it lies in shared memory).
+// One row (mx_fp4_gemv.cu), which lies in shared memory; the rule that takes it ends at 6144 columns.
 struct GemvArgs {
     int K, N;
     const uint8_t *q, *sx;   // the row, its scales

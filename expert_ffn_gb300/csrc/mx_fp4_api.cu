@@ -84,7 +84,7 @@ mx_status check_rows(const mx_fp4_rows *r, const char *name, bool operand)
 }
 
 // One row by mx_fp4_gemv.cu, while its CTAs' rounds over the SMs have few steps of 1024 columns: 2112 x 2816 (one round
-// of three) 3.3 us, by the tensor cores 5.1; 2112 x 4096 3.8, 5.3; 3328 x 2816 (two of three) 4.4, 5.2; 4096 x 4096 (two of
+// of three) 3.1 us, by the tensor cores 5.1; 2112 x 4096 3.8, 5.3; 3328 x 2816 (two of three) 4.4, 5.2; 4096 x 4096 (two of
 // four) 5.5, 5.6; 704 x 8192 (one of eight) 5.4, 5.4; 14336 x 4096 14.5, 6.8.
 bool one_row(int rows, const int32_t *offsets, const mx_fp4_matrix &w)
 {

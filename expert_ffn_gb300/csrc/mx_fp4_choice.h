@@ -54,7 +54,7 @@ inline Choice choose(int rows, bool grouped, int E, int FT, int KB, int sms)
         }
     }
     // Few units of many stages: clusters of four split the inner dimension, of eight where a few such clusters do.  A
-    // cluster costs 1 to 1.5 us: 20 x 4096 x 4096 (16 stages) whole 6.2 us, in four 6.0, 64 rows 6.6, 6.8; 2112 x 5120 6.8, 5.9 and
+    // cluster costs 1 to 1.5 us: 20 x 4096 x 4096 (16 stages, blocks of 16) whole 6.2 us, in four 6.0, 64 rows 6.6, 6.8; 2112 x 5120 6.8, 5.9 and
     // 7.3, 6.8; 4096 x 2048 4.8, 5.3.  In two it gains nothing while more do not fit (20 x 7680 x 8192 9.9 and 10.0 us), and 17
     // units in eight wait for room (a GPC holds one or two clusters of eight; 20 x 2112 x 8192 10.9 us, in four 6.4).  A
     // cluster has one unit: the kernel keeps no partial sums of a second.

@@ -29,11 +29,11 @@
 // cluster of `cl` CTAs splits the inner dimension of one unit, and its partial sums are added
 // through distributed shared memory in rank order.
 //
-// What bounds it: 4096 x 4096 x 4096 takes 30 us, of which the MMAs are 18 (7.6 PFLOP/s, what
-// another 4096 columns of K add); the rest is launch, the first fill, the last tile's results,
-// and results that reach memory.  32768 rows of 256 matrices 1024 x 4096 are bound by HBM, 118 us
-// (0.85 of the copy rate); 64 x 4096 x 4096 by its chain, 6.2 us: launch, fill, the MMAs of
-// sixteen stages.
+// What bounds it: 4096 x 4096 x 4096 takes 30 us, of which another 4096 columns of K add 18 (7.6
+// PFLOP/s: the slope of this form, K = 64 by one CTA; the chip's FP4 rate is higher); the rest is launch, the first fill, the
+// last tile's results, and results that reach memory.  32768 rows of 256 matrices 1024 x 4096 are bound by HBM, 119 us
+// (0.85 of the copy rate); 64 x 4096 x 4096 by its chain on 32 SMs, 6.6 us (blocks of 32: 6.3): launch, fill,
+// the MMAs of sixteen stages.  So are a few rows of grouped matrices, which no cluster splits: 8 rows of 8 matrices 704 x 2816 6.6 us.
 //
 // Every wait is bounded: a wait that gives up sets the caller's error word and ends the
 // CTA's work.

@@ -13,17 +13,19 @@
 //
 // Exactness.  Where an fp32 score (with a bias, or the sum of a run's two best)
 // decides, the chosen ones and the next are looked at once more: any two neighbours
-// within their error bounds, about one token in a thousand, send the token to a loop that
-// compares the candidates in fp64.  Without a bias experts compare by their logits, which no
-// rounding has touched.
+// within their error bounds send the token to a loop that compares the candidates in fp64.
+// With random biases that is about one token in a thousand of fp32 logits with sigmoids; but bf16 logits
+// are often equal, and with a bias of zeros, as a balance bias begins, some third of the tokens go there: 4096 x 256
+// without runs, slots grouped, sigmoid 16.6 us (random biases 14.3), softmax 29.4 (21.4).  Without
+// a bias experts compare by their logits, which no rounding has touched (12.5).
 //
 // Grouping.  One selecting block (up to eight tokens) puts its slots in order itself; of few the last to end those of
 // all.  Of more each leaves its tokens' counts by expert, and the placing kernel's blocks each add up all of them (bytes, an expert's
 // neighbouring, so that 4096 tokens of 256 experts are 32 KB and four blocks' one dp4a) and put
 // their own tokens' slots in order.
 //
-// What bounds it: 4096 x 256 fp32 logits are 4 MB, 0.6 us of HBM; instructions (some 600 a token) and
-// a launch or two are the rest.
+// What bounds it: 4096 x 256 fp32 logits are 4 MB, 0.6 us of HBM.  Choosing takes 9.0 us of the whole 15.4: a warp's chain
+// of some 1170 instructions a token (31 % of the issue slots, 48 % of the warps), then the placing launch.
 #include "mx_common.cuh"
 #include "mx_host.h"
 #include "mx_internal.h"
@@ -39,7 +41,7 @@ namespace {
 
 // Warps of a selecting block: eight.  When many tokens' slots are grouped 32 (16 for more than 256 experts,
 // whose keys take more registers), so that the placing blocks have fewer counts to add up: 4096 x 256 in runs
-// 15.1 us (by eight 18.9), 2048 13; but 32 warps on one SM take each other's time: 333 x 60 by eight 6.8 us, by
+// 15.4 us (by eight 18.9), 2048 13; but 32 warps on one SM take each other's time: 333 x 60 by eight 6.8 us, by
 // 32 8.1.
 constexpr int kWarps = 8;
 constexpr int many_warps(int P) { return P <= 8 ? 32 : 16; }
@@ -48,8 +50,10 @@ constexpr int kRuns = 512;    // selecting blocks when many tokens' slots are gr
 constexpr int kMaxRun = 224;  // tokens of a block at most (its counts are bytes)
 constexpr int kPlaceWarps = 16, kPlaceBlocks = 128;
 constexpr int kMaxTokens = 1 << 30;
-// Slots up to which the last selecting block places them all: one launch less, of about 2.5 us on the host, for 9 tokens 5.4
-// us instead of 5.6, 333 x 60 top-4 7.0 instead of 6.5, 256 x 256 top-8 9.4 instead of 8.5 (512 x 256 top-8 15.0, 8.9).
+// Slots up to which the last selecting block places them all: one launch less.  That is for single calls, which the host
+// bounds (2.5 us a launch; 333 x 60 top-4 7.9 us a call instead of 10.3); in a captured graph it costs up to 0.9 us of the
+// device's time: 9 tokens 5.4 us instead of 5.6, 333 x 60 top-4 6.8 instead of 6.5, 256 x 256 top-8 9.4 instead of 8.5
+// (512 x 256 top-8 15.0 instead of 8.9).
 constexpr int kLastSlots = 2048;
 
 struct Args {

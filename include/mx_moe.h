@@ -576,6 +576,9 @@ MX_API mx_status mx_fp4_pack_scales(const void *scales, int64_t ld, int rows, in
  *                q = e2m1(fl32(x * fl32(1 / fl32(s t)))), zero where fl32(s t) < 2^-126
  * rounded to nearest, ties to even, at most 6; a zero keeps its sign.  A block with
  * a NaN or an infinity gets a NaN scale and zeros, and dequantises to NaN.
+ * The e8m0 scale clips nothing.  It is not that of the OCP MX conversion, 2^(floor(log2 a) - 2), which
+ * is half of it where a is above 1.5 times the power of two below it, and clips the block's largest
+ * values there: the codes of such blocks differ.
  *   x    device [rows][cols] of `dtype`, row pitch ldx elements
  *   out  only its rows' ceil(cols / 2) bytes and the scales are written
  */
@@ -608,8 +611,9 @@ MX_API size_t mx_fp4_matmul_workspace_bytes(const mx_fp4_matrix *w, int rows);
  * one another than fp32 tells apart are compared in fp64, and without a bias
  * experts are compared by their logits.  A NaN logit counts as -inf; a c or a
  * run's score that is NaN (by the bias) ranks as -inf.  Logits that equal the largest
- * share the softmax where that is infinite.  Where the chosen sigmoids are all
- * below e^-700, they count as 0, and so do their renormalised weights.
+ * share the softmax where that is infinite, and so do the chosen in a renormalised one
+ * where all of them are -inf.  Where the chosen sigmoids are all below e^-700, they count
+ * as 0, and so do their renormalised weights.
  * ------------------------------------------------------------------------ */
 typedef enum { MX_SOFTMAX = 0, MX_SIGMOID = 1 } mx_score;
 
